@@ -1,4 +1,5 @@
-"""MI355X-native (gfx950) HLQ/HOT linear-layer backward.
+"""MI355X-native (gfx950) HLQ/HOT linear-layer backward, with the operators of a
+training step around it.
 
 The compute lives in ``libhlq.so`` (hand-written HIP kernels behind the C ABI
 of ``include/hlq.h``); :mod:`hadamard_rank_linear_amd.hlq` is its ctypes
@@ -19,7 +20,12 @@ _BINDING_NAMES = {
     "HLQ_LQS_STATS", "HLQ_LQS_THRESHOLD", "hlq_conv_backward",
     "hlq_conv_backward_workspace_size", "hlq_conv_gemm_acc", "hlq_linear_backward_ablation",
     "hlq_ablation_workspace_size", "VARIANT_NAMES", "HLQ_VAR_HQ4", "HLQ_VAR_Q4", "HLQ_VAR_HLA8_INT",
-    "HLQ_VAR_HLA8_EXT",
+    "HLQ_VAR_HLA8_EXT", "HLQ_NORM_L2", "HLQ_NORM_INF", "hlq_layer_norm_forward",
+    "hlq_layer_norm_backward", "hlq_layer_norm_backward_workspace_size",
+    "hlq_token_logprob_forward", "hlq_token_logprob_backward", "hlq_policy_loss",
+    "hlq_policy_loss_logits", "hlq_policy_loss_workspace_size", "hlq_preference_loss",
+    "hlq_preference_loss_workspace_size", "hlq_clip_grad_norm",
+    "hlq_clip_grad_norm_workspace_size",
 }
 
 

@@ -18,7 +18,9 @@ SOURCES = [("hlq_tr.hip", f"hlq_tr{n}", [f"-DHLQ_TR_N={n}"]) for n in (16, 32, 6
     ("hlq_gemm.hip", "hlq_gemm", []), ("hlq_lqs.hip", "hlq_lqs", []),
     ("hlq_acbp.hip", "hlq_acbp", []), ("hlq_noalloc.hip", "hlq_noalloc", []),
     ("hlq_ablation.hip", "hlq_ablation", []),
-    ("hlq_api.cpp", "hlq_api", [])]
+    ("hlq_norm.hip", "hlq_norm", []), ("hlq_logprob.hip", "hlq_logprob", []),
+    ("hlq_clip.hip", "hlq_clip", []),
+    ("hlq_api.cpp", "hlq_api", []), ("hlq_train_api.cpp", "hlq_train_api", [])]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -194,7 +194,7 @@ hlq::TrArgs make_tr_args(const Layout& L, const void* g_y, int gy_dtype, const u
 
 extern "C" {
 
-int hlq_version(void) { return 200; }
+int hlq_version(void) { return 210; }
 
 const char* hlq_status_string(int status) {
   switch (status) {
@@ -209,6 +209,7 @@ const char* hlq_status_string(int status) {
     case HLQ_ERR_OVERFLOW: return "an INT32 accumulator could overflow (O or T*rank/block too large)";
     case HLQ_ERR_WORKSPACE: return "workspace missing or too small";
     case HLQ_ERR_HIP: return "HIP runtime error while enqueueing";
+    case HLQ_ERR_VALUE: return "a scalar argument is out of its range";
     default: return "unknown status";
   }
 }

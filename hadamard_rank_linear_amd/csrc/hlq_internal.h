@@ -209,6 +209,91 @@ hipError_t launch_forward(const uint16_t* x, const uint16_t* w, int64_t T, int64
                           float* y32, uint16_t* y16, uint8_t* codes, float* scales,
                           hipStream_t s);
 
+// ---- operators of a training step around the linear layer (dtype and
+// param_dt: HLQ_F32 or HLQ_BF16 as in hlq.h)
+
+// Layer norm forward (hlq_norm.hip); residual and h, bias may be null.
+struct NormFwd {
+  const void *x, *residual, *weight, *bias;
+  int param_dt;
+  int64_t T, C;
+  float eps;
+  void *y, *h;
+  float *mean, *rstd;
+};
+// Layer norm backward; g_h and g_bias may be null.  part: parts x 2 x C
+// partial column sums (parts = norm_parts(T, C, dtype)).
+struct NormBwd {
+  const void *g_y, *h, *g_h;
+  const float *mean, *rstd;
+  const void* weight;
+  int param_dt;
+  int64_t T, C, parts;
+  void *g_x, *g_weight, *g_bias;
+  float* part;
+};
+int64_t norm_parts(int64_t T, int64_t C, int dtype);
+hipError_t launch_norm_forward(const NormFwd& a, int dtype, hipStream_t s);
+hipError_t launch_norm_backward(const NormBwd& a, int dtype, hipStream_t s);
+
+// Rows of logits (hlq_logprob.hip): row t of T at element t * ld, V long.
+struct LogitArgs {
+  const void* logits;
+  const int64_t* targets;
+  int64_t T, V, ld, g_ld;
+  double scale;
+  float c;  // scale * log2(e): exp(scale x) = 2^(c x)
+  float *logprob, *stats;
+  const float* g_logprob;
+  void* g_x;
+};
+// Policy loss on log probabilities; weight and ref_logprob may be null.
+// terms: T x 3 addends of sums.
+struct PolicyArgs {
+  const float *logprob, *old_logprob, *advantage, *weight, *ref_logprob;
+  int64_t T;
+  double clip_low, clip_high, kl_coef;
+  float *sums, *g_logprob;
+  double* terms;
+};
+// Preference loss over P pairs; weight and ref_logprob may be null.  terms: P.
+struct PrefArgs {
+  const float *logprob, *ref_logprob, *weight;
+  const int64_t* start;
+  int64_t P, T;
+  double beta, smoothing;
+  int mean;
+  float *loss, *margin, *g_logprob;
+  double* terms;
+};
+hipError_t launch_logprob(const LogitArgs& a, int dtype, hipStream_t s);
+hipError_t launch_logprob_grad(const LogitArgs& a, int dtype, hipStream_t s);
+hipError_t launch_policy_logits(const LogitArgs& a, const PolicyArgs& p, int dtype, hipStream_t s);
+hipError_t launch_policy(const PolicyArgs& p, hipStream_t s);
+hipError_t launch_preference(const PrefArgs& p, hipStream_t s);
+
+// Gradient clipping (hlq_clip.hip): part of a list of tensors, passed by value
+// (a kernel's arguments hold 4 KiB).  size: elements, at most 2^30, with bit 31
+// set for bf16.  Tensor i is chunks first[i] .. first[i + 1] - 1 of CLIP_CHUNK
+// elements; chunks: all of them.
+constexpr int CLIP_LIST = 160;
+constexpr int64_t CLIP_MAX_SIZE = int64_t(1) << 30;
+constexpr int CLIP_CHUNK = 8192;
+constexpr unsigned CLIP_GROUPS = 1024;  // workgroups (partials) per launch at most
+struct ClipList {
+  const void* grad[CLIP_LIST];
+  void* out[CLIP_LIST];
+  uint32_t size[CLIP_LIST], first[CLIP_LIST];
+  uint32_t chunks;
+  int count, in_place;
+};
+static_assert(sizeof(ClipList) <= 4000, "kernel arguments");
+hipError_t launch_clip_norm(const ClipList& l, int kind, double* part, unsigned groups,
+                            hipStream_t s);
+// norm (null: not written) by the first workgroup.
+hipError_t launch_clip_scale(const ClipList& l, int kind, const double* part, int64_t parts,
+                             double max_norm, double* norm, unsigned groups, hipStream_t s);
+
 hipError_t launch_gemm_finalize(const int32_t* partial, int splits, int64_t M,
                                 int64_t N, const float* sa, int sa_step,
                                 const float* sb, int sb_step, float alpha, float* C,

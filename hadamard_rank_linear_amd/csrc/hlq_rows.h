@@ -1,0 +1,169 @@
+// Device helpers of the row-wise kernels (layer norm, logits, gradient
+// clipping): 16-byte pieces of rows that start at any element, and wave and
+// workgroup reductions.  Header-only, internal.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "hlq_device.h"
+
+namespace hlq {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// A piece: 16 bytes of a row, 4 fp32 or 8 bf16 elements (dtype DT: 0 or 1).
+template <int DT>
+struct Piece {
+  static constexpr int N = DT == 0 ? 4 : 8;
+  typedef typename std::conditional<DT == 0, float, uint16_t>::type Elem;
+};
+
+// Piece at element e, of which the row holds n (n >= N: all of it, one
+// 16-byte load; the row may start at any element: gfx950 takes element-aligned
+// 16-byte accesses, at one more cache line per wave).  Elements past the row
+// read as zero and are not touched.
+template <int DT>
+__device__ __forceinline__ u32x4 load_piece(const void* base, int64_t e, int64_t n) {
+  typedef typename Piece<DT>::Elem E;
+  const E* p = static_cast<const E*>(base) + e;
+  u32x4 r = {0u, 0u, 0u, 0u};
+  if (n >= Piece<DT>::N) {
+    __builtin_memcpy(&r, p, 16);
+  } else {
+#pragma unroll
+    for (int k = 0; k < Piece<DT>::N; ++k)
+      if (k < n) {
+        if constexpr (DT == 0) r[k] = __float_as_uint(p[k]);
+        else r[k / 2] |= (uint32_t)p[k] << (16 * (k & 1));
+      }
+  }
+  return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void store_piece(void* base, int64_t e, int64_t n, u32x4 r) {
+  typedef typename Piece<DT>::Elem E;
+  E* p = static_cast<E*>(base) + e;
+  if (n >= Piece<DT>::N) {
+    __builtin_memcpy(p, &r, 16);
+  } else {
+#pragma unroll
+    for (int k = 0; k < Piece<DT>::N; ++k)
+      if (k < n) {
+        if constexpr (DT == 0) p[k] = __uint_as_float(r[k]);
+        else p[k] = (uint16_t)(r[k / 2] >> (16 * (k & 1)));
+      }
+  }
+}
+
+// Element k of a piece in fp32 (exact).
+template <int DT>
+__device__ __forceinline__ float piece_at(const u32x4& r, int k) {
+  if constexpr (DT == 0) return __uint_as_float(r[k]);
+  else return (k & 1) ? bf16_hi(r[k / 2]) : bf16_lo(r[k / 2]);
+}
+
+// fp32 values to a piece, each rounded to nearest even when DT is bf16 (the
+// one rounding of an output; v_cvt_pk_bf16_f32).
+template <int DT>
+__device__ __forceinline__ u32x4 make_piece(const float (&v)[Piece<DT>::N]) {
+  u32x4 r;
+  if constexpr (DT == 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = __float_as_uint(v[k]);
+  } else {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const b2 p = __builtin_convertvector((f2){v[2 * k], v[2 * k + 1]}, b2);
+      uint32_t u;
+      __builtin_memcpy(&u, &p, 4);
+      r[k] = u;
+    }
+  }
+  return r;
+}
+
+// N consecutive parameters (weight or bias) from element c of C in fp32;
+// past the end: zero.
+template <int N>
+__device__ __forceinline__ void load_params(const void* base, int dt, int64_t c, int64_t C,
+                                            float (&v)[N]) {
+  const int64_t n = C - c;
+  if (dt == 0) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      const u32x4 r = load_piece<0>(base, c + j, n - j);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[j + k] = __uint_as_float(r[k]);
+    }
+  } else if constexpr (N == 8) {
+    const u32x4 r = load_piece<1>(base, c, n);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = piece_at<1>(r, k);
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + c;
+    if (n >= 4) {
+      uint32_t r[2];
+      __builtin_memcpy(r, p, 8);
+      v[0] = bf16_lo(r[0]); v[1] = bf16_hi(r[0]);
+      v[2] = bf16_lo(r[1]); v[3] = bf16_hi(r[1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = k < n ? bf16_lo(p[k]) : 0.f;
+    }
+  }
+}
+
+// ------------------------------------------------------------ reductions
+// Sum over groups of W neighbouring lanes (W a power of two up to 64); every
+// lane gets its group's sum, added in the same order whatever the lane.
+template <int W, typename V>
+__device__ __forceinline__ V lanes_sum(V v) {
+#pragma unroll
+  for (int m = W / 2; m >= 1; m >>= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
+  return v;
+}
+
+// Over a workgroup of W threads (a multiple of 64, up to 1024).  sm holds
+// W / 64 values and may be used again after the next barrier.
+template <int W, typename V>
+__device__ __forceinline__ V group_sum(V v, V* sm) {
+  v = lanes_sum<64>(v);
+  if constexpr (W > 64) {
+    if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = sm[threadIdx.x & (W / 64 - 1)];
+    v = lanes_sum<W / 64>(v);
+  }
+  return v;
+}
+
+template <int W>
+__device__ __forceinline__ float group_max(float v, float* sm) {
+  v = lanes_max(v);
+  if constexpr (W > 64) {
+    if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = sm[threadIdx.x & (W / 64 - 1)];
+#pragma unroll
+    for (int m = W / 128; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
+  }
+  return v;
+}
+
+// One workgroup per row up to 2^20 workgroups (a launch holds fewer than 2^32
+// threads); kernels step through the rows by the grid.
+static inline dim3 rows_grid(int64_t T) { return dim3((unsigned)(T < (1 << 20) ? T : 1 << 20)); }
+
+}  // namespace hlq

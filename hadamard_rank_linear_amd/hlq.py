@@ -1,4 +1,6 @@
-"""Python binding of libhlq.so, the gfx950 HLQ/HOT linear-layer backward.
+"""Python binding of libhlq.so, the gfx950 HLQ/HOT linear-layer backward and
+the operators of a training step around it (layer norm, token log
+probabilities with the policy and preference losses, gradient clipping).
 
 Argument marshalling only: every step of the backward runs in the HIP kernels
 behind the C ABI declared in ``include/hlq.h``.  torch supplies device memory
@@ -18,6 +20,7 @@ LIB_PATH = os.environ.get("HLQ_LIBRARY") or os.path.join(HERE, "libhlq.so")
 HLQ_F32, HLQ_BF16 = 0, 1
 HLQ_PER_TOKEN, HLQ_PER_TENSOR = 0, 1
 HLQ_SUM, HLQ_MEAN = 0, 1
+HLQ_NORM_L2, HLQ_NORM_INF = 0, 1
 STEP_NAMES = ("tr_max", "tr_reduce", "tr_quant", "gemm_gx", "gemm_gw")
 HLQ_STEPS_ALL = (1 << len(STEP_NAMES)) - 1
 
@@ -40,6 +43,18 @@ EXPORTED = (
     "hlq_lqs_workspace_size",
     "hlq_lqs_accumulate",
     "hlq_lqs_select",
+    "hlq_layer_norm_forward",
+    "hlq_layer_norm_backward_workspace_size",
+    "hlq_layer_norm_backward",
+    "hlq_token_logprob_forward",
+    "hlq_token_logprob_backward",
+    "hlq_policy_loss_workspace_size",
+    "hlq_policy_loss",
+    "hlq_policy_loss_logits",
+    "hlq_preference_loss_workspace_size",
+    "hlq_preference_loss",
+    "hlq_clip_grad_norm_workspace_size",
+    "hlq_clip_grad_norm",
     "hlq_status_string",
     "hlq_version",
 )
@@ -113,6 +128,33 @@ def _load():
     lib.hlq_lqs_select.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.c_double,
                                    ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]
     lib.hlq_lqs_select.restype = I32
+    F64 = ctypes.c_double
+    lib.hlq_layer_norm_forward.argtypes = [P, P, I32, P, P, I32, I64, I64, F64, P, P, P, P, P]
+    lib.hlq_layer_norm_forward.restype = I32
+    lib.hlq_layer_norm_backward_workspace_size.argtypes = [I64, I64, I32]
+    lib.hlq_layer_norm_backward_workspace_size.restype = SZ
+    lib.hlq_layer_norm_backward.argtypes = [P, P, P, I32, P, P, P, I32, I64, I64, P, P, P, P, SZ,
+                                            P]
+    lib.hlq_layer_norm_backward.restype = I32
+    lib.hlq_token_logprob_forward.argtypes = [P, I32, I64, P, I64, I64, F64, P, P, P]
+    lib.hlq_token_logprob_forward.restype = I32
+    lib.hlq_token_logprob_backward.argtypes = [P, P, I32, I64, P, P, I64, I64, F64, P, I64, P]
+    lib.hlq_token_logprob_backward.restype = I32
+    lib.hlq_policy_loss_workspace_size.argtypes = [I64]
+    lib.hlq_policy_loss_workspace_size.restype = SZ
+    lib.hlq_policy_loss.argtypes = [P, P, P, P, P, I64, F64, F64, F64, P, P, P, SZ, P]
+    lib.hlq_policy_loss.restype = I32
+    lib.hlq_policy_loss_logits.argtypes = [P, I32, I64, P, P, P, P, P, I64, I64, F64, F64, F64,
+                                           F64, P, P, P, I64, P, SZ, P]
+    lib.hlq_policy_loss_logits.restype = I32
+    lib.hlq_preference_loss_workspace_size.argtypes = [I64]
+    lib.hlq_preference_loss_workspace_size.restype = SZ
+    lib.hlq_preference_loss.argtypes = [P, P, P, P, I64, I64, F64, F64, I32, P, P, P, P, SZ, P]
+    lib.hlq_preference_loss.restype = I32
+    lib.hlq_clip_grad_norm_workspace_size.argtypes = [P, I64]
+    lib.hlq_clip_grad_norm_workspace_size.restype = SZ
+    lib.hlq_clip_grad_norm.argtypes = [P, P, P, P, I64, F64, I32, P, P, SZ, P]
+    lib.hlq_clip_grad_norm.restype = I32
     lib.hlq_status_string.argtypes = [I32]
     lib.hlq_status_string.restype = ctypes.c_char_p
     lib.hlq_version.argtypes = []
@@ -495,6 +537,324 @@ def hlq_lqs_select(stats, threshold=HLQ_LQS_THRESHOLD):
     _check("hlq_lqs_select", _lib.hlq_lqs_select(arr, float(threshold), ctypes.byref(gx),
                                                  ctypes.byref(gw)))
     return gx.value, gw.value
+
+
+# ------------------------------------------------------------ training step
+
+def _hold(stream, *ts):
+    """Tells the allocator that ``ts``, allocated for the current stream, are
+    used on ``stream`` (None: the current one)."""
+    if stream is not None:
+        for t in ts:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _workspace(workspace, need, device):
+    import torch
+    if workspace is None:
+        return torch.empty((max(need, 256),), dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8 or workspace.dim() != 1:
+        raise TypeError("workspace must be a 1-D uint8 tensor")
+    return workspace
+
+
+def _params(weight, bias, C):
+    _expect("weight", weight, weight.dtype, (C,))
+    if bias is not None:
+        _expect("bias", bias, weight.dtype, (C,))
+
+
+def hlq_layer_norm_forward(x, weight, bias=None, eps=1e-5, residual=None, y=None, h=None,
+                           stream=None):
+    """Layer norm of h = x + residual over the last dimension: returns (y, h,
+    mean, rstd).
+
+    x [..., C] is fp32 or bf16, ``residual`` None or like x, ``weight`` and
+    ``bias`` [C] fp32 or bf16 (bias None: none).  h, rounded to x's type, is x
+    itself when there is no residual.  mean and rstd (fp32, one per row) are
+    kept for :func:`hlq_layer_norm_backward`.
+    """
+    import torch
+    C = x.shape[-1] if x.dim() else 0
+    T = x.numel() // C if C else 0
+    _params(weight, bias, C)
+    if residual is not None:
+        _expect("residual", residual, x.dtype, x.shape)
+        if h is None:
+            h = torch.empty_like(x, memory_format=torch.contiguous_format)
+        _expect("h", h, x.dtype, x.shape)
+    elif h is not None:
+        raise ValueError("h is an output of the residual addition: no residual was given")
+    if y is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    _expect("y", y, x.dtype, x.shape)
+    stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device)
+    _require_cuda(x, residual, weight, bias, y, h)
+    mean, rstd = stats[0], stats[1]
+    _check("hlq_layer_norm_forward", _lib.hlq_layer_norm_forward(
+        _ptr(x), _ptr(residual), _dtype_code(x), _ptr(weight), _ptr(bias), _dtype_code(weight),
+        T, C, eps, _ptr(y), _ptr(h), _ptr(mean), _ptr(rstd), _stream(stream)))
+    _hold(stream, y, h, stats)
+    return y, (x if residual is None else h), mean, rstd
+
+
+def hlq_layer_norm_backward_workspace_size(T, C, dtype=HLQ_F32) -> int:
+    return int(_lib.hlq_layer_norm_backward_workspace_size(T, C, dtype))
+
+
+def hlq_layer_norm_backward(g_y, h, mean, rstd, weight, g_h=None, with_bias=True, g_x=None,
+                            workspace=None, stream=None):
+    """Backward of :func:`hlq_layer_norm_forward`: returns (g_x, g_weight,
+    g_bias), g_bias None without ``with_bias``.
+
+    g_y and h [..., C] (h the normalised input the forward call returned),
+    ``g_h`` the gradient that reaches h along the residual stream (None: none),
+    all of one type; g_weight and g_bias have the type of weight.  g_x is the
+    gradient of x and of the residual alike.
+    """
+    import torch
+    C = h.shape[-1] if h.dim() else 0
+    T = h.numel() // C if C else 0
+    _params(weight, None, C)
+    _expect("g_y", g_y, h.dtype, h.shape)
+    _expect("mean", mean, torch.float32, h.shape[:-1])
+    _expect("rstd", rstd, torch.float32, h.shape[:-1])
+    if g_h is not None:
+        _expect("g_h", g_h, h.dtype, h.shape)
+    if g_x is None:
+        g_x = torch.empty_like(h, memory_format=torch.contiguous_format)
+    _expect("g_x", g_x, h.dtype, h.shape)
+    g_p = torch.empty((2 if with_bias else 1, C), dtype=weight.dtype, device=h.device)
+    code = _dtype_code(h)
+    workspace = _workspace(workspace, _lib.hlq_layer_norm_backward_workspace_size(T, C, code),
+                           h.device)
+    _require_cuda(g_y, h, mean, rstd, weight, g_h, g_x, workspace)
+    g_w, g_b = g_p[0], (g_p[1] if with_bias else None)
+    _check("hlq_layer_norm_backward", _lib.hlq_layer_norm_backward(
+        _ptr(g_y), _ptr(h), _ptr(g_h), code, _ptr(mean), _ptr(rstd), _ptr(weight),
+        _dtype_code(weight), T, C, _ptr(g_x), _ptr(g_w), _ptr(g_b), _ptr(workspace),
+        _nbytes(workspace), _stream(stream)))
+    _hold(stream, g_x, g_p, workspace)
+    return g_x, g_w, g_b
+
+
+def _rows(name, t, shape=None):
+    """(rows, length, pitch) of a 2-D GPU tensor whose rows are packed; the
+    pitch between rows is free (a slice of a padded vocabulary)."""
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be {'a 2-D tensor' if shape is None else shape}, got "
+                         f"{tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    T, V = t.shape
+    ld = t.stride(0) if T > 1 else V
+    if (V > 1 and t.stride(1) != 1) or ld < V:
+        raise ValueError(f"{name}: the elements of a row must be contiguous and rows not overlap")
+    return T, V, ld
+
+
+def _per_token(T, like, **named):
+    """fp32 [T] tensors (None allowed) on the device of ``like``."""
+    import torch
+    for name, t in named.items():
+        if t is not None:
+            _expect(name, t, torch.float32, (T,))
+    _require_cuda(*named.values())
+    for t in named.values():
+        if t is not None and t.device != like.device:
+            raise ValueError(f"tensors on different devices: {like.device} and {t.device}")
+
+
+def _targets(targets, T, like):
+    import torch
+    _expect("targets", targets, torch.int64, (T,))
+    _require_cuda(targets)
+    if targets.device != like.device:
+        raise ValueError(f"tensors on different devices: {like.device} and {targets.device}")
+
+
+def hlq_token_logprob_forward(logits, targets, scale=1.0, stream=None):
+    """Log probability of ``targets`` [T] (int64) under softmax(scale *
+    logits), logits [T, V] fp32 or bf16: returns (logprob [T], stats [T, 2])
+    fp32, stats being each row's maximum and sum of exponentials above it.
+
+    Targets outside [0, V) (such as -100) are ignored: log probability 0, the
+    row not read.  The rows of logits may have any pitch.
+    """
+    import torch
+    T, V, ld = _rows("logits", logits)
+    _targets(targets, T, logits)
+    logprob = torch.empty((T,), dtype=torch.float32, device=logits.device)
+    stats = torch.empty((T, 2), dtype=torch.float32, device=logits.device)
+    _check("hlq_token_logprob_forward", _lib.hlq_token_logprob_forward(
+        _ptr(logits), _dtype_code(logits), ld, _ptr(targets), T, V, scale, _ptr(logprob),
+        _ptr(stats), _stream(stream)))
+    _hold(stream, logprob, stats)
+    return logprob, stats
+
+
+def hlq_token_logprob_backward(g_logprob, logits, targets, stats, scale=1.0, g_x=None,
+                               stream=None):
+    """Gradient [T, V] of logits from that of the log probabilities
+    (:func:`hlq_token_logprob_forward`'s), in the type of logits."""
+    import torch
+    T, V, ld = _rows("logits", logits)
+    _targets(targets, T, logits)
+    _per_token(T, logits, g_logprob=g_logprob)
+    _expect("stats", stats, torch.float32, (T, 2))
+    _require_cuda(g_logprob, stats)
+    if g_x is None:
+        g_x = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+    _expect("g_x", g_x, logits.dtype, (T, V))
+    g_ld = _rows("g_x", g_x)[2]
+    _check("hlq_token_logprob_backward", _lib.hlq_token_logprob_backward(
+        _ptr(g_logprob), _ptr(logits), _dtype_code(logits), ld, _ptr(targets), _ptr(stats), T, V,
+        scale, _ptr(g_x), g_ld, _stream(stream)))
+    _hold(stream, g_x)
+    return g_x
+
+
+def hlq_policy_loss_workspace_size(T) -> int:
+    return int(_lib.hlq_policy_loss_workspace_size(T))
+
+
+def hlq_policy_loss(logprob, old_logprob, advantage, weight=None, ref_logprob=None, clip_low=0.2,
+                    clip_high=0.2, kl_coef=0.0, workspace=None, stream=None):
+    """Clipped policy loss with a KL term from log probabilities [T]: returns
+    (sums [3], g_logprob [T]), sums = (loss, weighted KL estimate, weight of
+    the clipped tokens).  ``ref_logprob`` goes with a kl_coef other than 0; a
+    weight of 0 takes a token out (weight None: ones)."""
+    import torch
+    T, dev = logprob.numel(), logprob.device
+    _per_token(T, logprob, logprob=logprob, old_logprob=old_logprob, advantage=advantage,
+               weight=weight, ref_logprob=ref_logprob)
+    sums = torch.empty((3,), dtype=torch.float32, device=dev)
+    g_logprob = torch.empty((T,), dtype=torch.float32, device=dev)
+    workspace = _workspace(workspace, hlq_policy_loss_workspace_size(T), dev)
+    _require_cuda(logprob, workspace)
+    _check("hlq_policy_loss", _lib.hlq_policy_loss(
+        _ptr(logprob), _ptr(old_logprob), _ptr(advantage), _ptr(weight), _ptr(ref_logprob), T,
+        clip_low, clip_high, kl_coef, _ptr(sums), _ptr(g_logprob), _ptr(workspace),
+        _nbytes(workspace), _stream(stream)))
+    _hold(stream, sums, g_logprob, workspace)
+    return sums, g_logprob
+
+
+def hlq_policy_loss_logits(logits, targets, old_logprob, advantage, weight=None, ref_logprob=None,
+                           scale=1.0, clip_low=0.2, clip_high=0.2, kl_coef=0.0, g_x=None,
+                           workspace=None, stream=None):
+    """:func:`hlq_token_logprob_forward`, :func:`hlq_policy_loss` and
+    :func:`hlq_token_logprob_backward` in one pass over logits [T, V]: returns
+    (sums [3], logprob [T], g_x [T, V]).  Tokens whose weight is 0 or whose
+    target is ignored do not count; their rows are not read."""
+    import torch
+    T, V, ld = _rows("logits", logits)
+    dev = logits.device
+    _targets(targets, T, logits)
+    _per_token(T, logits, old_logprob=old_logprob, advantage=advantage, weight=weight,
+               ref_logprob=ref_logprob)
+    if g_x is None:
+        g_x = torch.empty((T, V), dtype=logits.dtype, device=dev)
+    _expect("g_x", g_x, logits.dtype, (T, V))
+    g_ld = _rows("g_x", g_x)[2]
+    sums = torch.empty((3,), dtype=torch.float32, device=dev)
+    logprob = torch.empty((T,), dtype=torch.float32, device=dev)
+    workspace = _workspace(workspace, hlq_policy_loss_workspace_size(T), dev)
+    _require_cuda(workspace)
+    _check("hlq_policy_loss_logits", _lib.hlq_policy_loss_logits(
+        _ptr(logits), _dtype_code(logits), ld, _ptr(targets), _ptr(old_logprob), _ptr(advantage),
+        _ptr(weight), _ptr(ref_logprob), T, V, scale, clip_low, clip_high, kl_coef, _ptr(sums),
+        _ptr(logprob), _ptr(g_x), g_ld, _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    _hold(stream, g_x, sums, logprob, workspace)
+    return sums, logprob, g_x
+
+
+def hlq_preference_loss_workspace_size(P) -> int:
+    return int(_lib.hlq_preference_loss_workspace_size(P))
+
+
+def hlq_preference_loss(logprob, start, beta, ref_logprob=None, weight=None, label_smoothing=0.0,
+                        reduction=HLQ_SUM, workspace=None, stream=None):
+    """Preference loss over P pairs of packed sequences, from log
+    probabilities [T]: returns (loss [1], margin [P], g_logprob [T]).
+
+    ``start`` [2P + 1] (int64, on the GPU) holds the sequences' bounds, 0 to
+    T, the P chosen ones first; ``reduction`` HLQ_SUM scores a sequence by the
+    sum of weight * (logprob - ref_logprob), HLQ_MEAN by its weighted mean.
+    """
+    import torch
+    T, dev = logprob.numel(), logprob.device
+    _per_token(T, logprob, logprob=logprob, ref_logprob=ref_logprob, weight=weight)
+    if start.dtype != torch.int64 or start.dim() != 1 or start.numel() % 2 != 1:
+        raise ValueError("start must be an int64 tensor of 2P + 1 bounds")
+    P = start.numel() // 2
+    loss = torch.empty((1,), dtype=torch.float32, device=dev)
+    margin = torch.empty((P,), dtype=torch.float32, device=dev)
+    g_logprob = torch.empty((T,), dtype=torch.float32, device=dev)
+    workspace = _workspace(workspace, hlq_preference_loss_workspace_size(P), dev)
+    _require_cuda(logprob, start, workspace)
+    _check("hlq_preference_loss", _lib.hlq_preference_loss(
+        _ptr(logprob), _ptr(ref_logprob), _ptr(weight), _ptr(start), P, T, beta, label_smoothing,
+        reduction, _ptr(loss), _ptr(margin), _ptr(g_logprob), _ptr(workspace), _nbytes(workspace),
+        _stream(stream)))
+    _hold(stream, loss, margin, g_logprob, workspace)
+    return loss, margin, g_logprob
+
+
+def _dense(t) -> bool:
+    """Whether the elements of t fill one stretch of memory, in any order of
+    its dimensions."""
+    n = 1
+    for stride, size in sorted(zip(t.stride(), t.shape)):
+        if size != 1:
+            if stride != n:
+                return False
+            n *= size
+    return True
+
+
+def hlq_clip_grad_norm_workspace_size(sizes) -> int:
+    """Workspace bytes of hlq_clip_grad_norm for tensors of ``sizes`` elements."""
+    sizes = list(sizes)
+    return int(_lib.hlq_clip_grad_norm_workspace_size(
+        (ctypes.c_int64 * len(sizes))(*sizes), len(sizes)))
+
+
+def hlq_clip_grad_norm(grads, max_norm, norm_kind=HLQ_NORM_L2, out=None, workspace=None,
+                       stream=None):
+    """Scales ``grads`` (fp32 and bf16 GPU tensors) by min(1, max_norm / (norm
+    + 1e-6)), norm their global norm (HLQ_NORM_L2 or HLQ_NORM_INF), in place
+    or into ``out`` (tensors of the same types, shapes and strides).  Returns
+    the norm, a float64 GPU tensor [1]; the host does not wait for it."""
+    import torch
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    n = len(grads)
+    if len(outs) != n:
+        raise ValueError(f"{n} gradients and {len(outs)} outputs")
+    dev = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
+    codes = []
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        if not g.is_cuda or g.device != dev:
+            raise ValueError(f"gradient {i} is on {g.device}, expected {dev}")
+        if not g.is_contiguous() and not _dense(g):
+            raise ValueError(f"gradient {i} is not dense")
+        if o is not g and (o.dtype != g.dtype or o.shape != g.shape or o.device != dev or
+                           o.stride() != g.stride()):
+            raise ValueError(f"output {i} must match its gradient's type, shape and strides")
+        codes.append(_dtype_code(g))
+    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+    src = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
+    dst = None if out is None else (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs])
+    norm = torch.empty((1,), dtype=torch.float64, device=dev)
+    workspace = _workspace(workspace, _lib.hlq_clip_grad_norm_workspace_size(sizes, n), dev)
+    _require_cuda(norm, workspace)
+    _check("hlq_clip_grad_norm", _lib.hlq_clip_grad_norm(
+        src, dst, sizes, (ctypes.c_int * n)(*codes), n, max_norm, norm_kind, _ptr(norm),
+        _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    _hold(stream, norm, workspace)
+    return norm
 
 
 def lib_handle():

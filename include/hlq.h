@@ -54,7 +54,8 @@ typedef enum hlq_status {
   HLQ_ERR_ALIGN = 7,     /* a data pointer is not 16-byte aligned             */
   HLQ_ERR_OVERFLOW = 8,  /* an INT32 accumulator could overflow              */
   HLQ_ERR_WORKSPACE = 9, /* workspace NULL or smaller than required           */
-  HLQ_ERR_HIP = 10       /* the HIP runtime refused a launch                  */
+  HLQ_ERR_HIP = 10,      /* the HIP runtime refused a launch                  */
+  HLQ_ERR_VALUE = 11     /* a scalar argument is out of its range             */
 } hlq_status;
 
 /* Element type of g_y, w and of the forward activation x. */
@@ -393,6 +394,185 @@ hlq_status hlq_lqs_accumulate(const void* g_y, int gy_dtype, const uint8_t* x_co
                               void* stream);
 hlq_status hlq_lqs_select(const double* stats, double threshold, int* gx_mode,
                           int* gw_mode);
+
+/* ------------------------------------------------------------------------
+ * Operators of a training step around the linear layer: layer norm, token log
+ * probabilities with the policy and preference losses on them, and gradient
+ * clipping by the global norm.
+ *
+ * They follow the conventions above with two differences.  Data pointers need
+ * the alignment of their elements only (rows of odd length, and views into a
+ * packed buffer, start anywhere); the workspace still needs 16 bytes.  A
+ * count of rows, tokens or tensors may be zero, and the pointers of the
+ * operands that are then empty may be NULL.  Every sum is kept in fp32 or
+ * fp64 in an order fixed by the sizes alone, so results are reproducible; an
+ * output in bf16 is rounded once, to nearest even.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Layer norm over the last dimension, with the residual addition in front.
+ *   h = x + residual, rounded to the type of x   (h = x without residual)
+ *   mean = 1/C sum_c h_c,   rstd = (1/C sum_c (h_c - mean)^2 + eps)^(-1/2)
+ *   y = (h - mean) * rstd * weight + bias
+ *   x, residual  [T][C] f32 or bf16 (dtype); residual NULL: none.
+ *   weight, bias [C] f32 or bf16 (param_dtype); bias NULL: none.
+ *   y            [T][C] out, dtype.
+ *   h            [T][C] out, dtype: the sum, for the residual stream and the
+ *                backward pass; NULL exactly when residual is.
+ *   mean, rstd   [T] f32 out, for the backward pass.
+ * One launch.  Errors: HLQ_ERR_NULL, HLQ_ERR_DTYPE, HLQ_ERR_SHAPE (T < 0,
+ * C < 1, T or C >= 2^31), HLQ_ERR_VALUE (eps negative or not finite),
+ * HLQ_ERR_ALIGN.
+ */
+hlq_status hlq_layer_norm_forward(const void* x, const void* residual, int dtype,
+                                  const void* weight, const void* bias, int param_dtype,
+                                  int64_t T, int64_t C, double eps, void* y, void* h,
+                                  float* mean, float* rstd, void* stream);
+
+/*
+ * Backward of the layer norm.  With n = (h - mean) * rstd and u = g_y * weight,
+ *   g_x      = rstd * (u - 1/C sum_c u - n * 1/C sum_c u n) + g_h
+ *   g_weight = sum_t g_y * n,   g_bias = sum_t g_y
+ * g_x is the gradient of x and of residual alike.
+ *   g_y      [T][C] dtype, the gradient of y.
+ *   h        [T][C] dtype, the normalised input (x itself without residual).
+ *   g_h      [T][C] dtype, the gradient that reaches h along the residual
+ *            stream; NULL: none.
+ *   mean, rstd [T] f32, from the forward call.
+ *   g_x      [T][C] out, dtype.
+ *   g_weight, g_bias [C] out, param_dtype; g_bias NULL: not computed.
+ *   workspace at least hlq_layer_norm_backward_workspace_size(T, C, dtype)
+ *            bytes: per-workgroup column sums (0 for an invalid shape).
+ * Two launches.  Errors as above and HLQ_ERR_WORKSPACE.
+ */
+size_t hlq_layer_norm_backward_workspace_size(int64_t T, int64_t C, int dtype);
+hlq_status hlq_layer_norm_backward(const void* g_y, const void* h, const void* g_h, int dtype,
+                                   const float* mean, const float* rstd, const void* weight,
+                                   int param_dtype, int64_t T, int64_t C, void* g_x,
+                                   void* g_weight, void* g_bias, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * Log probability of one target per row of logits.  With z = scale * logits,
+ *   logprob[t] = z[t][target] - log sum_v exp(z[t][v])
+ *   stats[t]   = (max_v logits[t][v], sum_v exp(z[t][v] - max_v z[t][v]))
+ *   logits   T rows of V elements, dtype, row t at element t * ld (ld >= V).
+ *   targets  [T] int64; one outside [0, V) is ignored: its row is not read,
+ *            logprob is 0 and stats (0, 1).
+ *   scale    the inverse temperature, > 0 and finite.
+ *   logprob  [T] f32 out;  stats [T][2] f32 out, for the backward pass.
+ * Logits of -inf have probability zero; a row of nothing else has logprob
+ * -inf and stats (-inf, 0).  A NaN or +inf in a row makes its logprob NaN.
+ * Errors: HLQ_ERR_NULL, HLQ_ERR_DTYPE, HLQ_ERR_SHAPE (T < 0, V < 1, ld < V,
+ * T or V >= 2^31), HLQ_ERR_VALUE (scale), HLQ_ERR_ALIGN.
+ */
+hlq_status hlq_token_logprob_forward(const void* logits, int dtype, int64_t ld,
+                                     const int64_t* targets, int64_t T, int64_t V, double scale,
+                                     float* logprob, float* stats, void* stream);
+
+/*
+ * Gradient of the logits from that of the log probabilities,
+ *   g_x[t][v] = g_logprob[t] * scale * ([v == target] - softmax(z[t])[v]),
+ * the softmax taken from stats.
+ *   g_logprob [T] f32.  Rows whose g_logprob is zero, whose target is ignored
+ *            or which hold nothing but -inf get zeros, and are not read.
+ *   g_x      T rows of V elements out, dtype, row t at element t * g_ld.
+ * One launch.  Errors as above (HLQ_ERR_SHAPE also for g_ld < V).
+ */
+hlq_status hlq_token_logprob_backward(const float* g_logprob, const void* logits, int dtype,
+                                      int64_t ld, const int64_t* targets, const float* stats,
+                                      int64_t T, int64_t V, double scale, void* g_x,
+                                      int64_t g_ld, void* stream);
+
+/*
+ * Clipped policy loss with a KL term, from log probabilities:
+ *   r_t = exp(logprob - old),   d_t = ref - logprob
+ *   loss = sum_t w_t (kl_coef * (exp(d_t) - d_t - 1)
+ *                     - min(r_t A_t, clamp(r_t, 1 - clip_low, 1 + clip_high) A_t))
+ *   logprob, old_logprob, advantage [T] f32.
+ *   weight   [T] f32: 0 takes a token out, whatever its other values are (1/n
+ *            for a mean over n tokens); NULL: every token has weight 1.
+ *   ref_logprob [T] f32 of the reference policy; NULL exactly when kl_coef is
+ *            0.  Only logprob has a gradient.
+ *   sums     [3] f32 out: the loss, sum_t w_t (exp(d_t) - d_t - 1), and the
+ *            weight of the tokens whose clamped term was the smaller one.
+ *   g_logprob [T] f32 out, the gradient of the loss.
+ *   workspace at least hlq_policy_loss_workspace_size(T) bytes.
+ * clip_low in [0, 1], clip_high >= 0, kl_coef >= 0, all finite
+ * (HLQ_ERR_VALUE).  Two launches.
+ */
+size_t hlq_policy_loss_workspace_size(int64_t T);
+hlq_status hlq_policy_loss(const float* logprob, const float* old_logprob,
+                           const float* advantage, const float* weight,
+                           const float* ref_logprob, int64_t T, double clip_low,
+                           double clip_high, double kl_coef, float* sums, float* g_logprob,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * hlq_token_logprob_forward, hlq_policy_loss and hlq_token_logprob_backward
+ * in one pass over the logits.
+ *   logprob  [T] f32 out; 0 where the weight is 0 or the target is ignored
+ *            (such a token does not count in the loss, its row is not read).
+ *   g_x      T rows of V elements out: the gradient of the loss.
+ * The other arguments, the workspace and the errors as there.
+ */
+hlq_status hlq_policy_loss_logits(const void* logits, int dtype, int64_t ld,
+                                  const int64_t* targets, const float* old_logprob,
+                                  const float* advantage, const float* weight,
+                                  const float* ref_logprob, int64_t T, int64_t V, double scale,
+                                  double clip_low, double clip_high, double kl_coef,
+                                  float* sums, float* logprob, void* g_x, int64_t g_ld,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Preference loss over P pairs of sequences, from log probabilities:
+ *   s_q      = sum over the tokens of sequence q of w_t (logprob_t - ref_t)
+ *              (HLQ_MEAN: divided by sum w_t, 0 where that is not positive)
+ *   margin_p = beta (s_p - s_{P+p})
+ *   loss     = 1/P sum_p -(1 - e) log sigmoid(margin_p) - e log sigmoid(-margin_p)
+ * with e = label_smoothing.
+ *   logprob  [T] f32; ref_logprob [T] f32 or NULL (no reference policy).
+ *   weight   [T] f32 or NULL (ones); 0 takes a token out, whatever its values.
+ *   start    [2P + 1] int64, non-decreasing from 0 to T: sequence q is tokens
+ *            start[q] .. start[q+1] - 1; the chosen ones are 0 .. P-1, the
+ *            rejected ones P .. 2P-1 in the same order.  Read on the device
+ *            and limited to [0, T] there.
+ *   loss     [1] f32, margin [P] f32, g_logprob [T] f32 out.
+ *   workspace at least hlq_preference_loss_workspace_size(P) bytes.
+ * beta > 0 and finite, 0 <= label_smoothing <= 1 (HLQ_ERR_VALUE), reduction
+ * HLQ_SUM or HLQ_MEAN (HLQ_ERR_MODE), P >= 1 (HLQ_ERR_SHAPE).
+ */
+size_t hlq_preference_loss_workspace_size(int64_t P);
+hlq_status hlq_preference_loss(const float* logprob, const float* ref_logprob,
+                               const float* weight, const int64_t* start, int64_t P, int64_t T,
+                               double beta, double label_smoothing, int reduction, float* loss,
+                               float* margin, float* g_logprob, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * Clipping of gradients by their global norm:
+ *   norm = (sum of v^2)^(1/2)   (HLQ_NORM_L2)   or   max |v|   (HLQ_NORM_INF)
+ *   out  = grad * min(1, max_norm / (norm + 1e-6))
+ * over all elements v of all tensors.  Nothing is read back by the host.
+ *   grads, outs [count] host arrays of device pointers; outs NULL: in place.
+ *            outs[i] may equal grads[i]; no other overlap.  Read during the
+ *            call only.
+ *   sizes    [count] elements of each tensor (0 allowed).
+ *   dtypes   [count] HLQ_F32 or HLQ_BF16, of grads[i] and outs[i].
+ *   max_norm >= 0 (HLQ_ERR_VALUE); +inf leaves gradients of finite norm alone.
+ *   norm     [1] f64 out (device).
+ *   workspace at least hlq_clip_grad_norm_workspace_size(sizes, count) bytes.
+ * An infinite norm gives the factor 0 (NaN where the gradient is infinite), a
+ * NaN in a gradient makes the norm and every output NaN.  One launch for the
+ * norm and one for the scaling per 160 tensors (a tensor of more than 2^30
+ * elements counts once per 2^30).
+ */
+enum { HLQ_NORM_L2 = 0, HLQ_NORM_INF = 1 };
+size_t hlq_clip_grad_norm_workspace_size(const int64_t* sizes, int64_t count);
+hlq_status hlq_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* sizes,
+                              const int* dtypes, int64_t count, double max_norm, int norm_kind,
+                              double* norm, void* workspace, size_t workspace_bytes,
+                              void* stream);
 
 /* Static text for a status code (never NULL). */
 const char* hlq_status_string(int status);
