@@ -17,10 +17,73 @@
 namespace hlq {
 
 // ------------------------------------------------------------ rows in registers
-// L lanes hold a row, M pieces each (L * M pieces cover it): one read of every
-// operand, the statistics and the output from registers.  L up to 64: a
-// workgroup of B threads takes B / L rows, sums over lanes alone; above: one
-// row per workgroup (B = L).
+// L lanes hold a row, M quads (4 elements) each: one read of every operand,
+// the statistics and the output from registers.  L up to 64: a workgroup of B
+// threads takes B / L rows and sums over lanes alone; above: one row per
+// workgroup (B = L).  Quads rather than 16-byte pieces of bf16: twice the
+// lanes per row, so half the registers per thread and twice the waves, which
+// is what hides the latency of a row.
+//
+// Addresses are a scalar base (the wave's first row) and a 32-bit byte offset
+// per lane.  Rows are at least 4 long here.  When C is no multiple of 4, the
+// last quad of a row is read ending at the row's end and shifted into place,
+// so nothing outside the row is read, and it is written by elements.
+
+template <int DT>
+struct Quad {
+  typedef typename std::conditional<DT == 0, u32x4, u32x2>::type Raw;
+  static constexpr int BYTES = DT == 0 ? 16 : 8;
+};
+
+// The quad at element c of a row (lane's offset `off` bytes from base); skip =
+// the elements by which a row's last quad passes its end; `last`: this is it.
+template <int DT>
+__device__ __forceinline__ typename Quad<DT>::Raw load_quad(const char* base, uint32_t off,
+                                                            bool in_row, bool last, int skip) {
+  typename Quad<DT>::Raw r = {};
+  if (in_row) {
+    const uint32_t back = last ? (uint32_t)skip * (Quad<DT>::BYTES / 4) : 0u;
+    __builtin_memcpy(&r, base + (off - back), Quad<DT>::BYTES);
+    if (last && skip) {
+      if constexpr (DT == 0) {
+        if (skip & 1) r = (u32x4){r[1], r[2], r[3], 0u};
+        if (skip & 2) r = (u32x4){r[2], r[3], 0u, 0u};
+      } else {
+        if (skip & 1) r = (u32x2){(r[0] >> 16) | (r[1] << 16), r[1] >> 16};
+        if (skip & 2) r = (u32x2){r[1], 0u};
+      }
+    }
+  }
+  return r;
+}
+
+template <int DT>
+__device__ __forceinline__ float quad_at(const typename Quad<DT>::Raw& r, int k) {
+  if constexpr (DT == 0) return __uint_as_float(r[k]);
+  else return (k & 1) ? bf16_hi(r[k / 2]) : bf16_lo(r[k / 2]);
+}
+
+template <int DT>
+__device__ __forceinline__ typename Quad<DT>::Raw make_quad(const float (&v)[4]) {
+  if constexpr (DT == 0) return make_piece<0>(v);
+  else return (u32x2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+}
+
+template <int DT>
+__device__ __forceinline__ void store_quad(char* base, uint32_t off, bool in_row, bool last,
+                                           int skip, const typename Quad<DT>::Raw& r) {
+  if (!in_row) return;
+  if (!(last && skip)) {
+    __builtin_memcpy(base + off, &r, Quad<DT>::BYTES);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (k + skip < 4) {
+        if constexpr (DT == 0) reinterpret_cast<uint32_t*>(base + off)[k] = r[k];
+        else reinterpret_cast<uint16_t*>(base + off)[k] = (uint16_t)(r[k / 2] >> (16 * (k & 1)));
+      }
+  }
+}
 
 // Sum over the L lanes of a row (every lane gets it).
 template <int L>
@@ -29,71 +92,108 @@ __device__ __forceinline__ float row_sum(float v, float* sm) {
   else return group_sum<L>(v, sm);
 }
 
+// Where a thread stands: lane of its row, and the wave's first row within a
+// workgroup's B / L rows.
+template <int L>
+struct RowLane {
+  int lane, wave_row, sub;  // row = workgroup's first + wave_row (scalar) + sub
+  __device__ __forceinline__ RowLane() {
+    lane = threadIdx.x % L;
+    if constexpr (L <= 64) {
+      wave_row = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * (64 / L);
+      sub = (threadIdx.x & 63) / L;
+    } else {
+      wave_row = sub = 0;
+    }
+  }
+};
+
+// Four parameters (weight or bias) at element c, zero past the end.
+__device__ __forceinline__ void load_quad_params(const void* base, int dt, uint32_t c, bool in_row,
+                                                 bool last, int skip, float (&v)[4]) {
+  if (dt == 0) {
+    const u32x4 r = load_quad<0>(static_cast<const char*>(base), c * 4, in_row, last, skip);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = quad_at<0>(r, k);
+  } else {
+    const u32x2 r = load_quad<1>(static_cast<const char*>(base), c * 2, in_row, last, skip);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = quad_at<1>(r, k);
+  }
+}
+
 template <int DT, int L, int M, int B>
 __global__ __launch_bounds__(B) void k_norm_fwd(NormFwd a) {
-  constexpr int N = Piece<DT>::N, R = B / L;
+  typedef typename Quad<DT>::Raw Raw;
+  constexpr int R = B / L, ES = DT == 0 ? 4 : 2;
   __shared__ float sm[2][16];
-  const int lane = threadIdx.x % L;
-  const int64_t C = a.C;
+  const RowLane<L> at;
+  const uint32_t C = (uint32_t)a.C;
+  const int skip = (4 - (int)(C & 3)) & 3;
   for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.T; r0 += (int64_t)gridDim.x * R) {
-    const int64_t row = r0 + threadIdx.x / L;
-    // a group past the last row holds zeros and writes nothing
-    const int64_t base = row * C, n = row < a.T ? C : 0;
-    u32x4 x[M];
+    const int64_t first = r0 + at.wave_row, base = first * a.C * ES;
+    const bool live = first + at.sub < a.T;  // a group past the last row writes nothing
+    uint32_t c0 = (uint32_t)at.lane * 4, row_off = (uint32_t)at.sub * C * ES;
+    // computed anew for every row: else the compiler keeps a 64-bit pointer
+    // per operand and quad across the loop instead of base + offset
+    asm volatile("" : "+v"(c0), "+v"(row_off));
+    Raw x[M];
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < M; ++j) {
-      const int64_t c = (int64_t)(lane + j * L) * N;
-      x[j] = load_piece<DT>(a.x, base + c, n - c);
+      const uint32_t c = c0 + j * L * 4;
+      x[j] = load_quad<DT>(static_cast<const char*>(a.x) + base, row_off + c * ES, live && c < C,
+                           c + 4 > C, skip);
     }
     if (a.residual) {
-      u32x4 q[M];
+      Raw q[M];
 #pragma unroll
       for (int j = 0; j < M; ++j) {
-        const int64_t c = (int64_t)(lane + j * L) * N;
-        q[j] = load_piece<DT>(a.residual, base + c, n - c);
+        const uint32_t c = c0 + j * L * 4;
+        q[j] = load_quad<DT>(static_cast<const char*>(a.residual) + base, row_off + c * ES,
+                             live && c < C, c + 4 > C, skip);
       }
 #pragma unroll
       for (int j = 0; j < M; ++j) {
-        const int64_t c = (int64_t)(lane + j * L) * N;
-        float v[N];
+        const uint32_t c = c0 + j * L * 4;
+        float v[4];
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = piece_at<DT>(x[j], k) + piece_at<DT>(q[j], k);
-        x[j] = make_piece<DT>(v);
-        store_piece<DT>(a.h, base + c, n - c, x[j]);
+        for (int k = 0; k < 4; ++k) v[k] = quad_at<DT>(x[j], k) + quad_at<DT>(q[j], k);
+        x[j] = make_quad<DT>(v);
+        store_quad<DT>(static_cast<char*>(a.h) + base, row_off + c * ES, live && c < C, c + 4 > C,
+                       skip, x[j]);
       }
     }
 #pragma unroll
     for (int j = 0; j < M; ++j)
 #pragma unroll
-      for (int k = 0; k < N; ++k) sum += piece_at<DT>(x[j], k);
+      for (int k = 0; k < 4; ++k) sum += quad_at<DT>(x[j], k);
     const float mean = row_sum<L>(sum, sm[0]) / (float)C;
     float sq = 0.f;
 #pragma unroll
     for (int j = 0; j < M; ++j) {
-      const int64_t c = (int64_t)(lane + j * L) * N;
+      const uint32_t c = c0 + j * L * 4;
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const float d = piece_at<DT>(x[j], k) - mean;
+      for (int k = 0; k < 4; ++k) {
+        const float d = quad_at<DT>(x[j], k) - mean;
         sq += c + k < C ? d * d : 0.f;
       }
     }
     const float rstd = 1.0f / sqrtf(row_sum<L>(sq, sm[1]) / (float)C + a.eps);
-    if (lane == 0 && n) {
-      a.mean[row] = mean;
-      a.rstd[row] = rstd;
+    if (at.lane == 0 && live) {
+      a.mean[first + at.sub] = mean;
+      a.rstd[first + at.sub] = rstd;
     }
 #pragma unroll
     for (int j = 0; j < M; ++j) {
-      const int64_t c = (int64_t)(lane + j * L) * N;
-      if (c < n) {
-        float w[N], b[N] = {}, y[N];
-        load_params<N>(a.weight, a.param_dt, c, C, w);
-        if (a.bias) load_params<N>(a.bias, a.param_dt, c, C, b);
+      const uint32_t c = c0 + j * L * 4;
+      float w[4], b[4] = {}, y[4];
+      load_quad_params(a.weight, a.param_dt, c, c < C, c + 4 > C, skip, w);
+      if (a.bias) load_quad_params(a.bias, a.param_dt, c, c < C, c + 4 > C, skip, b);
 #pragma unroll
-        for (int k = 0; k < N; ++k) y[k] = (piece_at<DT>(x[j], k) - mean) * rstd * w[k] + b[k];
-        store_piece<DT>(a.y, base + c, n - c, make_piece<DT>(y));
-      }
+      for (int k = 0; k < 4; ++k) y[k] = (quad_at<DT>(x[j], k) - mean) * rstd * w[k] + b[k];
+      store_quad<DT>(static_cast<char*>(a.y) + base, row_off + c * ES, live && c < C, c + 4 > C,
+                     skip, make_quad<DT>(y));
     }
     if constexpr (L > 64) __syncthreads();  // sm is used again
   }
@@ -103,40 +203,45 @@ __global__ __launch_bounds__(B) void k_norm_fwd(NormFwd a) {
 // registers; at the end the groups of a workgroup join theirs (lanes of a wave
 // first, then the waves through LDS) and write one partial.
 template <int DT, int L, int M, int B>
-__global__ __launch_bounds__(B) void k_norm_bwd(NormBwd a) {
-  constexpr int N = Piece<DT>::N, R = B / L, COLS = L * M * N;
+__global__ __launch_bounds__(B, 4) void k_norm_bwd(NormBwd a) {
+  typedef typename Quad<DT>::Raw Raw;
+  constexpr int R = B / L, COLS = L * M * 4, ES = DT == 0 ? 4 : 2;
   __shared__ float sm[2][16];
-  extern __shared__ float cols[];  // L <= 64: [B / 64][COLS]
-  const int lane = threadIdx.x % L;
-  const int64_t C = a.C;
-  float gw[M][N] = {}, gb[M][N] = {};
+  __shared__ float cols[L <= 64 ? B / 64 * COLS : 1];
+  const RowLane<L> at;
+  const uint32_t C = (uint32_t)a.C;
+  const int skip = (4 - (int)(C & 3)) & 3;
+  float gw[M][4] = {}, gb[M][4] = {};
   for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.T; r0 += (int64_t)gridDim.x * R) {
-    const int64_t row = r0 + threadIdx.x / L;
-    const int64_t base = row * C, n = row < a.T ? C : 0;
-    u32x4 g[M], h[M], q[M];
+    const int64_t first = r0 + at.wave_row, base = first * a.C * ES;
+    const bool live = first + at.sub < a.T;
+    uint32_t c0 = (uint32_t)at.lane * 4, row_off = (uint32_t)at.sub * C * ES;
+    // computed anew for every row: else the compiler keeps a 64-bit pointer
+    // per operand and quad across the loop instead of base + offset
+    asm volatile("" : "+v"(c0), "+v"(row_off));
+    Raw g[M], h[M], q[M];
 #pragma unroll
     for (int j = 0; j < M; ++j) {
-      const int64_t c = (int64_t)(lane + j * L) * N;
-      g[j] = load_piece<DT>(a.g_y, base + c, n - c);
-      h[j] = load_piece<DT>(a.h, base + c, n - c);
+      const uint32_t c = c0 + j * L * 4;
+      g[j] = load_quad<DT>(static_cast<const char*>(a.g_y) + base, row_off + c * ES, live && c < C,
+                           c + 4 > C, skip);
+      h[j] = load_quad<DT>(static_cast<const char*>(a.h) + base, row_off + c * ES, live && c < C,
+                           c + 4 > C, skip);
+      if (a.g_h)
+        q[j] = load_quad<DT>(static_cast<const char*>(a.g_h) + base, row_off + c * ES,
+                             live && c < C, c + 4 > C, skip);
     }
-    if (a.g_h) {
-#pragma unroll
-      for (int j = 0; j < M; ++j) {
-        const int64_t c = (int64_t)(lane + j * L) * N;
-        q[j] = load_piece<DT>(a.g_h, base + c, n - c);
-      }
-    }
-    const float mean = n ? a.mean[row] : 0.f, rstd = n ? a.rstd[row] : 0.f;
+    const float mean = live ? a.mean[first + at.sub] : 0.f;
+    const float rstd = live ? a.rstd[first + at.sub] : 0.f;
     float su = 0.f, sn = 0.f;
 #pragma unroll
     for (int j = 0; j < M; ++j) {
-      const int64_t c = (int64_t)(lane + j * L) * N;
-      float w[N];
-      load_params<N>(a.weight, a.param_dt, c, C, w);  // zero past the row
+      const uint32_t c = c0 + j * L * 4;
+      float w[4];
+      load_quad_params(a.weight, a.param_dt, c, c < C, c + 4 > C, skip, w);
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const float v = piece_at<DT>(g[j], k), x = (piece_at<DT>(h[j], k) - mean) * rstd;
+      for (int k = 0; k < 4; ++k) {
+        const float v = quad_at<DT>(g[j], k), x = (quad_at<DT>(h[j], k) - mean) * rstd;
         const float u = v * w[k];
         su += u;
         sn += u * x;
@@ -148,33 +253,32 @@ __global__ __launch_bounds__(B) void k_norm_bwd(NormBwd a) {
     sn = row_sum<L>(sn, sm[1]) / (float)C;
 #pragma unroll
     for (int j = 0; j < M; ++j) {
-      const int64_t c = (int64_t)(lane + j * L) * N;
-      if (c < n) {
-        float w[N], o[N];
-        load_params<N>(a.weight, a.param_dt, c, C, w);
+      const uint32_t c = c0 + j * L * 4;
+      float w[4], o[4];
+      load_quad_params(a.weight, a.param_dt, c, c < C, c + 4 > C, skip, w);
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-          o[k] = rstd * (piece_at<DT>(g[j], k) * w[k] - su -
-                         (piece_at<DT>(h[j], k) - mean) * rstd * sn);
-        if (a.g_h) {
+      for (int k = 0; k < 4; ++k)
+        o[k] = rstd * (quad_at<DT>(g[j], k) * w[k] - su -
+                       (quad_at<DT>(h[j], k) - mean) * rstd * sn);
+      if (a.g_h) {
 #pragma unroll
-          for (int k = 0; k < N; ++k) o[k] += piece_at<DT>(q[j], k);
-        }
-        store_piece<DT>(a.g_x, base + c, n - c, make_piece<DT>(o));
+        for (int k = 0; k < 4; ++k) o[k] += quad_at<DT>(q[j], k);
       }
+      store_quad<DT>(static_cast<char*>(a.g_x) + base, row_off + c * ES, live && c < C, c + 4 > C,
+                     skip, make_quad<DT>(o));
     }
     if constexpr (L > 64) __syncthreads();  // sm is used again
   }
-  float* part = a.part + (int64_t)blockIdx.x * 2 * C;
+  float* part = a.part + (int64_t)blockIdx.x * 2 * a.C;
   if constexpr (L > 64) {
 #pragma unroll
     for (int j = 0; j < M; ++j)
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int64_t c = (int64_t)(lane + j * L) * N + k;
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t c = (uint32_t)(at.lane + j * L) * 4 + k;
         if (c < C) {
           part[c] = gw[j][k];
-          part[C + c] = gb[j][k];
+          part[a.C + c] = gb[j][k];
         }
       }
   } else {
@@ -185,19 +289,19 @@ __global__ __launch_bounds__(B) void k_norm_bwd(NormBwd a) {
 #pragma unroll
       for (int j = 0; j < M; ++j)
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
+        for (int k = 0; k < 4; ++k) {
           float v = side ? gb[j][k] : gw[j][k];
 #pragma unroll
           for (int m = L; m < 64; m <<= 1) v += __shfl_xor(v, m);
-          if ((threadIdx.x & 63) < L) cols[wave * COLS + (lane + j * L) * N + k] = v;
+          if ((threadIdx.x & 63) < L) cols[wave * COLS + (at.lane + j * L) * 4 + k] = v;
         }
       __syncthreads();
-      for (int c = threadIdx.x; c < COLS; c += B)
+      for (uint32_t c = threadIdx.x; c < COLS; c += B)
         if (c < C) {
           float v = cols[c];
 #pragma unroll
           for (int w = 1; w < B / 64; ++w) v += cols[w * COLS + c];
-          part[side * C + c] = v;
+          part[side * a.C + c] = v;
         }
     }
   }
@@ -361,25 +465,16 @@ __global__ __launch_bounds__(1024) void k_norm_fold(NormBwd a) {
 }
 
 // ------------------------------------------------------------ launches
-// Lanes and pieces per row for rows of `pieces` 16-byte pieces.
-enum NormRow { ROW_8x1, ROW_16x1, ROW_32x1, ROW_32x2, ROW_32x3, ROW_64x2, ROW_64x3, ROW_256x1,
-               ROW_256x2, ROW_256x3, ROW_256x4, ROW_1024x2, ROW_1024x4, ROW_WIDE };
+// Lanes and quads per row, by the length of the row.
+enum NormRow { ROW_8x1, ROW_16x1, ROW_32x1, ROW_64x1, ROW_64x2, ROW_64x3, ROW_64x4, ROW_256x2,
+               ROW_256x3, ROW_256x4, ROW_512x3, ROW_512x4, ROW_1024x3, ROW_1024x4, ROW_WIDE };
+static const int norm_lanes[] = {8, 16, 32, 64, 64, 64, 64, 256, 256, 256, 512, 512, 1024, 1024};
+static const int norm_quads[] = {1, 1, 1, 1, 2, 3, 4, 2, 3, 4, 3, 4, 3, 4};
 
-static NormRow norm_row(int64_t pieces, bool backward) {
-  if (pieces <= 8) return ROW_8x1;
-  if (pieces <= 16) return ROW_16x1;
-  if (pieces <= 32) return ROW_32x1;
-  if (pieces <= 64) return ROW_32x2;
-  if (pieces <= 96) return ROW_32x3;
-  if (pieces <= 128) return ROW_64x2;
-  if (pieces <= 192) return ROW_64x3;
-  if (pieces <= 256) return ROW_256x1;
-  if (pieces <= 512) return ROW_256x2;
-  if (pieces <= 768) return ROW_256x3;
-  if (pieces <= 1024) return ROW_256x4;
-  if (pieces <= 2048) return ROW_1024x2;
-  // (the column sums of 4 pieces do not fit a thread's registers beside them)
-  if (pieces <= 4096 && !backward) return ROW_1024x4;
+static NormRow norm_row(int64_t C) {
+  if (C < 4) return ROW_WIDE;
+  for (int r = 0; r < ROW_WIDE; ++r)
+    if (C <= 4 * norm_lanes[r] * norm_quads[r]) return (NormRow)r;
   return ROW_WIDE;
 }
 
@@ -387,45 +482,40 @@ static NormRow norm_row(int64_t pieces, bool backward) {
   case ROW_8x1: F(8, 1, BS); break;                                                         \
   case ROW_16x1: F(16, 1, BS); break;                                                       \
   case ROW_32x1: F(32, 1, BS); break;                                                       \
-  case ROW_32x2: F(32, 2, BS); break;                                                       \
-  case ROW_32x3: F(32, 3, BS); break;                                                       \
+  case ROW_64x1: F(64, 1, BS); break;                                                       \
   case ROW_64x2: F(64, 2, BS); break;                                                       \
   case ROW_64x3: F(64, 3, BS); break;                                                       \
-  case ROW_256x1: F(256, 1, 256); break;                                                    \
+  case ROW_64x4: F(64, 4, BS); break;                                                       \
   case ROW_256x2: F(256, 2, 256); break;                                                    \
   case ROW_256x3: F(256, 3, 256); break;                                                    \
   case ROW_256x4: F(256, 4, 256); break;                                                    \
-  case ROW_1024x2: F(1024, 2, 1024); break;
+  case ROW_512x3: F(512, 3, 512); break;                                                    \
+  case ROW_512x4: F(512, 4, 512); break;                                                    \
+  case ROW_1024x3: F(1024, 3, 1024); break;                                                 \
+  case ROW_1024x4: F(1024, 4, 1024); break;
 
-static int norm_lanes(NormRow r) {
-  static const int lanes[] = {8, 16, 32, 32, 32, 64, 64, 256, 256, 256, 256, 1024, 1024};
-  return lanes[r];
-}
 constexpr int NORM_BWD_THREADS = 512;  // workgroups of the backward kernel, L <= 64
 
 // Workgroups of the backward kernel, each leaving one partial: up to 1024
 // threads per CU.
-int64_t norm_parts(int64_t T, int64_t C, int dtype) {
-  const NormRow r = norm_row((C + (dtype == 0 ? 3 : 7)) / (dtype == 0 ? 4 : 8), true);
+int64_t norm_parts(int64_t T, int64_t C) {
+  const NormRow r = norm_row(C);
   if (r == ROW_WIDE) return (T + 31) / 32 < 256 ? (T + 31) / 32 : 256;
-  const int L = norm_lanes(r), B = L <= 64 ? NORM_BWD_THREADS : L;
+  const int L = norm_lanes[r], B = L <= 64 ? NORM_BWD_THREADS : L;
   const int64_t need = (T + B / L - 1) / (B / L), most = 256 * 1024 / B;
   return need < most ? need : most;
 }
 
 hipError_t launch_norm_forward(const NormFwd& a, int dtype, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
-  const int N = dtype == 0 ? 4 : 8;
-  const NormRow r = norm_row((a.C + N - 1) / N, false);
 #define HLQ_F(L, M, B)                                                                      \
   do {                                                                                      \
     const dim3 g = rows_grid((a.T + B / L - 1) / (B / L));                                  \
     if (dtype == 0) hipLaunchKernelGGL((k_norm_fwd<0, L, M, B>), g, dim3(B), 0, s, a);      \
     else hipLaunchKernelGGL((k_norm_fwd<1, L, M, B>), g, dim3(B), 0, s, a);                 \
   } while (0)
-  switch (r) {
+  switch (norm_row(a.C)) {
     HLQ_NORM_ROWS(HLQ_F, 256)
-    case ROW_1024x4: HLQ_F(1024, 4, 1024); break;
     case ROW_WIDE:
       if (dtype == 0) hipLaunchKernelGGL(k_norm_fwd_wide<0>, rows_grid(a.T), dim3(256), 0, s, a);
       else hipLaunchKernelGGL(k_norm_fwd_wide<1>, rows_grid(a.T), dim3(256), 0, s, a);
@@ -436,15 +526,13 @@ hipError_t launch_norm_forward(const NormFwd& a, int dtype, hipStream_t s) {
 
 hipError_t launch_norm_backward(const NormBwd& a, int dtype, hipStream_t s) {
   const int N = dtype == 0 ? 4 : 8;
-  const NormRow r = norm_row((a.C + N - 1) / N, true);
   const dim3 g((unsigned)a.parts), wide(cdiv(a.C, 64 * N), (unsigned)a.parts);
 #define HLQ_B(L, M, B)                                                                      \
   do {                                                                                      \
-    const size_t lds = L <= 64 ? (size_t)B / 64 * L * M * N * 4 : 0;                        \
-    if (dtype == 0) hipLaunchKernelGGL((k_norm_bwd<0, L, M, B>), g, dim3(B), lds, s, a);    \
-    else hipLaunchKernelGGL((k_norm_bwd<1, L, M, B>), g, dim3(B), lds, s, a);               \
+    if (dtype == 0) hipLaunchKernelGGL((k_norm_bwd<0, L, M, B>), g, dim3(B), 0, s, a);    \
+    else hipLaunchKernelGGL((k_norm_bwd<1, L, M, B>), g, dim3(B), 0, s, a);               \
   } while (0)
-  if (a.T) switch (r) {
+  if (a.T) switch (norm_row(a.C)) {
     HLQ_NORM_ROWS(HLQ_B, NORM_BWD_THREADS)
     default:
       if (dtype == 0) {

@@ -12,6 +12,7 @@
 
 namespace hlq {
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // A piece: 16 bytes of a row, 4 fp32 or 8 bf16 elements (dtype DT: 0 or 1).
@@ -66,6 +67,16 @@ __device__ __forceinline__ float piece_at(const u32x4& r, int k) {
   else return (k & 1) ? bf16_hi(r[k / 2]) : bf16_lo(r[k / 2]);
 }
 
+// Two fp32 values, each rounded to nearest even, as a pair of bf16.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  const b2 p = __builtin_convertvector((f2){lo, hi}, b2);
+  uint32_t u;
+  __builtin_memcpy(&u, &p, 4);
+  return u;
+}
+
 // fp32 values to a piece, each rounded to nearest even when DT is bf16 (the
 // one rounding of an output; v_cvt_pk_bf16_f32).
 template <int DT>
@@ -75,15 +86,8 @@ __device__ __forceinline__ u32x4 make_piece(const float (&v)[Piece<DT>::N]) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) r[k] = __float_as_uint(v[k]);
   } else {
-    typedef float f2 __attribute__((ext_vector_type(2)));
-    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const b2 p = __builtin_convertvector((f2){v[2 * k], v[2 * k + 1]}, b2);
-      uint32_t u;
-      __builtin_memcpy(&u, &p, 4);
-      r[k] = u;
-    }
+    for (int k = 0; k < 4; ++k) r[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
   }
   return r;
 }
