@@ -241,8 +241,10 @@ struct LogitArgs {
   const void* logits;
   const int64_t* targets;
   int64_t T, V, ld, g_ld;
+  int64_t row0;  // first row of the launch (set by the launch functions)
   double scale;
-  float c;  // scale * log2(e): exp(scale x) = 2^(c x)
+  // exp(scale x) = 2^(c x): c = scale * log2(e) in fp32, and as c_hi + c_lo, c_lo > 0
+  float c, c_hi, c_lo;
   float *logprob, *stats;
   const float* g_logprob;
   void* g_x;
@@ -266,9 +268,9 @@ struct PrefArgs {
   float *loss, *margin, *g_logprob;
   double* terms;
 };
-hipError_t launch_logprob(const LogitArgs& a, int dtype, hipStream_t s);
-hipError_t launch_logprob_grad(const LogitArgs& a, int dtype, hipStream_t s);
-hipError_t launch_policy_logits(const LogitArgs& a, const PolicyArgs& p, int dtype, hipStream_t s);
+hipError_t launch_logprob(LogitArgs a, int dtype, hipStream_t s);
+hipError_t launch_logprob_grad(LogitArgs a, int dtype, hipStream_t s);
+hipError_t launch_policy_logits(LogitArgs a, const PolicyArgs& p, int dtype, hipStream_t s);
 hipError_t launch_policy(const PolicyArgs& p, hipStream_t s);
 hipError_t launch_preference(const PrefArgs& p, hipStream_t s);
 

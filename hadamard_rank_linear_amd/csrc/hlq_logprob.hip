@@ -22,9 +22,89 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 // -inf has been seen (their exponentials are then 0, not exp(-inf + inf)).
 __device__ __forceinline__ float ref_of(float m) { return m == -__builtin_huge_valf() ? 0.f : m; }
 
-// The running maximum m and sum s of a thread over P pieces.
+// exp(scale d) for d <= 0, scale log2(e) = c_hi + c_lo.  c rounded to fp32
+// alone shifts every exponential of a sum the same way (2e-7 of a typical log
+// probability, and a sequence adds hundreds); c_lo > 0, so -inf stays -inf.
+__device__ __forceinline__ float exp_scaled(float d, float c_hi, float c_lo) {
+  return exp2_hw(__builtin_fmaf(d, c_hi, d * c_lo));
+}
+
+// ------------------------------------------------------------ pieces of a row
+// A row is split into 16-byte pieces, thread i of W taking pieces i, i + W, ...
+// Addresses are a scalar base and a 32-bit byte offset.  What lies past the
+// row reads as -inf, which adds nothing to the sum.  A row whose length is no
+// multiple of the piece has its last piece read ending at the row's end and
+// shifted into place (rows shorter than a piece: by elements).
+template <int DT>
+struct Row {
+  static constexpr int N = Piece<DT>::N, ES = DT == 0 ? 4 : 2;
+  static constexpr uint32_t FILL = DT == 0 ? 0xFF800000u : 0xFF80FF80u;
+  const char* base;  // uniform
+  uint32_t V;
+
+  __device__ __forceinline__ u32x4 load(uint32_t e) const {
+    u32x4 r = {FILL, FILL, FILL, FILL};
+    if (e < V) {
+      if (V < (uint32_t)N) {
+        short_row(r);
+      } else {
+        const uint32_t skip = e + N > V ? e + N - V : 0u;
+        __builtin_memcpy(&r, base + (e - skip) * ES, 16);
+        if (skip) {
+          if constexpr (DT == 0) {
+            if (skip & 1) r = (u32x4){r[1], r[2], r[3], FILL};
+            if (skip & 2) r = (u32x4){r[2], r[3], FILL, FILL};
+          } else {
+            if (skip & 1)
+              r = (u32x4){(r[0] >> 16) | (r[1] << 16), (r[1] >> 16) | (r[2] << 16),
+                          (r[2] >> 16) | (r[3] << 16), (r[3] >> 16) | (FILL << 16)};
+            if (skip & 2) r = (u32x4){r[1], r[2], r[3], FILL};
+            if (skip & 4) r = (u32x4){r[2], r[3], FILL, FILL};
+          }
+        }
+      }
+    }
+    return r;
+  }
+
+  __device__ __forceinline__ void short_row(u32x4& r) const {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if ((uint32_t)k < V) {
+        if constexpr (DT == 0) {
+          r[k] = reinterpret_cast<const uint32_t*>(base)[k];
+        } else {
+          const uint32_t v = *reinterpret_cast<const uint16_t*>(base + 2 * k);
+          r[k / 2] = (k & 1) ? (r[k / 2] & 0xFFFFu) | (v << 16) : (r[k / 2] & 0xFFFF0000u) | v;
+        }
+      }
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ void store_row(char* base, uint32_t e, uint32_t V, const u32x4& r) {
+  constexpr int N = Piece<DT>::N, ES = DT == 0 ? 4 : 2;
+  if (e + N <= V) {
+    __builtin_memcpy(base + e * ES, &r, 16);
+  } else if (e < V) {
+#pragma unroll
+    for (int k = 0; k < N - 1; ++k)
+      if (e + k < V) {
+        if constexpr (DT == 0) reinterpret_cast<uint32_t*>(base + e * ES)[k] = r[k];
+        else reinterpret_cast<uint16_t*>(base + e * ES)[k] = (uint16_t)(r[k / 2] >> (16 * (k & 1)));
+      }
+  }
+}
+
+// Makes the compiler unpack a piece again where it is used next, instead of
+// keeping its elements in a register each from one use to the other.
+__device__ __forceinline__ void keep_packed(u32x4& r) { asm volatile("" : "+v"(r)); }
+
+// Maximum and sum relative to it of P pieces, joined to a thread's running
+// (m, s).
 template <int DT, int P>
-__device__ __forceinline__ void accumulate(const u32x4 (&r)[P], float c, float& m, float& s) {
+__device__ __forceinline__ void accumulate(u32x4 (&r)[P], const LogitArgs& a, float& m,
+                                           float& s) {
   constexpr int N = Piece<DT>::N;
   float top = m;
 #pragma unroll
@@ -32,53 +112,42 @@ __device__ __forceinline__ void accumulate(const u32x4 (&r)[P], float c, float& 
 #pragma unroll
     for (int k = 0; k < N; ++k) top = fmaxf(top, piece_at<DT>(r[j], k));
   const float ref = ref_of(top);
-  float t = s * exp2_hw((m - ref) * c);
+  float t = s * exp_scaled(m - ref, a.c_hi, a.c_lo);
 #pragma unroll
-  for (int j = 0; j < P; ++j)
+  for (int j = 0; j < P; ++j) {
+    keep_packed(r[j]);
 #pragma unroll
-    for (int k = 0; k < N; ++k) t += exp2_hw((piece_at<DT>(r[j], k) - ref) * c);
+    for (int k = 0; k < N; ++k) t += exp_scaled(piece_at<DT>(r[j], k) - ref, a.c_hi, a.c_lo);
+  }
   m = top;
   s = t;
 }
 
-// A piece whose elements past the row are -inf.
-template <int DT>
-__device__ __forceinline__ u32x4 load_logits(const void* base, int64_t e, int64_t n) {
-  constexpr int N = Piece<DT>::N;
-  u32x4 r = load_piece<DT>(base, e, n);
-  if (n < N) {
+// Joins the threads' (m, s) over a workgroup of W; every thread gets the row's.  sm: [2][16] floats.
+template <int W>
+__device__ __forceinline__ void join_stats(const LogitArgs& a, float (*sm)[16], float& m,
+                                           float& s) {
+  float top = lanes_max(m);
+  s = lanes_sum<64>(s * exp_scaled(m - ref_of(top), a.c_hi, a.c_lo));
+  if constexpr (W > 64) {
+    if ((threadIdx.x & 63) == 0) {
+      sm[0][threadIdx.x >> 6] = top;
+      sm[1][threadIdx.x >> 6] = s;
+    }
+    __syncthreads();
+    m = sm[0][threadIdx.x & (W / 64 - 1)];
+    s = sm[1][threadIdx.x & (W / 64 - 1)];
+    top = m;
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (k >= n) {
-        if constexpr (DT == 0) r[k] = 0xFF800000u;
-        else r[k / 2] = (k & 1) ? (r[k / 2] & 0xFFFFu) | 0xFF800000u : 0xFF80u;
-      }
+    for (int k = W / 128; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor(top, k));
+    s = lanes_sum<W / 64>(s * exp_scaled(m - ref_of(top), a.c_hi, a.c_lo));
   }
-  return r;
+  m = top;
 }
 
-// Maximum and sum of a row over a workgroup of W threads (every thread gets
-// both).  sm: 2 * W / 64 values.
-template <int DT, int W>
-__device__ __forceinline__ void row_stats(const void* x, int64_t base, int64_t V, float c, float* sm,
-                                          float& m, float& s) {
-  constexpr int N = Piece<DT>::N, P = 4;
-  m = -__builtin_huge_valf();
-  s = 0.f;
-  int64_t v = threadIdx.x * N;
-  for (; v + (P - 1) * W * N + N <= V; v += P * W * N) {
-    u32x4 r[P];
-#pragma unroll
-    for (int j = 0; j < P; ++j) r[j] = load_piece<DT>(x, base + v + j * W * N, N);
-    accumulate<DT, P>(r, c, m, s);
-  }
-  for (; v < V; v += W * N) {
-    u32x4 r[1] = {load_logits<DT>(x, base + v, V - v)};
-    accumulate<DT, 1>(r, c, m, s);
-  }
-  const float top = group_max<W>(m, sm);
-  s = group_sum<W>(s * exp2_hw((m - ref_of(top)) * c), sm + W / 64);
-  m = top;
+template <int DT>
+__device__ __forceinline__ Row<DT> row_of(const LogitArgs& a, int64_t row) {
+  return Row<DT>{static_cast<const char*>(a.logits) + row * a.ld * Row<DT>::ES, (uint32_t)a.V};
 }
 
 __device__ __forceinline__ double logprob_of(float xt, float m, float s, double scale) {
@@ -86,61 +155,89 @@ __device__ __forceinline__ double logprob_of(float xt, float m, float s, double 
   return ((double)xt - (double)m) * scale - log((double)s);
 }
 
-// Gradient of a row: f ([v = t] - e_v / s) with f = g * scale; f / s is
-// rounded once, then each product once, then the output.
+// Log probabilities: a workgroup of W threads per row, P pieces of a thread in
+// flight at a time.
+template <int DT, int W, int P>
+__global__ __launch_bounds__(W) void k_logprob(LogitArgs a) {
+  constexpr int N = Piece<DT>::N;
+  __shared__ float sm[2][16];
+  const int64_t row = a.row0 + blockIdx.x, t = a.targets[row];
+  float m = 0.f, s = 1.f, lp = 0.f;
+  if (t >= 0 && t < a.V) {
+    const Row<DT> x = row_of<DT>(a, row);
+    const float xt = load1<DT>(x.base, t);
+    m = -__builtin_huge_valf();
+    s = 0.f;
+    for (uint32_t e0 = threadIdx.x * N; e0 < x.V; e0 += W * N * P) {
+      u32x4 r[P];
+#pragma unroll
+      for (int j = 0; j < P; ++j) r[j] = x.load(e0 + j * W * N);
+      accumulate<DT, P>(r, a, m, s);
+    }
+    join_stats<W>(a, sm, m, s);
+    if (threadIdx.x == 0) lp = (float)logprob_of(xt, m, s, a.scale);
+  }
+  if (threadIdx.x == 0) {
+    a.logprob[row] = lp;
+    a.stats[2 * row] = m;
+    a.stats[2 * row + 1] = s;
+  }
+}
+
+// Gradient of a row's piece at element e: f ([v = t] - e_v / s), k_s = -f / s.
+template <int DT>
+__device__ __forceinline__ u32x4 gradient_piece(const u32x4& r, uint32_t e, uint32_t t, float c,
+                                                float f, float k_s, float m) {
+  constexpr int N = Piece<DT>::N;
+  float o[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) o[k] = k_s * exp2_hw((piece_at<DT>(r, k) - m) * c);
+  if (t - e < (uint32_t)N) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) o[k] += t - e == (uint32_t)k ? f : 0.f;
+  }
+  return make_piece<DT>(o);
+}
+
 template <int DT, int W>
-__device__ __forceinline__ void row_gradient(const void* x, int64_t base, void* g_x, int64_t g_base,
-                                             int64_t V, int64_t t, float c, float f, float m,
-                                             float s) {
+__device__ __forceinline__ void zero_row(const LogitArgs& a, int64_t row) {
+  constexpr int N = Piece<DT>::N;
+  char* g = static_cast<char*>(a.g_x) + row * a.g_ld * Row<DT>::ES;
+  const u32x4 z = {0u, 0u, 0u, 0u};
+  for (uint32_t e = threadIdx.x * N; e < (uint32_t)a.V; e += W * N)
+    store_row<DT>(g, e, (uint32_t)a.V, z);
+}
+
+// Reads a row again and writes its gradient, P pieces of a thread in flight.
+template <int DT, int W, int P>
+__device__ __forceinline__ void row_gradient(const LogitArgs& a, int64_t row, uint32_t t, float f,
+                                             float m, float s) {
   constexpr int N = Piece<DT>::N;
   if (f == 0.f || s == 0.f) {
-    const u32x4 z = {0u, 0u, 0u, 0u};
-    for (int64_t v = threadIdx.x * N; v < V; v += W * N) store_piece<DT>(g_x, g_base + v, V - v, z);
+    zero_row<DT, W>(a, row);
     return;
   }
+  const Row<DT> x = row_of<DT>(a, row);
+  char* g = static_cast<char*>(a.g_x) + row * a.g_ld * Row<DT>::ES;
   const float k_s = -f / s;
-  for (int64_t v = threadIdx.x * N; v < V; v += W * N) {
-    const u32x4 r = load_piece<DT>(x, base + v, V - v);
-    float o[N];
+  for (uint32_t e0 = threadIdx.x * N; e0 < x.V; e0 += W * N * P) {
+    u32x4 r[P];
 #pragma unroll
-    for (int k = 0; k < N; ++k) o[k] = k_s * exp2_hw((piece_at<DT>(r, k) - m) * c);
-    if (t >= v && t < v + N) {
+    for (int j = 0; j < P; ++j) r[j] = x.load(e0 + j * W * N);
 #pragma unroll
-      for (int k = 0; k < N; ++k) o[k] += t - v == k ? f : 0.f;
+    for (int j = 0; j < P; ++j) {
+      const uint32_t e = e0 + j * W * N;
+      store_row<DT>(g, e, x.V, gradient_piece<DT>(r[j], e, t, a.c, f, k_s, m));
     }
-    store_piece<DT>(g_x, g_base + v, V - v, make_piece<DT>(o));
   }
 }
 
-template <int DT, int W>
-__global__ __launch_bounds__(W) void k_logprob(LogitArgs a) {
-  __shared__ float sm[2 * W / 64];
-  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
-    const int64_t t = a.targets[row];
-    float m = 0.f, s = 1.f, lp = 0.f;
-    if (t >= 0 && t < a.V) {
-      row_stats<DT, W>(a.logits, row * a.ld, a.V, a.c, sm, m, s);
-      if (threadIdx.x == 0)
-        lp = (float)logprob_of(load1<DT>(a.logits, row * a.ld + t), m, s, a.scale);
-    }
-    if (threadIdx.x == 0) {
-      a.logprob[row] = lp;
-      a.stats[2 * row] = m;
-      a.stats[2 * row + 1] = s;
-    }
-    __syncthreads();  // sm is used again
-  }
-}
-
-template <int DT, int W>
+template <int DT, int W, int P>
 __global__ __launch_bounds__(W) void k_logprob_grad(LogitArgs a) {
-  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
-    const int64_t t = a.targets[row];
-    const bool live = t >= 0 && t < a.V;
-    const float f = live ? a.g_logprob[row] * (float)a.scale : 0.f;
-    row_gradient<DT, W>(a.logits, row * a.ld, a.g_x, row * a.g_ld, a.V, t, a.c, f,
-                        a.stats[2 * row], a.stats[2 * row + 1]);
-  }
+  const int64_t row = a.row0 + blockIdx.x, t = a.targets[row];
+  const bool live = t >= 0 && t < a.V;
+  const float f = live ? a.g_logprob[row] * (float)a.scale : 0.f;
+  row_gradient<DT, W, P>(a, row, (uint32_t)t, f, a.stats[2 * row], a.stats[2 * row + 1]);
 }
 
 // ------------------------------------------------------------ policy loss
@@ -170,29 +267,80 @@ __device__ __forceinline__ bool policy_counts(const PolicyArgs& p, int64_t i) {
   return !p.weight || p.weight[i] != 0.f;
 }
 
-template <int DT, int W>
-__global__ __launch_bounds__(W) void k_policy_logits(LogitArgs a, PolicyArgs p) {
-  __shared__ float sm[2 * W / 64], sg;
-  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
-    const int64_t t = a.targets[row];
-    const bool live = t >= 0 && t < a.V && policy_counts(p, row);
-    float m = 0.f, s = 1.f;
-    if (live) row_stats<DT, W>(a.logits, row * a.ld, a.V, a.c, sm, m, s);
-    if (threadIdx.x == 0) {
-      double term[3] = {0.0, 0.0, 0.0}, lp = 0.0, g = 0.0;
-      if (live) {
-        lp = logprob_of(load1<DT>(a.logits, row * a.ld + t), m, s, a.scale);
-        g = policy_token(p, row, lp, term);
-      }
-      a.logprob[row] = (float)lp;
-#pragma unroll
-      for (int k = 0; k < 3; ++k) p.terms[3 * row + k] = term[k];
-      sg = (float)g * (float)a.scale;
+// The row's loss terms and the gradient of its log probability, by thread 0;
+// every thread gets the gradient.
+template <int DT>
+__device__ __forceinline__ float policy_row(const LogitArgs& a, const PolicyArgs& p, int64_t row,
+                                            bool live, float xt, float m, float s, float* sg) {
+  if (threadIdx.x == 0) {
+    double term[3] = {0.0, 0.0, 0.0}, lp = 0.0, g = 0.0;
+    if (live) {
+      lp = logprob_of(xt, m, s, a.scale);
+      g = policy_token(p, row, lp, term);
     }
-    __syncthreads();
-    row_gradient<DT, W>(a.logits, row * a.ld, a.g_x, row * a.g_ld, a.V, t, a.c, sg, m, s);
-    __syncthreads();  // sm and sg are used again
+    a.logprob[row] = (float)lp;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) p.terms[3 * row + k] = term[k];
+    *sg = (float)g * (float)a.scale;
   }
+  __syncthreads();
+  return *sg;
+}
+
+// Rows of up to W * P pieces: held in registers between the statistics and the
+// gradient, so that the logits are read once.
+template <int DT, int W, int P>
+__global__ __launch_bounds__(W, 4) void k_policy_regs(LogitArgs a, PolicyArgs p) {
+  constexpr int N = Piece<DT>::N;
+  __shared__ float sm[2][16], sg;
+  const int64_t row = a.row0 + blockIdx.x, t = a.targets[row];
+  const bool live = t >= 0 && t < a.V && policy_counts(p, row);
+  const Row<DT> x = row_of<DT>(a, row);
+  u32x4 r[P];
+  float m = -__builtin_huge_valf(), s = 0.f, xt = 0.f;
+  if (live) {
+    xt = load1<DT>(x.base, t);
+#pragma unroll
+    for (int j = 0; j < P; ++j) r[j] = x.load((threadIdx.x + j * W) * N);
+    accumulate<DT, P>(r, a, m, s);
+    join_stats<W>(a, sm, m, s);
+  }
+  const float f = policy_row<DT>(a, p, row, live, xt, m, s, &sg);
+  if (f == 0.f || s == 0.f) {
+    zero_row<DT, W>(a, row);
+    return;
+  }
+  char* g = static_cast<char*>(a.g_x) + row * a.g_ld * Row<DT>::ES;
+  const float k_s = -f / s;
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    keep_packed(r[j]);
+    const uint32_t e = (threadIdx.x + j * W) * N;
+    store_row<DT>(g, e, x.V, gradient_piece<DT>(r[j], e, (uint32_t)t, a.c, f, k_s, m));
+  }
+}
+
+// Longer rows are read twice, the second time partly from cache.
+template <int DT, int W, int P>
+__global__ __launch_bounds__(W) void k_policy_long(LogitArgs a, PolicyArgs p) {
+  constexpr int N = Piece<DT>::N;
+  __shared__ float sm[2][16], sg;
+  const int64_t row = a.row0 + blockIdx.x, t = a.targets[row];
+  const bool live = t >= 0 && t < a.V && policy_counts(p, row);
+  float m = -__builtin_huge_valf(), s = 0.f, xt = 0.f;
+  if (live) {
+    const Row<DT> x = row_of<DT>(a, row);
+    xt = load1<DT>(x.base, t);
+    for (uint32_t e0 = threadIdx.x * N; e0 < x.V; e0 += W * N * P) {
+      u32x4 r[P];
+#pragma unroll
+      for (int j = 0; j < P; ++j) r[j] = x.load(e0 + j * W * N);
+      accumulate<DT, P>(r, a, m, s);
+    }
+    join_stats<W>(a, sm, m, s);
+  }
+  const float f = policy_row<DT>(a, p, row, live, xt, m, s, &sg);
+  row_gradient<DT, W, P>(a, row, (uint32_t)t, f, m, s);
 }
 
 __global__ __launch_bounds__(256) void k_policy(PolicyArgs p) {
@@ -268,31 +416,64 @@ __global__ __launch_bounds__(256) void k_preference(PrefArgs p) {
   }
 }
 
-#define HLQ_ROWS(K, ...)                                                                      \
-  if (dtype == 0)                                                                             \
-    hipLaunchKernelGGL((K<0, 1024>), rows_grid(a.T), dim3(1024), 0, s, __VA_ARGS__);     \
-  else                                                                                        \
-    hipLaunchKernelGGL((K<1, 1024>), rows_grid(a.T), dim3(1024), 0, s, __VA_ARGS__)
+// ------------------------------------------------------------ launches
+// Threads per row: a wave for short rows, 256 threads where rows are many, and
+// 1024 for long rows that are too few to fill the chip.
+static int row_threads(int64_t T, int64_t pieces) {
+  if (T >= 512) return pieces <= 256 ? 64 : 256;
+  return pieces <= 64 ? 64 : (pieces <= 512 ? 256 : 1024);
+}
 
-hipError_t launch_logprob(const LogitArgs& a, int dtype, hipStream_t s) {
+static int64_t row_pieces(int64_t V, int dtype) { return dtype == 0 ? (V + 3) / 4 : (V + 7) / 8; }
+
+// One workgroup per row, 2^20 rows a launch (a launch holds fewer than 2^32
+// threads).
+#define HLQ_ROW_LAUNCH(K, W, P, ...)                                                           \
+  for (a.row0 = 0; a.row0 < a.T; a.row0 += 1 << 20) {                                          \
+    const dim3 g = rows_grid(a.T - a.row0);                                                    \
+    if (dtype == 0) hipLaunchKernelGGL((K<0, W, P>), g, dim3(W), 0, s, __VA_ARGS__);           \
+    else hipLaunchKernelGGL((K<1, W, P>), g, dim3(W), 0, s, __VA_ARGS__);                      \
+  }
+
+hipError_t launch_logprob(LogitArgs a, int dtype, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
-  HLQ_ROWS(k_logprob, a);
+  switch (row_threads(a.T, row_pieces(a.V, dtype))) {
+    case 64: HLQ_ROW_LAUNCH(k_logprob, 64, 4, a); break;
+    case 256: HLQ_ROW_LAUNCH(k_logprob, 256, 4, a); break;
+    default: HLQ_ROW_LAUNCH(k_logprob, 1024, 4, a); break;
+  }
   return hipGetLastError();
 }
 
-hipError_t launch_logprob_grad(const LogitArgs& a, int dtype, hipStream_t s) {
+hipError_t launch_logprob_grad(LogitArgs a, int dtype, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
-  HLQ_ROWS(k_logprob_grad, a);
+  switch (row_threads(a.T, row_pieces(a.V, dtype))) {
+    case 64: HLQ_ROW_LAUNCH(k_logprob_grad, 64, 2, a); break;
+    case 256: HLQ_ROW_LAUNCH(k_logprob_grad, 256, 2, a); break;
+    default: HLQ_ROW_LAUNCH(k_logprob_grad, 1024, 2, a); break;
+  }
   return hipGetLastError();
 }
 
-hipError_t launch_policy_logits(const LogitArgs& a, const PolicyArgs& p, int dtype,
+hipError_t launch_policy_logits(LogitArgs a, const PolicyArgs& p, int dtype,
                                 hipStream_t s) {
-  if (a.T) { HLQ_ROWS(k_policy_logits, a, p); }
+  const int64_t n = row_pieces(a.V, dtype);
+  if (a.T) {
+    const bool few = a.T < 256;  // fewer rows than CUs: more threads a row
+    if (n <= 256 && !(few && n > 64)) { HLQ_ROW_LAUNCH(k_policy_regs, 64, 4, a, p); }
+    else if (n <= 1024 && !(few && n > 256)) { HLQ_ROW_LAUNCH(k_policy_regs, 256, 4, a, p); }
+    else if (n <= 2048 && !few) { HLQ_ROW_LAUNCH(k_policy_regs, 256, 8, a, p); }
+    else if (n <= 4096 && !few) { HLQ_ROW_LAUNCH(k_policy_regs, 256, 16, a, p); }
+    else if (n <= 4096) { HLQ_ROW_LAUNCH(k_policy_regs, 1024, 4, a, p); }
+    else if (n <= 8192) { HLQ_ROW_LAUNCH(k_policy_regs, 512, 16, a, p); }
+    else if (n <= 12288) { HLQ_ROW_LAUNCH(k_policy_regs, 1024, 12, a, p); }
+    else if (n <= 16384) { HLQ_ROW_LAUNCH(k_policy_regs, 1024, 16, a, p); }
+    else { HLQ_ROW_LAUNCH(k_policy_long, 1024, 4, a, p); }
+  }
   hipLaunchKernelGGL(k_terms<3>, dim3(1), dim3(1024), 0, s, p.terms, p.T, 1.0, p.sums);
   return hipGetLastError();
 }
-#undef HLQ_ROWS
+#undef HLQ_ROW_LAUNCH
 
 hipError_t launch_policy(const PolicyArgs& p, hipStream_t s) {
   if (p.T) hipLaunchKernelGGL(k_policy, dim3(cdiv(p.T, 256)), dim3(256), 0, s, p);

@@ -44,10 +44,13 @@ hlq_status check_workspace(const void* ws, size_t have, size_t need) {
 
 bool norm_shape_ok(int64_t T, int64_t C) { return T >= 0 && T < kMax && C >= 1 && C < kMax; }
 
-// Rows of logits: T x V at pitch ld.
+// Rows of logits: T x V at pitch ld.  A row's bytes are addressed in 32 bits.
 bool rows_ok(int64_t T, int64_t V, int64_t ld) {
-  return T >= 0 && T < kMax && V >= 1 && V < kMax && ld >= V && ld < (int64_t(1) << 40);
+  return T >= 0 && T < kMax && V >= 1 && V < kMax / 2 && ld >= V && ld < (int64_t(1) << 40);
 }
+
+// Its exponent scale * log2(e) splits into two normal fp32 numbers.
+bool scale_ok(double v) { return v >= 0x1p-64 && v <= 0x1p64; }
 
 hlq::LogitArgs logit_args(const void* logits, int64_t ld, const int64_t* targets, int64_t T,
                           int64_t V, double scale) {
@@ -56,7 +59,10 @@ hlq::LogitArgs logit_args(const void* logits, int64_t ld, const int64_t* targets
   a.targets = targets;
   a.T = T; a.V = V; a.ld = ld; a.g_ld = V;
   a.scale = scale;
-  a.c = (float)(scale * 1.4426950408889634074);
+  const double c = scale * 1.4426950408889634074;
+  a.c = (float)c;
+  a.c_hi = std::nextafter((float)c, 0.f);
+  a.c_lo = (float)(c - (double)a.c_hi);
   return a;
 }
 
@@ -125,7 +131,7 @@ hlq_status hlq_token_logprob_forward(const void* logits, int dtype, int64_t ld,
   if (T && any_null({logits, targets, logprob, stats})) return HLQ_ERR_NULL;
   if (!dtype_ok(dtype)) return HLQ_ERR_DTYPE;
   if (!rows_ok(T, V, ld)) return HLQ_ERR_SHAPE;
-  if (!positive(scale)) return HLQ_ERR_VALUE;
+  if (!scale_ok(scale)) return HLQ_ERR_VALUE;
   if (!aligned(logits, esize(dtype)) || !aligned(targets, 8) || !all_aligned(4, {logprob, stats}))
     return HLQ_ERR_ALIGN;
   hlq::LogitArgs a = logit_args(logits, ld, targets, T, V, scale);
@@ -142,7 +148,7 @@ hlq_status hlq_token_logprob_backward(const float* g_logprob, const void* logits
   if (T && any_null({g_logprob, logits, targets, stats, g_x})) return HLQ_ERR_NULL;
   if (!dtype_ok(dtype)) return HLQ_ERR_DTYPE;
   if (!rows_ok(T, V, ld) || !rows_ok(T, V, g_ld)) return HLQ_ERR_SHAPE;
-  if (!positive(scale)) return HLQ_ERR_VALUE;
+  if (!scale_ok(scale)) return HLQ_ERR_VALUE;
   if (!all_aligned(esize(dtype), {logits, g_x}) || !aligned(targets, 8) ||
       !all_aligned(4, {g_logprob, stats}))
     return HLQ_ERR_ALIGN;
@@ -191,7 +197,7 @@ hlq_status hlq_policy_loss_logits(const void* logits, int dtype, int64_t ld,
     return HLQ_ERR_NULL;
   if (!dtype_ok(dtype)) return HLQ_ERR_DTYPE;
   if (!rows_ok(T, V, ld) || !rows_ok(T, V, g_ld)) return HLQ_ERR_SHAPE;
-  if (!positive(scale) || !policy_values_ok(clip_low, clip_high, kl_coef)) return HLQ_ERR_VALUE;
+  if (!scale_ok(scale) || !policy_values_ok(clip_low, clip_high, kl_coef)) return HLQ_ERR_VALUE;
   if (T && (ref_logprob != nullptr) != (kl_coef != 0.0)) return HLQ_ERR_NULL;
   if (!all_aligned(esize(dtype), {logits, g_x}) || !aligned(targets, 8) ||
       !all_aligned(4, {old_logprob, advantage, weight, ref_logprob, sums, logprob}))

@@ -459,12 +459,12 @@ hlq_status hlq_layer_norm_backward(const void* g_y, const void* h, const void* g
  *   logits   T rows of V elements, dtype, row t at element t * ld (ld >= V).
  *   targets  [T] int64; one outside [0, V) is ignored: its row is not read,
  *            logprob is 0 and stats (0, 1).
- *   scale    the inverse temperature, > 0 and finite.
+ *   scale    the inverse temperature, 2^-64 to 2^64.
  *   logprob  [T] f32 out;  stats [T][2] f32 out, for the backward pass.
  * Logits of -inf have probability zero; a row of nothing else has logprob
  * -inf and stats (-inf, 0).  A NaN or +inf in a row makes its logprob NaN.
  * Errors: HLQ_ERR_NULL, HLQ_ERR_DTYPE, HLQ_ERR_SHAPE (T < 0, V < 1, ld < V,
- * T or V >= 2^31), HLQ_ERR_VALUE (scale), HLQ_ERR_ALIGN.
+ * T >= 2^31, V >= 2^30), HLQ_ERR_VALUE (scale), HLQ_ERR_ALIGN.
  */
 hlq_status hlq_token_logprob_forward(const void* logits, int dtype, int64_t ld,
                                      const int64_t* targets, int64_t T, int64_t V, double scale,
