@@ -150,9 +150,19 @@ __device__ __forceinline__ Row<DT> row_of(const LogitArgs& a, int64_t row) {
   return Row<DT>{static_cast<const char*>(a.logits) + row * a.ld * Row<DT>::ES, (uint32_t)a.V};
 }
 
+// scale (x_t - m) - log s; s is 0 (nothing but -inf), NaN, or at least 1.  The
+// logarithm splits off the exponent, so fp32 suffices for the rest of it: off
+// by 2^-25, where log(double) costs a row about as much as all its reductions.
 __device__ __forceinline__ double logprob_of(float xt, float m, float s, double scale) {
-  if (s == 0.f) return -__builtin_huge_val();  // nothing but -inf
-  return ((double)xt - (double)m) * scale - log((double)s);
+  if (!(s >= 1.f)) return s == 0.f ? -__builtin_huge_val() : (double)s;
+  const uint32_t b = __float_as_uint(s);
+  int e = (int)(b >> 23) - 127;
+  float f = __uint_as_float((b & 0x7FFFFFu) | 0x3F800000u);
+  if (f >= 1.5f) {
+    f *= 0.5f;
+    ++e;
+  }
+  return ((double)xt - (double)m) * scale - ((double)e * 0.69314718055994530942 + (double)logf(f));
 }
 
 // Log probabilities: a workgroup of W threads per row, P pieces of a thread in
@@ -241,21 +251,30 @@ __global__ __launch_bounds__(W) void k_logprob_grad(LogitArgs a) {
 }
 
 // ------------------------------------------------------------ policy loss
+// What a token brings to the loss besides its log probability.
+struct PolicyToken {
+  float old, advantage, weight, ref;
+};
+__device__ __forceinline__ PolicyToken policy_load(const PolicyArgs& p, int64_t i) {
+  return PolicyToken{p.old_logprob[i], p.advantage[i], p.weight ? p.weight[i] : 1.f,
+                     p.ref_logprob ? p.ref_logprob[i] : 0.f};
+}
+
 // The terms of one token, in fp64 from the log probability: w times the loss,
 // the KL estimate and whether the clamped ratio counted; returns the gradient.
-__device__ __forceinline__ double policy_token(const PolicyArgs& p, int64_t i, double lp,
+__device__ __forceinline__ double policy_token(const PolicyArgs& p, const PolicyToken& q, double lp,
                                                double (&term)[3]) {
-  const double w = p.weight ? (double)p.weight[i] : 1.0, A = (double)p.advantage[i];
-  const double r = exp(lp - (double)p.old_logprob[i]);
+  const double w = (double)q.weight, A = (double)q.advantage;
+  const double r = exp(lp - (double)q.old);
   const double lo = 1.0 - p.clip_low, hi = 1.0 + p.clip_high;
   const double bounded = r < lo ? lo : (r > hi ? hi : r);
   const double free_ = r * A, clipped = bounded * A;
   const bool cut = clipped < free_;
   double kl = 0.0, g = cut ? 0.0 : -free_;
   if (p.ref_logprob) {
-    const double d = (double)p.ref_logprob[i] - lp;
-    kl = expm1(d) - d;
-    g -= p.kl_coef * expm1(d);
+    const double d = (double)q.ref - lp, x = expm1(d);
+    kl = x - d;
+    g -= p.kl_coef * x;
   }
   term[0] = w * (p.kl_coef * kl - (cut ? clipped : free_));
   term[1] = w * kl;
@@ -263,20 +282,16 @@ __device__ __forceinline__ double policy_token(const PolicyArgs& p, int64_t i, d
   return w * g;
 }
 
-__device__ __forceinline__ bool policy_counts(const PolicyArgs& p, int64_t i) {
-  return !p.weight || p.weight[i] != 0.f;
-}
-
 // The row's loss terms and the gradient of its log probability, by thread 0;
 // every thread gets the gradient.
-template <int DT>
 __device__ __forceinline__ float policy_row(const LogitArgs& a, const PolicyArgs& p, int64_t row,
-                                            bool live, float xt, float m, float s, float* sg) {
+                                            const PolicyToken& q, bool live, float xt, float m,
+                                            float s, float* sg) {
   if (threadIdx.x == 0) {
     double term[3] = {0.0, 0.0, 0.0}, lp = 0.0, g = 0.0;
     if (live) {
       lp = logprob_of(xt, m, s, a.scale);
-      g = policy_token(p, row, lp, term);
+      g = policy_token(p, q, lp, term);
     }
     a.logprob[row] = (float)lp;
 #pragma unroll
@@ -294,7 +309,8 @@ __global__ __launch_bounds__(W, 4) void k_policy_regs(LogitArgs a, PolicyArgs p)
   constexpr int N = Piece<DT>::N;
   __shared__ float sm[2][16], sg;
   const int64_t row = a.row0 + blockIdx.x, t = a.targets[row];
-  const bool live = t >= 0 && t < a.V && policy_counts(p, row);
+  const PolicyToken q = policy_load(p, row);
+  const bool live = t >= 0 && t < a.V && q.weight != 0.f;
   const Row<DT> x = row_of<DT>(a, row);
   u32x4 r[P];
   float m = -__builtin_huge_valf(), s = 0.f, xt = 0.f;
@@ -305,7 +321,7 @@ __global__ __launch_bounds__(W, 4) void k_policy_regs(LogitArgs a, PolicyArgs p)
     accumulate<DT, P>(r, a, m, s);
     join_stats<W>(a, sm, m, s);
   }
-  const float f = policy_row<DT>(a, p, row, live, xt, m, s, &sg);
+  const float f = policy_row(a, p, row, q, live, xt, m, s, &sg);
   if (f == 0.f || s == 0.f) {
     zero_row<DT, W>(a, row);
     return;
@@ -326,7 +342,8 @@ __global__ __launch_bounds__(W) void k_policy_long(LogitArgs a, PolicyArgs p) {
   constexpr int N = Piece<DT>::N;
   __shared__ float sm[2][16], sg;
   const int64_t row = a.row0 + blockIdx.x, t = a.targets[row];
-  const bool live = t >= 0 && t < a.V && policy_counts(p, row);
+  const PolicyToken q = policy_load(p, row);
+  const bool live = t >= 0 && t < a.V && q.weight != 0.f;
   float m = -__builtin_huge_valf(), s = 0.f, xt = 0.f;
   if (live) {
     const Row<DT> x = row_of<DT>(a, row);
@@ -339,7 +356,7 @@ __global__ __launch_bounds__(W) void k_policy_long(LogitArgs a, PolicyArgs p) {
     }
     join_stats<W>(a, sm, m, s);
   }
-  const float f = policy_row<DT>(a, p, row, live, xt, m, s, &sg);
+  const float f = policy_row(a, p, row, q, live, xt, m, s, &sg);
   row_gradient<DT, W, P>(a, row, (uint32_t)t, f, m, s);
 }
 
@@ -347,7 +364,8 @@ __global__ __launch_bounds__(256) void k_policy(PolicyArgs p) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= p.T) return;
   double term[3] = {0.0, 0.0, 0.0}, g = 0.0;
-  if (policy_counts(p, i)) g = policy_token(p, i, (double)p.logprob[i], term);
+  const PolicyToken q = policy_load(p, i);
+  if (q.weight != 0.f) g = policy_token(p, q, (double)p.logprob[i], term);
   p.g_logprob[i] = (float)g;
 #pragma unroll
   for (int k = 0; k < 3; ++k) p.terms[3 * i + k] = term[k];
@@ -417,11 +435,22 @@ __global__ __launch_bounds__(256) void k_preference(PrefArgs p) {
 }
 
 // ------------------------------------------------------------ launches
-// Threads per row: a wave for short rows, 256 threads where rows are many, and
-// 1024 for long rows that are too few to fill the chip.
-static int row_threads(int64_t T, int64_t pieces) {
-  if (T >= 512) return pieces <= 256 ? 64 : 256;
-  return pieces <= 64 ? 64 : (pieces <= 512 ? 256 : 1024);
+// Threads per row of n pieces: a wave for short rows, the whole of a
+// workgroup's 1024 for long ones (4096 x 128256 bf16 scored with 64, 256, 512
+// and 1024 threads a row: 193, 188, 183 and 176 us; 8190 x 32000: 104, 97, 90
+// and 95; 8190 x 1000: 12, 18, 25 and 44), and more where the rows are too few
+// to fill the chip (3 x 32003: 18.8, 8.9, 7.9 and 7.8).
+static int score_threads(int64_t T, int64_t n) {
+  if (T < 256) return n <= 64 ? 64 : (n <= 512 ? 256 : 1024);
+  return n <= 256 ? 64 : (n <= 2048 ? 256 : (n <= 8192 ? 512 : 1024));
+}
+
+// The same for the gradient (4096 x 128256 bf16 with 64, 256, 512 and 1024
+// threads: 430, 420, 413 and 394 us; 8190 x 32000: 222, 207, 194 and 177;
+// 8190 x 1000: 10, 11, 14 and 23).
+static int grad_threads(int64_t T, int64_t n) {
+  if (T < 256) return n <= 64 ? 64 : (n <= 512 ? 256 : 1024);
+  return n <= 256 ? 64 : (n <= 1024 ? 256 : 1024);
 }
 
 static int64_t row_pieces(int64_t V, int dtype) { return dtype == 0 ? (V + 3) / 4 : (V + 7) / 8; }
@@ -437,9 +466,10 @@ static int64_t row_pieces(int64_t V, int dtype) { return dtype == 0 ? (V + 3) / 
 
 hipError_t launch_logprob(LogitArgs a, int dtype, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
-  switch (row_threads(a.T, row_pieces(a.V, dtype))) {
+  switch (score_threads(a.T, row_pieces(a.V, dtype))) {
     case 64: HLQ_ROW_LAUNCH(k_logprob, 64, 4, a); break;
     case 256: HLQ_ROW_LAUNCH(k_logprob, 256, 4, a); break;
+    case 512: HLQ_ROW_LAUNCH(k_logprob, 512, 4, a); break;
     default: HLQ_ROW_LAUNCH(k_logprob, 1024, 4, a); break;
   }
   return hipGetLastError();
@@ -447,10 +477,10 @@ hipError_t launch_logprob(LogitArgs a, int dtype, hipStream_t s) {
 
 hipError_t launch_logprob_grad(LogitArgs a, int dtype, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
-  switch (row_threads(a.T, row_pieces(a.V, dtype))) {
+  switch (grad_threads(a.T, row_pieces(a.V, dtype))) {
     case 64: HLQ_ROW_LAUNCH(k_logprob_grad, 64, 2, a); break;
     case 256: HLQ_ROW_LAUNCH(k_logprob_grad, 256, 2, a); break;
-    default: HLQ_ROW_LAUNCH(k_logprob_grad, 1024, 2, a); break;
+    default: HLQ_ROW_LAUNCH(k_logprob_grad, 1024, 4, a); break;
   }
   return hipGetLastError();
 }
