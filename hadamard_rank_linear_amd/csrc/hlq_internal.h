@@ -242,6 +242,7 @@ struct LogitArgs {
   const int64_t* targets;
   int64_t T, V, ld, g_ld;
   int64_t row0;  // first row of the launch (set by the launch functions)
+  int stream;    // the rows exceed the last-level cache
   double scale;
   // exp(scale x) = 2^(c x): c = scale * log2(e) in fp32, and as c_hi + c_lo, c_lo > 0
   float c, c_hi, c_lo;

@@ -35,7 +35,16 @@ __device__ __forceinline__ float exp_scaled(float d, float c_hi, float c_lo) {
 // row reads as -inf, which adds nothing to the sum.  A row whose length is no
 // multiple of the piece has its last piece read ending at the row's end and
 // shifted into place (rows shorter than a piece: by elements).
-template <int DT>
+//
+// ST (streaming): the rows together exceed the 256 MB of last-level cache, so
+// what passes through it is gone before anything reads it again; non-temporal
+// accesses keep it from displacing what is in use.  Scoring 4096 x 128256 bf16
+// takes 154 us instead of 174, 8190 x 32000 60 instead of 100, the policy loss
+// over 2048 x 128256 184 instead of 192.  The gradient kernel is the other way
+// about (148 us with, 140 without, at 8190 x 32000 after its scoring).
+typedef u32x4 Loose __attribute__((aligned(2)));  // at any element
+
+template <int DT, bool ST>
 struct Row {
   static constexpr int N = Piece<DT>::N, ES = DT == 0 ? 4 : 2;
   static constexpr uint32_t FILL = DT == 0 ? 0xFF800000u : 0xFF80FF80u;
@@ -49,7 +58,9 @@ struct Row {
         short_row(r);
       } else {
         const uint32_t skip = e + N > V ? e + N - V : 0u;
-        __builtin_memcpy(&r, base + (e - skip) * ES, 16);
+        const char* at = base + (e - skip) * ES;
+        if constexpr (ST) r = __builtin_nontemporal_load(reinterpret_cast<const Loose*>(at));
+        else r = *reinterpret_cast<const Loose*>(at);
         if (skip) {
           if constexpr (DT == 0) {
             if (skip & 1) r = (u32x4){r[1], r[2], r[3], FILL};
@@ -81,11 +92,13 @@ struct Row {
   }
 };
 
-template <int DT>
+template <int DT, bool ST>
 __device__ __forceinline__ void store_row(char* base, uint32_t e, uint32_t V, const u32x4& r) {
   constexpr int N = Piece<DT>::N, ES = DT == 0 ? 4 : 2;
   if (e + N <= V) {
-    __builtin_memcpy(base + e * ES, &r, 16);
+    Loose* at = reinterpret_cast<Loose*>(base + e * ES);
+    if constexpr (ST) __builtin_nontemporal_store(r, at);
+    else *at = r;
   } else if (e < V) {
 #pragma unroll
     for (int k = 0; k < N - 1; ++k)
@@ -145,9 +158,9 @@ __device__ __forceinline__ void join_stats(const LogitArgs& a, float (*sm)[16], 
   m = top;
 }
 
-template <int DT>
-__device__ __forceinline__ Row<DT> row_of(const LogitArgs& a, int64_t row) {
-  return Row<DT>{static_cast<const char*>(a.logits) + row * a.ld * Row<DT>::ES, (uint32_t)a.V};
+template <int DT, bool ST>
+__device__ __forceinline__ Row<DT, ST> row_of(const LogitArgs& a, int64_t row) {
+  return Row<DT, ST>{static_cast<const char*>(a.logits) + row * a.ld * Row<DT, ST>::ES, (uint32_t)a.V};
 }
 
 // scale (x_t - m) - log s; s is 0 (nothing but -inf), NaN, or at least 1.  The
@@ -167,14 +180,14 @@ __device__ __forceinline__ double logprob_of(float xt, float m, float s, double 
 
 // Log probabilities: a workgroup of W threads per row, P pieces of a thread in
 // flight at a time.
-template <int DT, int W, int P>
+template <int DT, bool ST, int W, int P>
 __global__ __launch_bounds__(W) void k_logprob(LogitArgs a) {
   constexpr int N = Piece<DT>::N;
   __shared__ float sm[2][16];
   const int64_t row = a.row0 + blockIdx.x, t = a.targets[row];
   float m = 0.f, s = 1.f, lp = 0.f;
   if (t >= 0 && t < a.V) {
-    const Row<DT> x = row_of<DT>(a, row);
+    const Row<DT, ST> x = row_of<DT, ST>(a, row);
     const float xt = load1<DT>(x.base, t);
     m = -__builtin_huge_valf();
     s = 0.f;
@@ -209,13 +222,13 @@ __device__ __forceinline__ u32x4 gradient_piece(const u32x4& r, uint32_t e, uint
   return make_piece<DT>(o);
 }
 
-template <int DT, int W>
+template <int DT, bool ST, int W>
 __device__ __forceinline__ void zero_row(const LogitArgs& a, int64_t row) {
   constexpr int N = Piece<DT>::N;
-  char* g = static_cast<char*>(a.g_x) + row * a.g_ld * Row<DT>::ES;
+  char* g = static_cast<char*>(a.g_x) + row * a.g_ld * Row<DT, ST>::ES;
   const u32x4 z = {0u, 0u, 0u, 0u};
   for (uint32_t e = threadIdx.x * N; e < (uint32_t)a.V; e += W * N)
-    store_row<DT>(g, e, (uint32_t)a.V, z);
+    store_row<DT, ST>(g, e, (uint32_t)a.V, z);
 }
 
 // Reads a row again and writes its gradient, P pieces of a thread in flight.
@@ -224,11 +237,11 @@ __device__ __forceinline__ void row_gradient(const LogitArgs& a, int64_t row, ui
                                              float m, float s) {
   constexpr int N = Piece<DT>::N;
   if (f == 0.f || s == 0.f) {
-    zero_row<DT, W>(a, row);
+    zero_row<DT, false, W>(a, row);
     return;
   }
-  const Row<DT> x = row_of<DT>(a, row);
-  char* g = static_cast<char*>(a.g_x) + row * a.g_ld * Row<DT>::ES;
+  const Row<DT, false> x = row_of<DT, false>(a, row);
+  char* g = static_cast<char*>(a.g_x) + row * a.g_ld * Row<DT, false>::ES;
   const float k_s = -f / s;
   for (uint32_t e0 = threadIdx.x * N; e0 < x.V; e0 += W * N * P) {
     u32x4 r[P];
@@ -237,7 +250,7 @@ __device__ __forceinline__ void row_gradient(const LogitArgs& a, int64_t row, ui
 #pragma unroll
     for (int j = 0; j < P; ++j) {
       const uint32_t e = e0 + j * W * N;
-      store_row<DT>(g, e, x.V, gradient_piece<DT>(r[j], e, t, a.c, f, k_s, m));
+      store_row<DT, false>(g, e, x.V, gradient_piece<DT>(r[j], e, t, a.c, f, k_s, m));
     }
   }
 }
@@ -304,14 +317,14 @@ __device__ __forceinline__ float policy_row(const LogitArgs& a, const PolicyArgs
 
 // Rows of up to W * P pieces: held in registers between the statistics and the
 // gradient, so that the logits are read once.
-template <int DT, int W, int P>
+template <int DT, bool ST, int W, int P>
 __global__ __launch_bounds__(W, 4) void k_policy_regs(LogitArgs a, PolicyArgs p) {
   constexpr int N = Piece<DT>::N;
   __shared__ float sm[2][16], sg;
   const int64_t row = a.row0 + blockIdx.x, t = a.targets[row];
   const PolicyToken q = policy_load(p, row);
   const bool live = t >= 0 && t < a.V && q.weight != 0.f;
-  const Row<DT> x = row_of<DT>(a, row);
+  const Row<DT, ST> x = row_of<DT, ST>(a, row);
   u32x4 r[P];
   float m = -__builtin_huge_valf(), s = 0.f, xt = 0.f;
   if (live) {
@@ -323,21 +336,21 @@ __global__ __launch_bounds__(W, 4) void k_policy_regs(LogitArgs a, PolicyArgs p)
   }
   const float f = policy_row(a, p, row, q, live, xt, m, s, &sg);
   if (f == 0.f || s == 0.f) {
-    zero_row<DT, W>(a, row);
+    zero_row<DT, ST, W>(a, row);
     return;
   }
-  char* g = static_cast<char*>(a.g_x) + row * a.g_ld * Row<DT>::ES;
+  char* g = static_cast<char*>(a.g_x) + row * a.g_ld * Row<DT, ST>::ES;
   const float k_s = -f / s;
 #pragma unroll
   for (int j = 0; j < P; ++j) {
     keep_packed(r[j]);
     const uint32_t e = (threadIdx.x + j * W) * N;
-    store_row<DT>(g, e, x.V, gradient_piece<DT>(r[j], e, (uint32_t)t, a.c, f, k_s, m));
+    store_row<DT, ST>(g, e, x.V, gradient_piece<DT>(r[j], e, (uint32_t)t, a.c, f, k_s, m));
   }
 }
 
 // Longer rows are read twice, the second time partly from cache.
-template <int DT, int W, int P>
+template <int DT, bool ST, int W, int P>
 __global__ __launch_bounds__(W) void k_policy_long(LogitArgs a, PolicyArgs p) {
   constexpr int N = Piece<DT>::N;
   __shared__ float sm[2][16], sg;
@@ -346,7 +359,7 @@ __global__ __launch_bounds__(W) void k_policy_long(LogitArgs a, PolicyArgs p) {
   const bool live = t >= 0 && t < a.V && q.weight != 0.f;
   float m = -__builtin_huge_valf(), s = 0.f, xt = 0.f;
   if (live) {
-    const Row<DT> x = row_of<DT>(a, row);
+    const Row<DT, ST> x = row_of<DT, ST>(a, row);
     xt = load1<DT>(x.base, t);
     for (uint32_t e0 = threadIdx.x * N; e0 < x.V; e0 += W * N * P) {
       u32x4 r[P];
@@ -442,7 +455,7 @@ __global__ __launch_bounds__(256) void k_preference(PrefArgs p) {
 // to fill the chip (3 x 32003: 18.8, 8.9, 7.9 and 7.8).
 static int score_threads(int64_t T, int64_t n) {
   if (T < 256) return n <= 64 ? 64 : (n <= 512 ? 256 : 1024);
-  return n <= 256 ? 64 : (n <= 2048 ? 256 : (n <= 8192 ? 512 : 1024));
+  return n <= 256 ? 64 : (n <= 2048 ? 256 : 512);
 }
 
 // The same for the gradient (4096 x 128256 bf16 with 64, 256, 512 and 1024
@@ -460,8 +473,14 @@ static int64_t row_pieces(int64_t V, int dtype) { return dtype == 0 ? (V + 3) / 
 #define HLQ_ROW_LAUNCH(K, W, P, ...)                                                           \
   for (a.row0 = 0; a.row0 < a.T; a.row0 += 1 << 20) {                                          \
     const dim3 g = rows_grid(a.T - a.row0);                                                    \
-    if (dtype == 0) hipLaunchKernelGGL((K<0, W, P>), g, dim3(W), 0, s, __VA_ARGS__);           \
-    else hipLaunchKernelGGL((K<1, W, P>), g, dim3(W), 0, s, __VA_ARGS__);                      \
+    if (dtype == 0 && a.stream)                                                                \
+      hipLaunchKernelGGL((K<0, true, W, P>), g, dim3(W), 0, s, __VA_ARGS__);                   \
+    else if (dtype == 0)                                                                       \
+      hipLaunchKernelGGL((K<0, false, W, P>), g, dim3(W), 0, s, __VA_ARGS__);                  \
+    else if (a.stream)                                                                         \
+      hipLaunchKernelGGL((K<1, true, W, P>), g, dim3(W), 0, s, __VA_ARGS__);                   \
+    else                                                                                       \
+      hipLaunchKernelGGL((K<1, false, W, P>), g, dim3(W), 0, s, __VA_ARGS__);                  \
   }
 
 hipError_t launch_logprob(LogitArgs a, int dtype, hipStream_t s) {
@@ -477,11 +496,18 @@ hipError_t launch_logprob(LogitArgs a, int dtype, hipStream_t s) {
 
 hipError_t launch_logprob_grad(LogitArgs a, int dtype, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
-  switch (grad_threads(a.T, row_pieces(a.V, dtype))) {
-    case 64: HLQ_ROW_LAUNCH(k_logprob_grad, 64, 2, a); break;
-    case 256: HLQ_ROW_LAUNCH(k_logprob_grad, 256, 2, a); break;
-    default: HLQ_ROW_LAUNCH(k_logprob_grad, 1024, 4, a); break;
+#define HLQ_GRAD(W, P)                                                                         \
+  for (a.row0 = 0; a.row0 < a.T; a.row0 += 1 << 20) {                                          \
+    const dim3 g = rows_grid(a.T - a.row0);                                                    \
+    if (dtype == 0) hipLaunchKernelGGL((k_logprob_grad<0, W, P>), g, dim3(W), 0, s, a);        \
+    else hipLaunchKernelGGL((k_logprob_grad<1, W, P>), g, dim3(W), 0, s, a);                   \
   }
+  switch (grad_threads(a.T, row_pieces(a.V, dtype))) {
+    case 64: HLQ_GRAD(64, 2); break;
+    case 256: HLQ_GRAD(256, 2); break;
+    default: HLQ_GRAD(1024, 4); break;
+  }
+#undef HLQ_GRAD
   return hipGetLastError();
 }
 

@@ -52,12 +52,13 @@ bool rows_ok(int64_t T, int64_t V, int64_t ld) {
 // Its exponent scale * log2(e) splits into two normal fp32 numbers.
 bool scale_ok(double v) { return v >= 0x1p-64 && v <= 0x1p64; }
 
-hlq::LogitArgs logit_args(const void* logits, int64_t ld, const int64_t* targets, int64_t T,
-                          int64_t V, double scale) {
+hlq::LogitArgs logit_args(const void* logits, int dtype, int64_t ld, const int64_t* targets,
+                          int64_t T, int64_t V, double scale) {
   hlq::LogitArgs a = {};
   a.logits = logits;
   a.targets = targets;
   a.T = T; a.V = V; a.ld = ld; a.g_ld = V;
+  a.stream = T * V * (int64_t)esize(dtype) > (int64_t(256) << 20);
   a.scale = scale;
   const double c = scale * 1.4426950408889634074;
   a.c = (float)c;
@@ -134,7 +135,7 @@ hlq_status hlq_token_logprob_forward(const void* logits, int dtype, int64_t ld,
   if (!scale_ok(scale)) return HLQ_ERR_VALUE;
   if (!aligned(logits, esize(dtype)) || !aligned(targets, 8) || !all_aligned(4, {logprob, stats}))
     return HLQ_ERR_ALIGN;
-  hlq::LogitArgs a = logit_args(logits, ld, targets, T, V, scale);
+  hlq::LogitArgs a = logit_args(logits, dtype, ld, targets, T, V, scale);
   a.logprob = logprob;
   a.stats = stats;
   HLQ_TRY(hlq::launch_logprob(a, dtype, static_cast<hipStream_t>(stream)));
@@ -152,7 +153,7 @@ hlq_status hlq_token_logprob_backward(const float* g_logprob, const void* logits
   if (!all_aligned(esize(dtype), {logits, g_x}) || !aligned(targets, 8) ||
       !all_aligned(4, {g_logprob, stats}))
     return HLQ_ERR_ALIGN;
-  hlq::LogitArgs a = logit_args(logits, ld, targets, T, V, scale);
+  hlq::LogitArgs a = logit_args(logits, dtype, ld, targets, T, V, scale);
   a.g_logprob = g_logprob;
   a.stats = const_cast<float*>(stats);
   a.g_x = g_x;
@@ -205,7 +206,7 @@ hlq_status hlq_policy_loss_logits(const void* logits, int dtype, int64_t ld,
   const hlq_status st =
       check_workspace(workspace, workspace_bytes, hlq_policy_loss_workspace_size(T));
   if (st != HLQ_OK) return st;
-  hlq::LogitArgs a = logit_args(logits, ld, targets, T, V, scale);
+  hlq::LogitArgs a = logit_args(logits, dtype, ld, targets, T, V, scale);
   a.logprob = logprob;
   a.g_x = g_x;
   a.g_ld = g_ld;
