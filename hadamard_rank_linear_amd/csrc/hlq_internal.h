@@ -277,11 +277,12 @@ hipError_t launch_preference(const PrefArgs& p, hipStream_t s);
 
 // Gradient clipping (hlq_clip.hip): part of a list of tensors, passed by value
 // (a kernel's arguments hold 4 KiB).  size: elements, at most 2^30, with bit 31
-// set for bf16.  Tensor i is chunks first[i] .. first[i + 1] - 1 of CLIP_CHUNK
-// elements; chunks: all of them.
+// set for bf16.  Tensor i is chunks first[i] .. first[i + 1] - 1 of CLIP_BYTES;
+// chunks: all of them.
 constexpr int CLIP_LIST = 160;
 constexpr int64_t CLIP_MAX_SIZE = int64_t(1) << 30;
-constexpr int CLIP_CHUNK = 8192;
+constexpr int CLIP_BYTES = 32768;
+constexpr int CLIP_PIECES = 8;
 constexpr unsigned CLIP_GROUPS = 1024;  // workgroups (partials) per launch at most
 struct ClipList {
   const void* grad[CLIP_LIST];
@@ -291,11 +292,13 @@ struct ClipList {
   int count, in_place;
 };
 static_assert(sizeof(ClipList) <= 4000, "kernel arguments");
+// stream: the gradients exceed the last-level cache.
 hipError_t launch_clip_norm(const ClipList& l, int kind, double* part, unsigned groups,
-                            hipStream_t s);
+                            bool stream, hipStream_t s);
 // norm (null: not written) by the first workgroup.
 hipError_t launch_clip_scale(const ClipList& l, int kind, const double* part, int64_t parts,
-                             double max_norm, double* norm, unsigned groups, hipStream_t s);
+                             double max_norm, double* norm, unsigned groups, bool stream,
+                             hipStream_t s);
 
 hipError_t launch_gemm_finalize(const int32_t* partial, int splits, int64_t M,
                                 int64_t N, const float* sa, int sa_step,

@@ -42,7 +42,6 @@ __device__ __forceinline__ float exp_scaled(float d, float c_hi, float c_lo) {
 // takes 154 us instead of 174, 8190 x 32000 60 instead of 100, the policy loss
 // over 2048 x 128256 184 instead of 192.  The gradient kernel is the other way
 // about (148 us with, 140 without, at 8190 x 32000 after its scoring).
-typedef u32x4 Loose __attribute__((aligned(2)));  // at any element
 
 template <int DT, bool ST>
 struct Row {

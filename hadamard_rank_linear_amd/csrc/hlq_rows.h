@@ -14,6 +14,7 @@ namespace hlq {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 Loose __attribute__((aligned(2)));  // 16 bytes at any element
 
 // A piece: 16 bytes of a row, 4 fp32 or 8 bf16 elements (dtype DT: 0 or 1).
 template <int DT>

@@ -14,6 +14,7 @@
 namespace {
 
 constexpr int64_t kMax = int64_t(1) << 31;
+constexpr int64_t kLastLevelCache = int64_t(256) << 20;
 
 bool dtype_ok(int dt) { return dt == HLQ_F32 || dt == HLQ_BF16; }
 size_t esize(int dt) { return dt == HLQ_F32 ? 4 : 2; }
@@ -58,7 +59,7 @@ hlq::LogitArgs logit_args(const void* logits, int dtype, int64_t ld, const int64
   a.logits = logits;
   a.targets = targets;
   a.T = T; a.V = V; a.ld = ld; a.g_ld = V;
-  a.stream = T * V * (int64_t)esize(dtype) > (int64_t(256) << 20);
+  a.stream = T * V * (int64_t)esize(dtype) > kLastLevelCache;
   a.scale = scale;
   const double c = scale * 1.4426950408889634074;
   a.c = (float)c;
@@ -254,8 +255,8 @@ unsigned clip_groups(uint32_t chunks) {
   return chunks < hlq::CLIP_GROUPS ? chunks : hlq::CLIP_GROUPS;
 }
 
-// Walks the tensors in lists that fit a kernel's arguments, calling f on each
-// (sizes must be valid).  Empty tensors are left out.
+// Walks the tensors in lists that fit a kernel's arguments, calling f on each.
+// Empty tensors are left out.
 template <typename F>
 hlq_status for_lists(const void* const* grads, void* const* outs, const int64_t* sizes,
                      const int* dtypes, int64_t count, F f) {
@@ -263,18 +264,18 @@ hlq_status for_lists(const void* const* grads, void* const* outs, const int64_t*
   l.count = 0;
   l.chunks = 0;
   l.in_place = 1;
-  for (int64_t i = 0; i < count; ++i)
+  for (int64_t i = 0; i < count; ++i) {
+    const size_t es = esize(dtypes[i]);
     for (int64_t at = 0; at < sizes[i]; at += hlq::CLIP_MAX_SIZE) {
       const int64_t left = sizes[i] - at;
       const int64_t n = left < hlq::CLIP_MAX_SIZE ? left : hlq::CLIP_MAX_SIZE;
-      const size_t skip = dtypes ? (size_t)at * esize(dtypes[i]) : 0;
       const int k = l.count;
-      l.grad[k] = grads ? static_cast<const char*>(grads[i]) + skip : nullptr;
-      l.out[k] = outs ? static_cast<char*>(outs[i]) + skip : const_cast<void*>(l.grad[k]);
+      l.grad[k] = grads ? static_cast<const char*>(grads[i]) + at * es : nullptr;
+      l.out[k] = outs ? static_cast<char*>(outs[i]) + at * es : const_cast<void*>(l.grad[k]);
       if (l.out[k] != l.grad[k]) l.in_place = 0;
-      l.size[k] = (uint32_t)n | (dtypes && dtypes[i] == HLQ_BF16 ? 0x80000000u : 0u);
+      l.size[k] = (uint32_t)n | (dtypes[i] == HLQ_BF16 ? 0x80000000u : 0u);
       l.first[k] = l.chunks;
-      l.chunks += (uint32_t)((n + hlq::CLIP_CHUNK - 1) / hlq::CLIP_CHUNK);
+      l.chunks += (uint32_t)((n * es + hlq::CLIP_BYTES - 1) / hlq::CLIP_BYTES);
       if (++l.count == hlq::CLIP_LIST) {
         const hlq_status st = f(l);
         if (st != HLQ_OK) return st;
@@ -283,20 +284,15 @@ hlq_status for_lists(const void* const* grads, void* const* outs, const int64_t*
         l.in_place = 1;
       }
     }
+  }
   return l.count ? f(l) : HLQ_OK;
 }
 
-// Partials of the norm, -1 for an invalid list.
-int64_t clip_parts(const int64_t* sizes, int64_t count) {
-  if (count < 0 || count >= (int64_t(1) << 24) || (count && !sizes)) return -1;
+bool clip_sizes_ok(const int64_t* sizes, int64_t count) {
+  if (count < 0 || count >= (int64_t(1) << 24)) return false;
   for (int64_t i = 0; i < count; ++i)
-    if (sizes[i] < 0 || sizes[i] >= (int64_t(1) << 40)) return -1;
-  int64_t parts = 0;
-  for_lists(nullptr, nullptr, sizes, nullptr, count, [&](const hlq::ClipList& l) {
-    parts += clip_groups(l.chunks);
-    return HLQ_OK;
-  });
-  return parts;
+    if (sizes[i] < 0 || sizes[i] >= (int64_t(1) << 40)) return false;
+  return true;
 }
 
 }  // namespace
@@ -304,8 +300,12 @@ int64_t clip_parts(const int64_t* sizes, int64_t count) {
 extern "C" {
 
 size_t hlq_clip_grad_norm_workspace_size(const int64_t* sizes, int64_t count) {
-  const int64_t parts = clip_parts(sizes, count);
-  return parts > 0 ? (size_t)parts * 8 : 0;
+  if ((count > 0 && !sizes) || !clip_sizes_ok(sizes, count)) return 0;
+  // one partial per workgroup, CLIP_GROUPS at most per list of CLIP_LIST
+  int64_t entries = 0;
+  for (int64_t i = 0; i < count; ++i)
+    entries += (sizes[i] + hlq::CLIP_MAX_SIZE - 1) / hlq::CLIP_MAX_SIZE;
+  return (size_t)((entries + hlq::CLIP_LIST - 1) / hlq::CLIP_LIST) * hlq::CLIP_GROUPS * 8;
 }
 
 hlq_status hlq_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* sizes,
@@ -313,39 +313,41 @@ hlq_status hlq_clip_grad_norm(const void* const* grads, void* const* outs, const
                               double* norm, void* workspace, size_t workspace_bytes,
                               void* stream) {
   if (!norm || (count > 0 && any_null({grads, sizes, dtypes}))) return HLQ_ERR_NULL;
-  const int64_t parts = clip_parts(sizes, count);
-  if (parts < 0) return HLQ_ERR_SHAPE;
+  if (!clip_sizes_ok(sizes, count)) return HLQ_ERR_SHAPE;
   if (norm_kind != HLQ_NORM_L2 && norm_kind != HLQ_NORM_INF) return HLQ_ERR_MODE;
   if (!(max_norm >= 0.0)) return HLQ_ERR_VALUE;
+  int64_t bytes = 0;
   for (int64_t i = 0; i < count; ++i) {
     if (!dtype_ok(dtypes[i])) return HLQ_ERR_DTYPE;
     if (sizes[i] && (!grads[i] || (outs && !outs[i]))) return HLQ_ERR_NULL;
     if (!aligned(grads[i], esize(dtypes[i])) || (outs && !aligned(outs[i], esize(dtypes[i]))))
       return HLQ_ERR_ALIGN;
+    bytes += sizes[i] * (int64_t)esize(dtypes[i]);
   }
   if (!aligned(norm, 8)) return HLQ_ERR_ALIGN;
-  const hlq_status st = check_workspace(workspace, workspace_bytes, (size_t)parts * 8);
+  const hlq_status st = check_workspace(workspace, workspace_bytes,
+                                        hlq_clip_grad_norm_workspace_size(sizes, count));
   if (st != HLQ_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool large = bytes > kLastLevelCache;
   double* part = static_cast<double*>(workspace);
-  int64_t at = 0;
+  int64_t parts = 0;
   hlq_status r = for_lists(grads, outs, sizes, dtypes, count, [&](const hlq::ClipList& l) {
-    const unsigned groups = clip_groups(l.chunks);
-    HLQ_TRY(hlq::launch_clip_norm(l, norm_kind, part + at, groups, s));
-    at += groups;
+    HLQ_TRY(hlq::launch_clip_norm(l, norm_kind, part + parts, clip_groups(l.chunks), large, s));
+    parts += clip_groups(l.chunks);
     return HLQ_OK;
   });
   if (r != HLQ_OK) return r;
   bool first = true;
   r = for_lists(grads, outs, sizes, dtypes, count, [&](const hlq::ClipList& l) {
     HLQ_TRY(hlq::launch_clip_scale(l, norm_kind, part, parts, max_norm, first ? norm : nullptr,
-                                   clip_groups(l.chunks), s));
+                                   clip_groups(l.chunks), large, s));
     first = false;
     return HLQ_OK;
   });
   if (r != HLQ_OK || !first) return r;
   hlq::ClipList none = {};  // no elements: the norm is 0
-  HLQ_TRY(hlq::launch_clip_scale(none, norm_kind, part, 0, max_norm, norm, 1, s));
+  HLQ_TRY(hlq::launch_clip_scale(none, norm_kind, part, 0, max_norm, norm, 1, false, s));
   return HLQ_OK;
 }
 
