@@ -1,4 +1,5 @@
-"""Build the gfx950 HIP library libhlq.so in-tree with hipcc.
+"""Build the gfx950 HIP library libhlq.so and the Python module _hlq_torch.so
+in-tree with hipcc and the host's C++ compiler.
 
 Each source compiles to an object of its own (in parallel), then one link."""
 from __future__ import annotations
@@ -7,12 +8,14 @@ import concurrent.futures
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhlq.so")
+EXT = os.path.join(HERE, "_hlq_torch.so")
 # (source, object, extra flags): the transform kernels build once per block size
 SOURCES = [("hlq_tr.hip", f"hlq_tr{n}", [f"-DHLQ_TR_N={n}"]) for n in (16, 32, 64, 128)] + [
     ("hlq_gemm.hip", "hlq_gemm", []), ("hlq_lqs.hip", "hlq_lqs", []),
@@ -23,6 +26,7 @@ SOURCES = [("hlq_tr.hip", f"hlq_tr{n}", [f"-DHLQ_TR_N={n}"]) for n in (16, 32, 6
     ("hlq_api.cpp", "hlq_api", []), ("hlq_train_api.cpp", "hlq_train_api", [])]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
 
 # Numerics flags: no FMA contraction (the transforms must round every add),
 # IEEE division, denormals kept; packed fp32 instructions disabled.
@@ -41,7 +45,21 @@ def _run(cmd, verbose):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("hipcc failed: " + " ".join(cmd[-3:]))
+        raise RuntimeError("build failed: " + " ".join(cmd[-3:]))
+
+
+def _ext_command(out):
+    """The binding's native half: host code against torch's C++ API."""
+    import torch
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    inc = [os.path.join(home, "include"), os.path.join(home, "include/torch/csrc/api/include"),
+           "/opt/rocm/include", sysconfig.get_paths()["include"]]
+    lib = os.path.join(home, "lib")
+    return [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1",
+            "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f for i in inc for f in ("-isystem", i)], "-o", out,
+            os.path.join(CSRC, "hlq_torch.cpp"), "-L", lib, "-ltorch_python", "-ltorch",
+            "-ltorch_cpu", "-lc10", "-lc10_hip", "-ldl"]
 
 
 def build(verbose: bool = False) -> str:
@@ -52,12 +70,14 @@ def build(verbose: bool = False) -> str:
         o = os.path.join(OBJ, name + ".o")
         objs.append(o)
         cmds.append([HIPCC, *FLAGS, *extra, *inc, "-c", "-o", o, os.path.join(CSRC, src)])
+    cmds.append(_ext_command(EXT + ".tmp"))
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(cmds)) as ex:
         for f in [ex.submit(_run, c, verbose) for c in cmds]:
             f.result()
     tmp = LIB + ".tmp"
     _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs], verbose)
     os.replace(tmp, LIB)
+    os.replace(EXT + ".tmp", EXT)
     return LIB
 
 

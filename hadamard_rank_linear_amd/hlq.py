@@ -540,6 +540,30 @@ def hlq_lqs_select(stats, threshold=HLQ_LQS_THRESHOLD):
 
 
 # ------------------------------------------------------------ training step
+# These operators' tensors are checked, their outputs allocated and the library
+# called by the native module _hlq_torch (csrc/hlq_torch.cpp).
+
+_native_module = None
+
+
+def _native():
+    global _native_module
+    if _native_module is None:
+        import torch  # noqa: F401  (the module links against its libraries)
+        try:
+            from . import _hlq_torch
+        except ImportError as e:
+            raise ImportError("the native binding _hlq_torch.so is missing or does not load: build "
+                              "it with `python -m hadamard_rank_linear_amd.build`") from e
+        _hlq_torch.bind(_lib._handle, _check)
+        _native_module = _hlq_torch
+    return _native_module
+
+
+def _raw(stream):
+    """The raw stream of a ``torch.cuda.Stream``, None for the current one."""
+    return None if stream is None else stream.cuda_stream
+
 
 def _hold(stream, *ts):
     """Tells the allocator that ``ts``, allocated for the current stream, are
@@ -548,21 +572,6 @@ def _hold(stream, *ts):
         for t in ts:
             if t is not None:
                 t.record_stream(stream)
-
-
-def _workspace(workspace, need, device):
-    import torch
-    if workspace is None:
-        return torch.empty((max(need, 256),), dtype=torch.uint8, device=device)
-    if workspace.dtype != torch.uint8 or workspace.dim() != 1:
-        raise TypeError("workspace must be a 1-D uint8 tensor")
-    return workspace
-
-
-def _params(weight, bias, C):
-    _expect("weight", weight, weight.dtype, (C,))
-    if bias is not None:
-        _expect("bias", bias, weight.dtype, (C,))
 
 
 def hlq_layer_norm_forward(x, weight, bias=None, eps=1e-5, residual=None, y=None, h=None,
@@ -575,28 +584,9 @@ def hlq_layer_norm_forward(x, weight, bias=None, eps=1e-5, residual=None, y=None
     itself when there is no residual.  mean and rstd (fp32, one per row) are
     kept for :func:`hlq_layer_norm_backward`.
     """
-    import torch
-    C = x.shape[-1] if x.dim() else 0
-    T = x.numel() // C if C else 0
-    _params(weight, bias, C)
-    if residual is not None:
-        _expect("residual", residual, x.dtype, x.shape)
-        if h is None:
-            h = torch.empty_like(x, memory_format=torch.contiguous_format)
-        _expect("h", h, x.dtype, x.shape)
-    elif h is not None:
-        raise ValueError("h is an output of the residual addition: no residual was given")
-    if y is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
-    _expect("y", y, x.dtype, x.shape)
-    stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device)
-    _require_cuda(x, residual, weight, bias, y, h)
-    mean, rstd = stats[0], stats[1]
-    _check("hlq_layer_norm_forward", _lib.hlq_layer_norm_forward(
-        _ptr(x), _ptr(residual), _dtype_code(x), _ptr(weight), _ptr(bias), _dtype_code(weight),
-        T, C, eps, _ptr(y), _ptr(h), _ptr(mean), _ptr(rstd), _stream(stream)))
-    _hold(stream, y, h, stats)
-    return y, (x if residual is None else h), mean, rstd
+    out = _native().layer_norm_forward(x, weight, bias, eps, residual, y, h, _raw(stream))
+    _hold(stream, *out)
+    return out
 
 
 def hlq_layer_norm_backward_workspace_size(T, C, dtype=HLQ_F32) -> int:
@@ -613,65 +603,10 @@ def hlq_layer_norm_backward(g_y, h, mean, rstd, weight, g_h=None, with_bias=True
     all of one type; g_weight and g_bias have the type of weight.  g_x is the
     gradient of x and of the residual alike.
     """
-    import torch
-    C = h.shape[-1] if h.dim() else 0
-    T = h.numel() // C if C else 0
-    _params(weight, None, C)
-    _expect("g_y", g_y, h.dtype, h.shape)
-    _expect("mean", mean, torch.float32, h.shape[:-1])
-    _expect("rstd", rstd, torch.float32, h.shape[:-1])
-    if g_h is not None:
-        _expect("g_h", g_h, h.dtype, h.shape)
-    if g_x is None:
-        g_x = torch.empty_like(h, memory_format=torch.contiguous_format)
-    _expect("g_x", g_x, h.dtype, h.shape)
-    g_p = torch.empty((2 if with_bias else 1, C), dtype=weight.dtype, device=h.device)
-    code = _dtype_code(h)
-    workspace = _workspace(workspace, _lib.hlq_layer_norm_backward_workspace_size(T, C, code),
-                           h.device)
-    _require_cuda(g_y, h, mean, rstd, weight, g_h, g_x, workspace)
-    g_w, g_b = g_p[0], (g_p[1] if with_bias else None)
-    _check("hlq_layer_norm_backward", _lib.hlq_layer_norm_backward(
-        _ptr(g_y), _ptr(h), _ptr(g_h), code, _ptr(mean), _ptr(rstd), _ptr(weight),
-        _dtype_code(weight), T, C, _ptr(g_x), _ptr(g_w), _ptr(g_b), _ptr(workspace),
-        _nbytes(workspace), _stream(stream)))
-    _hold(stream, g_x, g_p, workspace)
-    return g_x, g_w, g_b
-
-
-def _rows(name, t, shape=None):
-    """(rows, length, pitch) of a 2-D GPU tensor whose rows are packed; the
-    pitch between rows is free (a slice of a padded vocabulary)."""
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must be {'a 2-D tensor' if shape is None else shape}, got "
-                         f"{tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError("tensors must live on the GPU")
-    T, V = t.shape
-    ld = t.stride(0) if T > 1 else V
-    if (V > 1 and t.stride(1) != 1) or ld < V:
-        raise ValueError(f"{name}: the elements of a row must be contiguous and rows not overlap")
-    return T, V, ld
-
-
-def _per_token(T, like, **named):
-    """fp32 [T] tensors (None allowed) on the device of ``like``."""
-    import torch
-    for name, t in named.items():
-        if t is not None:
-            _expect(name, t, torch.float32, (T,))
-    _require_cuda(*named.values())
-    for t in named.values():
-        if t is not None and t.device != like.device:
-            raise ValueError(f"tensors on different devices: {like.device} and {t.device}")
-
-
-def _targets(targets, T, like):
-    import torch
-    _expect("targets", targets, torch.int64, (T,))
-    _require_cuda(targets)
-    if targets.device != like.device:
-        raise ValueError(f"tensors on different devices: {like.device} and {targets.device}")
+    out = _native().layer_norm_backward(g_y, h, mean, rstd, weight, g_h, with_bias, g_x,
+                                        workspace, _raw(stream))
+    _hold(stream, *out)
+    return out[:3]
 
 
 def hlq_token_logprob_forward(logits, targets, scale=1.0, stream=None):
@@ -680,37 +615,20 @@ def hlq_token_logprob_forward(logits, targets, scale=1.0, stream=None):
     fp32, stats being each row's maximum and sum of exponentials above it.
 
     Targets outside [0, V) (such as -100) are ignored: log probability 0, the
-    row not read.  The rows of logits may have any pitch.
+    row not read.  The rows of logits may have any pitch (a slice of a padded
+    vocabulary).
     """
-    import torch
-    T, V, ld = _rows("logits", logits)
-    _targets(targets, T, logits)
-    logprob = torch.empty((T,), dtype=torch.float32, device=logits.device)
-    stats = torch.empty((T, 2), dtype=torch.float32, device=logits.device)
-    _check("hlq_token_logprob_forward", _lib.hlq_token_logprob_forward(
-        _ptr(logits), _dtype_code(logits), ld, _ptr(targets), T, V, scale, _ptr(logprob),
-        _ptr(stats), _stream(stream)))
-    _hold(stream, logprob, stats)
-    return logprob, stats
+    out = _native().token_logprob_forward(logits, targets, scale, _raw(stream))
+    _hold(stream, *out)
+    return out
 
 
 def hlq_token_logprob_backward(g_logprob, logits, targets, stats, scale=1.0, g_x=None,
                                stream=None):
     """Gradient [T, V] of logits from that of the log probabilities
     (:func:`hlq_token_logprob_forward`'s), in the type of logits."""
-    import torch
-    T, V, ld = _rows("logits", logits)
-    _targets(targets, T, logits)
-    _per_token(T, logits, g_logprob=g_logprob)
-    _expect("stats", stats, torch.float32, (T, 2))
-    _require_cuda(g_logprob, stats)
-    if g_x is None:
-        g_x = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
-    _expect("g_x", g_x, logits.dtype, (T, V))
-    g_ld = _rows("g_x", g_x)[2]
-    _check("hlq_token_logprob_backward", _lib.hlq_token_logprob_backward(
-        _ptr(g_logprob), _ptr(logits), _dtype_code(logits), ld, _ptr(targets), _ptr(stats), T, V,
-        scale, _ptr(g_x), g_ld, _stream(stream)))
+    g_x = _native().token_logprob_backward(g_logprob, logits, targets, stats, scale, g_x,
+                                           _raw(stream))
     _hold(stream, g_x)
     return g_x
 
@@ -725,20 +643,10 @@ def hlq_policy_loss(logprob, old_logprob, advantage, weight=None, ref_logprob=No
     (sums [3], g_logprob [T]), sums = (loss, weighted KL estimate, weight of
     the clipped tokens).  ``ref_logprob`` goes with a kl_coef other than 0; a
     weight of 0 takes a token out (weight None: ones)."""
-    import torch
-    T, dev = logprob.numel(), logprob.device
-    _per_token(T, logprob, logprob=logprob, old_logprob=old_logprob, advantage=advantage,
-               weight=weight, ref_logprob=ref_logprob)
-    sums = torch.empty((3,), dtype=torch.float32, device=dev)
-    g_logprob = torch.empty((T,), dtype=torch.float32, device=dev)
-    workspace = _workspace(workspace, hlq_policy_loss_workspace_size(T), dev)
-    _require_cuda(logprob, workspace)
-    _check("hlq_policy_loss", _lib.hlq_policy_loss(
-        _ptr(logprob), _ptr(old_logprob), _ptr(advantage), _ptr(weight), _ptr(ref_logprob), T,
-        clip_low, clip_high, kl_coef, _ptr(sums), _ptr(g_logprob), _ptr(workspace),
-        _nbytes(workspace), _stream(stream)))
-    _hold(stream, sums, g_logprob, workspace)
-    return sums, g_logprob
+    out = _native().policy_loss(logprob, old_logprob, advantage, weight, ref_logprob, clip_low,
+                                clip_high, kl_coef, workspace, _raw(stream))
+    _hold(stream, *out)
+    return out[:2]
 
 
 def hlq_policy_loss_logits(logits, targets, old_logprob, advantage, weight=None, ref_logprob=None,
@@ -748,26 +656,11 @@ def hlq_policy_loss_logits(logits, targets, old_logprob, advantage, weight=None,
     :func:`hlq_token_logprob_backward` in one pass over logits [T, V]: returns
     (sums [3], logprob [T], g_x [T, V]).  Tokens whose weight is 0 or whose
     target is ignored do not count; their rows are not read."""
-    import torch
-    T, V, ld = _rows("logits", logits)
-    dev = logits.device
-    _targets(targets, T, logits)
-    _per_token(T, logits, old_logprob=old_logprob, advantage=advantage, weight=weight,
-               ref_logprob=ref_logprob)
-    if g_x is None:
-        g_x = torch.empty((T, V), dtype=logits.dtype, device=dev)
-    _expect("g_x", g_x, logits.dtype, (T, V))
-    g_ld = _rows("g_x", g_x)[2]
-    sums = torch.empty((3,), dtype=torch.float32, device=dev)
-    logprob = torch.empty((T,), dtype=torch.float32, device=dev)
-    workspace = _workspace(workspace, hlq_policy_loss_workspace_size(T), dev)
-    _require_cuda(workspace)
-    _check("hlq_policy_loss_logits", _lib.hlq_policy_loss_logits(
-        _ptr(logits), _dtype_code(logits), ld, _ptr(targets), _ptr(old_logprob), _ptr(advantage),
-        _ptr(weight), _ptr(ref_logprob), T, V, scale, clip_low, clip_high, kl_coef, _ptr(sums),
-        _ptr(logprob), _ptr(g_x), g_ld, _ptr(workspace), _nbytes(workspace), _stream(stream)))
-    _hold(stream, g_x, sums, logprob, workspace)
-    return sums, logprob, g_x
+    out = _native().policy_loss_logits(logits, targets, old_logprob, advantage, weight,
+                                       ref_logprob, scale, clip_low, clip_high, kl_coef, g_x,
+                                       workspace, _raw(stream))
+    _hold(stream, *out)
+    return out[:3]
 
 
 def hlq_preference_loss_workspace_size(P) -> int:
@@ -783,35 +676,10 @@ def hlq_preference_loss(logprob, start, beta, ref_logprob=None, weight=None, lab
     T, the P chosen ones first; ``reduction`` HLQ_SUM scores a sequence by the
     sum of weight * (logprob - ref_logprob), HLQ_MEAN by its weighted mean.
     """
-    import torch
-    T, dev = logprob.numel(), logprob.device
-    _per_token(T, logprob, logprob=logprob, ref_logprob=ref_logprob, weight=weight)
-    if start.dtype != torch.int64 or start.dim() != 1 or start.numel() % 2 != 1:
-        raise ValueError("start must be an int64 tensor of 2P + 1 bounds")
-    P = start.numel() // 2
-    loss = torch.empty((1,), dtype=torch.float32, device=dev)
-    margin = torch.empty((P,), dtype=torch.float32, device=dev)
-    g_logprob = torch.empty((T,), dtype=torch.float32, device=dev)
-    workspace = _workspace(workspace, hlq_preference_loss_workspace_size(P), dev)
-    _require_cuda(logprob, start, workspace)
-    _check("hlq_preference_loss", _lib.hlq_preference_loss(
-        _ptr(logprob), _ptr(ref_logprob), _ptr(weight), _ptr(start), P, T, beta, label_smoothing,
-        reduction, _ptr(loss), _ptr(margin), _ptr(g_logprob), _ptr(workspace), _nbytes(workspace),
-        _stream(stream)))
-    _hold(stream, loss, margin, g_logprob, workspace)
-    return loss, margin, g_logprob
-
-
-def _dense(t) -> bool:
-    """Whether the elements of t fill one stretch of memory, in any order of
-    its dimensions."""
-    n = 1
-    for stride, size in sorted(zip(t.stride(), t.shape)):
-        if size != 1:
-            if stride != n:
-                return False
-            n *= size
-    return True
+    out = _native().preference_loss(logprob, start, beta, ref_logprob, weight, label_smoothing,
+                                    reduction, workspace, _raw(stream))
+    _hold(stream, *out)
+    return out[:3]
 
 
 def hlq_clip_grad_norm_workspace_size(sizes) -> int:
@@ -823,36 +691,19 @@ def hlq_clip_grad_norm_workspace_size(sizes) -> int:
 
 def hlq_clip_grad_norm(grads, max_norm, norm_kind=HLQ_NORM_L2, out=None, workspace=None,
                        stream=None):
-    """Scales ``grads`` (fp32 and bf16 GPU tensors) by min(1, max_norm / (norm
-    + 1e-6)), norm their global norm (HLQ_NORM_L2 or HLQ_NORM_INF), in place
-    or into ``out`` (tensors of the same types, shapes and strides).  Returns
-    the norm, a float64 GPU tensor [1]; the host does not wait for it."""
-    import torch
-    grads = list(grads)
-    outs = grads if out is None else list(out)
-    n = len(grads)
-    if len(outs) != n:
-        raise ValueError(f"{n} gradients and {len(outs)} outputs")
-    dev = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
-    codes = []
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        if not g.is_cuda or g.device != dev:
-            raise ValueError(f"gradient {i} is on {g.device}, expected {dev}")
-        if not g.is_contiguous() and not _dense(g):
-            raise ValueError(f"gradient {i} is not dense")
-        if o is not g and (o.dtype != g.dtype or o.shape != g.shape or o.device != dev or
-                           o.stride() != g.stride()):
-            raise ValueError(f"output {i} must match its gradient's type, shape and strides")
-        codes.append(_dtype_code(g))
-    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
-    src = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
-    dst = None if out is None else (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs])
-    norm = torch.empty((1,), dtype=torch.float64, device=dev)
-    workspace = _workspace(workspace, _lib.hlq_clip_grad_norm_workspace_size(sizes, n), dev)
-    _require_cuda(norm, workspace)
-    _check("hlq_clip_grad_norm", _lib.hlq_clip_grad_norm(
-        src, dst, sizes, (ctypes.c_int * n)(*codes), n, max_norm, norm_kind, _ptr(norm),
-        _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    """Scales ``grads`` (fp32 and bf16 GPU tensors, dense in any order of their
+    dimensions) by min(1, max_norm / (norm + 1e-6)), norm their global norm
+    (HLQ_NORM_L2 or HLQ_NORM_INF), in place or into ``out`` (tensors of the
+    same types, shapes and strides).  Returns the norm, a float64 GPU tensor
+    [1]; the host does not wait for it."""
+    if not isinstance(grads, (list, tuple)):
+        grads = list(grads)
+    device = None
+    if not grads:
+        import torch
+        device = torch.cuda.current_device()
+    norm, workspace = _native().clip_grad_norm(grads, max_norm, norm_kind, out, workspace,
+                                               _raw(stream), device)
     _hold(stream, norm, workspace)
     return norm
 
