@@ -31,5 +31,7 @@ _BINDING_NAMES = {
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
-        return getattr(importlib.import_module(".hlq", __name__), name)
+        # kept in the package, so that this lookup (3.6 us) is not part of every call
+        value = globals()[name] = getattr(importlib.import_module(".hlq", __name__), name)
+        return value
     raise AttributeError(name)
