@@ -30,10 +30,14 @@ __device__ __forceinline__ float exp_scaled(float d, float c_hi, float c_lo) {
 }
 
 // ------------------------------------------------------------ pieces of a row
-// A row is split into 16-byte pieces, thread i of W taking pieces i, i + W, ...
-// Addresses are a scalar base and a 32-bit byte offset.  What lies past the
-// row reads as -inf, which adds nothing to the sum.  A row whose length is no
-// multiple of the piece has its last piece read ending at the row's end and
+// A row is split into 16-byte pieces at 16-byte boundaries, thread i of W taking
+// pieces i, i + W, ...  Positions count elements from the boundary at or before
+// the row's start, so the row is positions head .. end - 1; addresses are a
+// scalar base and a 32-bit byte offset.  Rows of an odd length start anywhere:
+// pieces cut at the row's own start would cross boundaries in every access
+// (the gradient of 4096 x 32003 bf16 takes ALIGN_A us that way, ALIGN_B here).
+// What lies outside the row reads as -inf, which adds nothing to the sum.  The
+// first and the last piece are read where they lie whole within the row and
 // shifted into place (rows shorter than a piece: by elements).
 //
 // ST (streaming): the rows together exceed the 256 MB of last-level cache, so
@@ -47,66 +51,102 @@ template <int DT, bool ST>
 struct Row {
   static constexpr int N = Piece<DT>::N, ES = DT == 0 ? 4 : 2;
   static constexpr uint32_t FILL = DT == 0 ? 0xFF800000u : 0xFF80FF80u;
-  const char* base;  // uniform
-  uint32_t V;
+  const char* base;  // of position 0 (uniform)
+  uint32_t head, end;
 
-  __device__ __forceinline__ u32x4 load(uint32_t e) const {
+  __device__ __forceinline__ Row(const void* x, int64_t row, int64_t ld, int64_t V) {
+    base = static_cast<const char*>(x) + row * ld * ES;
+    head = (uint32_t)(reinterpret_cast<uintptr_t>(base) & 15u) / ES;
+    base -= head * ES;
+    end = head + (uint32_t)V;
+  }
+
+  __device__ __forceinline__ u32x4 at(uint32_t p) const {
+    const Loose* q = reinterpret_cast<const Loose*>(base + p * ES);
+    if constexpr (ST) return __builtin_nontemporal_load(q);
+    else return *q;
+  }
+
+  // The piece at position p (a multiple of N).
+  __device__ __forceinline__ u32x4 load(uint32_t p) const {
     u32x4 r = {FILL, FILL, FILL, FILL};
-    if (e < V) {
-      if (V < (uint32_t)N) {
-        short_row(r);
-      } else {
-        const uint32_t skip = e + N > V ? e + N - V : 0u;
-        const char* at = base + (e - skip) * ES;
-        if constexpr (ST) r = __builtin_nontemporal_load(reinterpret_cast<const Loose*>(at));
-        else r = *reinterpret_cast<const Loose*>(at);
-        if (skip) {
-          if constexpr (DT == 0) {
-            if (skip & 1) r = (u32x4){r[1], r[2], r[3], FILL};
-            if (skip & 2) r = (u32x4){r[2], r[3], FILL, FILL};
-          } else {
-            if (skip & 1)
-              r = (u32x4){(r[0] >> 16) | (r[1] << 16), (r[1] >> 16) | (r[2] << 16),
-                          (r[2] >> 16) | (r[3] << 16), (r[3] >> 16) | (FILL << 16)};
-            if (skip & 2) r = (u32x4){r[1], r[2], r[3], FILL};
-            if (skip & 4) r = (u32x4){r[2], r[3], FILL, FILL};
-          }
-        }
-      }
-    }
+    if (p >= head && p + N <= end) r = at(p);
+    else if (p < end) edge(p, r);
     return r;
   }
 
-  __device__ __forceinline__ void short_row(u32x4& r) const {
+  __device__ __forceinline__ void edge(uint32_t p, u32x4& r) const {
+    if (end - head < (uint32_t)N) {
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      if ((uint32_t)k < V) {
-        if constexpr (DT == 0) {
-          r[k] = reinterpret_cast<const uint32_t*>(base)[k];
-        } else {
-          const uint32_t v = *reinterpret_cast<const uint16_t*>(base + 2 * k);
-          r[k / 2] = (k & 1) ? (r[k / 2] & 0xFFFFu) | (v << 16) : (r[k / 2] & 0xFFFF0000u) | v;
+      for (int k = 0; k < N; ++k)
+        if (p + k >= head && p + k < end) {
+          if constexpr (DT == 0) {
+            r[k] = reinterpret_cast<const uint32_t*>(base)[p + k];
+          } else {
+            const uint32_t v = reinterpret_cast<const uint16_t*>(base)[p + k];
+            r[k / 2] = (k & 1) ? (r[k / 2] & 0xFFFFu) | (v << 16) : (r[k / 2] & 0xFFFF0000u) | v;
+          }
         }
+    } else if (p < head) {
+      r = at(head);
+      const uint32_t up = head - p;
+      if constexpr (DT == 0) {
+        if (up & 1) r = (u32x4){FILL, r[0], r[1], r[2]};
+        if (up & 2) r = (u32x4){FILL, FILL, r[0], r[1]};
+      } else {
+        if (up & 1)
+          r = (u32x4){(FILL >> 16) | (r[0] << 16), (r[0] >> 16) | (r[1] << 16),
+                      (r[1] >> 16) | (r[2] << 16), (r[2] >> 16) | (r[3] << 16)};
+        if (up & 2) r = (u32x4){FILL, r[0], r[1], r[2]};
+        if (up & 4) r = (u32x4){FILL, FILL, r[0], r[1]};
       }
+    } else {
+      r = at(end - N);
+      const uint32_t down = p + N - end;
+      if constexpr (DT == 0) {
+        if (down & 1) r = (u32x4){r[1], r[2], r[3], FILL};
+        if (down & 2) r = (u32x4){r[2], r[3], FILL, FILL};
+      } else {
+        if (down & 1)
+          r = (u32x4){(r[0] >> 16) | (r[1] << 16), (r[1] >> 16) | (r[2] << 16),
+                      (r[2] >> 16) | (r[3] << 16), (r[3] >> 16) | (FILL << 16)};
+        if (down & 2) r = (u32x4){r[1], r[2], r[3], FILL};
+        if (down & 4) r = (u32x4){r[2], r[3], FILL, FILL};
+      }
+    }
+  }
+
+  __device__ __forceinline__ float element(uint32_t t) const {
+    return load1<DT>(base, head + t);
   }
 };
 
+// Stores a piece of a row of the gradient, positions as in its row of logits.
 template <int DT, bool ST>
-__device__ __forceinline__ void store_row(char* base, uint32_t e, uint32_t V, const u32x4& r) {
-  constexpr int N = Piece<DT>::N, ES = DT == 0 ? 4 : 2;
-  if (e + N <= V) {
-    Loose* at = reinterpret_cast<Loose*>(base + e * ES);
-    if constexpr (ST) __builtin_nontemporal_store(r, at);
-    else *at = r;
-  } else if (e < V) {
-#pragma unroll
-    for (int k = 0; k < N - 1; ++k)
-      if (e + k < V) {
-        if constexpr (DT == 0) reinterpret_cast<uint32_t*>(base + e * ES)[k] = r[k];
-        else reinterpret_cast<uint16_t*>(base + e * ES)[k] = (uint16_t)(r[k / 2] >> (16 * (k & 1)));
-      }
+struct OutRow {
+  static constexpr int N = Piece<DT>::N, ES = DT == 0 ? 4 : 2;
+  char* base;
+  uint32_t head, end;
+
+  __device__ __forceinline__ OutRow(const LogitArgs& a, int64_t row, uint32_t head_)
+      : head(head_), end(head_ + (uint32_t)a.V) {
+    base = static_cast<char*>(a.g_x) + row * a.g_ld * ES - head * ES;
   }
-}
+  __device__ __forceinline__ void store(uint32_t p, const u32x4& r) const {
+    if (p >= head && p + N <= end) {
+      Loose* q = reinterpret_cast<Loose*>(base + p * ES);
+      if constexpr (ST) __builtin_nontemporal_store(r, q);
+      else *q = r;
+    } else if (p < end) {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (p + k >= head && p + k < end) {
+          if constexpr (DT == 0) reinterpret_cast<uint32_t*>(base)[p + k] = r[k];
+          else reinterpret_cast<uint16_t*>(base)[p + k] = (uint16_t)(r[k / 2] >> (16 * (k & 1)));
+        }
+    }
+  }
+};
 
 // Makes the compiler unpack a piece again where it is used next, instead of
 // keeping its elements in a register each from one use to the other.
@@ -159,7 +199,7 @@ __device__ __forceinline__ void join_stats(const LogitArgs& a, float (*sm)[16], 
 
 template <int DT, bool ST>
 __device__ __forceinline__ Row<DT, ST> row_of(const LogitArgs& a, int64_t row) {
-  return Row<DT, ST>{static_cast<const char*>(a.logits) + row * a.ld * Row<DT, ST>::ES, (uint32_t)a.V};
+  return Row<DT, ST>(a.logits, row, a.ld, a.V);
 }
 
 // scale (x_t - m) - log s; s is 0 (nothing but -inf), NaN, or at least 1.  The
@@ -187,10 +227,10 @@ __global__ __launch_bounds__(W) void k_logprob(LogitArgs a) {
   float m = 0.f, s = 1.f, lp = 0.f;
   if (t >= 0 && t < a.V) {
     const Row<DT, ST> x = row_of<DT, ST>(a, row);
-    const float xt = load1<DT>(x.base, t);
+    const float xt = x.element((uint32_t)t);
     m = -__builtin_huge_valf();
     s = 0.f;
-    for (uint32_t e0 = threadIdx.x * N; e0 < x.V; e0 += W * N * P) {
+    for (uint32_t e0 = threadIdx.x * N; e0 < x.end; e0 += W * N * P) {
       u32x4 r[P];
 #pragma unroll
       for (int j = 0; j < P; ++j) r[j] = x.load(e0 + j * W * N);
@@ -206,7 +246,8 @@ __global__ __launch_bounds__(W) void k_logprob(LogitArgs a) {
   }
 }
 
-// Gradient of a row's piece at element e: f ([v = t] - e_v / s), k_s = -f / s.
+// Gradient of a row's piece at position e: f ([v = t] - e_v / s), k_s = -f / s,
+// t the target's position.
 template <int DT>
 __device__ __forceinline__ u32x4 gradient_piece(const u32x4& r, uint32_t e, uint32_t t, float c,
                                                 float f, float k_s, float m) {
@@ -222,12 +263,9 @@ __device__ __forceinline__ u32x4 gradient_piece(const u32x4& r, uint32_t e, uint
 }
 
 template <int DT, bool ST, int W>
-__device__ __forceinline__ void zero_row(const LogitArgs& a, int64_t row) {
-  constexpr int N = Piece<DT>::N;
-  char* g = static_cast<char*>(a.g_x) + row * a.g_ld * Row<DT, ST>::ES;
+__device__ __forceinline__ void zero_row(const OutRow<DT, ST>& g) {
   const u32x4 z = {0u, 0u, 0u, 0u};
-  for (uint32_t e = threadIdx.x * N; e < (uint32_t)a.V; e += W * N)
-    store_row<DT, ST>(g, e, (uint32_t)a.V, z);
+  for (uint32_t e = threadIdx.x * g.N; e < g.end; e += W * g.N) g.store(e, z);
 }
 
 // Reads a row again and writes its gradient, P pieces of a thread in flight.
@@ -235,21 +273,21 @@ template <int DT, int W, int P>
 __device__ __forceinline__ void row_gradient(const LogitArgs& a, int64_t row, uint32_t t, float f,
                                              float m, float s) {
   constexpr int N = Piece<DT>::N;
+  const Row<DT, false> x = row_of<DT, false>(a, row);
+  const OutRow<DT, false> g(a, row, x.head);
   if (f == 0.f || s == 0.f) {
-    zero_row<DT, false, W>(a, row);
+    zero_row<DT, false, W>(g);
     return;
   }
-  const Row<DT, false> x = row_of<DT, false>(a, row);
-  char* g = static_cast<char*>(a.g_x) + row * a.g_ld * Row<DT, false>::ES;
   const float k_s = -f / s;
-  for (uint32_t e0 = threadIdx.x * N; e0 < x.V; e0 += W * N * P) {
+  for (uint32_t e0 = threadIdx.x * N; e0 < x.end; e0 += W * N * P) {
     u32x4 r[P];
 #pragma unroll
     for (int j = 0; j < P; ++j) r[j] = x.load(e0 + j * W * N);
 #pragma unroll
     for (int j = 0; j < P; ++j) {
       const uint32_t e = e0 + j * W * N;
-      store_row<DT, false>(g, e, x.V, gradient_piece<DT>(r[j], e, t, a.c, f, k_s, m));
+      g.store(e, gradient_piece<DT>(r[j], e, x.head + t, a.c, f, k_s, m));
     }
   }
 }
@@ -327,24 +365,24 @@ __global__ __launch_bounds__(W, 4) void k_policy_regs(LogitArgs a, PolicyArgs p)
   u32x4 r[P];
   float m = -__builtin_huge_valf(), s = 0.f, xt = 0.f;
   if (live) {
-    xt = load1<DT>(x.base, t);
+    xt = x.element((uint32_t)t);
 #pragma unroll
     for (int j = 0; j < P; ++j) r[j] = x.load((threadIdx.x + j * W) * N);
     accumulate<DT, P>(r, a, m, s);
     join_stats<W>(a, sm, m, s);
   }
   const float f = policy_row(a, p, row, q, live, xt, m, s, &sg);
+  const OutRow<DT, ST> g(a, row, x.head);
   if (f == 0.f || s == 0.f) {
-    zero_row<DT, ST, W>(a, row);
+    zero_row<DT, ST, W>(g);
     return;
   }
-  char* g = static_cast<char*>(a.g_x) + row * a.g_ld * Row<DT, ST>::ES;
   const float k_s = -f / s;
 #pragma unroll
   for (int j = 0; j < P; ++j) {
     keep_packed(r[j]);
     const uint32_t e = (threadIdx.x + j * W) * N;
-    store_row<DT, ST>(g, e, x.V, gradient_piece<DT>(r[j], e, (uint32_t)t, a.c, f, k_s, m));
+    g.store(e, gradient_piece<DT>(r[j], e, x.head + (uint32_t)t, a.c, f, k_s, m));
   }
 }
 
@@ -359,8 +397,8 @@ __global__ __launch_bounds__(W) void k_policy_long(LogitArgs a, PolicyArgs p) {
   float m = -__builtin_huge_valf(), s = 0.f, xt = 0.f;
   if (live) {
     const Row<DT, ST> x = row_of<DT, ST>(a, row);
-    xt = load1<DT>(x.base, t);
-    for (uint32_t e0 = threadIdx.x * N; e0 < x.V; e0 += W * N * P) {
+    xt = x.element((uint32_t)t);
+    for (uint32_t e0 = threadIdx.x * N; e0 < x.end; e0 += W * N * P) {
       u32x4 r[P];
 #pragma unroll
       for (int j = 0; j < P; ++j) r[j] = x.load(e0 + j * W * N);
@@ -508,7 +546,12 @@ static int grad_threads(int64_t T, int64_t n) {
   return n <= 256 ? 64 : (n <= 1024 ? 256 : 1024);
 }
 
-static int64_t row_pieces(int64_t V, int dtype) { return dtype == 0 ? (V + 3) / 4 : (V + 7) / 8; }
+// Pieces of a row, at most: one more where rows do not start at a boundary.
+static int64_t row_pieces(const LogitArgs& a, int dtype) {
+  const int64_t N = dtype == 0 ? 4 : 8;
+  const bool at_boundary = (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0 && a.ld % N == 0;
+  return (a.V + (at_boundary ? 0 : N - 1) + N - 1) / N;
+}
 
 // One workgroup per row, 2^20 rows a launch (a launch holds fewer than 2^32
 // threads).
@@ -527,7 +570,7 @@ static int64_t row_pieces(int64_t V, int dtype) { return dtype == 0 ? (V + 3) / 
 
 hipError_t launch_logprob(LogitArgs a, int dtype, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
-  switch (score_threads(a.T, row_pieces(a.V, dtype))) {
+  switch (score_threads(a.T, row_pieces(a, dtype))) {
     case 64: HLQ_ROW_LAUNCH(k_logprob, 64, 4, a); break;
     case 256: HLQ_ROW_LAUNCH(k_logprob, 256, 4, a); break;
     case 512: HLQ_ROW_LAUNCH(k_logprob, 512, 4, a); break;
@@ -544,7 +587,7 @@ hipError_t launch_logprob_grad(LogitArgs a, int dtype, hipStream_t s) {
     if (dtype == 0) hipLaunchKernelGGL((k_logprob_grad<0, W, P>), g, dim3(W), 0, s, a);        \
     else hipLaunchKernelGGL((k_logprob_grad<1, W, P>), g, dim3(W), 0, s, a);                   \
   }
-  switch (grad_threads(a.T, row_pieces(a.V, dtype))) {
+  switch (grad_threads(a.T, row_pieces(a, dtype))) {
     case 64: HLQ_GRAD(64, 2); break;
     case 256: HLQ_GRAD(256, 2); break;
     default: HLQ_GRAD(1024, 4); break;
@@ -555,7 +598,7 @@ hipError_t launch_logprob_grad(LogitArgs a, int dtype, hipStream_t s) {
 
 hipError_t launch_policy_logits(LogitArgs a, const PolicyArgs& p, int dtype,
                                 hipStream_t s) {
-  const int64_t n = row_pieces(a.V, dtype);
+  const int64_t n = row_pieces(a, dtype);
   if (a.T) {
     const bool few = a.T < 256;  // fewer rows than CUs: more threads a row
     if (n <= 256 && !(few && n > 64)) { HLQ_ROW_LAUNCH(k_policy_regs, 64, 4, a, p); }
