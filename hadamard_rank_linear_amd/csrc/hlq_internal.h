@@ -242,7 +242,7 @@ struct LogitArgs {
   const int64_t* targets;
   int64_t T, V, ld, g_ld;
   int64_t row0;  // first row of the launch (set by the launch functions)
-  int stream;    // the rows exceed the last-level cache
+  int stream;    // read past the last-level cache
   double scale;
   // exp(scale x) = 2^(c x): c = scale * log2(e) in fp32, and as c_hi + c_lo, c_lo > 0
   float c, c_hi, c_lo;
@@ -292,7 +292,7 @@ struct ClipList {
   int count, in_place;
 };
 static_assert(sizeof(ClipList) <= 4000, "kernel arguments");
-// stream: the gradients exceed the last-level cache.
+// stream: past the last-level cache.
 hipError_t launch_clip_norm(const ClipList& l, int kind, double* part, unsigned groups,
                             bool stream, hipStream_t s);
 // norm (null: not written) by the first workgroup.

@@ -35,17 +35,16 @@ __device__ __forceinline__ float exp_scaled(float d, float c_hi, float c_lo) {
 // the row's start, so the row is positions head .. end - 1; addresses are a
 // scalar base and a 32-bit byte offset.  Rows of an odd length start anywhere:
 // pieces cut at the row's own start would cross boundaries in every access
-// (the gradient of 4096 x 32003 bf16 takes ALIGN_A us that way, ALIGN_B here).
+// (the gradient of 4096 x 32003 bf16 takes 115 us that way, 87 here).
 // What lies outside the row reads as -inf, which adds nothing to the sum.  The
 // first and the last piece are read where they lie whole within the row and
 // shifted into place (rows shorter than a piece: by elements).
 //
-// ST (streaming): the rows together exceed the 256 MB of last-level cache, so
-// what passes through it is gone before anything reads it again; non-temporal
-// accesses keep it from displacing what is in use.  Scoring 4096 x 128256 bf16
-// takes 154 us instead of 174, 8190 x 32000 60 instead of 100, the policy loss
-// over 2048 x 128256 184 instead of 192.  The gradient kernel is the other way
-// about (148 us with, 140 without, at 8190 x 32000 after its scoring).
+// ST (streaming): non-temporal accesses, for rows that together would pass
+// through the last-level cache without being found there again.  Scoring 4096 x
+// 128256 bf16 takes 154 us instead of 174, 8190 x 32000 60 instead of 100, the
+// policy loss over 2048 x 128256 184 instead of 192.  The gradient kernel is the
+// other way about (148 us with, 140 without, at 8190 x 32000 after its scoring).
 
 template <int DT, bool ST>
 struct Row {

@@ -443,9 +443,10 @@ __global__ __launch_bounds__(256) void k_norm_columns(NormBwd a) {
 
 // Fold of the partial column sums part [parts][2][C] in a fixed order, in
 // fp64: 16 columns per workgroup, its 64 groups of 16 lanes take every 64th
-// part; blockIdx.y 0: g_weight, 1: g_bias.
+// part and are joined within each wave, then across the 16 waves;
+// blockIdx.y 0: g_weight, 1: g_bias.
 __global__ __launch_bounds__(1024) void k_norm_fold(NormBwd a) {
-  __shared__ double sm[64][17];
+  __shared__ double sm[16][16];
   const int lane = threadIdx.x & 15, slot = threadIdx.x >> 4;
   const int64_t C = a.C, c = (int64_t)blockIdx.x * 16 + lane;
   double s = 0.0;
@@ -453,11 +454,16 @@ __global__ __launch_bounds__(1024) void k_norm_fold(NormBwd a) {
 #pragma unroll 8
     for (int64_t p = slot; p < a.parts; p += 64) s += (double)a.part[(p * 2 + blockIdx.y) * C + c];
   }
-  sm[slot][lane] = s;
+  s += __shfl_xor(s, 16);
+  s += __shfl_xor(s, 32);
+  if ((threadIdx.x & 63) < 16) sm[threadIdx.x >> 6][lane] = s;
   __syncthreads();
+  if (threadIdx.x >= 64) return;
+  const int q = threadIdx.x >> 4;
+  s = (sm[4 * q][lane] + sm[4 * q + 1][lane]) + (sm[4 * q + 2][lane] + sm[4 * q + 3][lane]);
+  s += __shfl_xor(s, 16);
+  s += __shfl_xor(s, 32);
   if (threadIdx.x < 16 && c < C) {
-#pragma unroll 8
-    for (int w = 1; w < 64; ++w) s += sm[w][lane];
     void* out = blockIdx.y ? a.g_bias : a.g_weight;
     if (a.param_dt == 0) static_cast<float*>(out)[c] = (float)s;
     else static_cast<__bf16*>(out)[c] = (__bf16)(float)s;

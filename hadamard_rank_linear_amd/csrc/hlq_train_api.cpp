@@ -14,7 +14,15 @@
 namespace {
 
 constexpr int64_t kMax = int64_t(1) << 31;
-constexpr int64_t kLastLevelCache = int64_t(256) << 20;
+// Data of this size and more is read past the last-level cache (256 MB): with
+// what is written beside it, it would not be found there again, and filling the
+// cache evicts what earlier kernels left there to be written back.  Measured
+// with inputs another kernel has just displaced: scoring 1023 x 48003 fp32 (196
+// MB) 34 us past the cache and 57 through it, 4096 x 32000 bf16 46 and 76;
+// clipping 48, 100 and 220 MB 33, 59 and 122 us and 39, 75 and 159.  With inputs
+// just written: clipping 32 and 64 MB 30 and 43 us, and 24 and 38; the gradient
+// after scoring 500 and 1024 x 32000 bf16 14 and 24 us, and 11 and 22.
+constexpr int64_t kStreamBytes = int64_t(96) << 20;
 
 bool dtype_ok(int dt) { return dt == HLQ_F32 || dt == HLQ_BF16; }
 size_t esize(int dt) { return dt == HLQ_F32 ? 4 : 2; }
@@ -59,7 +67,7 @@ hlq::LogitArgs logit_args(const void* logits, int dtype, int64_t ld, const int64
   a.logits = logits;
   a.targets = targets;
   a.T = T; a.V = V; a.ld = ld; a.g_ld = V;
-  a.stream = T * V * (int64_t)esize(dtype) > kLastLevelCache;
+  a.stream = T * V * (int64_t)esize(dtype) > kStreamBytes;
   a.scale = scale;
   const double c = scale * 1.4426950408889634074;
   a.c = (float)c;
@@ -329,7 +337,7 @@ hlq_status hlq_clip_grad_norm(const void* const* grads, void* const* outs, const
                                         hlq_clip_grad_norm_workspace_size(sizes, count));
   if (st != HLQ_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool large = bytes > kLastLevelCache;
+  const bool large = bytes > kStreamBytes;
   double* part = static_cast<double*>(workspace);
   int64_t parts = 0;
   hlq_status r = for_lists(grads, outs, sizes, dtypes, count, [&](const hlq::ClipList& l) {
