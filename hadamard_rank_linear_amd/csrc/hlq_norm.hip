@@ -442,13 +442,13 @@ __global__ __launch_bounds__(256) void k_norm_columns(NormBwd a) {
 }
 
 // Fold of the partial column sums part [parts][2][C] in a fixed order, in
-// fp64: 16 columns per workgroup, its 64 groups of 16 lanes take every 64th
-// part and are joined within each wave, then across the 16 waves;
-// blockIdx.y 0: g_weight, 1: g_bias.
-__global__ __launch_bounds__(1024) void k_norm_fold(NormBwd a) {
+// fp64: 16 columns per workgroup from column col0 on, its 64 groups of 16 lanes
+// take every 64th part and are joined within each wave, then across the 16
+// waves; blockIdx.y 0: g_weight, 1: g_bias.
+__global__ __launch_bounds__(1024) void k_norm_fold(NormBwd a, int64_t col0) {
   __shared__ double sm[16][16];
   const int lane = threadIdx.x & 15, slot = threadIdx.x >> 4;
-  const int64_t C = a.C, c = (int64_t)blockIdx.x * 16 + lane;
+  const int64_t C = a.C, c = col0 + (int64_t)blockIdx.x * 16 + lane;
   double s = 0.0;
   if (c < C) {
 #pragma unroll 8
@@ -550,7 +550,11 @@ hipError_t launch_norm_backward(const NormBwd& a, int dtype, hipStream_t s) {
       }
   }
 #undef HLQ_B
-  hipLaunchKernelGGL(k_norm_fold, dim3(cdiv(a.C, 16), a.g_bias ? 2 : 1), dim3(1024), 0, s, a);
+  // 2^24 columns a launch (a launch holds fewer than 2^32 threads)
+  for (int64_t c = 0; c < a.C; c += 1 << 24) {
+    const int64_t n = a.C - c < (1 << 24) ? a.C - c : 1 << 24;
+    hipLaunchKernelGGL(k_norm_fold, dim3(cdiv(n, 16), a.g_bias ? 2 : 1), dim3(1024), 0, s, a, c);
+  }
   return hipGetLastError();
 }
 #undef HLQ_NORM_ROWS

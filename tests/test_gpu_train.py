@@ -212,6 +212,19 @@ def test_layer_norm_repeats_bit_for_bit():
     assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
+def test_layer_norm_backward_of_one_endless_row():
+    # more columns than one launch of the fold takes; a single row's bias gradient is g_y itself
+    torch, h = _torch(), _h()
+    C = (1 << 26) + 5
+    _say(f"layer norm backward T=1 C={C}")
+    g_y = torch.randn(1, C, device="cuda").bfloat16()
+    x, w = torch.randn(1, C, device="cuda").bfloat16(), torch.ones(C, device="cuda").bfloat16()
+    one = torch.ones(1, device="cuda")
+    _, g_w, g_b = h.hlq_layer_norm_backward(g_y, x, 0 * one, one, w)
+    torch.cuda.synchronize()
+    assert torch.equal(g_b, g_y[0]) and torch.equal(g_w, (g_y[0].float() * x[0].float()).bfloat16())
+
+
 # ------------------------------------------------------------ log probabilities
 
 LOGIT_SHAPES = [(1, 1), (3, 2), (5, 7), (2, 513), (17, 1000), (4, 4099), (3, 32003), (2, 65536),
