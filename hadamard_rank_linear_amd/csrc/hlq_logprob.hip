@@ -503,6 +503,11 @@ __device__ __forceinline__ double preference_pair(const PrefArgs& p, int64_t pai
       p.g_logprob[t] = w != 0.f ? (float)((double)w * gq) : 0.f;
     }
   }
+  if (pair == 0) {  // tokens of no sequence, before the first bound or from the last one on
+    const int64_t before = bound(p.start[0], 0, p.T), from = bound(p.start[2 * p.P], before, p.T);
+    for (int64_t t = lane; t < before; t += G) p.g_logprob[t] = 0.f;
+    for (int64_t t = from + lane; t < p.T; t += G) p.g_logprob[t] = 0.f;
+  }
   return log1p(x) + (z < 0.0 ? -(1.0 - e) * z : e * z);
 }
 

@@ -672,8 +672,9 @@ def hlq_preference_loss(logprob, start, beta, ref_logprob=None, weight=None, lab
     """Preference loss over P pairs of packed sequences, from log
     probabilities [T]: returns (loss [1], margin [P], g_logprob [T]).
 
-    ``start`` [2P + 1] (int64, on the GPU) holds the sequences' bounds, 0 to
-    T, the P chosen ones first; ``reduction`` HLQ_SUM scores a sequence by the
+    ``start`` [2P + 1] (int64, on the GPU) holds the sequences' bounds,
+    within 0 to T, the P chosen ones first (tokens outside every sequence get a
+    gradient of zero); ``reduction`` HLQ_SUM scores a sequence by the
     sum of weight * (logprob - ref_logprob), HLQ_MEAN by its weighted mean.
     """
     out = _native().preference_loss(logprob, start, beta, ref_logprob, weight, label_smoothing,

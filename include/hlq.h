@@ -533,10 +533,11 @@ hlq_status hlq_policy_loss_logits(const void* logits, int dtype, int64_t ld,
  * with e = label_smoothing.
  *   logprob  [T] f32; ref_logprob [T] f32 or NULL (no reference policy).
  *   weight   [T] f32 or NULL (ones); 0 takes a token out, whatever its values.
- *   start    [2P + 1] int64, non-decreasing from 0 to T: sequence q is tokens
+ *   start    [2P + 1] int64, non-decreasing within 0 to T: sequence q is tokens
  *            start[q] .. start[q+1] - 1; the chosen ones are 0 .. P-1, the
  *            rejected ones P .. 2P-1 in the same order.  Read on the device
- *            and limited to [0, T] there.
+ *            and limited to [0, T] there; tokens before start[0] or from
+ *            start[2P] on belong to no sequence, and their gradient is zero.
  *   loss     [1] f32, margin [P] f32, g_logprob [T] f32 out.
  *   workspace at least hlq_preference_loss_workspace_size(P) bytes.
  * beta > 0 and finite, 0 <= label_smoothing <= 1 (HLQ_ERR_VALUE), reduction

@@ -520,6 +520,23 @@ def test_preference_loss_of_bad_bounds_stays_inside():
     assert loss.item() == pytest.approx(math.log(2), rel=1e-6) and (margin == 0).all()
 
 
+@pytest.mark.parametrize("pad", [5, 3000])
+def test_preference_loss_of_a_padded_batch(pad):
+    # tokens before the first and behind the last sequence: no part in the loss, gradient zero
+    torch, h = _torch(), _h()
+    _say(f"preference: {pad} tokens of no sequence on either side")
+    g = torch.Generator(device="cuda").manual_seed(pad)
+    lp = -torch.rand(40 + 2 * pad, generator=g, device="cuda")
+    start = torch.tensor([0, 7, 20, 21, 40], device="cuda")
+    inner = h.hlq_preference_loss(lp[pad:pad + 40], start, 0.3)
+    h.hlq_preference_loss(torch.full_like(lp, -3.0), start * (lp.numel() // 40), 0.3)
+    outer = h.hlq_preference_loss(lp, start + pad, 0.3)
+    torch.cuda.synchronize()
+    assert torch.equal(outer[0], inner[0]) and torch.equal(outer[1], inner[1])
+    assert torch.equal(outer[2][pad:pad + 40], inner[2])
+    assert (outer[2][:pad] == 0).all() and (outer[2][pad + 40:] == 0).all()
+
+
 def test_preference_loss_of_far_margins():
     torch, h = _torch(), _h()
     _say("preference: margins far from zero")
