@@ -59,7 +59,7 @@ def _ext_command(out):
             "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *[f for i in inc for f in ("-isystem", i)], "-o", out,
             os.path.join(CSRC, "hlq_torch.cpp"), "-L", lib, "-ltorch_python", "-ltorch",
-            "-ltorch_cpu", "-lc10", "-lc10_hip", "-ldl"]
+            "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip", "-ldl"]
 
 
 def build(verbose: bool = False) -> str:

@@ -186,21 +186,15 @@ __global__ __launch_bounds__(CLIP_THREADS) void k_clip_scale(ClipList l, int kin
 
 hipError_t launch_clip_norm(const ClipList& l, int kind, double* part, unsigned groups,
                             bool stream, hipStream_t s) {
-  const dim3 g(groups), b(CLIP_THREADS);
-  if (stream) hipLaunchKernelGGL(k_clip_norm<true>, g, b, 0, s, l, kind, part);
-  else hipLaunchKernelGGL(k_clip_norm<false>, g, b, 0, s, l, kind, part);
-  return hipGetLastError();
+  return launch(stream ? k_clip_norm<true> : k_clip_norm<false>, dim3(groups), CLIP_THREADS, s, l,
+                kind, part);
 }
 
 hipError_t launch_clip_scale(const ClipList& l, int kind, const double* part, int64_t parts,
                              double max_norm, double* norm, unsigned groups, bool stream,
                              hipStream_t s) {
-  const dim3 g(groups), b(CLIP_THREADS);
-  if (stream)
-    hipLaunchKernelGGL(k_clip_scale<true>, g, b, 0, s, l, kind, part, parts, max_norm, norm);
-  else
-    hipLaunchKernelGGL(k_clip_scale<false>, g, b, 0, s, l, kind, part, parts, max_norm, norm);
-  return hipGetLastError();
+  return launch(stream ? k_clip_scale<true> : k_clip_scale<false>, dim3(groups), CLIP_THREADS, s,
+                l, kind, part, parts, max_norm, norm);
 }
 
 }  // namespace hlq

@@ -559,85 +559,102 @@ static int64_t row_pieces(const LogitArgs& a, int dtype) {
 
 // One workgroup per row, 2^20 rows a launch (a launch holds fewer than 2^32
 // threads).
-#define HLQ_ROW_LAUNCH(K, W, P, ...)                                                           \
-  for (a.row0 = 0; a.row0 < a.T; a.row0 += 1 << 20) {                                          \
-    const dim3 g = rows_grid(a.T - a.row0);                                                    \
-    if (dtype == 0 && a.stream)                                                                \
-      hipLaunchKernelGGL((K<0, true, W, P>), g, dim3(W), 0, s, __VA_ARGS__);                   \
-    else if (dtype == 0)                                                                       \
-      hipLaunchKernelGGL((K<0, false, W, P>), g, dim3(W), 0, s, __VA_ARGS__);                  \
-    else if (a.stream)                                                                         \
-      hipLaunchKernelGGL((K<1, true, W, P>), g, dim3(W), 0, s, __VA_ARGS__);                   \
-    else                                                                                       \
-      hipLaunchKernelGGL((K<1, false, W, P>), g, dim3(W), 0, s, __VA_ARGS__);                  \
-  }
+template <typename F>
+static hipError_t for_rows(LogitArgs& a, F f) {
+  hipError_t e = hipSuccess;
+  for (a.row0 = 0; a.row0 < a.T && e == hipSuccess; a.row0 += 1 << 20) e = f(rows_grid(a.T - a.row0));
+  return e;
+}
+
+template <int W, int P>
+static hipError_t logprob_rows(LogitArgs& a, int dtype, hipStream_t s) {
+  return for_rows(a, [&](dim3 g) {
+    if (dtype == 0)
+      return a.stream ? launch(k_logprob<0, true, W, P>, g, W, s, a)
+                      : launch(k_logprob<0, false, W, P>, g, W, s, a);
+    return a.stream ? launch(k_logprob<1, true, W, P>, g, W, s, a)
+                    : launch(k_logprob<1, false, W, P>, g, W, s, a);
+  });
+}
 
 hipError_t launch_logprob(LogitArgs a, int dtype, hipStream_t s) {
-  if (a.T == 0) return hipSuccess;
   switch (score_threads(a.T, row_pieces(a, dtype))) {
-    case 64: HLQ_ROW_LAUNCH(k_logprob, 64, 4, a); break;
-    case 256: HLQ_ROW_LAUNCH(k_logprob, 256, 4, a); break;
-    case 512: HLQ_ROW_LAUNCH(k_logprob, 512, 4, a); break;
-    default: HLQ_ROW_LAUNCH(k_logprob, 1024, 4, a); break;
+    case 64: return logprob_rows<64, 4>(a, dtype, s);
+    case 256: return logprob_rows<256, 4>(a, dtype, s);
+    case 512: return logprob_rows<512, 4>(a, dtype, s);
+    default: return logprob_rows<1024, 4>(a, dtype, s);
   }
-  return hipGetLastError();
+}
+
+template <int W, int P>
+static hipError_t grad_rows(LogitArgs& a, int dtype, hipStream_t s) {
+  return for_rows(a, [&](dim3 g) {
+    return dtype == 0 ? launch(k_logprob_grad<0, W, P>, g, W, s, a)
+                      : launch(k_logprob_grad<1, W, P>, g, W, s, a);
+  });
 }
 
 hipError_t launch_logprob_grad(LogitArgs a, int dtype, hipStream_t s) {
-  if (a.T == 0) return hipSuccess;
-#define HLQ_GRAD(W, P)                                                                         \
-  for (a.row0 = 0; a.row0 < a.T; a.row0 += 1 << 20) {                                          \
-    const dim3 g = rows_grid(a.T - a.row0);                                                    \
-    if (dtype == 0) hipLaunchKernelGGL((k_logprob_grad<0, W, P>), g, dim3(W), 0, s, a);        \
-    else hipLaunchKernelGGL((k_logprob_grad<1, W, P>), g, dim3(W), 0, s, a);                   \
-  }
   switch (grad_threads(a.T, row_pieces(a, dtype))) {
-    case 64: HLQ_GRAD(64, 2); break;
-    case 256: HLQ_GRAD(256, 2); break;
-    default: HLQ_GRAD(1024, 4); break;
+    case 64: return grad_rows<64, 2>(a, dtype, s);
+    case 256: return grad_rows<256, 2>(a, dtype, s);
+    default: return grad_rows<1024, 4>(a, dtype, s);
   }
-#undef HLQ_GRAD
-  return hipGetLastError();
+}
+
+template <int W, int P>
+static hipError_t policy_rows(LogitArgs& a, const PolicyArgs& p, int dtype, hipStream_t s) {
+  return for_rows(a, [&](dim3 g) {
+    if (dtype == 0)
+      return a.stream ? launch(k_policy_regs<0, true, W, P>, g, W, s, a, p)
+                      : launch(k_policy_regs<0, false, W, P>, g, W, s, a, p);
+    return a.stream ? launch(k_policy_regs<1, true, W, P>, g, W, s, a, p)
+                    : launch(k_policy_regs<1, false, W, P>, g, W, s, a, p);
+  });
+}
+
+static hipError_t policy_long_rows(LogitArgs& a, const PolicyArgs& p, int dtype, hipStream_t s) {
+  return for_rows(a, [&](dim3 g) {
+    if (dtype == 0)
+      return a.stream ? launch(k_policy_long<0, true, 1024, 4>, g, 1024, s, a, p)
+                      : launch(k_policy_long<0, false, 1024, 4>, g, 1024, s, a, p);
+    return a.stream ? launch(k_policy_long<1, true, 1024, 4>, g, 1024, s, a, p)
+                    : launch(k_policy_long<1, false, 1024, 4>, g, 1024, s, a, p);
+  });
 }
 
 hipError_t launch_policy_logits(LogitArgs a, const PolicyArgs& p, int dtype,
                                 hipStream_t s) {
   const int64_t n = row_pieces(a, dtype);
-  if (a.T) {
-    const bool few = a.T < 256;  // fewer rows than CUs: more threads a row
-    if (n <= 256 && !(few && n > 64)) { HLQ_ROW_LAUNCH(k_policy_regs, 64, 4, a, p); }
-    else if (n <= 1024 && !(few && n > 256)) { HLQ_ROW_LAUNCH(k_policy_regs, 256, 4, a, p); }
-    else if (n <= 2048 && !few) { HLQ_ROW_LAUNCH(k_policy_regs, 256, 8, a, p); }
-    else if (n <= 4096 && !few) { HLQ_ROW_LAUNCH(k_policy_regs, 256, 16, a, p); }
-    else if (n <= 4096) { HLQ_ROW_LAUNCH(k_policy_regs, 1024, 4, a, p); }
-    else if (n <= 8192) { HLQ_ROW_LAUNCH(k_policy_regs, 512, 16, a, p); }
-    else if (n <= 12288) { HLQ_ROW_LAUNCH(k_policy_regs, 1024, 12, a, p); }
-    else if (n <= 16384) { HLQ_ROW_LAUNCH(k_policy_regs, 1024, 16, a, p); }
-    else { HLQ_ROW_LAUNCH(k_policy_long, 1024, 4, a, p); }
-  }
-  hipLaunchKernelGGL(k_terms<3>, dim3(1), dim3(1024), 0, s, p.terms, p.T, 1.0, p.sums);
-  return hipGetLastError();
+  const bool few = a.T < 256;  // fewer rows than CUs: more threads a row
+  hipError_t e;
+  if (n <= 256 && !(few && n > 64)) e = policy_rows<64, 4>(a, p, dtype, s);
+  else if (n <= 1024 && !(few && n > 256)) e = policy_rows<256, 4>(a, p, dtype, s);
+  else if (n <= 2048 && !few) e = policy_rows<256, 8>(a, p, dtype, s);
+  else if (n <= 4096 && !few) e = policy_rows<256, 16>(a, p, dtype, s);
+  else if (n <= 4096) e = policy_rows<1024, 4>(a, p, dtype, s);
+  else if (n <= 8192) e = policy_rows<512, 16>(a, p, dtype, s);
+  else if (n <= 12288) e = policy_rows<1024, 12>(a, p, dtype, s);
+  else if (n <= 16384) e = policy_rows<1024, 16>(a, p, dtype, s);
+  else e = policy_long_rows(a, p, dtype, s);
+  if (e != hipSuccess) return e;
+  return launch(k_terms<3>, dim3(1), 1024, s, p.terms, p.T, 1.0, p.sums);
 }
-#undef HLQ_ROW_LAUNCH
 
 hipError_t launch_policy(const PolicyArgs& p, hipStream_t s) {
-  if (p.T) hipLaunchKernelGGL(k_policy, dim3(cdiv(p.T, 256)), dim3(256), 0, s, p);
-  hipLaunchKernelGGL(k_terms<3>, dim3(1), dim3(1024), 0, s, p.terms, p.T, 1.0, p.sums);
-  return hipGetLastError();
+  const hipError_t e = p.T ? launch(k_policy, dim3(cdiv(p.T, 256)), 256, s, p) : hipSuccess;
+  if (e != hipSuccess) return e;
+  return launch(k_terms<3>, dim3(1), 1024, s, p.terms, p.T, 1.0, p.sums);
 }
 
 hipError_t launch_preference(const PrefArgs& p, hipStream_t s) {
   // one launch where a wave has one pair, and a short one in the mean (2 pairs
   // of 150 tokens: 4.8 us instead of 4.8 + 1.8 and a launch's gap; 32 pairs of
   // 256 tokens, ragged: 20 us instead of 6.8 + 4)
-  if (p.P <= 16 && p.T <= 256 * p.P) {
-    hipLaunchKernelGGL(k_preference_small, dim3(1), dim3(1024), 0, s, p);
-    return hipGetLastError();
-  }
-  hipLaunchKernelGGL(k_preference, dim3((unsigned)p.P), dim3(1024), 0, s, p);
-  hipLaunchKernelGGL(k_terms<1>, dim3(1), dim3(1024), 0, s, p.terms, p.P, 1.0 / (double)p.P,
-                     p.loss);
-  return hipGetLastError();
+  if (p.P <= 16 && p.T <= 256 * p.P) return launch(k_preference_small, dim3(1), 1024, s, p);
+  const hipError_t e = launch(k_preference, dim3((unsigned)p.P), 1024, s, p);
+  if (e != hipSuccess) return e;
+  return launch(k_terms<1>, dim3(1), 1024, s, p.terms, p.P, 1.0 / (double)p.P, p.loss);
 }
 
 }  // namespace hlq

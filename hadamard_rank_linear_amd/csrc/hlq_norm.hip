@@ -199,6 +199,19 @@ __global__ __launch_bounds__(B) void k_norm_fwd(NormFwd a) {
   }
 }
 
+// Column sum c of a workgroup's rows (side 0: of g_y n, 1: of g_y): a partial
+// for the fold, or the output itself where there is one workgroup.
+__device__ __forceinline__ void put_param(void* out, int dt, int64_t c, float v) {
+  if (dt == 0) static_cast<float*>(out)[c] = v;
+  else static_cast<__bf16*>(out)[c] = (__bf16)v;
+}
+__device__ __forceinline__ void put_column(const NormBwd& a, int64_t part, int side, int64_t c,
+                                           float v) {
+  if (a.parts > 1) a.part[(part * 2 + side) * a.C + c] = v;
+  else if (side == 0) put_param(a.g_weight, a.param_dt, c, v);
+  else if (a.g_bias) put_param(a.g_bias, a.param_dt, c, v);
+}
+
 // Gradient of the rows and, over the rows a group takes, its column sums in
 // registers; at the end the groups of a workgroup join theirs (lanes of a wave
 // first, then the waves through LDS) and write one partial.
@@ -269,7 +282,6 @@ __global__ __launch_bounds__(B, 4) void k_norm_bwd(NormBwd a) {
     }
     if constexpr (L > 64) __syncthreads();  // sm is used again
   }
-  float* part = a.part + (int64_t)blockIdx.x * 2 * a.C;
   if constexpr (L > 64) {
 #pragma unroll
     for (int j = 0; j < M; ++j)
@@ -277,8 +289,8 @@ __global__ __launch_bounds__(B, 4) void k_norm_bwd(NormBwd a) {
       for (int k = 0; k < 4; ++k) {
         const uint32_t c = (uint32_t)(at.lane + j * L) * 4 + k;
         if (c < C) {
-          part[c] = gw[j][k];
-          part[a.C + c] = gb[j][k];
+          put_column(a, blockIdx.x, 0, c, gw[j][k]);
+          put_column(a, blockIdx.x, 1, c, gb[j][k]);
         }
       }
   } else {
@@ -301,7 +313,7 @@ __global__ __launch_bounds__(B, 4) void k_norm_bwd(NormBwd a) {
           float v = cols[c];
 #pragma unroll
           for (int w = 1; w < B / 64; ++w) v += cols[w * COLS + c];
-          part[side * a.C + c] = v;
+          put_column(a, blockIdx.x, side, c, v);
         }
     }
   }
@@ -436,8 +448,8 @@ __global__ __launch_bounds__(256) void k_norm_columns(NormBwd a) {
     const int l = e / (2 * N), k = e % (2 * N);
     const int64_t col = ((int64_t)blockIdx.x * 64 + l) * N + k / 2;
     if (col < C)
-      a.part[((int64_t)blockIdx.y * 2 + (k & 1)) * C + col] =
-          (sm[0][l][k] + sm[1][l][k]) + (sm[2][l][k] + sm[3][l][k]);
+      put_column(a, blockIdx.y, k & 1, col,
+                 (sm[0][l][k] + sm[1][l][k]) + (sm[2][l][k] + sm[3][l][k]));
   }
 }
 
@@ -463,11 +475,8 @@ __global__ __launch_bounds__(1024) void k_norm_fold(NormBwd a, int64_t col0) {
   s = (sm[4 * q][lane] + sm[4 * q + 1][lane]) + (sm[4 * q + 2][lane] + sm[4 * q + 3][lane]);
   s += __shfl_xor(s, 16);
   s += __shfl_xor(s, 32);
-  if (threadIdx.x < 16 && c < C) {
-    void* out = blockIdx.y ? a.g_bias : a.g_weight;
-    if (a.param_dt == 0) static_cast<float*>(out)[c] = (float)s;
-    else static_cast<__bf16*>(out)[c] = (__bf16)(float)s;
-  }
+  if (threadIdx.x < 16 && c < C)
+    put_param(blockIdx.y ? a.g_bias : a.g_weight, a.param_dt, c, (float)s);
 }
 
 // ------------------------------------------------------------ launches
@@ -503,12 +512,18 @@ static NormRow norm_row(int64_t C) {
 constexpr int NORM_BWD_THREADS = 512;  // workgroups of the backward kernel, L <= 64
 
 // Workgroups of the backward kernel, each leaving one partial: up to 1024
-// threads per CU.
+// threads per CU.  Few rows are one workgroup's, which writes the parameters'
+// gradients itself: up to NORM_ALONE rounds of it (GPU time of 1, 2 and 4 rounds
+// in one launch, and of as many rows in two: 64 columns 3.8, 4.6, 5.4 and 5.1
+// us; 768 4.3, 6.3, 10.1 and 6.5; 4096 6.2, 9.0, 14.4 and 8.5; the second launch
+// costs the host 2.3 us).
+constexpr int NORM_ALONE = 2;
 int64_t norm_parts(int64_t T, int64_t C) {
   const NormRow r = norm_row(C);
   if (r == ROW_WIDE) return (T + 31) / 32 < 256 ? (T + 31) / 32 : 256;
   const int L = norm_lanes[r], B = L <= 64 ? NORM_BWD_THREADS : L;
   const int64_t need = (T + B / L - 1) / (B / L), most = 256 * 1024 / B;
+  if (T > 0 && need <= NORM_ALONE) return 1;
   return need < most ? need : most;
 }
 
@@ -517,45 +532,48 @@ hipError_t launch_norm_forward(const NormFwd& a, int dtype, hipStream_t s) {
 #define HLQ_F(L, M, B)                                                                      \
   do {                                                                                      \
     const dim3 g = rows_grid((a.T + B / L - 1) / (B / L));                                  \
-    if (dtype == 0) hipLaunchKernelGGL((k_norm_fwd<0, L, M, B>), g, dim3(B), 0, s, a);      \
-    else hipLaunchKernelGGL((k_norm_fwd<1, L, M, B>), g, dim3(B), 0, s, a);                 \
+    if (dtype == 0) return launch(k_norm_fwd<0, L, M, B>, g, B, s, a);                      \
+    return launch(k_norm_fwd<1, L, M, B>, g, B, s, a);                                      \
   } while (0)
   switch (norm_row(a.C)) {
     HLQ_NORM_ROWS(HLQ_F, 256)
-    case ROW_WIDE:
-      if (dtype == 0) hipLaunchKernelGGL(k_norm_fwd_wide<0>, rows_grid(a.T), dim3(256), 0, s, a);
-      else hipLaunchKernelGGL(k_norm_fwd_wide<1>, rows_grid(a.T), dim3(256), 0, s, a);
+    default: break;
   }
 #undef HLQ_F
-  return hipGetLastError();
+  if (dtype == 0) return launch(k_norm_fwd_wide<0>, rows_grid(a.T), 256, s, a);
+  return launch(k_norm_fwd_wide<1>, rows_grid(a.T), 256, s, a);
 }
 
-hipError_t launch_norm_backward(const NormBwd& a, int dtype, hipStream_t s) {
+// g_x and the partial column sums.
+static hipError_t launch_norm_gx(const NormBwd& a, int dtype, hipStream_t s) {
   const int N = dtype == 0 ? 4 : 8;
   const dim3 g((unsigned)a.parts), wide(cdiv(a.C, 64 * N), (unsigned)a.parts);
 #define HLQ_B(L, M, B)                                                                      \
   do {                                                                                      \
-    if (dtype == 0) hipLaunchKernelGGL((k_norm_bwd<0, L, M, B>), g, dim3(B), 0, s, a);    \
-    else hipLaunchKernelGGL((k_norm_bwd<1, L, M, B>), g, dim3(B), 0, s, a);               \
+    if (dtype == 0) return launch(k_norm_bwd<0, L, M, B>, g, B, s, a);                      \
+    return launch(k_norm_bwd<1, L, M, B>, g, B, s, a);                                      \
   } while (0)
-  if (a.T) switch (norm_row(a.C)) {
+  switch (norm_row(a.C)) {
     HLQ_NORM_ROWS(HLQ_B, NORM_BWD_THREADS)
-    default:
-      if (dtype == 0) {
-        hipLaunchKernelGGL(k_norm_gx_wide<0>, rows_grid(a.T), dim3(256), 0, s, a);
-        hipLaunchKernelGGL(k_norm_columns<0>, wide, dim3(256), 0, s, a);
-      } else {
-        hipLaunchKernelGGL(k_norm_gx_wide<1>, rows_grid(a.T), dim3(256), 0, s, a);
-        hipLaunchKernelGGL(k_norm_columns<1>, wide, dim3(256), 0, s, a);
-      }
+    default: break;
   }
 #undef HLQ_B
+  const hipError_t e = dtype == 0 ? launch(k_norm_gx_wide<0>, rows_grid(a.T), 256, s, a)
+                                  : launch(k_norm_gx_wide<1>, rows_grid(a.T), 256, s, a);
+  if (e != hipSuccess) return e;
+  if (dtype == 0) return launch(k_norm_columns<0>, wide, 256, s, a);
+  return launch(k_norm_columns<1>, wide, 256, s, a);
+}
+
+hipError_t launch_norm_backward(const NormBwd& a, int dtype, hipStream_t s) {
+  hipError_t e = a.T ? launch_norm_gx(a, dtype, s) : hipSuccess;
+  if (a.parts == 1) return e;
   // 2^24 columns a launch (a launch holds fewer than 2^32 threads)
-  for (int64_t c = 0; c < a.C; c += 1 << 24) {
+  for (int64_t c = 0; c < a.C && e == hipSuccess; c += 1 << 24) {
     const int64_t n = a.C - c < (1 << 24) ? a.C - c : 1 << 24;
-    hipLaunchKernelGGL(k_norm_fold, dim3(cdiv(n, 16), a.g_bias ? 2 : 1), dim3(1024), 0, s, a, c);
+    e = launch(k_norm_fold, dim3(cdiv(n, 16), a.g_bias ? 2 : 1), 1024, s, a, c);
   }
-  return hipGetLastError();
+  return e;
 }
 #undef HLQ_NORM_ROWS
 

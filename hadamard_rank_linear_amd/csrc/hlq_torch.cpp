@@ -11,6 +11,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <dlfcn.h>
@@ -158,19 +159,45 @@ P* ptr(const Tensor& t) {
   return static_cast<P*>(t.data_ptr());
 }
 
+// A new contiguous tensor on the GPU of `like`, from torch's allocator without
+// the way through the dispatcher.
+Tensor make(const at::Device& device, ScalarType type, IntArrayRef shape) {
+  return at::detail::empty_cuda(shape, type, device, std::nullopt);
+}
 Tensor make(const Tensor& like, ScalarType type, IntArrayRef shape) {
-  return at::empty(shape, like.options().dtype(type).memory_format(at::MemoryFormat::Contiguous));
+  return make(like.device(), type, shape);
 }
 
-// The GPU of a call is current while it lasts; its stream is the given raw one
-// or the current one.
+// The GPU of a call is current while it lasts; its stream is the given
+// torch.cuda.Stream or the current one (None).
 struct Launch {
   c10::DeviceGuard guard;
+  PyObject* given;
   void* stream;
-  Launch(const Tensor& like, PyObject* raw) : guard(like.device()) {
-    stream = raw == Py_None ? c10::hip::getCurrentHIPStream(like.device().index()).stream()
-                            : PyLong_AsVoidPtr(raw);
+  Launch(const Tensor& like, PyObject* o) : Launch(like.device(), o) {}
+  Launch(const at::Device& device, PyObject* o) : guard(device), given(o == Py_None ? nullptr : o) {
+    if (!given) {
+      stream = c10::hip::getCurrentHIPStream(device.index()).stream();
+      return;
+    }
+    PyObject* raw = PyObject_GetAttrString(given, "cuda_stream");
+    if (!raw) throw python_error();
+    stream = PyLong_AsVoidPtr(raw);
+    Py_DECREF(raw);
     if (PyErr_Occurred()) throw python_error();
+  }
+  // Tells the allocator that tensors, allocated for the current stream, are
+  // used on the given one.
+  void hold(std::initializer_list<const Tensor*> ts) const {
+    if (!given) return;
+    for (const Tensor* t : ts) {
+      if (!t) continue;
+      PyObject* o = THPVariable_Wrap(*t);
+      PyObject* r = o ? PyObject_CallMethod(o, "record_stream", "O", given) : nullptr;
+      Py_XDECREF(o);
+      if (!r) throw python_error();
+      Py_DECREF(r);
+    }
   }
 };
 
@@ -244,12 +271,13 @@ PyObject* layer_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         lib.hlq_layer_norm_forward(ptr(x), ptr(residual), code(x), ptr(w), ptr(b), code(w), T, C,
                                    eps, ptr(y), h ? ptr(*h) : nullptr, ptr<float>(mean),
                                    ptr<float>(rstd), on.stream));
+  on.hold({&y, h ? &*h : &x, &mean, &rstd});
   return tuple(wrap(y), wrap(h ? *h : x), wrap(mean), wrap(rstd));
   END_HANDLE_TH_ERRORS
 }
 
 // (g_y, h, mean, rstd, weight, g_h, with_bias, g_x, workspace, stream)
-//   -> (g_x, g_weight, g_bias, workspace)
+//   -> (g_x, g_weight, g_bias)
 PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 10);
@@ -274,16 +302,17 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   same_gpu(h, {&h, &g_y, &mean, &rstd, &w, g_h, g_x_in});
   const Launch on(h, a[9]);
   const Tensor g_x = g_x_in ? *g_x_in : make(h, h.scalar_type(), h.sizes());
-  const Tensor g_w = make(w, w.scalar_type(), {C});
+  const Tensor g_w = make(h, w.scalar_type(), {C});
   std::optional<Tensor> g_b;
-  if (with_bias) g_b = make(w, w.scalar_type(), {C});
+  if (with_bias) g_b = make(h, w.scalar_type(), {C});
   const Tensor ws =
       workspace(ws_in, lib.hlq_layer_norm_backward_workspace_size(T, C, code(h)), h);
   check("hlq_layer_norm_backward",
         lib.hlq_layer_norm_backward(ptr(g_y), ptr(h), ptr(g_h), code(h), ptr<float>(mean),
                                     ptr<float>(rstd), ptr(w), code(w), T, C, ptr(g_x), ptr(g_w),
                                     g_b ? ptr(*g_b) : nullptr, ptr(ws), ws.numel(), on.stream));
-  return tuple(wrap(g_x), wrap(g_w), g_b ? wrap(*g_b) : none(), wrap(ws));
+  on.hold({&g_x, &g_w, g_b ? &*g_b : nullptr, &ws});
+  return tuple(wrap(g_x), wrap(g_w), g_b ? wrap(*g_b) : none());
   END_HANDLE_TH_ERRORS
 }
 
@@ -323,6 +352,7 @@ PyObject* token_logprob_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   check("hlq_token_logprob_forward",
         lib.hlq_token_logprob_forward(ptr(x), code(x), ld, ptr<int64_t>(t), T, x.size(1), scale,
                                       ptr<float>(lp), ptr<float>(stats), on.stream));
+  on.hold({&lp, &stats});
   return tuple(wrap(lp), wrap(stats));
   END_HANDLE_TH_ERRORS
 }
@@ -351,6 +381,7 @@ PyObject* token_logprob_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         lib.hlq_token_logprob_backward(ptr<float>(g), ptr(x), code(x), ld, ptr<int64_t>(t),
                                        ptr<float>(stats), T, V, scale, ptr(g_x), g_ld,
                                        on.stream));
+  on.hold({&g_x});
   return wrap(g_x);
   END_HANDLE_TH_ERRORS
 }
@@ -372,7 +403,7 @@ struct PolicyInputs {
 };
 
 // (logprob, old, advantage, weight, ref, clip_low, clip_high, kl_coef, workspace, stream)
-//   -> (sums, g_logprob, workspace)
+//   -> (sums, g_logprob)
 PyObject* policy_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 10);
@@ -392,12 +423,13 @@ PyObject* policy_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
         lib.hlq_policy_loss(ptr<float>(lp), ptr<float>(in.old), ptr<float>(in.advantage),
                             ptr<float>(in.weight), ptr<float>(in.ref), T, lo, hi, kl,
                             ptr<float>(sums), ptr<float>(g), ptr(ws), ws.numel(), on.stream));
-  return tuple(wrap(sums), wrap(g), wrap(ws));
+  on.hold({&sums, &g, &ws});
+  return tuple(wrap(sums), wrap(g));
   END_HANDLE_TH_ERRORS
 }
 
 // (logits, targets, old, advantage, weight, ref, scale, clip_low, clip_high, kl_coef, g_x,
-//  workspace, stream) -> (sums, logprob, g_x, workspace)
+//  workspace, stream) -> (sums, logprob, g_x)
 PyObject* policy_loss_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 13);
@@ -426,12 +458,13 @@ PyObject* policy_loss_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                    ptr<float>(in.ref), T, V, scale, lo, hi, kl, ptr<float>(sums),
                                    ptr<float>(lp), ptr(g_x), g_ld, ptr(ws), ws.numel(),
                                    on.stream));
-  return tuple(wrap(sums), wrap(lp), wrap(g_x), wrap(ws));
+  on.hold({&sums, &lp, &g_x, &ws});
+  return tuple(wrap(sums), wrap(lp), wrap(g_x));
   END_HANDLE_TH_ERRORS
 }
 
 // (logprob, start, beta, ref, weight, label_smoothing, reduction, workspace, stream)
-//   -> (loss, margin, g_logprob, workspace)
+//   -> (loss, margin, g_logprob)
 PyObject* preference_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 9);
@@ -460,7 +493,8 @@ PyObject* preference_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 ptr<int64_t>(start), P, T, beta, e, (int)reduction,
                                 ptr<float>(loss), ptr<float>(margin), ptr<float>(g), ptr(ws),
                                 ws.numel(), on.stream));
-  return tuple(wrap(loss), wrap(margin), wrap(g), wrap(ws));
+  on.hold({&loss, &margin, &g, &ws});
+  return tuple(wrap(loss), wrap(margin), wrap(g));
   END_HANDLE_TH_ERRORS
 }
 
@@ -479,7 +513,7 @@ struct Items {
   PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(seq, i); }
 };
 
-// (grads, max_norm, norm_kind, out, workspace, stream, device) -> (norm, workspace)
+// (grads, max_norm, norm_kind, out, workspace, stream, device) -> norm
 PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 7);
@@ -516,16 +550,16 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       dst[i] = o.data_ptr();
     }
   }
-  const auto options = at::TensorOptions().device(device);
-  const Tensor norm = at::empty({1}, options.dtype(at::kDouble));
-  const Launch on(norm, a[5]);
+  const Launch on(device, a[5]);
+  const Tensor norm = make(device, ScalarType::Double, {1});
   const Tensor ws =
       workspace(ws_in, lib.hlq_clip_grad_norm_workspace_size(sizes.data(), N), norm);
   check("hlq_clip_grad_norm",
         lib.hlq_clip_grad_norm(src.data(), in_place ? nullptr : dst.data(), sizes.data(),
                                types.data(), N, max_norm, (int)kind, ptr<double>(norm), ptr(ws),
                                ws.numel(), on.stream));
-  return tuple(wrap(norm), wrap(ws));
+  on.hold({&norm, &ws});
+  return wrap(norm);
   END_HANDLE_TH_ERRORS
 }
 

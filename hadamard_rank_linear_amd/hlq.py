@@ -543,12 +543,12 @@ def hlq_lqs_select(stats, threshold=HLQ_LQS_THRESHOLD):
 # These operators' tensors are checked, their outputs allocated and the library
 # called by the native module _hlq_torch (csrc/hlq_torch.cpp).
 
-_native_module = None
+class _Unloaded:
+    """Stands for the native module until the first call: loads it, binds it to
+    this library and takes itself out of the way."""
 
-
-def _native():
-    global _native_module
-    if _native_module is None:
+    def __getattr__(self, name):
+        global _native
         import torch  # noqa: F401  (the module links against its libraries)
         try:
             from . import _hlq_torch
@@ -556,22 +556,11 @@ def _native():
             raise ImportError("the native binding _hlq_torch.so is missing or does not load: build "
                               "it with `python -m hadamard_rank_linear_amd.build`") from e
         _hlq_torch.bind(_lib._handle, _check)
-        _native_module = _hlq_torch
-    return _native_module
+        _native = _hlq_torch
+        return getattr(_hlq_torch, name)
 
 
-def _raw(stream):
-    """The raw stream of a ``torch.cuda.Stream``, None for the current one."""
-    return None if stream is None else stream.cuda_stream
-
-
-def _hold(stream, *ts):
-    """Tells the allocator that ``ts``, allocated for the current stream, are
-    used on ``stream`` (None: the current one)."""
-    if stream is not None:
-        for t in ts:
-            if t is not None:
-                t.record_stream(stream)
+_native = _Unloaded()
 
 
 def hlq_layer_norm_forward(x, weight, bias=None, eps=1e-5, residual=None, y=None, h=None,
@@ -584,9 +573,7 @@ def hlq_layer_norm_forward(x, weight, bias=None, eps=1e-5, residual=None, y=None
     itself when there is no residual.  mean and rstd (fp32, one per row) are
     kept for :func:`hlq_layer_norm_backward`.
     """
-    out = _native().layer_norm_forward(x, weight, bias, eps, residual, y, h, _raw(stream))
-    _hold(stream, *out)
-    return out
+    return _native.layer_norm_forward(x, weight, bias, eps, residual, y, h, stream)
 
 
 def hlq_layer_norm_backward_workspace_size(T, C, dtype=HLQ_F32) -> int:
@@ -603,10 +590,8 @@ def hlq_layer_norm_backward(g_y, h, mean, rstd, weight, g_h=None, with_bias=True
     all of one type; g_weight and g_bias have the type of weight.  g_x is the
     gradient of x and of the residual alike.
     """
-    out = _native().layer_norm_backward(g_y, h, mean, rstd, weight, g_h, with_bias, g_x,
-                                        workspace, _raw(stream))
-    _hold(stream, *out)
-    return out[:3]
+    return _native.layer_norm_backward(g_y, h, mean, rstd, weight, g_h, with_bias, g_x,
+                                       workspace, stream)
 
 
 def hlq_token_logprob_forward(logits, targets, scale=1.0, stream=None):
@@ -618,19 +603,14 @@ def hlq_token_logprob_forward(logits, targets, scale=1.0, stream=None):
     row not read.  The rows of logits may have any pitch (a slice of a padded
     vocabulary).
     """
-    out = _native().token_logprob_forward(logits, targets, scale, _raw(stream))
-    _hold(stream, *out)
-    return out
+    return _native.token_logprob_forward(logits, targets, scale, stream)
 
 
 def hlq_token_logprob_backward(g_logprob, logits, targets, stats, scale=1.0, g_x=None,
                                stream=None):
     """Gradient [T, V] of logits from that of the log probabilities
     (:func:`hlq_token_logprob_forward`'s), in the type of logits."""
-    g_x = _native().token_logprob_backward(g_logprob, logits, targets, stats, scale, g_x,
-                                           _raw(stream))
-    _hold(stream, g_x)
-    return g_x
+    return _native.token_logprob_backward(g_logprob, logits, targets, stats, scale, g_x, stream)
 
 
 def hlq_policy_loss_workspace_size(T) -> int:
@@ -643,10 +623,8 @@ def hlq_policy_loss(logprob, old_logprob, advantage, weight=None, ref_logprob=No
     (sums [3], g_logprob [T]), sums = (loss, weighted KL estimate, weight of
     the clipped tokens).  ``ref_logprob`` goes with a kl_coef other than 0; a
     weight of 0 takes a token out (weight None: ones)."""
-    out = _native().policy_loss(logprob, old_logprob, advantage, weight, ref_logprob, clip_low,
-                                clip_high, kl_coef, workspace, _raw(stream))
-    _hold(stream, *out)
-    return out[:2]
+    return _native.policy_loss(logprob, old_logprob, advantage, weight, ref_logprob, clip_low,
+                               clip_high, kl_coef, workspace, stream)
 
 
 def hlq_policy_loss_logits(logits, targets, old_logprob, advantage, weight=None, ref_logprob=None,
@@ -656,11 +634,9 @@ def hlq_policy_loss_logits(logits, targets, old_logprob, advantage, weight=None,
     :func:`hlq_token_logprob_backward` in one pass over logits [T, V]: returns
     (sums [3], logprob [T], g_x [T, V]).  Tokens whose weight is 0 or whose
     target is ignored do not count; their rows are not read."""
-    out = _native().policy_loss_logits(logits, targets, old_logprob, advantage, weight,
-                                       ref_logprob, scale, clip_low, clip_high, kl_coef, g_x,
-                                       workspace, _raw(stream))
-    _hold(stream, *out)
-    return out[:3]
+    return _native.policy_loss_logits(logits, targets, old_logprob, advantage, weight,
+                                      ref_logprob, scale, clip_low, clip_high, kl_coef, g_x,
+                                      workspace, stream)
 
 
 def hlq_preference_loss_workspace_size(P) -> int:
@@ -677,10 +653,8 @@ def hlq_preference_loss(logprob, start, beta, ref_logprob=None, weight=None, lab
     gradient of zero); ``reduction`` HLQ_SUM scores a sequence by the
     sum of weight * (logprob - ref_logprob), HLQ_MEAN by its weighted mean.
     """
-    out = _native().preference_loss(logprob, start, beta, ref_logprob, weight, label_smoothing,
-                                    reduction, workspace, _raw(stream))
-    _hold(stream, *out)
-    return out[:3]
+    return _native.preference_loss(logprob, start, beta, ref_logprob, weight, label_smoothing,
+                                   reduction, workspace, stream)
 
 
 def hlq_clip_grad_norm_workspace_size(sizes) -> int:
@@ -703,10 +677,7 @@ def hlq_clip_grad_norm(grads, max_norm, norm_kind=HLQ_NORM_L2, out=None, workspa
     if not grads:
         import torch
         device = torch.cuda.current_device()
-    norm, workspace = _native().clip_grad_norm(grads, max_norm, norm_kind, out, workspace,
-                                               _raw(stream), device)
-    _hold(stream, norm, workspace)
-    return norm
+    return _native.clip_grad_norm(grads, max_norm, norm_kind, out, workspace, stream, device)
 
 
 def lib_handle():

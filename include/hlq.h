@@ -443,7 +443,7 @@ hlq_status hlq_layer_norm_forward(const void* x, const void* residual, int dtype
  *   g_weight, g_bias [C] out, param_dtype; g_bias NULL: not computed.
  *   workspace at least hlq_layer_norm_backward_workspace_size(T, C, dtype)
  *            bytes: per-workgroup column sums (0 for an invalid shape).
- * Two launches.  Errors as above and HLQ_ERR_WORKSPACE.
+ * Two launches, one for a few rows.  Errors as above and HLQ_ERR_WORKSPACE.
  */
 size_t hlq_layer_norm_backward_workspace_size(int64_t T, int64_t C, int dtype);
 hlq_status hlq_layer_norm_backward(const void* g_y, const void* h, const void* g_h, int dtype,
