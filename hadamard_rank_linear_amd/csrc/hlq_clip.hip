@@ -95,8 +95,7 @@ __device__ __forceinline__ void clip_take(const u32x4& r, int kind, double& sq, 
 }
 
 __device__ __forceinline__ uint32_t group_umax(uint32_t v, uint32_t* sm) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
+  v = lanes_join<64>(v, [](uint32_t p, uint32_t q) { return max(p, q); });
   if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = v;
   __syncthreads();
   v = sm[0];

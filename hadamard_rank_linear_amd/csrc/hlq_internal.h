@@ -222,7 +222,7 @@ struct NormFwd {
   float *mean, *rstd;
 };
 // Layer norm backward; g_h and g_bias may be null.  part: parts x 2 x C
-// partial column sums (parts = norm_parts(T, C)).
+// partial column sums (parts = norm_parts(T, C, dtype)).
 struct NormBwd {
   const void *g_y, *h, *g_h;
   const float *mean, *rstd;
@@ -232,7 +232,7 @@ struct NormBwd {
   void *g_x, *g_weight, *g_bias;
   float* part;
 };
-int64_t norm_parts(int64_t T, int64_t C);
+int64_t norm_parts(int64_t T, int64_t C, int dtype);
 hipError_t launch_norm_forward(const NormFwd& a, int dtype, hipStream_t s);
 hipError_t launch_norm_backward(const NormBwd& a, int dtype, hipStream_t s);
 

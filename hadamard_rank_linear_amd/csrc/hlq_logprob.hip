@@ -188,9 +188,7 @@ __device__ __forceinline__ void join_stats(const LogitArgs& a, float (*sm)[16], 
     __syncthreads();
     m = sm[0][threadIdx.x & (W / 64 - 1)];
     s = sm[1][threadIdx.x & (W / 64 - 1)];
-    top = m;
-#pragma unroll
-    for (int k = W / 128; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor(top, k));
+    top = lanes_max<W / 64>(m);
     s = lanes_sum<W / 64>(s * exp_scaled(m - ref_of(top), a.c_hi, a.c_lo));
   }
   m = top;

@@ -92,6 +92,25 @@ __device__ __forceinline__ float row_sum(float v, float* sm) {
   else return group_sum<L>(v, sm);
 }
 
+// Two sums at once: one exchange through LDS.
+template <int L>
+__device__ __forceinline__ void row_sums(float (&v)[2], float (*sm)[16]) {
+  if constexpr (L <= 64) {
+    v[0] = lanes_sum<L>(v[0]);
+    v[1] = lanes_sum<L>(v[1]);
+  } else {
+    v[0] = lanes_sum<64>(v[0]);
+    v[1] = lanes_sum<64>(v[1]);
+    if ((threadIdx.x & 63) == 0) {
+      sm[0][threadIdx.x >> 6] = v[0];
+      sm[1][threadIdx.x >> 6] = v[1];
+    }
+    __syncthreads();
+    v[0] = lanes_sum<L / 64>(sm[0][threadIdx.x & (L / 64 - 1)]);
+    v[1] = lanes_sum<L / 64>(sm[1][threadIdx.x & (L / 64 - 1)]);
+  }
+}
+
 // Where a thread stands: lane of its row, and the wave's first row within a
 // workgroup's B / L rows.
 template <int L>
@@ -122,80 +141,124 @@ __device__ __forceinline__ void load_quad_params(const void* base, int dt, uint3
   }
 }
 
-template <int DT, int L, int M, int B>
-__global__ __launch_bounds__(B) void k_norm_fwd(NormFwd a) {
-  typedef typename Quad<DT>::Raw Raw;
-  constexpr int R = B / L, ES = DT == 0 ? 4 : 2;
-  __shared__ float sm[2][16];
-  const RowLane<L> at;
-  const uint32_t C = (uint32_t)a.C;
-  const int skip = (4 - (int)(C & 3)) & 3;
-  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.T; r0 += (int64_t)gridDim.x * R) {
-    const int64_t first = r0 + at.wave_row, base = first * a.C * ES;
-    const bool live = first + at.sub < a.T;  // a group past the last row writes nothing
-    uint32_t c0 = (uint32_t)at.lane * 4, row_off = (uint32_t)at.sub * C * ES;
-    // computed anew for every row: else the compiler keeps a 64-bit pointer
-    // per operand and quad across the loop instead of base + offset
-    asm volatile("" : "+v"(c0), "+v"(row_off));
-    Raw x[M];
-    float sum = 0.f;
+// M quads of a row in registers: quad j of a lane is elements (lane + j L) 4
+// and on.
+template <int DT, int L, int M>
+struct RowQuads {
+  typename Quad<DT>::Raw v[M];
+  __device__ __forceinline__ void load(const void* p, int64_t base, uint32_t off, uint32_t c0,
+                                       uint32_t C, int skip, bool live) {
+    constexpr int ES = DT == 0 ? 4 : 2;
 #pragma unroll
     for (int j = 0; j < M; ++j) {
       const uint32_t c = c0 + j * L * 4;
-      x[j] = load_quad<DT>(static_cast<const char*>(a.x) + base, row_off + c * ES, live && c < C,
+      v[j] = load_quad<DT>(static_cast<const char*>(p) + base, off + c * ES, live && c < C,
                            c + 4 > C, skip);
     }
+  }
+  __device__ __forceinline__ float at(int j, int k) const { return quad_at<DT>(v[j], k); }
+};
+
+// Where a workgroup's group of L lanes reads its row of round r0.
+template <int DT, int L>
+struct RowAt {
+  int64_t row, base;
+  uint32_t c0, off;
+  bool live;  // a group past the last row reads and writes nothing
+  __device__ __forceinline__ RowAt(const RowLane<L>& at, int64_t r0, int64_t T, int64_t C) {
+    const int64_t first = r0 + at.wave_row;
+    row = first + at.sub;
+    base = first * C * (DT == 0 ? 4 : 2);
+    live = row < T;
+    c0 = (uint32_t)at.lane * 4;
+    off = (uint32_t)at.sub * (uint32_t)C * (DT == 0 ? 4 : 2);
+    // computed anew for every row: else the compiler keeps a 64-bit pointer
+    // per operand and quad across the loop instead of base + offset
+    asm volatile("" : "+v"(c0), "+v"(off));
+  }
+};
+
+// A workgroup takes rounds of B / L rows, the grid's width apart.  Weight and
+// bias stay in registers (an fp32 weight is twice the bytes of a bf16 row, and
+// reading it again for every row kept the vector L1 busier than the row did),
+// and a round's operands are loaded while the one before is worked on.  With 64
+// MiB operands, bf16: 45 us at 64 columns (65 with a workgroup per round), 46 at
+// 768 (49), 44 at 4096 (50, and 47 without the loads ahead), 53 at 1100 (73);
+// fp32 42 to 45 us, 256 MiB at 6 TB/s.
+template <int DT, int L, int M, int B>
+__global__ __launch_bounds__(B, 4) void k_norm_fwd(NormFwd a) {
+  constexpr int R = B / L, ES = DT == 0 ? 4 : 2;
+  __shared__ float sm[2][2][16];
+  const RowLane<L> at;
+  const uint32_t C = (uint32_t)a.C;
+  const int skip = (4 - (int)(C & 3)) & 3;
+  const int64_t step = (int64_t)gridDim.x * R;
+  int64_t r0 = (int64_t)blockIdx.x * R;
+  RowQuads<DT, L, M> x, q;
+  {
+    const RowAt<DT, L> p(at, r0, a.T, a.C);
+    x.load(a.x, p.base, p.off, p.c0, C, skip, p.live);
+    if (a.residual) q.load(a.residual, p.base, p.off, p.c0, C, skip, p.live);
+  }
+  float w[M][4], b[M][4] = {};
+#pragma unroll
+  for (int j = 0; j < M; ++j) {
+    const uint32_t c = (uint32_t)(at.lane + j * L) * 4;
+    load_quad_params(a.weight, a.param_dt, c, c < C, c + 4 > C, skip, w[j]);
+    if (a.bias) load_quad_params(a.bias, a.param_dt, c, c < C, c + 4 > C, skip, b[j]);
+  }
+  for (int turn = 0; r0 < a.T; r0 += step, turn ^= 1) {
+    RowQuads<DT, L, M> nx, nq;
+    {
+      const RowAt<DT, L> n(at, r0 + step, a.T, a.C);
+      nx.load(a.x, n.base, n.off, n.c0, C, skip, n.live);
+      if (a.residual) nq.load(a.residual, n.base, n.off, n.c0, C, skip, n.live);
+    }
+    const RowAt<DT, L> p(at, r0, a.T, a.C);
+    float sum = 0.f;
     if (a.residual) {
-      Raw q[M];
 #pragma unroll
       for (int j = 0; j < M; ++j) {
-        const uint32_t c = c0 + j * L * 4;
-        q[j] = load_quad<DT>(static_cast<const char*>(a.residual) + base, row_off + c * ES,
-                             live && c < C, c + 4 > C, skip);
-      }
-#pragma unroll
-      for (int j = 0; j < M; ++j) {
-        const uint32_t c = c0 + j * L * 4;
+        const uint32_t c = p.c0 + j * L * 4;
         float v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = quad_at<DT>(x[j], k) + quad_at<DT>(q[j], k);
-        x[j] = make_quad<DT>(v);
-        store_quad<DT>(static_cast<char*>(a.h) + base, row_off + c * ES, live && c < C, c + 4 > C,
-                       skip, x[j]);
+        for (int k = 0; k < 4; ++k) v[k] = x.at(j, k) + q.at(j, k);
+        x.v[j] = make_quad<DT>(v);
+        store_quad<DT>(static_cast<char*>(a.h) + p.base, p.off + c * ES, p.live && c < C,
+                       c + 4 > C, skip, x.v[j]);
       }
     }
 #pragma unroll
     for (int j = 0; j < M; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum += quad_at<DT>(x[j], k);
-    const float mean = row_sum<L>(sum, sm[0]) / (float)C;
+      for (int k = 0; k < 4; ++k) sum += x.at(j, k);
+    const float mean = row_sum<L>(sum, sm[turn][0]) / (float)C;
     float sq = 0.f;
 #pragma unroll
     for (int j = 0; j < M; ++j) {
-      const uint32_t c = c0 + j * L * 4;
+      const uint32_t c = p.c0 + j * L * 4;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float d = quad_at<DT>(x[j], k) - mean;
+        const float d = x.at(j, k) - mean;
         sq += c + k < C ? d * d : 0.f;
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<L>(sq, sm[1]) / (float)C + a.eps);
-    if (at.lane == 0 && live) {
-      a.mean[first + at.sub] = mean;
-      a.rstd[first + at.sub] = rstd;
+    const float rstd = 1.0f / sqrtf(row_sum<L>(sq, sm[turn][1]) / (float)C + a.eps);
+    if (at.lane == 0 && p.live) {
+      a.mean[p.row] = mean;
+      a.rstd[p.row] = rstd;
     }
 #pragma unroll
     for (int j = 0; j < M; ++j) {
-      const uint32_t c = c0 + j * L * 4;
-      float w[4], b[4] = {}, y[4];
-      load_quad_params(a.weight, a.param_dt, c, c < C, c + 4 > C, skip, w);
-      if (a.bias) load_quad_params(a.bias, a.param_dt, c, c < C, c + 4 > C, skip, b);
+      const uint32_t c = p.c0 + j * L * 4;
+      float y[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) y[k] = (quad_at<DT>(x[j], k) - mean) * rstd * w[k] + b[k];
-      store_quad<DT>(static_cast<char*>(a.y) + base, row_off + c * ES, live && c < C, c + 4 > C,
+      for (int k = 0; k < 4; ++k) y[k] = (x.at(j, k) - mean) * rstd * w[j][k] + b[j][k];
+      store_quad<DT>(static_cast<char*>(a.y) + p.base, p.off + c * ES, p.live && c < C, c + 4 > C,
                      skip, make_quad<DT>(y));
     }
-    if constexpr (L > 64) __syncthreads();  // sm is used again
+    x = nx;
+    q = nq;
   }
 }
 
@@ -214,73 +277,74 @@ __device__ __forceinline__ void put_column(const NormBwd& a, int64_t part, int s
 
 // Gradient of the rows and, over the rows a group takes, its column sums in
 // registers; at the end the groups of a workgroup join theirs (lanes of a wave
-// first, then the waves through LDS) and write one partial.
+// first, then the waves through LDS) and write one partial.  The weight stays in
+// registers (KEEP) up to three quads a lane, with four it is read again.  With 64
+// MiB operands, fold included: bf16 51 us at 64 columns (70 with the weight read
+// for every row and sums through ds_bpermute), 50 at 768 (59), 56 at 4096 (77);
+// fp32 49 at 768 (50), 51 at 4096 (71).  Loading the next round ahead as the
+// forward kernel does changed nothing here (three operands in flight and 16 waves
+// a CU cover the latency) and cost the registers.
 template <int DT, int L, int M, int B>
 __global__ __launch_bounds__(B, 4) void k_norm_bwd(NormBwd a) {
-  typedef typename Quad<DT>::Raw Raw;
   constexpr int R = B / L, COLS = L * M * 4, ES = DT == 0 ? 4 : 2;
-  __shared__ float sm[2][16];
+  constexpr bool KEEP = M < 4;
+  __shared__ float sm[2][2][16];
   __shared__ float cols[L <= 64 ? B / 64 * COLS : 1];
   const RowLane<L> at;
   const uint32_t C = (uint32_t)a.C;
   const int skip = (4 - (int)(C & 3)) & 3;
-  float gw[M][4] = {}, gb[M][4] = {};
-  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.T; r0 += (int64_t)gridDim.x * R) {
-    const int64_t first = r0 + at.wave_row, base = first * a.C * ES;
-    const bool live = first + at.sub < a.T;
-    uint32_t c0 = (uint32_t)at.lane * 4, row_off = (uint32_t)at.sub * C * ES;
-    // computed anew for every row: else the compiler keeps a 64-bit pointer
-    // per operand and quad across the loop instead of base + offset
-    asm volatile("" : "+v"(c0), "+v"(row_off));
-    Raw g[M], h[M], q[M];
+  const int64_t step = (int64_t)gridDim.x * R;
+  int64_t r0 = (int64_t)blockIdx.x * R;
+  float keep[KEEP ? M : 1][4], gw[M][4] = {}, gb[M][4] = {};
+  auto weight = [&](uint32_t c0, int j, float(&w)[4]) {
+    const uint32_t c = c0 + j * L * 4;
+    load_quad_params(a.weight, a.param_dt, c, c < C, c + 4 > C, skip, w);
+  };
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int j = 0; j < M; ++j) weight((uint32_t)at.lane * 4, j, keep[j]);
+  }
+  for (int turn = 0; r0 < a.T; r0 += step, turn ^= 1) {
+    const RowAt<DT, L> p(at, r0, a.T, a.C);
+    RowQuads<DT, L, M> g, h, q;
+    g.load(a.g_y, p.base, p.off, p.c0, C, skip, p.live);
+    h.load(a.h, p.base, p.off, p.c0, C, skip, p.live);
+    if (a.g_h) q.load(a.g_h, p.base, p.off, p.c0, C, skip, p.live);
+    const float mean = p.live ? a.mean[p.row] : 0.f;
+    const float rstd = p.live ? a.rstd[p.row] : 0.f;
+    float s[2] = {0.f, 0.f};  // of u, of u n
 #pragma unroll
     for (int j = 0; j < M; ++j) {
-      const uint32_t c = c0 + j * L * 4;
-      g[j] = load_quad<DT>(static_cast<const char*>(a.g_y) + base, row_off + c * ES, live && c < C,
-                           c + 4 > C, skip);
-      h[j] = load_quad<DT>(static_cast<const char*>(a.h) + base, row_off + c * ES, live && c < C,
-                           c + 4 > C, skip);
-      if (a.g_h)
-        q[j] = load_quad<DT>(static_cast<const char*>(a.g_h) + base, row_off + c * ES,
-                             live && c < C, c + 4 > C, skip);
-    }
-    const float mean = live ? a.mean[first + at.sub] : 0.f;
-    const float rstd = live ? a.rstd[first + at.sub] : 0.f;
-    float su = 0.f, sn = 0.f;
-#pragma unroll
-    for (int j = 0; j < M; ++j) {
-      const uint32_t c = c0 + j * L * 4;
       float w[4];
-      load_quad_params(a.weight, a.param_dt, c, c < C, c + 4 > C, skip, w);
+      if constexpr (!KEEP) weight(p.c0, j, w);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float v = quad_at<DT>(g[j], k), x = (quad_at<DT>(h[j], k) - mean) * rstd;
-        const float u = v * w[k];
-        su += u;
-        sn += u * x;
+        const float v = g.at(j, k), x = (h.at(j, k) - mean) * rstd;
+        const float u = v * (KEEP ? keep[KEEP ? j : 0][k] : w[k]);
+        s[0] += u;
+        s[1] += u * x;
         gw[j][k] += v * x;
         gb[j][k] += v;
       }
     }
-    su = row_sum<L>(su, sm[0]) / (float)C;
-    sn = row_sum<L>(sn, sm[1]) / (float)C;
+    row_sums<L>(s, sm[turn]);
+    const float su = s[0] / (float)C, sn = s[1] / (float)C;
 #pragma unroll
     for (int j = 0; j < M; ++j) {
-      const uint32_t c = c0 + j * L * 4;
+      const uint32_t c = p.c0 + j * L * 4;
       float w[4], o[4];
-      load_quad_params(a.weight, a.param_dt, c, c < C, c + 4 > C, skip, w);
+      if constexpr (!KEEP) weight(p.c0, j, w);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        o[k] = rstd * (quad_at<DT>(g[j], k) * w[k] - su -
-                       (quad_at<DT>(h[j], k) - mean) * rstd * sn);
+        o[k] = rstd * (g.at(j, k) * (KEEP ? keep[KEEP ? j : 0][k] : w[k]) - su -
+                       (h.at(j, k) - mean) * rstd * sn);
       if (a.g_h) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] += quad_at<DT>(q[j], k);
+        for (int k = 0; k < 4; ++k) o[k] += q.at(j, k);
       }
-      store_quad<DT>(static_cast<char*>(a.g_x) + base, row_off + c * ES, live && c < C, c + 4 > C,
-                     skip, make_quad<DT>(o));
+      store_quad<DT>(static_cast<char*>(a.g_x) + p.base, p.off + c * ES, p.live && c < C,
+                     c + 4 > C, skip, make_quad<DT>(o));
     }
-    if constexpr (L > 64) __syncthreads();  // sm is used again
   }
   if constexpr (L > 64) {
 #pragma unroll
@@ -302,9 +366,7 @@ __global__ __launch_bounds__(B, 4) void k_norm_bwd(NormBwd a) {
       for (int j = 0; j < M; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          float v = side ? gb[j][k] : gw[j][k];
-#pragma unroll
-          for (int m = L; m < 64; m <<= 1) v += __shfl_xor(v, m);
+          const float v = lanes_sum_across<L>(side ? gb[j][k] : gw[j][k]);
           if ((threadIdx.x & 63) < L) cols[wave * COLS + (at.lane + j * L) * 4 + k] = v;
         }
       __syncthreads();
@@ -454,37 +516,40 @@ __global__ __launch_bounds__(256) void k_norm_columns(NormBwd a) {
 }
 
 // Fold of the partial column sums part [parts][2][C] in a fixed order, in
-// fp64: 16 columns per workgroup from column col0 on, its 64 groups of 16 lanes
-// take every 64th part and are joined within each wave, then across the 16
-// waves; blockIdx.y 0: g_weight, 1: g_bias.
+// fp64: FOLD columns per workgroup from column col0 on, its 1024 / FOLD groups
+// of lanes take the parts in turn and are joined within each wave, then across
+// the 16 waves; blockIdx.y 0: g_weight, 1: g_bias.
+// (16, 32 and 64 columns: the backward of 4096 columns fp32 takes 53.7, 51.2 and
+// 51.9 us, of 768 48.7, 49.7 and 49.0.)
+constexpr int FOLD = 32;
 __global__ __launch_bounds__(1024) void k_norm_fold(NormBwd a, int64_t col0) {
-  __shared__ double sm[16][16];
-  const int lane = threadIdx.x & 15, slot = threadIdx.x >> 4;
-  const int64_t C = a.C, c = col0 + (int64_t)blockIdx.x * 16 + lane;
+  __shared__ double sm[16][FOLD];
+  const int lane = threadIdx.x & (FOLD - 1), slot = threadIdx.x / FOLD;
+  const int64_t C = a.C, c = col0 + (int64_t)blockIdx.x * FOLD + lane;
   double s = 0.0;
   if (c < C) {
 #pragma unroll 8
-    for (int64_t p = slot; p < a.parts; p += 64) s += (double)a.part[(p * 2 + blockIdx.y) * C + c];
+    for (int64_t p = slot; p < a.parts; p += 1024 / FOLD)
+      s += (double)a.part[(p * 2 + blockIdx.y) * C + c];
   }
-  s += __shfl_xor(s, 16);
-  s += __shfl_xor(s, 32);
-  if ((threadIdx.x & 63) < 16) sm[threadIdx.x >> 6][lane] = s;
+  s = lanes_sum_across<FOLD>(s);
+  if ((threadIdx.x & 63) < FOLD) sm[threadIdx.x >> 6][lane] = s;
   __syncthreads();
-  if (threadIdx.x >= 64) return;
-  const int q = threadIdx.x >> 4;
-  s = (sm[4 * q][lane] + sm[4 * q + 1][lane]) + (sm[4 * q + 2][lane] + sm[4 * q + 3][lane]);
-  s += __shfl_xor(s, 16);
-  s += __shfl_xor(s, 32);
-  if (threadIdx.x < 16 && c < C)
-    put_param(blockIdx.y ? a.g_bias : a.g_weight, a.param_dt, c, (float)s);
+  if (threadIdx.x >= FOLD || c >= C) return;
+  s = 0.0;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) s += sm[q][lane];
+  put_param(blockIdx.y ? a.g_bias : a.g_weight, a.param_dt, c, (float)s);
 }
 
 // ------------------------------------------------------------ launches
 // Lanes and quads per row, by the length of the row.
-enum NormRow { ROW_8x1, ROW_16x1, ROW_32x1, ROW_64x1, ROW_64x2, ROW_64x3, ROW_64x4, ROW_256x2,
-               ROW_256x3, ROW_256x4, ROW_512x3, ROW_512x4, ROW_1024x3, ROW_1024x4, ROW_WIDE };
-static const int norm_lanes[] = {8, 16, 32, 64, 64, 64, 64, 256, 256, 256, 512, 512, 1024, 1024};
-static const int norm_quads[] = {1, 1, 1, 1, 2, 3, 4, 2, 3, 4, 3, 4, 3, 4};
+enum NormRow { ROW_8x1, ROW_16x1, ROW_32x1, ROW_64x1, ROW_64x2, ROW_64x3, ROW_64x4, ROW_128x3,
+               ROW_256x2, ROW_256x3, ROW_512x2, ROW_512x3, ROW_1024x2, ROW_1024x3, ROW_1024x4,
+               ROW_WIDE };
+static const int norm_lanes[] = {8, 16, 32, 64, 64, 64, 64, 128, 256, 256, 512, 512, 1024, 1024,
+                                 1024};
+static const int norm_quads[] = {1, 1, 1, 1, 2, 3, 4, 3, 2, 3, 2, 3, 2, 3, 4};
 
 static NormRow norm_row(int64_t C) {
   if (C < 4) return ROW_WIDE;
@@ -500,38 +565,49 @@ static NormRow norm_row(int64_t C) {
   case ROW_64x1: F(64, 1, BS); break;                                                       \
   case ROW_64x2: F(64, 2, BS); break;                                                       \
   case ROW_64x3: F(64, 3, BS); break;                                                       \
-  case ROW_64x4: F(64, 4, BS); break;                                                       \
+  case ROW_64x4: F(64, 4, BS); break;                                                    \
+  case ROW_128x3: F(128, 3, 128); break;                                                    \
   case ROW_256x2: F(256, 2, 256); break;                                                    \
   case ROW_256x3: F(256, 3, 256); break;                                                    \
-  case ROW_256x4: F(256, 4, 256); break;                                                    \
+  case ROW_512x2: F(512, 2, 512); break;                                                    \
   case ROW_512x3: F(512, 3, 512); break;                                                    \
-  case ROW_512x4: F(512, 4, 512); break;                                                    \
+  case ROW_1024x2: F(1024, 2, 1024); break;                                                 \
   case ROW_1024x3: F(1024, 3, 1024); break;                                                 \
   case ROW_1024x4: F(1024, 4, 1024); break;
 
 constexpr int NORM_BWD_THREADS = 512;  // workgroups of the backward kernel, L <= 64
 
+// At most `most` workgroups for `need` rounds of one, all with as many rounds.
+static int64_t even_rounds(int64_t need, int64_t most) {
+  const int64_t rounds = (need + most - 1) / most;
+  return (need + rounds - 1) / rounds;
+}
+
 // Workgroups of the backward kernel, each leaving one partial: up to 1024
-// threads per CU.  Few rows are one workgroup's, which writes the parameters'
-// gradients itself: up to NORM_ALONE rounds of it (GPU time of 1, 2 and 4 rounds
-// in one launch, and of as many rows in two: 64 columns 3.8, 4.6, 5.4 and 5.1
-// us; 768 4.3, 6.3, 10.1 and 6.5; 4096 6.2, 9.0, 14.4 and 8.5; the second launch
-// costs the host 2.3 us).
+// threads per CU, and half for fp32 rows of three quads a lane, which have as
+// many bytes in flight and are more columns to fold (1500 columns 55 us instead
+// of 62, 2500 52 and 61; bf16 64 and 67 the other way about).  Few rows are one
+// workgroup's, which writes the parameters' gradients itself: up to NORM_ALONE
+// rounds of it (GPU time of 1, 2 and 4 rounds in one launch, and of as many rows
+// in two: 768 columns 4.3, 6.3, 10.1 and 6.5 us; 4096 6.2, 9.0, 14.4 and 8.5; the
+// second launch costs the host 2.3 us).
 constexpr int NORM_ALONE = 2;
-int64_t norm_parts(int64_t T, int64_t C) {
+int64_t norm_parts(int64_t T, int64_t C, int dtype) {
   const NormRow r = norm_row(C);
   if (r == ROW_WIDE) return (T + 31) / 32 < 256 ? (T + 31) / 32 : 256;
   const int L = norm_lanes[r], B = L <= 64 ? NORM_BWD_THREADS : L;
-  const int64_t need = (T + B / L - 1) / (B / L), most = 256 * 1024 / B;
-  if (T > 0 && need <= NORM_ALONE) return 1;
-  return need < most ? need : most;
+  const int threads = dtype == 0 && L > 64 && L <= 512 && norm_quads[r] == 3 ? 512 : 1024;
+  const int64_t need = (T + B / L - 1) / (B / L), most = 256 * threads / B;
+  if (T == 0) return 0;
+  if (need <= NORM_ALONE) return 1;
+  return even_rounds(need, most);
 }
 
 hipError_t launch_norm_forward(const NormFwd& a, int dtype, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
 #define HLQ_F(L, M, B)                                                                      \
   do {                                                                                      \
-    const dim3 g = rows_grid((a.T + B / L - 1) / (B / L));                                  \
+    const dim3 g((unsigned)even_rounds((a.T + B / L - 1) / (B / L), 256 * 2048 / B));       \
     if (dtype == 0) return launch(k_norm_fwd<0, L, M, B>, g, B, s, a);                      \
     return launch(k_norm_fwd<1, L, M, B>, g, B, s, a);                                      \
   } while (0)
@@ -571,7 +647,7 @@ hipError_t launch_norm_backward(const NormBwd& a, int dtype, hipStream_t s) {
   // 2^24 columns a launch (a launch holds fewer than 2^32 threads)
   for (int64_t c = 0; c < a.C && e == hipSuccess; c += 1 << 24) {
     const int64_t n = a.C - c < (1 << 24) ? a.C - c : 1 << 24;
-    e = launch(k_norm_fold, dim3(cdiv(n, 16), a.g_bias ? 2 : 1), 1024, s, a, c);
+    e = launch(k_norm_fold, dim3(cdiv(n, FOLD), a.g_bias ? 2 : 1), 1024, s, a, c);
   }
   return e;
 }

@@ -125,19 +125,75 @@ __device__ __forceinline__ void load_params(const void* base, int dt, int64_t c,
 }
 
 // ------------------------------------------------------------ reductions
-// Sum over groups of W neighbouring lanes (W a power of two up to 64); every
-// lane gets its group's sum, added in the same order whatever the lane.
-template <int W, typename V>
-__device__ __forceinline__ V lanes_sum(V v) {
-#pragma unroll
-  for (int m = W / 2; m >= 1; m >>= 1) v += __shfl_xor(v, m);
-  return v;
+// The 32-bit values of a lane and of the lane at distance M (one of them p, the
+// other q): DPP for M up to 8, a swap of registers' halves for 16 and 32.
+template <int M>
+__device__ __forceinline__ void lanes_meet(uint32_t v, uint32_t& p, uint32_t& q) {
+  p = v;
+  if constexpr (M == 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    p = r[0];
+    q = r[1];
+  } else if constexpr (M == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    p = r[0];
+    q = r[1];
+  } else if constexpr (M == 8) {  // rotation of 16 by 8
+    q = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x128, 0xF, 0xF, true);
+  } else if constexpr (M == 4) {  // shift of 16 left by 4 for quads 0 and 2, right for 1 and 3
+    const int up = __builtin_amdgcn_update_dpp(0, (int)v, 0x104, 0xF, 0x5, false);
+    q = (uint32_t)__builtin_amdgcn_update_dpp(up, (int)v, 0x114, 0xF, 0xA, false);
+  } else {
+    q = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, M == 2 ? 0x4E : 0xB1, 0xF, 0xF, true);
+  }
 }
 
-__device__ __forceinline__ float lanes_max(float v) {
+// One stage of a butterfly: f (symmetric) of a lane's value and of the one at
+// distance M.
+template <int M, typename V, typename F>
+__device__ __forceinline__ V lanes_stage(V v, F f) {
+  constexpr int WORDS = sizeof(V) / 4;
+  uint32_t w[WORDS], p[WORDS], q[WORDS];
+  __builtin_memcpy(w, &v, sizeof v);
 #pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
+  for (int i = 0; i < WORDS; ++i) lanes_meet<M>(w[i], p[i], q[i]);
+  V a, b;
+  __builtin_memcpy(&a, p, sizeof v);
+  __builtin_memcpy(&b, q, sizeof v);
+  return f(a, b);
+}
+
+// Butterfly over groups of W neighbouring lanes (W a power of two up to 64);
+// every lane gets its group's result, the same bits.  All lanes of a group are
+// active.  No LDS instructions: a stage is a few cycles, through ds_bpermute
+// about a hundred.
+template <int W, typename V, typename F>
+__device__ __forceinline__ V lanes_join(V v, F f) {
+  if constexpr (W >= 64) v = lanes_stage<32>(v, f);
+  if constexpr (W >= 32) v = lanes_stage<16>(v, f);
+  if constexpr (W >= 16) v = lanes_stage<8>(v, f);
+  if constexpr (W >= 8) v = lanes_stage<4>(v, f);
+  if constexpr (W >= 4) v = lanes_stage<2>(v, f);
+  if constexpr (W >= 2) v = lanes_stage<1>(v, f);
   return v;
+}
+template <int W, typename V>
+__device__ __forceinline__ V lanes_sum(V v) {
+  return lanes_join<W>(v, [](V p, V q) { return p + q; });
+}
+// Sum over the lanes of a wave that are L apart (8, 16 or 32); every lane gets
+// its sum.
+template <int L, typename V>
+__device__ __forceinline__ V lanes_sum_across(V v) {
+  const auto add = [](V p, V q) { return p + q; };
+  if constexpr (L <= 8) v = lanes_stage<8>(v, add);
+  if constexpr (L <= 16) v = lanes_stage<16>(v, add);
+  if constexpr (L <= 32) v = lanes_stage<32>(v, add);
+  return v;
+}
+template <int W = 64>
+__device__ __forceinline__ float lanes_max(float v) {
+  return lanes_join<W>(v, [](float p, float q) { return fmaxf(p, q); });
 }
 
 // Over a workgroup of W threads (a multiple of 64, up to 1024).  sm holds
@@ -150,19 +206,6 @@ __device__ __forceinline__ V group_sum(V v, V* sm) {
     __syncthreads();
     v = sm[threadIdx.x & (W / 64 - 1)];
     v = lanes_sum<W / 64>(v);
-  }
-  return v;
-}
-
-template <int W>
-__device__ __forceinline__ float group_max(float v, float* sm) {
-  v = lanes_max(v);
-  if constexpr (W > 64) {
-    if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = sm[threadIdx.x & (W / 64 - 1)];
-#pragma unroll
-    for (int m = W / 128; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
   }
   return v;
 }

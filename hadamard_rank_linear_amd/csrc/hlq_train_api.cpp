@@ -109,7 +109,7 @@ hlq_status hlq_layer_norm_forward(const void* x, const void* residual, int dtype
 
 size_t hlq_layer_norm_backward_workspace_size(int64_t T, int64_t C, int dtype) {
   if (!norm_shape_ok(T, C) || !dtype_ok(dtype)) return 0;
-  return (size_t)hlq::norm_parts(T, C) * 2 * (size_t)C * 4;
+  return (size_t)hlq::norm_parts(T, C, dtype) * 2 * (size_t)C * 4;
 }
 
 hlq_status hlq_layer_norm_backward(const void* g_y, const void* h, const void* g_h, int dtype,
@@ -129,7 +129,7 @@ hlq_status hlq_layer_norm_backward(const void* g_y, const void* h, const void* g
                                         hlq_layer_norm_backward_workspace_size(T, C, dtype));
   if (st != HLQ_OK) return st;
   const hlq::NormBwd a = {g_y, h, g_h,      mean,   rstd, weight, param_dtype, T, C,
-                          hlq::norm_parts(T, C),
+                          hlq::norm_parts(T, C, dtype),
                           g_x, g_weight, g_bias, static_cast<float*>(workspace)};
   HLQ_TRY(hlq::launch_norm_backward(a, dtype, static_cast<hipStream_t>(stream)));
   return HLQ_OK;

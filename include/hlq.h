@@ -405,8 +405,9 @@ hlq_status hlq_lqs_select(const double* stats, double threshold, int* gx_mode,
  * packed buffer, start anywhere); the workspace still needs 16 bytes.  A
  * count of rows, tokens or tensors may be zero, and the pointers of the
  * operands that are then empty may be NULL.  Every sum is kept in fp32 or
- * fp64 in an order fixed by the sizes alone, so results are reproducible; an
- * output in bf16 is rounded once, to nearest even.
+ * fp64 in an order fixed by the sizes and, for rows of logits, by where in 16
+ * bytes a row starts, so results are reproducible; an output in bf16 is rounded
+ * once, to nearest even.
  * ------------------------------------------------------------------------ */
 
 /*
