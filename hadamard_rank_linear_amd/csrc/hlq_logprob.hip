@@ -151,25 +151,29 @@ struct OutRow {
 // keeping its elements in a register each from one use to the other.
 __device__ __forceinline__ void keep_packed(u32x4& r) { asm volatile("" : "+v"(r)); }
 
-// Maximum and sum relative to it of P pieces, joined to a thread's running
-// (m, s).
+// Maximum and sum relative to it of P pieces at positions e0, e0 + step, ...,
+// joined to a thread's running (m, s).  Pieces past the row's end cost nothing
+// where the whole wave's are.
 template <int DT, int P>
-__device__ __forceinline__ void accumulate(u32x4 (&r)[P], const LogitArgs& a, float& m,
-                                           float& s) {
+__device__ __forceinline__ void accumulate(u32x4 (&r)[P], uint32_t e0, uint32_t step, uint32_t end,
+                                           const LogitArgs& a, float& m, float& s) {
   constexpr int N = Piece<DT>::N;
   float top = m;
 #pragma unroll
   for (int j = 0; j < P; ++j)
+    if (e0 + j * step < end) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) top = fmaxf(top, piece_at<DT>(r[j], k));
+      for (int k = 0; k < N; ++k) top = fmaxf(top, piece_at<DT>(r[j], k));
+    }
   const float ref = ref_of(top);
   float t = s * exp_scaled(m - ref, a.c_hi, a.c_lo);
 #pragma unroll
-  for (int j = 0; j < P; ++j) {
-    keep_packed(r[j]);
+  for (int j = 0; j < P; ++j)
+    if (e0 + j * step < end) {
+      keep_packed(r[j]);
 #pragma unroll
-    for (int k = 0; k < N; ++k) t += exp_scaled(piece_at<DT>(r[j], k) - ref, a.c_hi, a.c_lo);
-  }
+      for (int k = 0; k < N; ++k) t += exp_scaled(piece_at<DT>(r[j], k) - ref, a.c_hi, a.c_lo);
+    }
   m = top;
   s = t;
 }
@@ -231,7 +235,7 @@ __global__ __launch_bounds__(W) void k_logprob(LogitArgs a) {
       u32x4 r[P];
 #pragma unroll
       for (int j = 0; j < P; ++j) r[j] = x.load(e0 + j * W * N);
-      accumulate<DT, P>(r, a, m, s);
+      accumulate<DT, P>(r, e0, W * N, x.end, a, m, s);
     }
     join_stats<W>(a, sm, m, s);
     if (threadIdx.x == 0) lp = (float)logprob_of(xt, m, s, a.scale);
@@ -284,7 +288,7 @@ __device__ __forceinline__ void row_gradient(const LogitArgs& a, int64_t row, ui
 #pragma unroll
     for (int j = 0; j < P; ++j) {
       const uint32_t e = e0 + j * W * N;
-      g.store(e, gradient_piece<DT>(r[j], e, x.head + t, a.c, f, k_s, m));
+      if (e < x.end) g.store(e, gradient_piece<DT>(r[j], e, x.head + t, a.c, f, k_s, m));
     }
   }
 }
@@ -365,7 +369,7 @@ __global__ __launch_bounds__(W, 4) void k_policy_regs(LogitArgs a, PolicyArgs p)
     xt = x.element((uint32_t)t);
 #pragma unroll
     for (int j = 0; j < P; ++j) r[j] = x.load((threadIdx.x + j * W) * N);
-    accumulate<DT, P>(r, a, m, s);
+    accumulate<DT, P>(r, threadIdx.x * N, W * N, x.end, a, m, s);
     join_stats<W>(a, sm, m, s);
   }
   const float f = policy_row(a, p, row, q, live, xt, m, s, &sg);
@@ -379,32 +383,63 @@ __global__ __launch_bounds__(W, 4) void k_policy_regs(LogitArgs a, PolicyArgs p)
   for (int j = 0; j < P; ++j) {
     keep_packed(r[j]);
     const uint32_t e = (threadIdx.x + j * W) * N;
-    g.store(e, gradient_piece<DT>(r[j], e, x.head + (uint32_t)t, a.c, f, k_s, m));
+    if (e < x.end)
+      g.store(e, gradient_piece<DT>(r[j], e, x.head + (uint32_t)t, a.c, f, k_s, m));
   }
 }
 
-// Longer rows are read twice, the second time partly from cache.
-template <int DT, bool ST, int W, int P>
-__global__ __launch_bounds__(W) void k_policy_long(LogitArgs a, PolicyArgs p) {
+// Longer rows: the first W * H pieces are held, the others are read twice, the
+// second time from the last-level cache (524 x 100003 fp32, H 0, 8 and 16: 122, 98
+// and 96 us; 400 x 131072: 117, 91 and 87).
+template <int DT, int W, int P, int H>
+__global__ __launch_bounds__(W, 4) void k_policy_long(LogitArgs a, PolicyArgs p) {
   constexpr int N = Piece<DT>::N;
+  constexpr uint32_t REST = W * H * N;
   __shared__ float sm[2][16], sg;
   const int64_t row = a.row0 + blockIdx.x, t = a.targets[row];
   const PolicyToken q = policy_load(p, row);
   const bool live = t >= 0 && t < a.V && q.weight != 0.f;
+  const Row<DT, false> x = row_of<DT, false>(a, row);
+  const Row<DT, true> once = row_of<DT, true>(a, row);
+  u32x4 held[H];
   float m = -__builtin_huge_valf(), s = 0.f, xt = 0.f;
   if (live) {
-    const Row<DT, ST> x = row_of<DT, ST>(a, row);
     xt = x.element((uint32_t)t);
-    for (uint32_t e0 = threadIdx.x * N; e0 < x.end; e0 += W * N * P) {
+    for (uint32_t e0 = REST + threadIdx.x * N; e0 < x.end; e0 += W * N * P) {
       u32x4 r[P];
 #pragma unroll
       for (int j = 0; j < P; ++j) r[j] = x.load(e0 + j * W * N);
-      accumulate<DT, P>(r, a, m, s);
+      accumulate<DT, P>(r, e0, W * N, x.end, a, m, s);
     }
+#pragma unroll
+    for (int j = 0; j < H; ++j) held[j] = once.load((threadIdx.x + j * W) * N);
+    accumulate<DT, H>(held, threadIdx.x * N, W * N, x.end, a, m, s);
     join_stats<W>(a, sm, m, s);
   }
   const float f = policy_row(a, p, row, q, live, xt, m, s, &sg);
-  row_gradient<DT, W, P>(a, row, (uint32_t)t, f, m, s);
+  const OutRow<DT, true> g(a, row, x.head);
+  if (f == 0.f || s == 0.f) {
+    zero_row<DT, true, W>(g);
+    return;
+  }
+  const float k_s = -f / s;
+  const uint32_t at = x.head + (uint32_t)t;
+#pragma unroll
+  for (int j = 0; j < H; ++j) {
+    keep_packed(held[j]);
+    const uint32_t e = (threadIdx.x + j * W) * N;
+    g.store(e, gradient_piece<DT>(held[j], e, at, a.c, f, k_s, m));
+  }
+  for (uint32_t e0 = REST + threadIdx.x * N; e0 < x.end; e0 += W * N * P) {
+    u32x4 r[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) r[j] = x.load(e0 + j * W * N);
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      const uint32_t e = e0 + j * W * N;
+      if (e < x.end) g.store(e, gradient_piece<DT>(r[j], e, at, a.c, f, k_s, m));
+    }
+  }
 }
 
 __global__ __launch_bounds__(256) void k_policy(PolicyArgs p) {
@@ -533,19 +568,21 @@ __global__ __launch_bounds__(1024) void k_preference_small(PrefArgs p) {
 // Threads per row of n pieces: a wave for short rows, the whole of a
 // workgroup's 1024 for long ones (4096 x 128256 bf16 scored with 64, 256, 512
 // and 1024 threads a row: 193, 188, 183 and 176 us; 8190 x 32000: 104, 97, 90
-// and 95; 8190 x 1000: 12, 18, 25 and 44), and more where the rows are too few
+// and 95; 8190 x 1000: 12, 18, 25 and 44; 15728 x 3000 with 64 and 256: 20 and
+// 27), and more where the rows are too few
 // to fill the chip (3 x 32003: 18.8, 8.9, 7.9 and 7.8).
 static int score_threads(int64_t T, int64_t n) {
   if (T < 256) return n <= 64 ? 64 : (n <= 512 ? 256 : 1024);
-  return n <= 256 ? 64 : (n <= 2048 ? 256 : 512);
+  return n <= 600 ? 64 : (n <= 2048 ? 256 : 512);
 }
 
 // The same for the gradient (4096 x 128256 bf16 with 64, 256, 512 and 1024
 // threads: 430, 420, 413 and 394 us; 8190 x 32000: 222, 207, 194 and 177;
-// 8190 x 1000: 10, 11, 14 and 23).
+// 8190 x 1000: 10, 11, 14 and 23; 12790 x 4099 fp32 with 256, 512 and 1024: 78, 75
+// and 103).
 static int grad_threads(int64_t T, int64_t n) {
   if (T < 256) return n <= 64 ? 64 : (n <= 512 ? 256 : 1024);
-  return n <= 256 ? 64 : (n <= 1024 ? 256 : 1024);
+  return n <= 256 ? 64 : (n <= 1024 ? 256 : n <= 2560 ? 512 : 1024);
 }
 
 // Pieces of a row, at most: one more where rows do not start at a boundary.
@@ -596,6 +633,7 @@ hipError_t launch_logprob_grad(LogitArgs a, int dtype, hipStream_t s) {
   switch (grad_threads(a.T, row_pieces(a, dtype))) {
     case 64: return grad_rows<64, 2>(a, dtype, s);
     case 256: return grad_rows<256, 2>(a, dtype, s);
+    case 512: return grad_rows<512, 4>(a, dtype, s);
     default: return grad_rows<1024, 4>(a, dtype, s);
   }
 }
@@ -613,23 +651,23 @@ static hipError_t policy_rows(LogitArgs& a, const PolicyArgs& p, int dtype, hipS
 
 static hipError_t policy_long_rows(LogitArgs& a, const PolicyArgs& p, int dtype, hipStream_t s) {
   return for_rows(a, [&](dim3 g) {
-    if (dtype == 0)
-      return a.stream ? launch(k_policy_long<0, true, 1024, 4>, g, 1024, s, a, p)
-                      : launch(k_policy_long<0, false, 1024, 4>, g, 1024, s, a, p);
-    return a.stream ? launch(k_policy_long<1, true, 1024, 4>, g, 1024, s, a, p)
-                    : launch(k_policy_long<1, false, 1024, 4>, g, 1024, s, a, p);
+    return dtype == 0 ? launch(k_policy_long<0, 1024, 4, 16>, g, 1024, s, a, p)
+                      : launch(k_policy_long<1, 1024, 4, 16>, g, 1024, s, a, p);
   });
 }
 
 hipError_t launch_policy_logits(LogitArgs a, const PolicyArgs& p, int dtype,
                                 hipStream_t s) {
+  // threads and pieces a thread for rows of n pieces; more threads where there
+  // are fewer rows than CUs (3276 x 32000 bf16 with 256 x 16 and 1024 x 4: 81
+  // and 75 us; 15728 x 3000 with 64 x 8 and 256 x 4: 44 and 49, but 11520 x 2048
+  // fp32 43 and 38)
   const int64_t n = row_pieces(a, dtype);
-  const bool few = a.T < 256;  // fewer rows than CUs: more threads a row
+  const bool few = a.T < 256;
   hipError_t e;
   if (n <= 256 && !(few && n > 64)) e = policy_rows<64, 4>(a, p, dtype, s);
   else if (n <= 1024 && !(few && n > 256)) e = policy_rows<256, 4>(a, p, dtype, s);
   else if (n <= 2048 && !few) e = policy_rows<256, 8>(a, p, dtype, s);
-  else if (n <= 4096 && !few) e = policy_rows<256, 16>(a, p, dtype, s);
   else if (n <= 4096) e = policy_rows<1024, 4>(a, p, dtype, s);
   else if (n <= 8192) e = policy_rows<512, 16>(a, p, dtype, s);
   else if (n <= 12288) e = policy_rows<1024, 12>(a, p, dtype, s);
