@@ -278,16 +278,17 @@ __device__ __forceinline__ void put_column(const NormBwd& a, int64_t part, int s
 // Gradient of the rows and, over the rows a group takes, its column sums in
 // registers; at the end the groups of a workgroup join theirs (lanes of a wave
 // first, then the waves through LDS) and write one partial.  The weight stays in
-// registers (KEEP) up to three quads a lane, with four it is read again.  With 64
-// MiB operands, fold included: bf16 51 us at 64 columns (70 with the weight read
-// for every row and sums through ds_bpermute), 50 at 768 (59), 56 at 4096 (77);
-// fp32 49 at 768 (50), 51 at 4096 (71).  Loading the next round ahead as the
-// forward kernel does changed nothing here (three operands in flight and 16 waves
-// a CU cover the latency) and cost the registers.
+// registers (KEEP), except for four quads a lane in fp32, where there is no room
+// and it is read again.  With 64 MiB operands, fold included: bf16 51 us at 64
+// columns (70 with the weight read for every row and sums through ds_bpermute), 50
+// at 768 (59), 49 at 1024 (59), 56 at 4096 (77); fp32 49 at 768 (50), 51 at 4096
+// (71).  Loading the next round ahead as the forward kernel does changed nothing
+// here (three operands in flight and 16 waves a CU cover the latency) and cost the
+// registers.
 template <int DT, int L, int M, int B>
 __global__ __launch_bounds__(B, 4) void k_norm_bwd(NormBwd a) {
   constexpr int R = B / L, COLS = L * M * 4, ES = DT == 0 ? 4 : 2;
-  constexpr bool KEEP = M < 4;
+  constexpr bool KEEP = M < 4 || DT == 1;
   __shared__ float sm[2][2][16];
   __shared__ float cols[L <= 64 ? B / 64 * COLS : 1];
   const RowLane<L> at;
@@ -543,7 +544,10 @@ __global__ __launch_bounds__(1024) void k_norm_fold(NormBwd a, int64_t col0) {
 }
 
 // ------------------------------------------------------------ launches
-// Lanes and quads per row, by the length of the row.
+// Lanes and quads per row, by the length of the row.  A wave has a row up to 1024
+// columns, without a barrier (forward of 1000 bf16 columns with 64 x 4 and 128 x 2:
+// 46 and 51 us); above, more lanes rather than a fourth quad (8192 columns fp32 with
+// 512 x 4 and 1024 x 2: 48 and 45), which the backward kernel has no registers for.
 enum NormRow { ROW_8x1, ROW_16x1, ROW_32x1, ROW_64x1, ROW_64x2, ROW_64x3, ROW_64x4, ROW_128x3,
                ROW_256x2, ROW_256x3, ROW_512x2, ROW_512x3, ROW_1024x2, ROW_1024x3, ROW_1024x4,
                ROW_WIDE };
@@ -584,13 +588,14 @@ static int64_t even_rounds(int64_t need, int64_t most) {
 }
 
 // Workgroups of the backward kernel, each leaving one partial: up to 1024
-// threads per CU, and half for fp32 rows of three quads a lane, which have as
-// many bytes in flight and are more columns to fold (1500 columns 55 us instead
-// of 62, 2500 52 and 61; bf16 64 and 67 the other way about).  Few rows are one
-// workgroup's, which writes the parameters' gradients itself: up to NORM_ALONE
-// rounds of it (GPU time of 1, 2 and 4 rounds in one launch, and of as many rows
-// in two: 768 columns 4.3, 6.3, 10.1 and 6.5 us; 4096 6.2, 9.0, 14.4 and 8.5; the
-// second launch costs the host 2.3 us).
+// threads per CU, which all run at once (so not evened out as above: 512 of them
+// take ViT-B's 1576 rounds in 19.8 us, 394 in 21.7), and half for fp32 rows of
+// three quads a lane, which have as many bytes in flight and are more columns to
+// fold (1500 columns 55 us instead of 62, 2500 52 and 61; bf16 64 and 67 the other
+// way about).  Few rows are one workgroup's, which writes the parameters'
+// gradients itself: up to NORM_ALONE rounds of it (GPU time of 1, 2 and 4 rounds
+// in one launch, and of as many rows in two: 768 columns 4.0, 5.2, 7.5 and 6.0 us;
+// 4096 4.4, 5.5, 7.6 and 6.7; the second launch costs the host 2.3 us).
 constexpr int NORM_ALONE = 2;
 int64_t norm_parts(int64_t T, int64_t C, int dtype) {
   const NormRow r = norm_row(C);
@@ -600,7 +605,7 @@ int64_t norm_parts(int64_t T, int64_t C, int dtype) {
   const int64_t need = (T + B / L - 1) / (B / L), most = 256 * threads / B;
   if (T == 0) return 0;
   if (need <= NORM_ALONE) return 1;
-  return even_rounds(need, most);
+  return need < most ? need : most;
 }
 
 hipError_t launch_norm_forward(const NormFwd& a, int dtype, hipStream_t s) {

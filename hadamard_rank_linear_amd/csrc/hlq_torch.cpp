@@ -6,7 +6,8 @@
 // of small tensors, where the work on the GPU takes 5 to 10 us.  The same steps
 // written in Python (with ctypes, as the linear layer's entry points are) took
 // the host 17 to 23 us per call and 185 us for the clipping of 146 tensors,
-// longer than the kernels run; here they take 5 to 7 and 20 us, kernel launches included.
+// longer than the kernels run; here they take 4 to 6 and 12 us, kernel launches
+// included.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
