@@ -189,6 +189,29 @@ def test_layer_norm_backward(T, C, name, param):
     _check_norm_backward(s, name, False, False, 1, param)
 
 
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("T,C", [(70001, 9), (9000, 200), (6000, 600), (5001, 1000), (4500, 1030),
+                                 (2100, 2050)])
+def test_layer_norm_of_many_rows(T, C, name):
+    """More rows than the launch's workgroups take at once, lanes past the last
+    row and past a row's end."""
+    _say(f"norm T={T} C={C} {name}")
+    s = _norm_case(T, C, name, "f32", T + C)
+    _check_norm_forward(s, name, True, True, 1)
+    _check_norm_forward(s, name, False, False, 0)
+    _check_norm_backward(s, name, True, True, 1)
+    _check_norm_backward(s, name, False, False, 0)
+
+
+@pytest.mark.parametrize("C", [8, 64, 770, 2048, 4100, 16384, 17001])
+def test_layer_norm_backward_of_few_rows(C):
+    # one workgroup's rounds, and one row more than they take
+    for T in (1, 2, 3, 17, 33):
+        _say(f"norm backward T={T} C={C}")
+        s = _norm_case(T, C, "bf16", "bf16", T + C)
+        _check_norm_backward(s, "bf16", False, T % 2 == 0, 0, "bf16")
+
+
 def test_layer_norm_of_no_rows():
     torch, h = _torch(), _h()
     _say("norm of no rows")
@@ -440,6 +463,17 @@ def test_policy_loss(T, V, name):
         t[1] = -100
     _check_policy(x, t, name, 1.0, 0.05, True, T + V)
     _check_policy(x, t, name, 1.25, 0.0, False, T + V + 1, offset=1, pitch=1)
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V", [(300, 2100), (300, 4099), (260, 4801), (257, 9001), (257, 17003)])
+def test_logits_of_more_rows_than_units(T, V, name):
+    # other threads per row than for the few rows above
+    _say(f"logits T={T} V={V} {name}")
+    x, t = _logits(T, V, name, T + V)
+    t[2] = -100
+    _check_logprob(x, t, name, 0.9, offset=1)
+    _check_policy(x, t, name, 1.0, 0.05, True, T + V, offset=3)
 
 
 def test_policy_loss_of_masked_tokens():
