@@ -609,7 +609,8 @@ def hlq_token_logprob_forward(logits, targets, scale=1.0, stream=None):
 def hlq_token_logprob_backward(g_logprob, logits, targets, stats, scale=1.0, g_x=None,
                                stream=None):
     """Gradient [T, V] of logits from that of the log probabilities
-    (:func:`hlq_token_logprob_forward`'s), in the type of logits."""
+    (:func:`hlq_token_logprob_forward`'s), in the type of logits.  ``g_x`` may
+    be ``logits``: the gradient takes their place."""
     return _native.token_logprob_backward(g_logprob, logits, targets, stats, scale, g_x, stream)
 
 
@@ -633,7 +634,8 @@ def hlq_policy_loss_logits(logits, targets, old_logprob, advantage, weight=None,
     """:func:`hlq_token_logprob_forward`, :func:`hlq_policy_loss` and
     :func:`hlq_token_logprob_backward` in one pass over logits [T, V]: returns
     (sums [3], logprob [T], g_x [T, V]).  Tokens whose weight is 0 or whose
-    target is ignored do not count; their rows are not read."""
+    target is ignored do not count; their rows are not read.  ``g_x`` may be
+    ``logits``: the gradient takes their place."""
     return _native.policy_loss_logits(logits, targets, old_logprob, advantage, weight,
                                       ref_logprob, scale, clip_low, clip_high, kl_coef, g_x,
                                       workspace, stream)

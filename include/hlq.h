@@ -477,7 +477,8 @@ hlq_status hlq_token_logprob_forward(const void* logits, int dtype, int64_t ld,
  * the softmax taken from stats.
  *   g_logprob [T] f32.  Rows whose g_logprob is zero, whose target is ignored
  *            or which hold nothing but -inf get zeros, and are not read.
- *   g_x      T rows of V elements out, dtype, row t at element t * g_ld.
+ *   g_x      T rows of V elements out, dtype, row t at element t * g_ld; may be
+ *            logits itself (g_ld = ld), no other overlap.
  * One launch.  Errors as above (HLQ_ERR_SHAPE also for g_ld < V).
  */
 hlq_status hlq_token_logprob_backward(const float* g_logprob, const void* logits, int dtype,
@@ -514,7 +515,8 @@ hlq_status hlq_policy_loss(const float* logprob, const float* old_logprob,
  * in one pass over the logits.
  *   logprob  [T] f32 out; 0 where the weight is 0 or the target is ignored
  *            (such a token does not count in the loss, its row is not read).
- *   g_x      T rows of V elements out: the gradient of the loss.
+ *   g_x      T rows of V elements out: the gradient of the loss; may be logits
+ *            itself (g_ld = ld), no other overlap.
  * The other arguments, the workspace and the errors as there.
  */
 hlq_status hlq_policy_loss_logits(const void* logits, int dtype, int64_t ld,

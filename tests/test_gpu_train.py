@@ -476,6 +476,46 @@ def test_logits_of_more_rows_than_units(T, V, name):
     _check_policy(x, t, name, 1.0, 0.05, True, T + V, offset=3)
 
 
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V", [(5, 3), (40, 1001), (300, 4099), (3, 65541), (2, 140001)])
+def test_logits_gradient_in_place(T, V, name):
+    # the gradient may take the place of the logits: the same bits
+    torch, h = _torch(), _h()
+    _say(f"gradient in place T={T} V={V} {name}")
+    x, t = _logits(T, V, name, T + V)
+    t[1] = -100
+    x, t = _dev(x, name, 1), t.cuda()
+    lp, stats = h.hlq_token_logprob_forward(x, t)
+    adv = torch.ones(T, device="cuda") - 2.0 * (torch.arange(T, device="cuda") % 2)
+    for f in (lambda v, g: h.hlq_token_logprob_backward(adv, v, t, stats, g_x=g),
+              lambda v, g: h.hlq_policy_loss_logits(v, t, lp, adv, g_x=g)[2]):
+        want = f(x, None)
+        own = _dev(x.cpu(), name, 1)
+        got = f(own, own)
+        torch.cuda.synchronize()
+        assert got.data_ptr() == own.data_ptr() and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+def test_logits_past_the_cache_equal_their_parts(name):
+    """Logits of more than 96 MB take non-temporal accesses; parts of them,
+    with as many threads per row, do not: the same bits."""
+    torch, h = _torch(), _h()
+    T, V = 1203, 50257
+    _say(f"T={T} V={V} {name}")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((T, V), generator=g, device="cuda").mul_(2.5).to(_dt(name))
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    old = torch.randn(T, generator=g, device="cuda") - 12.0
+    adv = torch.randn(T, generator=g, device="cuda")
+    whole = h.hlq_token_logprob_forward(x, t) + h.hlq_policy_loss_logits(x, t, old, adv)[1:]
+    for a in range(0, T, 401):
+        b = a + 401
+        part = h.hlq_token_logprob_forward(x[a:b], t[a:b]) + \
+            h.hlq_policy_loss_logits(x[a:b], t[a:b], old[a:b], adv[a:b])[1:]
+        assert all(torch.equal(p, w[a:b]) for p, w in zip(part, whole))
+
+
 def test_policy_loss_of_masked_tokens():
     torch, h = _torch(), _h()
     _say("policy: masked tokens hold anything")
@@ -621,6 +661,25 @@ def test_clip_grad_norm(sizes, kind, offset):
                 _within(_np(a), ref, tol + HALF[n] * (np.abs(ref) + tol) + 1e-38, "clipped")
             assert torch.equal(a, b)
             assert max_norm <= want or torch.equal(a, v)      # a factor of one changes nothing
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+def test_clip_past_the_cache(kind):
+    # more than 96 MB: non-temporal accesses, workgroups that take several chunks
+    torch, h = _torch(), _h()
+    _say(f"clip of 150 MB, kind {kind}")
+    g = torch.Generator(device="cuda").manual_seed(7)
+    v = [torch.randn(n, generator=g, device="cuda").mul_(1e-2).to(_dt(d))
+         for n, d in ((30_000_001, "f32"), (7, "bf16"), (15_000_003, "bf16"), (5, "f32"))]
+    d = [w.double() for w in v]
+    want = sum((w * w).sum() for w in d).sqrt() if kind == 0 else max(w.abs().max() for w in d)
+    norm = h.hlq_clip_grad_norm(v, 1e-3, kind)
+    torch.cuda.synchronize()
+    assert abs(norm.item() / want.item() - 1) < 1e-12      # 4.5e7 fp64 additions, in trees
+    f = 1e-3 / (want + 1e-6)
+    for got, w in zip(v, d):
+        half = torch.finfo(got.dtype).eps / 2
+        assert ((got.double() - w * f).abs() <= (w * f).abs() * (half + 2 * U)).all()
 
 
 @pytest.mark.parametrize("kind", [0, 1])
