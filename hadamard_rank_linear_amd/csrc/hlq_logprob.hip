@@ -269,36 +269,36 @@ __device__ __forceinline__ void zero_row(const OutRow<DT, ST>& g) {
   for (uint32_t e = threadIdx.x * g.N; e < g.end; e += W * g.N) g.store(e, z);
 }
 
-// Reads a row again and writes its gradient, P pieces of a thread in flight.
-template <int DT, int W, int P>
-__device__ __forceinline__ void row_gradient(const LogitArgs& a, int64_t row, uint32_t t, float f,
-                                             float m, float s) {
-  constexpr int N = Piece<DT>::N;
-  const Row<DT, false> x = row_of<DT, false>(a, row);
-  const OutRow<DT, false> g(a, row, x.head);
-  if (f == 0.f || s == 0.f) {
-    zero_row<DT, false, W>(g);
-    return;
-  }
-  const float k_s = -f / s;
-  for (uint32_t e0 = threadIdx.x * N; e0 < x.end; e0 += W * N * P) {
-    u32x4 r[P];
-#pragma unroll
-    for (int j = 0; j < P; ++j) r[j] = x.load(e0 + j * W * N);
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-      const uint32_t e = e0 + j * W * N;
-      if (e < x.end) g.store(e, gradient_piece<DT>(r[j], e, x.head + t, a.c, f, k_s, m));
-    }
-  }
-}
-
-template <int DT, int W, int P>
+// Reads a row again and writes its gradient, P pieces of a thread in flight.  Where
+// rows are few, gridDim.y workgroups share one (SHARED; a stride known only at run
+// time costs 8190 x 32000 bf16 9 us of 146 otherwise).
+template <int DT, int W, int P, bool SHARED>
 __global__ __launch_bounds__(W) void k_logprob_grad(LogitArgs a) {
+  constexpr int N = Piece<DT>::N;
   const int64_t row = a.row0 + blockIdx.x, t = a.targets[row];
   const bool live = t >= 0 && t < a.V;
   const float f = live ? a.g_logprob[row] * (float)a.scale : 0.f;
-  row_gradient<DT, W, P>(a, row, (uint32_t)t, f, a.stats[2 * row], a.stats[2 * row + 1]);
+  const float m = a.stats[2 * row], s = a.stats[2 * row + 1];
+  const Row<DT, false> x = row_of<DT, false>(a, row);
+  const OutRow<DT, false> g(a, row, x.head);
+  const uint32_t first = ((SHARED ? blockIdx.y * W : 0) + threadIdx.x) * N;
+  const uint32_t step = (SHARED ? gridDim.y : 1) * W * N;
+  if (f == 0.f || s == 0.f) {
+    const u32x4 z = {0u, 0u, 0u, 0u};
+    for (uint32_t e = first; e < g.end; e += step) g.store(e, z);
+    return;
+  }
+  const float k_s = -f / s;
+  for (uint32_t e0 = first; e0 < x.end; e0 += step * P) {
+    u32x4 r[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) r[j] = x.load(e0 + j * step);
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      const uint32_t e = e0 + j * step;
+      if (e < x.end) g.store(e, gradient_piece<DT>(r[j], e, x.head + (uint32_t)t, a.c, f, k_s, m));
+    }
+  }
 }
 
 // ------------------------------------------------------------ policy loss
@@ -569,19 +569,19 @@ __global__ __launch_bounds__(1024) void k_preference_small(PrefArgs p) {
 // workgroup's 1024 for long ones (4096 x 128256 bf16 scored with 64, 256, 512
 // and 1024 threads a row: 193, 188, 183 and 176 us; 8190 x 32000: 104, 97, 90
 // and 95; 8190 x 1000: 12, 18, 25 and 44; 15728 x 3000 with 64 and 256: 20 and
-// 27), and more where the rows are too few
-// to fill the chip (3 x 32003: 18.8, 8.9, 7.9 and 7.8).
+// 27), and more where the rows are too few to fill the chip (3 x 32003: 18.8, 8.9,
+// 7.9 and 7.8; what is left there is the arithmetic of one CU, 10 us for a row of
+// 131072, the same with 8 or 16 pieces of a thread in flight).
 static int score_threads(int64_t T, int64_t n) {
   if (T < 256) return n <= 64 ? 64 : (n <= 512 ? 256 : 1024);
   return n <= 600 ? 64 : (n <= 2048 ? 256 : 512);
 }
 
-// The same for the gradient (4096 x 128256 bf16 with 64, 256, 512 and 1024
+// The same for the gradient of 256 rows and more (4096 x 128256 bf16 with 64, 256, 512 and 1024
 // threads: 430, 420, 413 and 394 us; 8190 x 32000: 222, 207, 194 and 177;
 // 8190 x 1000: 10, 11, 14 and 23; 12790 x 4099 fp32 with 256, 512 and 1024: 78, 75
 // and 103).
-static int grad_threads(int64_t T, int64_t n) {
-  if (T < 256) return n <= 64 ? 64 : (n <= 512 ? 256 : 1024);
+static int grad_threads(int64_t n) {
   return n <= 256 ? 64 : (n <= 1024 ? 256 : n <= 2560 ? 512 : 1024);
 }
 
@@ -621,16 +621,25 @@ hipError_t launch_logprob(LogitArgs a, int dtype, hipStream_t s) {
   }
 }
 
-template <int W, int P>
-static hipError_t grad_rows(LogitArgs& a, int dtype, hipStream_t s) {
+template <int W, int P, bool SHARED = false>
+static hipError_t grad_rows(LogitArgs& a, int dtype, hipStream_t s, unsigned share = 1) {
   return for_rows(a, [&](dim3 g) {
-    return dtype == 0 ? launch(k_logprob_grad<0, W, P>, g, W, s, a)
-                      : launch(k_logprob_grad<1, W, P>, g, W, s, a);
+    g.y = share;
+    return dtype == 0 ? launch(k_logprob_grad<0, W, P, SHARED>, g, W, s, a)
+                      : launch(k_logprob_grad<1, W, P, SHARED>, g, W, s, a);
   });
 }
 
 hipError_t launch_logprob_grad(LogitArgs a, int dtype, hipStream_t s) {
-  switch (grad_threads(a.T, row_pieces(a, dtype))) {
+  const int64_t n = row_pieces(a, dtype);
+  if (a.T && a.T < 256) {
+    // rows shared by workgroups of 256 threads, four pieces a thread, two
+    // workgroups a CU (1, 16 and 64 rows of 131072 bf16 logits 2.9, 3.5 and 6.6 us,
+    // with 1024 threads a row 9.5, 10.1 and 11.8)
+    const int64_t share = 512 / a.T, most = (n + 1023) / 1024;
+    return grad_rows<256, 4, true>(a, dtype, s, (unsigned)(share < most ? share : most));
+  }
+  switch (grad_threads(n)) {
     case 64: return grad_rows<64, 2>(a, dtype, s);
     case 256: return grad_rows<256, 2>(a, dtype, s);
     case 512: return grad_rows<512, 4>(a, dtype, s);
