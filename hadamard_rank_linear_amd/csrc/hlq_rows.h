@@ -221,7 +221,10 @@ template <typename... P>
 static inline hipError_t launch(void (*kernel)(P...), dim3 grid, int threads, hipStream_t s,
                                 const typename std::decay<P>::type&... args) {
   void* at[] = {const_cast<void*>(static_cast<const void*>(&args))...};
-  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), at, 0, s);
+  const hipError_t e =
+      hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), at, 0, s);
+  if (e != hipSuccess) (void)hipGetLastError();  // reported here, not by the next call
+  return e;
 }
 
 }  // namespace hlq
