@@ -9,11 +9,13 @@
 // longer than the kernels run; here they take 4 to 6 and 12 us, kernel launches
 // included.
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/Stream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/StreamGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <dlfcn.h>
 #include <stdarg.h>
@@ -169,36 +171,52 @@ Tensor make(const Tensor& like, ScalarType type, IntArrayRef shape) {
   return make(like.device(), type, shape);
 }
 
-// The GPU of a call is current while it lasts; its stream is the given
-// torch.cuda.Stream or the current one (None).
+// The stream of an argument that has to be a torch.cuda.Stream of `device`.
+c10::Stream stream_of(PyObject* o, const at::Device& device) {
+  if (!THPStream_Check(o))
+    type_error("stream must be a torch.cuda.Stream, got %s", Py_TYPE(o)->tp_name);
+  const THPStream* s = reinterpret_cast<THPStream*>(o);
+  const c10::Stream stream =
+      c10::Stream::unpack3(s->stream_id, static_cast<c10::DeviceIndex>(s->device_index),
+                           static_cast<c10::DeviceType>(s->device_type));
+  if (stream.device() != device)
+    value_error("the stream is on %s, the tensors on %s", stream.device().str().c_str(),
+                device.str().c_str());
+  return stream;
+}
+
+// The GPU of a call is current while it lasts, and so is its stream: the given
+// torch.cuda.Stream or the one that was current (None).  Outputs and workspaces
+// then come from the pool of the stream that writes them; a block of the caller's
+// stream could be one that it has just freed and still has work in flight for.
 struct Launch {
   c10::DeviceGuard guard;
-  PyObject* given;
+  c10::OptionalStreamGuard on_given;
+  bool other = false;  // the given stream is not the caller's
   void* stream;
   Launch(const Tensor& like, PyObject* o) : Launch(like.device(), o) {}
-  Launch(const at::Device& device, PyObject* o) : guard(device), given(o == Py_None ? nullptr : o) {
-    if (!given) {
-      stream = c10::hip::getCurrentHIPStream(device.index()).stream();
-      return;
+  Launch(const at::Device& device, PyObject* o) : guard(device) {
+    if (o != Py_None) {
+      on_given.reset_stream(stream_of(o, device));
+      other = *on_given.original_stream() != *on_given.current_stream();
     }
-    PyObject* raw = PyObject_GetAttrString(given, "cuda_stream");
-    if (!raw) throw python_error();
-    stream = PyLong_AsVoidPtr(raw);
-    Py_DECREF(raw);
-    if (PyErr_Occurred()) throw python_error();
+    stream = c10::hip::getCurrentHIPStream(device.index()).stream();
   }
-  // Tells the allocator that tensors, allocated for the current stream, are
-  // used on the given one.
-  void hold(std::initializer_list<const Tensor*> ts) const {
-    if (!given) return;
-    for (const Tensor* t : ts) {
-      if (!t) continue;
-      PyObject* o = THPVariable_Wrap(*t);
-      PyObject* r = o ? PyObject_CallMethod(o, "record_stream", "O", given) : nullptr;
-      Py_XDECREF(o);
-      if (!r) throw python_error();
-      Py_DECREF(r);
-    }
+  // Tensors of the caller that the call reads or writes: if the caller drops
+  // them, their memory stays theirs until the given stream has passed the call.
+  void use(const Tensor& t) const {
+    if (other) t.record_stream(*on_given.current_stream());
+  }
+  void use(std::initializer_list<const Tensor*> ts) const {
+    for (const Tensor* t : ts)
+      if (t) use(*t);
+  }
+  // New tensors that the call returns: if dropped, theirs until the caller's stream
+  // has done with them.
+  void give(std::initializer_list<const Tensor*> ts) const {
+    if (!other) return;
+    for (const Tensor* t : ts)
+      if (t) t->record_stream(*on_given.original_stream());
   }
 };
 
@@ -263,6 +281,7 @@ PyObject* layer_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (y_in) expect("y", *y_in, x.scalar_type(), x.sizes());
   same_gpu(x, {&x, residual, &w, b, y_in, h_in});
   const Launch on(x, a[7]);
+  on.use({&x, residual, &w, b, y_in, h_in});
   const Tensor y = y_in ? *y_in : make(x, x.scalar_type(), x.sizes());
   std::optional<Tensor> h;
   if (residual) h = h_in ? *h_in : make(x, x.scalar_type(), x.sizes());
@@ -272,7 +291,7 @@ PyObject* layer_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         lib.hlq_layer_norm_forward(ptr(x), ptr(residual), code(x), ptr(w), ptr(b), code(w), T, C,
                                    eps, ptr(y), h ? ptr(*h) : nullptr, ptr<float>(mean),
                                    ptr<float>(rstd), on.stream));
-  on.hold({&y, h ? &*h : &x, &mean, &rstd});
+  on.give({&y, h ? &*h : nullptr, &mean, &rstd});
   return tuple(wrap(y), wrap(h ? *h : x), wrap(mean), wrap(rstd));
   END_HANDLE_TH_ERRORS
 }
@@ -302,6 +321,7 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (g_x_in) expect("g_x", *g_x_in, h.scalar_type(), h.sizes());
   same_gpu(h, {&h, &g_y, &mean, &rstd, &w, g_h, g_x_in});
   const Launch on(h, a[9]);
+  on.use({&h, &g_y, &mean, &rstd, &w, g_h, g_x_in, ws_in});
   const Tensor g_x = g_x_in ? *g_x_in : make(h, h.scalar_type(), h.sizes());
   const Tensor g_w = make(h, w.scalar_type(), {C});
   std::optional<Tensor> g_b;
@@ -312,7 +332,7 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         lib.hlq_layer_norm_backward(ptr(g_y), ptr(h), ptr(g_h), code(h), ptr<float>(mean),
                                     ptr<float>(rstd), ptr(w), code(w), T, C, ptr(g_x), ptr(g_w),
                                     g_b ? ptr(*g_b) : nullptr, ptr(ws), ws.numel(), on.stream));
-  on.hold({&g_x, &g_w, g_b ? &*g_b : nullptr, &ws});
+  on.give({&g_x, &g_w, g_b ? &*g_b : nullptr});
   return tuple(wrap(g_x), wrap(g_w), g_b ? wrap(*g_b) : none());
   END_HANDLE_TH_ERRORS
 }
@@ -349,11 +369,12 @@ PyObject* token_logprob_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   expect("targets", t, ScalarType::Long, {T});
   same_gpu(x, {&t});
   const Launch on(x, a[3]);
+  on.use({&x, &t});
   const Tensor lp = make(x, ScalarType::Float, {T}), stats = make(x, ScalarType::Float, {T, 2});
   check("hlq_token_logprob_forward",
         lib.hlq_token_logprob_forward(ptr(x), code(x), ld, ptr<int64_t>(t), T, x.size(1), scale,
                                       ptr<float>(lp), ptr<float>(stats), on.stream));
-  on.hold({&lp, &stats});
+  on.give({&lp, &stats});
   return tuple(wrap(lp), wrap(stats));
   END_HANDLE_TH_ERRORS
 }
@@ -375,6 +396,7 @@ PyObject* token_logprob_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   same_gpu(x, {&t, &g, &stats});
   if (g_x_in) expect("g_x", *g_x_in, x.scalar_type(), x.sizes());
   const Launch on(x, a[6]);
+  on.use({&g, &x, &t, &stats, g_x_in});
   const Tensor g_x = g_x_in ? *g_x_in : make(x, x.scalar_type(), {T, V});
   const int64_t g_ld = pitch("g_x", g_x);
   same_device(x, g_x);
@@ -382,7 +404,7 @@ PyObject* token_logprob_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         lib.hlq_token_logprob_backward(ptr<float>(g), ptr(x), code(x), ld, ptr<int64_t>(t),
                                        ptr<float>(stats), T, V, scale, ptr(g_x), g_ld,
                                        on.stream));
-  on.hold({&g_x});
+  on.give({&g_x});
   return wrap(g_x);
   END_HANDLE_TH_ERRORS
 }
@@ -418,13 +440,14 @@ PyObject* policy_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
   in.check(lp, T);
   same_gpu(lp, {&lp});
   const Launch on(lp, a[9]);
+  on.use({&lp, in.old, in.advantage, in.weight, in.ref, ws_in});
   const Tensor sums = make(lp, ScalarType::Float, {3}), g = make(lp, ScalarType::Float, {T});
   const Tensor ws = workspace(ws_in, lib.hlq_policy_loss_workspace_size(T), lp);
   check("hlq_policy_loss",
         lib.hlq_policy_loss(ptr<float>(lp), ptr<float>(in.old), ptr<float>(in.advantage),
                             ptr<float>(in.weight), ptr<float>(in.ref), T, lo, hi, kl,
                             ptr<float>(sums), ptr<float>(g), ptr(ws), ws.numel(), on.stream));
-  on.hold({&sums, &g, &ws});
+  on.give({&sums, &g});
   return tuple(wrap(sums), wrap(g));
   END_HANDLE_TH_ERRORS
 }
@@ -448,6 +471,7 @@ PyObject* policy_loss_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
   same_gpu(x, {&t});
   if (g_x_in) expect("g_x", *g_x_in, x.scalar_type(), x.sizes());
   const Launch on(x, a[12]);
+  on.use({&x, &t, in.old, in.advantage, in.weight, in.ref, g_x_in, ws_in});
   const Tensor g_x = g_x_in ? *g_x_in : make(x, x.scalar_type(), {T, V});
   const int64_t g_ld = pitch("g_x", g_x);
   same_device(x, g_x);
@@ -459,7 +483,7 @@ PyObject* policy_loss_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                    ptr<float>(in.ref), T, V, scale, lo, hi, kl, ptr<float>(sums),
                                    ptr<float>(lp), ptr(g_x), g_ld, ptr(ws), ws.numel(),
                                    on.stream));
-  on.hold({&sums, &lp, &g_x, &ws});
+  on.give({&sums, &lp, &g_x});
   return tuple(wrap(sums), wrap(lp), wrap(g_x));
   END_HANDLE_TH_ERRORS
 }
@@ -486,6 +510,7 @@ PyObject* preference_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t P = start.numel() / 2;
   same_gpu(lp, {&lp, ref, w, &start});
   const Launch on(lp, a[8]);
+  on.use({&lp, ref, w, &start, ws_in});
   const Tensor loss = make(lp, ScalarType::Float, {1}), margin = make(lp, ScalarType::Float, {P});
   const Tensor g = make(lp, ScalarType::Float, {T});
   const Tensor ws = workspace(ws_in, lib.hlq_preference_loss_workspace_size(P), lp);
@@ -494,7 +519,7 @@ PyObject* preference_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 ptr<int64_t>(start), P, T, beta, e, (int)reduction,
                                 ptr<float>(loss), ptr<float>(margin), ptr<float>(g), ptr(ws),
                                 ws.numel(), on.stream));
-  on.hold({&loss, &margin, &g, &ws});
+  on.give({&loss, &margin, &g});
   return tuple(wrap(loss), wrap(margin), wrap(g));
   END_HANDLE_TH_ERRORS
 }
@@ -552,6 +577,11 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
   }
   const Launch on(device, a[5]);
+  for (Py_ssize_t i = 0; i < N && on.other; ++i) {
+    on.use(THPVariable_Unpack(grads[i]));
+    if (!in_place) on.use(THPVariable_Unpack(outs[i]));
+  }
+  on.use({ws_in});
   const Tensor norm = make(device, ScalarType::Double, {1});
   const Tensor ws =
       workspace(ws_in, lib.hlq_clip_grad_norm_workspace_size(sizes.data(), N), norm);
@@ -559,7 +589,7 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         lib.hlq_clip_grad_norm(src.data(), in_place ? nullptr : dst.data(), sizes.data(),
                                types.data(), N, max_norm, (int)kind, ptr<double>(norm), ptr(ws),
                                ws.numel(), on.stream));
-  on.hold({&norm, &ws});
+  on.give({&norm});
   return wrap(norm);
   END_HANDLE_TH_ERRORS
 }

@@ -542,6 +542,12 @@ def hlq_lqs_select(stats, threshold=HLQ_LQS_THRESHOLD):
 # ------------------------------------------------------------ training step
 # These operators' tensors are checked, their outputs allocated and the library
 # called by the native module _hlq_torch (csrc/hlq_torch.cpp).
+#
+# ``stream`` (a torch.cuda.Stream of the tensors' GPU; None: the current one) is
+# current during the call: what is allocated belongs to it, and tensors that are
+# dropped after the call keep their memory until it has run.  As everywhere in
+# torch, the caller orders it after the work that makes the inputs, and the
+# outputs' readers after it.
 
 class _Unloaded:
     """Stands for the native module until the first call: loads it, binds it to

@@ -1,0 +1,177 @@
+"""Calls with ``stream=`` beside work that is still queued on the current
+stream, and tensors that are dropped while they are in use.
+
+The allocator hands a block that was freed on a stream to the next request of
+that stream at once, while the work that used it may still be queued.  So what
+a call writes on a given stream must not come from the current one's pool, and
+what it reads must not go back there before the given stream is done."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _say(msg):
+    print(f"\n[gpu-case] {msg}", flush=True)
+
+
+def _busy():
+    """Some 20 ms of work on the current stream."""
+    torch = _torch()
+    a = torch.ones((8192, 8192), dtype=torch.bfloat16, device="cuda")
+    for _ in range(20):
+        torch.mm(a, a)
+
+
+def _train_inputs():
+    torch = _torch()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")
+    T, C = 700, 1500
+    return dict(x=r(T, C), r=r(T, C), w=1 + 0.1 * r(C), b=r(C), g=r(T), old=r(T) - 7, adv=r(T),
+                mean=0.1 * r(T), rstd=1 + 0.1 * r(T).abs(), lp=-r(T).abs(),
+                t=torch.randint(0, C, (T,), generator=g, device="cuda"),
+                stats=torch.stack([r(T) + 5, 2 + r(T).abs()], 1).contiguous(),
+                start=torch.tensor([0, 100, 350, 500, T], device="cuda"))
+
+
+def _train_calls():
+    import hadamard_rank_linear_amd as h
+
+    def outs(s, st):                           # the caller's own tensors, of the stream that writes
+        with _torch().cuda.stream(st):
+            return [_torch().empty_like(s["x"])]
+
+    return {
+        "norm_forward": (_train_inputs, lambda s, st: h.hlq_layer_norm_forward(
+            s["x"], s["w"], s["b"], residual=s["r"], stream=st)),
+        "norm_backward": (_train_inputs, lambda s, st: h.hlq_layer_norm_backward(
+            s["r"], s["x"], s["mean"], s["rstd"], s["w"], stream=st)),
+        "score": (_train_inputs, lambda s, st: h.hlq_token_logprob_forward(s["x"], s["t"],
+                                                                           stream=st)),
+        "gradient": (_train_inputs, lambda s, st: [h.hlq_token_logprob_backward(
+            s["g"], s["x"], s["t"], s["stats"], stream=st)]),
+        "policy": (_train_inputs, lambda s, st: h.hlq_policy_loss(s["lp"], s["old"], s["adv"],
+                                                                  stream=st)),
+        "policy_logits": (_train_inputs, lambda s, st: h.hlq_policy_loss_logits(
+            s["x"], s["t"], s["old"], s["adv"], stream=st)),
+        "preference": (_train_inputs, lambda s, st: h.hlq_preference_loss(
+            s["lp"], s["start"], 0.3, stream=st)),
+        "clip": (_train_inputs, lambda s, st: (lambda o: [h.hlq_clip_grad_norm(
+            [s["x"]], 0.5, out=o, stream=st), *o])(outs(s, st))),
+    }
+
+
+def _calls():
+    return _train_calls()
+
+
+NAMES = ["norm_forward", "norm_backward", "score", "gradient", "policy", "policy_logits",
+         "preference", "clip"]
+
+
+def _same(got, want, what):
+    torch = _torch()
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert torch.equal(a, b), f"{what}: output {i}"
+
+
+def _spoil(shape, dtype):
+    torch = _torch()
+    return torch.empty(shape, dtype=dtype, device="cuda").fill_(
+        float("nan") if dtype.is_floating_point else 7)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_outputs_apart_from_queued_work(name):
+    torch = _torch()
+    _say(f"{name}: outputs beside queued work of the current stream")
+    inputs, call = _calls()[name]
+    s = inputs()
+    want = [v.clone() for v in call(s, None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    # blocks of the outputs' sizes and small ones, written late and freed at once
+    blocks = [torch.empty_like(v) for v in want] + \
+        [torch.empty(n, dtype=torch.uint8, device="cuda") for n in [256] * 32 + [1 << 15] * 8]
+    _busy()
+    for v in blocks:
+        v.fill_(float("nan") if v.is_floating_point() else 255)
+    del v, blocks
+    got = call(s, side)
+    _same(got, want, name)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_inputs_dropped_while_in_use(name):
+    torch = _torch()
+    _say(f"{name}: inputs dropped before the given stream reads them")
+    inputs, call = _calls()[name]
+    s = inputs()
+    want = [v.clone() for v in call(s, None)]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        _busy()                                # its own warm-up
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        _busy()
+    got = call(s, side)
+    shapes = [(v.shape, v.dtype) for v in s.values()]
+    del s
+    junk = [_spoil(*v) for v in shapes]
+    _same(got, want, name)
+    del junk
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_outputs_dropped_while_in_use(name):
+    torch = _torch()
+    _say(f"{name}: outputs dropped while the current stream reads them")
+    inputs, call = _calls()[name]
+    s = inputs()
+    want = [v.clone() for v in call(s, None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = call(s, side)
+    if name == "clip":                         # the clipped tensors are the caller's own
+        got, want = got[:1], want[:1]
+    torch.cuda.current_stream().wait_stream(side)
+    _busy()
+    kept = [v.clone() for v in got]
+    with torch.cuda.stream(side):
+        del got
+        junk = [_spoil(v.shape, v.dtype) for v in want]
+    _same(kept, want, name)
+    del junk
+
+
+def test_the_given_stream_is_current_and_no_longer():
+    torch = _torch()
+    import hadamard_rank_linear_amd as h
+    _say("streams: refusals, and the current stream after a call")
+    x, w = torch.randn(8, 64, device="cuda"), torch.ones(64, device="cuda")
+    before = torch.cuda.current_stream()
+    side = torch.cuda.Stream()
+    side.wait_stream(before)
+    y = h.hlq_layer_norm_forward(x, w, stream=side)[0]
+    assert torch.cuda.current_stream() == before
+    with torch.cuda.stream(side):
+        z = h.hlq_layer_norm_forward(x, w, stream=side)[0]
+        before.wait_stream(side)
+        u = h.hlq_layer_norm_forward(x, w, stream=before)[0]
+        assert torch.cuda.current_stream() == side
+    torch.cuda.synchronize()
+    assert torch.equal(y, z) and torch.equal(y, u)
+    for wrong in (0, "side", side.cuda_stream):
+        with pytest.raises((TypeError, AttributeError)):
+            h.hlq_layer_norm_forward(x, w, stream=wrong)
+    with pytest.raises(h.HLQError):            # a refused call leaves the stream as it was
+        h.hlq_layer_norm_forward(x, w, eps=math.nan, stream=side)
+    assert torch.cuda.current_stream() == before
