@@ -10,6 +10,8 @@ built (``python -m hadamard_rank_linear_amd.build``); there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -216,6 +218,35 @@ def _nbytes(t):
     return t.numel() * t.element_size()
 
 
+def _on_its_stream(f):
+    """For the entry points that allocate: a ``stream`` other than the current
+    one is current during the call, so that outputs and workspaces come from
+    the pool of the stream that writes them (a block of the current stream's
+    could be one that queued work there still uses).  Tensors that either
+    stream touches keep their memory, if they are dropped, until it has."""
+    at = list(inspect.signature(f).parameters).index("stream")
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return f(*args, **kw)
+        import torch
+        caller = torch.cuda.current_stream(stream.device)
+        if stream == caller:
+            return f(*args, **kw)
+        given = [t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor) and t.is_cuda]
+        for t in given:
+            t.record_stream(stream)
+        with torch.cuda.stream(stream):
+            out = f(*args, **kw)
+        for t in out if isinstance(out, tuple) else (out,):
+            if not any(t is g for g in given):
+                t.record_stream(caller)
+        return out
+    return call
+
+
 def version() -> int:
     return _lib.hlq_version()
 
@@ -224,6 +255,7 @@ def status_string(status: int) -> str:
     return _lib.hlq_status_string(status).decode()
 
 
+@_on_its_stream
 def hlq_compress_act(x, x_codes=None, x_scales=None, stream=None):
     """ACBP: x [T, I] (fp32/bf16, GPU) -> (codes uint8 [T, I/2], scales fp32 [T])."""
     import torch
@@ -240,6 +272,7 @@ def hlq_compress_act(x, x_codes=None, x_scales=None, stream=None):
     return x_codes, x_scales
 
 
+@_on_its_stream
 def hlq_linear_forward(x, w, y=None, y_dtype=None, compress=True, x_codes=None,
                        x_scales=None, stream=None):
     """y = x . w^T for bf16 x [T, I] and w [O, I] (I % 32 == 0) on the bf16
@@ -283,6 +316,7 @@ def hlq_workspace_layout_query(T, I, O, block, rank) -> dict:
     return {name: getattr(out, name) for name, _ in WorkspaceLayout._fields_}
 
 
+@_on_its_stream
 def hlq_linear_backward(g_y, x_codes, x_scales, w, block, rank,
                         gx_mode=HLQ_PER_TOKEN, gw_mode=HLQ_PER_TOKEN, reduction=HLQ_SUM,
                         g_x=None, g_w=None, workspace=None, stream=None, steps=None):
@@ -336,6 +370,7 @@ def _acc_out(workspace, t, shape):
 HLQ_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
+@_on_its_stream
 def hlq_linear_backward_noalloc(g_y, x_codes, x_scales, w, block, rank, gx_mode=HLQ_PER_TOKEN,
                                 gw_mode=HLQ_PER_TOKEN, reduction=HLQ_SUM, g_x=None, g_w=None,
                                 stream=None):
@@ -364,6 +399,7 @@ def hlq_linear_backward_noalloc(g_y, x_codes, x_scales, w, block, rank, gx_mode=
     return g_x, g_w
 
 
+@_on_its_stream
 def hlq_gemm_pair_acc(workspace, T, I, O, block, rank, acc_x=None, acc_w=None, stream=None):
     """INT32 accumulators (acc_x [T, I], acc_w [O, I]) of the one GEMM launch
     hlq_linear_backward runs, from a workspace it has filled."""
@@ -376,6 +412,7 @@ def hlq_gemm_pair_acc(workspace, T, I, O, block, rank, acc_x=None, acc_w=None, s
     return acc_x, acc_w
 
 
+@_on_its_stream
 def hlq_gemm_gx_acc(workspace, T, I, O, block, rank, acc_x=None, stream=None):
     acc_x = _acc_out(workspace, acc_x, (T, I))
     _require_cuda(workspace, acc_x)
@@ -384,6 +421,7 @@ def hlq_gemm_gx_acc(workspace, T, I, O, block, rank, acc_x=None, stream=None):
     return acc_x
 
 
+@_on_its_stream
 def hlq_gemm_gw_acc(workspace, T, I, O, block, rank, acc_w=None, stream=None):
     acc_w = _acc_out(workspace, acc_w, (O, I))
     _require_cuda(workspace, acc_w)
@@ -401,6 +439,7 @@ def _conv_out(H, R, stride, pad):
     return (H + 2 * pad - R) // stride + 1
 
 
+@_on_its_stream
 def hlq_conv_backward(g_y, x_codes, x_scales, w, N, H, W, C, R, S, stride, pad, block, rank,
                       gx_mode=HLQ_PER_TENSOR, gw_mode=HLQ_PER_TOKEN, reduction=HLQ_SUM,
                       g_x=None, g_w=None, workspace=None, stream=None):
@@ -434,6 +473,7 @@ def hlq_conv_backward(g_y, x_codes, x_scales, w, N, H, W, C, R, S, stride, pad, 
     return g_x, g_w
 
 
+@_on_its_stream
 def hlq_conv_gemm_acc(workspace, N, H, W, C, O, R, S, stride, pad, block, rank, stream=None):
     """INT32 accumulators (acc_x [N*H*W, C], acc_w [O, R*S*C]) of the
     convolution backward's GEMMs, from a workspace it has filled."""
@@ -454,6 +494,7 @@ def hlq_ablation_workspace_size(T, I, O, block, rank, gx_variant, gw_variant) ->
     return int(_lib.hlq_ablation_workspace_size(T, I, O, block, rank, gx_variant, gw_variant))
 
 
+@_on_its_stream
 def hlq_linear_backward_ablation(g_y, x_codes, x_scales, w, block, rank, gx_variant, gw_variant,
                                  gx_mode=HLQ_PER_TOKEN, gw_mode=HLQ_PER_TOKEN,
                                  reduction=HLQ_SUM, want_acc=False, stream=None):
@@ -495,6 +536,7 @@ def hlq_lqs_workspace_size(T, I, O, block, rank) -> int:
     return int(_lib.hlq_lqs_workspace_size(T, I, O, block, rank))
 
 
+@_on_its_stream
 def hlq_lqs_accumulate(g_y, x_codes, x_scales, w, block, rank, stats=None, workspace=None,
                        stream=None):
     """Add one calibration batch to the layer-wise quantizer selection

@@ -68,11 +68,51 @@ def _train_calls():
     }
 
 
+def _linear_inputs():
+    import hadamard_rank_linear_amd as h
+    torch = _torch()
+    g = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    x = r(1024, 512)
+    codes, scales = h.hlq_compress_act(x)
+    return dict(x=x, gy=r(1024, 256), w=r(256, 512), codes=codes, scales=scales)
+
+
+def _conv_inputs():
+    import hadamard_rank_linear_amd as h
+    torch = _torch()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    codes, scales = h.hlq_compress_act(r(512, 32))       # 2 images of 16 x 16, 32 channels
+    return dict(gy=r(512, 64), w=r(64, 9 * 32), codes=codes, scales=scales)
+
+
+def _linear_calls():
+    import hadamard_rank_linear_amd as h
+    four = lambda s: (s["gy"], s["codes"], s["scales"], s["w"])
+    return {
+        "compress": (_linear_inputs, lambda s, st: h.hlq_compress_act(s["x"], stream=st)),
+        "linear_forward": (_linear_inputs, lambda s, st: h.hlq_linear_forward(
+            s["x"], s["w"], stream=st)),
+        "linear_backward": (_linear_inputs, lambda s, st: h.hlq_linear_backward(
+            *four(s), 16, 8, stream=st)),
+        "linear_backward_noalloc": (_linear_inputs, lambda s, st: h.hlq_linear_backward_noalloc(
+            *four(s), 16, 8, stream=st)),
+        "ablation": (_linear_inputs, lambda s, st: h.hlq_linear_backward_ablation(
+            *four(s), 16, 8, h.HLQ_VAR_HQ4, h.HLQ_VAR_HLA8_INT, stream=st)),
+        "lqs": (_linear_inputs, lambda s, st: [h.hlq_lqs_accumulate(*four(s), 16, 8, stream=st)]),
+        "conv_backward": (_conv_inputs, lambda s, st: h.hlq_conv_backward(
+            *four(s), 2, 16, 16, 32, 3, 3, 1, 1, 16, 8, stream=st)),
+    }
+
+
 def _calls():
-    return _train_calls()
+    return {**_train_calls(), **_linear_calls()}
 
 
-NAMES = ["norm_forward", "norm_backward", "score", "gradient", "policy", "policy_logits",
+NAMES = ["compress", "linear_forward", "linear_backward", "linear_backward_noalloc", "ablation",
+         "lqs", "conv_backward",
+         "norm_forward", "norm_backward", "score", "gradient", "policy", "policy_logits",
          "preference", "clip"]
 
 
