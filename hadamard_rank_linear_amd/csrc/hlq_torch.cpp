@@ -227,6 +227,17 @@ void check(const char* name, hlq_status status) {
   throw python_error();
 }
 
+// Tensors of the caller that the call has written: autograd's version counter
+// tells a backward pass that what it saved is not there any more, as torch's own
+// in-place operations do (tensors made in inference mode have none).
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(std::initializer_list<const Tensor*> ts) {
+  for (const Tensor* t : ts)
+    if (t) written(*t);
+}
+
 Tensor workspace(const Tensor* given, size_t need, const Tensor& like) {
   if (!given) return make(like, ScalarType::Byte, {(int64_t)std::max<size_t>(need, 256)});
   if (given->scalar_type() != ScalarType::Byte || given->dim() != 1)
@@ -291,6 +302,7 @@ PyObject* layer_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         lib.hlq_layer_norm_forward(ptr(x), ptr(residual), code(x), ptr(w), ptr(b), code(w), T, C,
                                    eps, ptr(y), h ? ptr(*h) : nullptr, ptr<float>(mean),
                                    ptr<float>(rstd), on.stream));
+  written({y_in, h_in});
   on.give({&y, h ? &*h : nullptr, &mean, &rstd});
   return tuple(wrap(y), wrap(h ? *h : x), wrap(mean), wrap(rstd));
   END_HANDLE_TH_ERRORS
@@ -332,6 +344,7 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         lib.hlq_layer_norm_backward(ptr(g_y), ptr(h), ptr(g_h), code(h), ptr<float>(mean),
                                     ptr<float>(rstd), ptr(w), code(w), T, C, ptr(g_x), ptr(g_w),
                                     g_b ? ptr(*g_b) : nullptr, ptr(ws), ws.numel(), on.stream));
+  written({g_x_in});
   on.give({&g_x, &g_w, g_b ? &*g_b : nullptr});
   return tuple(wrap(g_x), wrap(g_w), g_b ? wrap(*g_b) : none());
   END_HANDLE_TH_ERRORS
@@ -404,6 +417,7 @@ PyObject* token_logprob_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         lib.hlq_token_logprob_backward(ptr<float>(g), ptr(x), code(x), ld, ptr<int64_t>(t),
                                        ptr<float>(stats), T, V, scale, ptr(g_x), g_ld,
                                        on.stream));
+  written({g_x_in});
   on.give({&g_x});
   return wrap(g_x);
   END_HANDLE_TH_ERRORS
@@ -483,6 +497,7 @@ PyObject* policy_loss_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                    ptr<float>(in.ref), T, V, scale, lo, hi, kl, ptr<float>(sums),
                                    ptr<float>(lp), ptr(g_x), g_ld, ptr(ws), ws.numel(),
                                    on.stream));
+  written({g_x_in});
   on.give({&sums, &lp, &g_x});
   return tuple(wrap(sums), wrap(lp), wrap(g_x));
   END_HANDLE_TH_ERRORS
@@ -589,6 +604,7 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         lib.hlq_clip_grad_norm(src.data(), in_place ? nullptr : dst.data(), sizes.data(),
                                types.data(), N, max_norm, (int)kind, ptr<double>(norm), ptr(ws),
                                ws.numel(), on.stream));
+  for (Py_ssize_t i = 0; i < N; ++i) written(THPVariable_Unpack((in_place ? grads : outs)[i]));
   on.give({&norm});
   return wrap(norm);
   END_HANDLE_TH_ERRORS
