@@ -541,7 +541,9 @@ __device__ __forceinline__ double preference_pair(const PrefArgs& p, int64_t pai
     for (int64_t t = lane; t < before; t += G) p.g_logprob[t] = 0.f;
     for (int64_t t = from + lane; t < p.T; t += G) p.g_logprob[t] = 0.f;
   }
-  return log1p(x) + (z < 0.0 ? -(1.0 - e) * z : e * z);
+  // an infinite margin counts where its side has a share (e or 1 - e), else not at all
+  const double part_z = z < 0.0 ? 1.0 - e : e;
+  return log1p(x) + (part_z == 0.0 ? 0.0 : part_z * fabs(z));
 }
 
 __global__ __launch_bounds__(1024) void k_preference(PrefArgs p) {

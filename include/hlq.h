@@ -536,6 +536,11 @@ hlq_status hlq_policy_loss_logits(const void* logits, int dtype, int64_t ld,
  * with e = label_smoothing.
  *   logprob  [T] f32; ref_logprob [T] f32 or NULL (no reference policy).
  *   weight   [T] f32 or NULL (ones); 0 takes a token out, whatever its values.
+ *            A token of logprob -inf (a banned target) makes the score of its
+ *            sequence -inf and the margin -inf or +inf: the loss then has the
+ *            limit's value (0 for a margin of +inf without smoothing), the
+ *            gradient is finite.  Where the reference gives it -inf too, or both
+ *            sequences of a pair hold one, the margin is NaN.
  *   start    [2P + 1] int64, non-decreasing within 0 to T: sequence q is tokens
  *            start[q] .. start[q+1] - 1; the chosen ones are 0 .. P-1, the
  *            rejected ones P .. 2P-1 in the same order.  Read on the device

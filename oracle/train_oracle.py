@@ -143,7 +143,8 @@ def preference_loss(logprob, start, beta, ref=None, weight=None, smoothing=0.0, 
     loss, g = 0.0, np.zeros(T)
     for p in range(P):
         z = margin[p]
-        loss += ((1.0 - smoothing) * _softplus(-z) + smoothing * _softplus(z)) / P
+        for part, v in ((1.0 - smoothing, -z), (smoothing, z)):
+            loss += part * _softplus(v) / P if part else 0.0
         slope = beta / P * (math.exp(-_softplus(-z)) - 1.0 + smoothing)
         for q, sign in ((p, 1.0), (P + p, -1.0)):
             for t in range(start[q], start[q + 1]):
