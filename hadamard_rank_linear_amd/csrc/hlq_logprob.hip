@@ -269,6 +269,26 @@ __device__ __forceinline__ void zero_row(const OutRow<DT, ST>& g) {
   for (uint32_t e = threadIdx.x * g.N; e < g.end; e += W * g.N) g.store(e, z);
 }
 
+// The gradient of a row whose f is infinite (a banned target under a KL term): its
+// limit, zero where [v = t] - e_v / s is, instead of inf * 0.  Rare, so the row is
+// read again, from `first` on, whatever the kernel holds of it.
+template <int DT, bool ST>
+__device__ __forceinline__ void limit_row(const Row<DT, ST>& x, const OutRow<DT, ST>& g,
+                                          uint32_t first, uint32_t step, uint32_t t, float c,
+                                          float f, float m, float s) {
+  constexpr int N = Piece<DT>::N;
+  for (uint32_t e = first; e < x.end; e += step) {
+    const u32x4 r = x.load(e);
+    float o[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float d = (t - e == (uint32_t)k ? 1.f : 0.f) - exp2_hw((piece_at<DT>(r, k) - m) * c) / s;
+      o[k] = d == 0.f ? 0.f : f * d;
+    }
+    g.store(e, make_piece<DT>(o));
+  }
+}
+
 // Reads a row again and writes its gradient, P pieces of a thread in flight.  Where
 // rows are few, gridDim.y workgroups share one (SHARED; a stride known only at run
 // time costs 8190 x 32000 bf16 9 us of 146 otherwise).
@@ -286,6 +306,10 @@ __global__ __launch_bounds__(W) void k_logprob_grad(LogitArgs a) {
   if (f == 0.f || s == 0.f) {
     const u32x4 z = {0u, 0u, 0u, 0u};
     for (uint32_t e = first; e < g.end; e += step) g.store(e, z);
+    return;
+  }
+  if (__builtin_isinf(f)) {
+    limit_row(x, g, first, step, x.head + (uint32_t)t, a.c, f, m, s);
     return;
   }
   const float k_s = -f / s;
@@ -319,12 +343,12 @@ __device__ __forceinline__ double policy_token(const PolicyArgs& p, const Policy
   const double r = exp(lp - (double)q.old);
   const double lo = 1.0 - p.clip_low, hi = 1.0 + p.clip_high;
   const double bounded = r < lo ? lo : (r > hi ? hi : r);
-  const double free_ = r * A, clipped = bounded * A;
+  const double free_ = A == 0.0 ? 0.0 : r * A, clipped = bounded * A;  // r may overflow
   const bool cut = clipped < free_;
   double kl = 0.0, g = cut ? 0.0 : -free_;
   if (p.ref_logprob) {
     const double d = (double)q.ref - lp, x = expm1(d);
-    kl = x - d;
+    kl = x == __builtin_huge_val() ? x : x - d;  // d = inf too, where lp is -inf
     g -= p.kl_coef * x;
   }
   term[0] = w * (p.kl_coef * kl - (cut ? clipped : free_));
@@ -378,6 +402,10 @@ __global__ __launch_bounds__(W, 4) void k_policy_regs(LogitArgs a, PolicyArgs p)
     zero_row<DT, ST, W>(g);
     return;
   }
+  if (__builtin_isinf(f)) {
+    limit_row(x, g, threadIdx.x * N, W * N, x.head + (uint32_t)t, a.c, f, m, s);
+    return;
+  }
   const float k_s = -f / s;
 #pragma unroll
   for (int j = 0; j < P; ++j) {
@@ -420,6 +448,10 @@ __global__ __launch_bounds__(W, 4) void k_policy_long(LogitArgs a, PolicyArgs p)
   const OutRow<DT, true> g(a, row, x.head);
   if (f == 0.f || s == 0.f) {
     zero_row<DT, true, W>(g);
+    return;
+  }
+  if (__builtin_isinf(f)) {
+    limit_row(once, g, threadIdx.x * N, W * N, x.head + (uint32_t)t, a.c, f, m, s);
     return;
   }
   const float k_s = -f / s;

@@ -476,7 +476,8 @@ hlq_status hlq_token_logprob_forward(const void* logits, int dtype, int64_t ld,
  *   g_x[t][v] = g_logprob[t] * scale * ([v == target] - softmax(z[t])[v]),
  * the softmax taken from stats.
  *   g_logprob [T] f32.  Rows whose g_logprob is zero, whose target is ignored
- *            or which hold nothing but -inf get zeros, and are not read.
+ *            or which hold nothing but -inf get zeros, and are not read.  An
+ *            infinite one gives zero where the factor in brackets is zero.
  *   g_x      T rows of V elements out, dtype, row t at element t * g_ld; may be
  *            logits itself (g_ld = ld), no other overlap.
  * One launch.  Errors as above (HLQ_ERR_SHAPE also for g_ld < V).
@@ -500,6 +501,12 @@ hlq_status hlq_token_logprob_backward(const float* g_logprob, const void* logits
  *            weight of the tokens whose clamped term was the smaller one.
  *   g_logprob [T] f32 out, the gradient of the loss.
  *   workspace at least hlq_policy_loss_workspace_size(T) bytes.
+ * A logprob of -inf (a banned target) has the ratio 0; with a KL term the loss
+ * and its estimate are then +inf and the gradient -inf, as the formula's limits
+ * are.  A reference of -inf makes the loss +inf and leaves the gradient finite.
+ * An advantage of 0 adds nothing, however large the ratio.  NaN where logprob and
+ * old_logprob, or logprob and a reference that counts, are both -inf: such
+ * tokens are taken out by their weight.
  * clip_low in [0, 1], clip_high >= 0, kl_coef >= 0, all finite
  * (HLQ_ERR_VALUE).  Two launches.
  */

@@ -94,9 +94,9 @@ def token_logprob_backward(g_logprob, logits, targets, scale=1.0):
         if m == -np.inf:
             continue
         e = np.exp(scale * (x - m))
-        out[t] = -e / e.sum()
-        out[t, targets[t]] += 1.0
-        out[t] *= scale * g_logprob[t]
+        d = -e / e.sum()
+        d[targets[t]] += 1.0
+        out[t][d != 0] = d[d != 0] * (scale * g_logprob[t])    # infinite ones: no inf * 0
     return out
 
 
@@ -110,12 +110,16 @@ def policy_loss(logprob, old, advantage, weight=None, ref=None, clip_low=0.2, cl
         w = 1.0 if weight is None else float(weight[t])
         if w == 0 or (counts is not None and not counts[t]):
             continue
-        r = math.exp(logprob[t] - old[t])
-        free, held = r * advantage[t], min(max(r, 1.0 - clip_low), 1.0 + clip_high) * advantage[t]
+        with np.errstate(over="ignore"):
+            r = float(np.exp(logprob[t] - old[t]))
+        free = r * advantage[t] if advantage[t] else 0.0
+        held = min(max(r, 1.0 - clip_low), 1.0 + clip_high) * advantage[t]
         kl, slope = 0.0, 0.0
         if kl_coef:
             d = float(ref[t]) - logprob[t]
-            kl, slope = math.expm1(d) - d, -math.expm1(d)
+            with np.errstate(over="ignore"):
+                away = float(np.expm1(d))
+            kl, slope = away - d if away < math.inf else away, -away
         sums += w * (kl_coef * kl - min(free, held)), w * kl, w if held < free else 0.0
         g[t] = w * (kl_coef * slope - (free if free <= held else 0.0))
     return sums, g

@@ -65,3 +65,87 @@ def test_preference_loss_of_banned_targets(P, length, mean, smoothing):
     bad[start[2]] = -INF                       # in a chosen one
     loss, margin = check(bad)
     assert margin[2] == -INF and math.isfinite(loss) == (smoothing == 1.0)
+
+
+# ------------------------------------------------------------ policy loss
+
+def _banned_case(T, V, name, seed):
+    """Logits whose first rows have targets that nothing can sample, with the
+    other inputs of the policy loss; which rows have a finite KL term."""
+    import torch
+    from test_gpu_train import _logits, _policy_inputs
+    x, t = _logits(T, V, name, seed)
+    low = torch.finfo(x.dtype).min
+    s = _policy_inputs(x, t, 1.0, seed, zero=0.0)
+    x[0, t[0]] = -INF                          # banned
+    x[1, t[1]] = low                           # banned by the type's lowest value
+    x[2] = -INF                                # nothing allowed
+    x[3] = -INF                                # the target is all that is allowed
+    x[3, t[3]] = 1.0
+    s["old"][3], s["ref"][3] = 0.1, -0.2       # (its log probability is 0)
+    s["ref"][4] = -INF                         # banned by the reference alone
+    s["old"][5], s["adv"][5] = low, 0.0        # by the old policy, without an advantage
+    s["w"][:] = 1.0 / T
+    return x, t, s, np.isin(np.arange(T), [0, 1, 2, 4], invert=True)
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V", [(8, 5), (8, 1001), (300, 1001), (300, 4099), (8, 32003),
+                                 (8, 65541), (8, 140001)])
+def test_policy_loss_of_banned_targets(T, V, name):
+    import torch
+    import hadamard_rank_linear_amd as h
+    from test_gpu_train import _clear_of_the_border, _dev, _gradient_tolerance, _logit_errors, \
+        _within
+    _say(f"policy: banned targets, T={T} V={V} {name}")
+    x, t, s, finite = _banned_case(T, V, name, T + V)
+    xn, tn = _np(x), t.numpy()
+    olp = o.token_logprob(xn, tn)[0]
+    assert olp[0] == -INF and olp[2] == -INF and -INF < olp[1] < -1e38 and olp[3] == 0.0
+    e_lp, e_s = _logit_errors(xn, tn, 1.0)
+    _clear_of_the_border(olp, s, 0.2, 0.28, 1e-3)
+    c = lambda v: torch.from_numpy(v).cuda()
+    for kl, keep in ((0.0, np.ones(T, bool)), (0.05, np.ones(T, bool)), (0.05, finite)):
+        w = np.where(keep, s["w"], 0.0).astype(np.float32)
+        ref = s["ref"] if kl else None
+        osums, og = o.policy_loss(olp, s["old"], s["adv"], w, ref, 0.2, 0.28, kl)
+        assert np.isfinite(osums).all() == (kl == 0.0 or not keep.all()) and not np.isnan(og).any()
+        want = o.token_logprob_backward(og, xn, tn)
+        args = [c(s["old"]), c(s["adv"]), c(w)]
+        kw = dict(ref_logprob=c(ref) if kl else None, clip_low=0.2, clip_high=0.28, kl_coef=kl)
+        out = []
+        for place in (False, True):            # the second time in place of the logits
+            dx = _dev(x, name, 1)
+            sums, lp, g_x = h.hlq_policy_loss_logits(dx, t.cuda(), *args, g_x=dx if place else None,
+                                                     **kw)
+            torch.cuda.synchronize()
+            out.append((sums, lp, g_x))
+        assert all(torch.equal(a, b) for a, b in zip(*out))
+        # the log probability's error moves the ratio and exp(d) in proportion
+        live = keep & np.isfinite(og) & np.isfinite(olp) & (olp > -1e38)
+        ratio = np.exp(np.where(live, np.minimum(olp - s["old"], 50.0), 0.0))
+        away = np.exp(np.where(live, np.minimum(s["ref"] - olp, 50.0), 0.0))
+        move = np.where(live, 1.01 * e_lp, 0.0) * w
+        e_g = move * (ratio * np.abs(s["adv"]) + kl * away)
+        tol = np.array([e_g.sum(), (move * np.abs(away - 1)).sum(), 0.0])
+        _within(_np(sums), osums, np.where(np.isfinite(osums), 1.01 * tol + 2 * U * np.abs(osums), 0)
+                + 1e-12, "sums")
+        fin = np.isfinite(og)
+        with np.errstate(invalid="ignore"):
+            g_tol = _gradient_tolerance(xn, tn, np.where(fin, og, 0.0), e_s, 1.0, name,
+                                        np.where(np.isfinite(want), want, 0.0))
+            half = 2.0 ** -8 if name == "bf16" else 0.0
+            for i in np.flatnonzero(live):
+                g_tol[i] += (1 + half) * np.abs(want[i]) * (e_g[i] / max(abs(og[i]), 1e-30) + 2 * U)
+        _within(_np(g_x), want, g_tol, "g_x")
+        # through the log probabilities
+        lp1, stats = h.hlq_token_logprob_forward(_dev(x, name, 1), t.cuda())
+        sums2, g_lp = h.hlq_policy_loss(lp1, *args, **kw)
+        g_x2 = h.hlq_token_logprob_backward(g_lp, _dev(x, name, 1), t.cuda(), stats)
+        torch.cuda.synchronize()
+        assert np.array_equal(np.isfinite(_np(sums2)), np.isfinite(osums))
+        assert not np.isnan(_np(sums2)).any() and not np.isnan(_np(g_lp)).any()
+        assert np.array_equal(_np(g_lp) == -INF, og == -INF)
+        assert np.array_equal(np.isinf(_np(g_x2)), np.isinf(want)) and \
+            not np.isnan(_np(g_x2)).any()
+        assert (_np(g_x2)[want == 0] == 0).all()
