@@ -268,12 +268,13 @@ struct PrefArgs {
   int mean;
   float *loss, *margin, *g_logprob;
   double* terms;
+  int64_t pair0;  // first pair of the launch (set by the launch function)
 };
 hipError_t launch_logprob(LogitArgs a, int dtype, hipStream_t s);
 hipError_t launch_logprob_grad(LogitArgs a, int dtype, hipStream_t s);
 hipError_t launch_policy_logits(LogitArgs a, const PolicyArgs& p, int dtype, hipStream_t s);
 hipError_t launch_policy(const PolicyArgs& p, hipStream_t s);
-hipError_t launch_preference(const PrefArgs& p, hipStream_t s);
+hipError_t launch_preference(PrefArgs p, hipStream_t s);
 
 // Gradient clipping (hlq_clip.hip): part of a list of tensors, passed by value
 // (a kernel's arguments hold 4 KiB).  size: elements, at most 2^30, with bit 31

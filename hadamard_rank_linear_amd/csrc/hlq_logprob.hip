@@ -580,8 +580,9 @@ __device__ __forceinline__ double preference_pair(const PrefArgs& p, int64_t pai
 
 __global__ __launch_bounds__(1024) void k_preference(PrefArgs p) {
   __shared__ double sm[16][4];
-  const double loss = preference_pair<1024>(p, blockIdx.x, sm);
-  if (threadIdx.x == 0) p.terms[blockIdx.x] = loss;
+  const int64_t pair = p.pair0 + blockIdx.x;
+  const double loss = preference_pair<1024>(p, pair, sm);
+  if (threadIdx.x == 0) p.terms[pair] = loss;
 }
 
 // All pairs in one workgroup, a wave per pair: one launch, no partials.
@@ -626,13 +627,17 @@ static int64_t row_pieces(const LogitArgs& a, int dtype) {
   return (a.V + (at_boundary ? 0 : N - 1) + N - 1) / N;
 }
 
-// One workgroup per row, 2^20 rows a launch (a launch holds fewer than 2^32
-// threads).
+// One workgroup per row (or pair), 2^20 of them a launch (a launch holds fewer than
+// 2^32 threads); `first` is where the kernel reads a launch's first one.
+template <typename F>
+static hipError_t for_rows(int64_t& first, int64_t n, F f) {
+  hipError_t e = hipSuccess;
+  for (first = 0; first < n && e == hipSuccess; first += 1 << 20) e = f(rows_grid(n - first));
+  return e;
+}
 template <typename F>
 static hipError_t for_rows(LogitArgs& a, F f) {
-  hipError_t e = hipSuccess;
-  for (a.row0 = 0; a.row0 < a.T && e == hipSuccess; a.row0 += 1 << 20) e = f(rows_grid(a.T - a.row0));
-  return e;
+  return for_rows(a.row0, a.T, f);
 }
 
 template <int W, int P>
@@ -726,12 +731,13 @@ hipError_t launch_policy(const PolicyArgs& p, hipStream_t s) {
   return launch(k_terms<3>, dim3(1), 1024, s, p.terms, p.T, 1.0, p.sums);
 }
 
-hipError_t launch_preference(const PrefArgs& p, hipStream_t s) {
+hipError_t launch_preference(PrefArgs p, hipStream_t s) {
   // one launch where a wave has one pair, and a short one in the mean (2 pairs
   // of 150 tokens: 4.8 us instead of 4.8 + 1.8 and a launch's gap; 32 pairs of
   // 256 tokens, ragged: 20 us instead of 6.8 + 4)
   if (p.P <= 16 && p.T <= 256 * p.P) return launch(k_preference_small, dim3(1), 1024, s, p);
-  const hipError_t e = launch(k_preference, dim3((unsigned)p.P), 1024, s, p);
+  const hipError_t e =
+      for_rows(p.pair0, p.P, [&](dim3 g) { return launch(k_preference, g, 1024, s, p); });
   if (e != hipSuccess) return e;
   return launch(k_terms<1>, dim3(1), 1024, s, p.terms, p.P, 1.0 / (double)p.P, p.loss);
 }

@@ -249,7 +249,7 @@ hlq_status hlq_preference_loss(const float* logprob, const float* ref_logprob,
   if (st != HLQ_OK) return st;
   const hlq::PrefArgs p = {logprob, ref_logprob, weight, start, P, T, beta, label_smoothing,
                            reduction == HLQ_MEAN, loss, margin, g_logprob,
-                           static_cast<double*>(workspace)};
+                           static_cast<double*>(workspace), 0};
   HLQ_TRY(hlq::launch_preference(p, static_cast<hipStream_t>(stream)));
   return HLQ_OK;
 }

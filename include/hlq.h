@@ -556,7 +556,8 @@ hlq_status hlq_policy_loss_logits(const void* logits, int dtype, int64_t ld,
  *   loss     [1] f32, margin [P] f32, g_logprob [T] f32 out.
  *   workspace at least hlq_preference_loss_workspace_size(P) bytes.
  * beta > 0 and finite, 0 <= label_smoothing <= 1 (HLQ_ERR_VALUE), reduction
- * HLQ_SUM or HLQ_MEAN (HLQ_ERR_MODE), P >= 1 (HLQ_ERR_SHAPE).
+ * HLQ_SUM or HLQ_MEAN (HLQ_ERR_MODE), 1 <= P < 2^24 and T < 2^31
+ * (HLQ_ERR_SHAPE).
  */
 size_t hlq_preference_loss_workspace_size(int64_t P);
 hlq_status hlq_preference_loss(const float* logprob, const float* ref_logprob,

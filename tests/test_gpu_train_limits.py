@@ -149,3 +149,27 @@ def test_policy_loss_of_banned_targets(T, V, name):
         assert np.array_equal(np.isinf(_np(g_x2)), np.isinf(want)) and \
             not np.isnan(_np(g_x2)).any()
         assert (_np(g_x2)[want == 0] == 0).all()
+
+
+# ------------------------------------------------------------ many pairs
+
+def test_preference_loss_of_more_pairs_than_a_launch_takes():
+    # more workgroups than a launch holds threads for; a token a sequence, so the
+    # margins are differences of single tokens
+    import torch
+    import hadamard_rank_linear_amd as h
+    P = (1 << 22) + 5
+    _say(f"preference: P={P}")
+    g = torch.Generator(device="cuda").manual_seed(9)
+    lp = -torch.rand(2 * P, generator=g, device="cuda")
+    start = torch.arange(2 * P + 1, device="cuda")
+    loss, margin, g_lp = h.hlq_preference_loss(lp, start, 0.5)
+    torch.cuda.synchronize()
+    d = lp.double()
+    z = 0.5 * (d[:P] - d[P:])
+    x = torch.exp(-z)
+    want = 0.5 / P * (1.0 / (1.0 + x) - 1.0)
+    assert ((margin - z).abs() <= 2 * U * z.abs()).all()
+    assert ((g_lp[:P] - want).abs() <= 2 * U * want.abs()).all()
+    assert torch.equal(g_lp[P:], -g_lp[:P])
+    assert abs(loss.item() - torch.log1p(x).mean().item()) <= 2 * U
