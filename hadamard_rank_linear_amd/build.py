@@ -1,10 +1,13 @@
 """Build the gfx950 HIP library libhlq.so and the Python module _hlq_torch.so
 in-tree with hipcc and the host's C++ compiler.
 
-Each source compiles to an object of its own (in parallel), then one link."""
+The library needs hipcc alone; the module, which the training step's operators
+are called through from Python, also needs torch.  Each source compiles to an
+object of its own (in parallel), then one link."""
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import subprocess
 import sys
@@ -70,14 +73,21 @@ def build(verbose: bool = False) -> str:
         o = os.path.join(OBJ, name + ".o")
         objs.append(o)
         cmds.append([HIPCC, *FLAGS, *extra, *inc, "-c", "-o", o, os.path.join(CSRC, src)])
-    cmds.append(_ext_command(EXT + ".tmp"))
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(cmds)) as ex:
+    ext = None
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(cmds) + 1) as ex:
+        if importlib.util.find_spec("torch") is not None:
+            ext = ex.submit(lambda: _run(_ext_command(EXT + ".tmp"), verbose))
         for f in [ex.submit(_run, c, verbose) for c in cmds]:
             f.result()
     tmp = LIB + ".tmp"
     _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs], verbose)
     os.replace(tmp, LIB)
-    os.replace(EXT + ".tmp", EXT)
+    if ext is None:
+        sys.stderr.write("torch is not installed: built without _hlq_torch.so, the Python "
+                         "binding of the training step's operators\n")
+    else:
+        ext.result()
+        os.replace(EXT + ".tmp", EXT)
     return LIB
 
 
