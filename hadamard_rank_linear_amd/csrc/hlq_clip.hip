@@ -131,12 +131,12 @@ __global__ __launch_bounds__(CLIP_THREADS) void k_clip_norm(ClipList l, int kind
 
 template <int DT, bool ST>
 __device__ __forceinline__ void clip_store(const ClipChunk& k, uint32_t at, const u32x4& r,
-                                           float coef) {
+                                           float coef, int shift) {
   constexpr int N = Piece<DT>::N;
   if (at >= k.bytes) return;
   float v[N];
 #pragma unroll
-  for (int e = 0; e < N; ++e) v[e] = piece_at<DT>(r, e) * coef;
+  for (int e = 0; e < N; ++e) v[e] = __builtin_ldexpf(piece_at<DT>(r, e) * coef, shift);
   const u32x4 o = make_piece<DT>(v);
   if (at + 16 <= k.bytes) {
     Loose* p = reinterpret_cast<Loose*>(k.out + at);
@@ -166,9 +166,15 @@ __global__ __launch_bounds__(CLIP_THREADS) void k_clip_scale(ClipList l, int kin
     v = (double)__uint_as_float(group_umax(top, smu));
   }
   if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = v;
-  const double f = max_norm / (v + 1e-6);
+  // The factor as coef 2^shift: where norms are so far above max_norm that fp32
+  // would hold it with few bits or none, though the outputs are ordinary numbers,
+  // its exponent is applied to the product (one more operation per element, hidden
+  // behind the memory).
+  double f = max_norm / (v + 1e-6);
+  int shift = 0;
+  if (f < 0x1p-100) f = frexp(f, &shift);
   const float coef = (float)(f >= 1.0 ? 1.0 : f);  // a NaN stays
-  if (l.in_place && coef == 1.0f) return;
+  if (l.in_place && coef == 1.0f && shift == 0) return;
   const ClipIndex index(l);
   for (uint32_t c = blockIdx.x; c < l.chunks; c += gridDim.x) {
     const ClipChunk k = index.chunk(l, c);
@@ -177,8 +183,8 @@ __global__ __launch_bounds__(CLIP_THREADS) void k_clip_scale(ClipList l, int kin
 #pragma unroll
     for (int j = 0; j < CLIP_PIECES; ++j) {
       const uint32_t at = (threadIdx.x + j * CLIP_THREADS) * 16;
-      if (k.bf16) clip_store<1, ST>(k, at, r[j], coef);
-      else clip_store<0, ST>(k, at, r[j], coef);
+      if (k.bf16) clip_store<1, ST>(k, at, r[j], coef, shift);
+      else clip_store<0, ST>(k, at, r[j], coef, shift);
     }
   }
 }

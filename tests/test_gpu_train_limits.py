@@ -173,3 +173,32 @@ def test_preference_loss_of_more_pairs_than_a_launch_takes():
     assert ((g_lp[:P] - want).abs() <= 2 * U * want.abs()).all()
     assert torch.equal(g_lp[P:], -g_lp[:P])
     assert abs(loss.item() - torch.log1p(x).mean().item()) <= 2 * U
+
+
+# ------------------------------------------------------------ clipping
+
+@pytest.mark.parametrize("kind", ["l2", "inf"])
+@pytest.mark.parametrize("value,max_norm", [(3e38, 1.0), (3e38, 1e-3), (1e20, 1e-25), (1e30, 1e-12),
+                                            (3e38, 1e-37), (1.0, 1e-30), (1.0, 1e-31)])
+def test_clip_by_a_factor_below_the_range(kind, value, max_norm):
+    # the factor (3e-33 to 1e-75 here) is no fp32 number, or one of few bits; its
+    # rounding, the product's and the output's are half a step each
+    import torch
+    import hadamard_rank_linear_amd as h
+    _say(f"clip of gradients of {value} to {max_norm}, {kind}")
+    rng = np.random.default_rng(4)
+    host = [torch.from_numpy(value * rng.uniform(0.1, 1.0, n)).to(dt)
+            for n, dt in ((1000, torch.float32), (9, torch.bfloat16), (4099, torch.float32))]
+    norm, want = o.clip_grad_norm([_np(v) for v in host], max_norm, kind == "inf")
+    code = h.HLQ_NORM_L2 if kind == "l2" else h.HLQ_NORM_INF
+    out = [torch.empty_like(v, device="cuda") for v in host]
+    got = h.hlq_clip_grad_norm(own := [v.cuda() for v in host], max_norm, code, out=out)
+    h.hlq_clip_grad_norm(own, max_norm, code)
+    torch.cuda.synchronize()
+    assert got.item() == pytest.approx(norm, rel=2.0 ** -33)
+    for a, b, v in zip(out, own, want):
+        half = torch.finfo(a.dtype).eps / 2
+        # below the type's normal range steps do not shrink any more: one of those
+        step = 2 * half * torch.finfo(a.dtype).smallest_normal
+        assert (np.abs(_np(a) - v) <= (2 * U + half * (1 + 2 * U)) * np.abs(v) + step).all()
+        assert torch.equal(a, b)
