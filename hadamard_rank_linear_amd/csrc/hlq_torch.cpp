@@ -18,6 +18,7 @@
 #include <c10/core/StreamGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <dlfcn.h>
+#include <limits.h>
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -142,12 +143,20 @@ double number(const char* name, PyObject* o) {
   return v;
 }
 
-long integer(const char* name, PyObject* o) {
-  const long v = PyLong_AsLong(o);
+int integer(const char* name, PyObject* o) {
+  int over = 0;
+  const long v = PyLong_AsLongAndOverflow(o, &over);
   if (v == -1 && PyErr_Occurred()) {
     PyErr_Clear();
     type_error("%s must be an integer, got %s", name, Py_TYPE(o)->tp_name);
   }
+  if (over || v < INT_MIN || v > INT_MAX) value_error("%s is out of range", name);
+  return (int)v;
+}
+
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
   return v;
 }
 
@@ -319,7 +328,7 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& rstd = tensor("rstd", a[3]);
   const Tensor& w = tensor("weight", a[4]);
   const Tensor* g_h = maybe("g_h", a[5]);
-  const int with_bias = PyObject_IsTrue(a[6]);
+  const bool with_bias = truth(a[6]);
   const Tensor* g_x_in = maybe("g_x", a[7]);
   const Tensor* ws_in = maybe("workspace", a[8]);
   if (!h.dim()) value_error("h must have at least one dimension");
@@ -514,7 +523,7 @@ PyObject* preference_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor* ref = maybe("ref_logprob", a[3]);
   const Tensor* w = maybe("weight", a[4]);
   const double e = number("label_smoothing", a[5]);
-  const long reduction = integer("reduction", a[6]);
+  const int reduction = integer("reduction", a[6]);
   const Tensor* ws_in = maybe("workspace", a[7]);
   const int64_t T = lp.numel();
   expect("logprob", lp, ScalarType::Float, {T});
@@ -531,7 +540,7 @@ PyObject* preference_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor ws = workspace(ws_in, lib.hlq_preference_loss_workspace_size(P), lp);
   check("hlq_preference_loss",
         lib.hlq_preference_loss(ptr<float>(lp), ptr<float>(ref), ptr<float>(w),
-                                ptr<int64_t>(start), P, T, beta, e, (int)reduction,
+                                ptr<int64_t>(start), P, T, beta, e, reduction,
                                 ptr<float>(loss), ptr<float>(margin), ptr<float>(g), ptr(ws),
                                 ws.numel(), on.stream));
   on.give({&loss, &margin, &g});
@@ -560,7 +569,7 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   count(n, 7);
   const Items grads(a[0]);
   const double max_norm = number("max_norm", a[1]);
-  const long kind = integer("norm_kind", a[2]);
+  const int kind = integer("norm_kind", a[2]);
   const bool in_place = a[3] == Py_None;
   const Items outs(in_place ? grads.seq : a[3]);
   const Tensor* ws_in = maybe("workspace", a[4]);
@@ -602,7 +611,7 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       workspace(ws_in, lib.hlq_clip_grad_norm_workspace_size(sizes.data(), N), norm);
   check("hlq_clip_grad_norm",
         lib.hlq_clip_grad_norm(src.data(), in_place ? nullptr : dst.data(), sizes.data(),
-                               types.data(), N, max_norm, (int)kind, ptr<double>(norm), ptr(ws),
+                               types.data(), N, max_norm, kind, ptr<double>(norm), ptr(ws),
                                ws.numel(), on.stream));
   for (Py_ssize_t i = 0; i < N; ++i) written(THPVariable_Unpack((in_place ? grads : outs)[i]));
   on.give({&norm});
