@@ -157,7 +157,8 @@ class HLQTokenLogprobFunction(torch.autograd.Function):
 
 
 def hlq_token_logprob(logits, targets, scale=1.0):
-    """Differentiable log probability of each target (fp32 [T])."""
+    """Differentiable log probability of each target (fp32 [T]), 0 for targets
+    outside [0, V), which the losses below count unless their weight is 0."""
     return HLQTokenLogprobFunction.apply(logits, targets, scale)
 
 

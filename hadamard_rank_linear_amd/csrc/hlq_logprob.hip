@@ -153,7 +153,9 @@ __device__ __forceinline__ void keep_packed(u32x4& r) { asm volatile("" : "+v"(r
 
 // Maximum and sum relative to it of P pieces at positions e0, e0 + step, ...,
 // joined to a thread's running (m, s).  Pieces past the row's end cost nothing
-// where the whole wave's are.
+// where the whole wave's are.  The sum is fp32: a thread adds V / threads terms and
+// the threads join over a tree, off by 4.5e-8 of a log probability at 128256 logits.
+// An fp64 sum (2.5e-8) would be a conversion and a wider addition for every logit.
 template <int DT, int P>
 __device__ __forceinline__ void accumulate(u32x4 (&r)[P], uint32_t e0, uint32_t step, uint32_t end,
                                            const LogitArgs& a, float& m, float& s) {
@@ -248,7 +250,9 @@ __global__ __launch_bounds__(W) void k_logprob(LogitArgs a) {
 }
 
 // Gradient of a row's piece at position e: f ([v = t] - e_v / s), k_s = -f / s,
-// t the target's position.
+// t the target's position.  The exponent has c in one word: off by 2^-24 of itself
+// and as much from the product, 1e-6 of an exponential 20 below the maximum (which is
+// 2e-9), and unlike in the sum nothing adds these errors up.
 template <int DT>
 __device__ __forceinline__ u32x4 gradient_piece(const u32x4& r, uint32_t e, uint32_t t, float c,
                                                 float f, float k_s, float m) {
@@ -600,22 +604,23 @@ __global__ __launch_bounds__(1024) void k_preference_small(PrefArgs p) {
 }
 
 // ------------------------------------------------------------ launches
-// Threads per row of n pieces: a wave for short rows, the whole of a
-// workgroup's 1024 for long ones (4096 x 128256 bf16 scored with 64, 256, 512
-// and 1024 threads a row: 193, 188, 183 and 176 us; 8190 x 32000: 104, 97, 90
-// and 95; 8190 x 1000: 12, 18, 25 and 44; 15728 x 3000 with 64 and 256: 20 and
-// 27), and more where the rows are too few to fill the chip (3 x 32003: 18.8, 8.9,
-// 7.9 and 7.8; what is left there is the arithmetic of one CU, 10 us for a row of
+// Threads per row of n pieces: a wave for short rows, 512 for long ones (scored
+// with 64, 256, 512 and 1024 threads a row, inputs displaced from the caches: 8190 x
+// 1000 bf16 6.5, 10.9, 18.1 and 32.2 us; 15728 x 3000 20.9, 25.3, 40.4 and 70.5;
+// 12790 x 4099 fp32 35.2, 36.9, 45.5 and 72.7; 8190 x 32000 bf16 87.3, 82.6, 78.2 and
+// 87.1; 4096 x 128256 183, 162, 159 and 153, the one shape where 1024 would be ahead),
+// and more where the rows are too few to fill the chip (3 x 32003: 16.0, 6.2, 5.7
+// and 5.6; what is left there is the arithmetic of one CU, 10 us for a row of
 // 131072, the same with 8 or 16 pieces of a thread in flight).
 static int score_threads(int64_t T, int64_t n) {
   if (T < 256) return n <= 64 ? 64 : (n <= 512 ? 256 : 1024);
   return n <= 600 ? 64 : (n <= 2048 ? 256 : 512);
 }
 
-// The same for the gradient of 256 rows and more (4096 x 128256 bf16 with 64, 256, 512 and 1024
-// threads: 430, 420, 413 and 394 us; 8190 x 32000: 222, 207, 194 and 177;
-// 8190 x 1000: 10, 11, 14 and 23; 12790 x 4099 fp32 with 256, 512 and 1024: 78, 75
-// and 103).
+// The same for the gradient of 256 rows and more (4096 x 128256 bf16 with 64, 256,
+// 512 and 1024 threads: 425, 420, 412 and 388 us; 8190 x 32000: 218, 206, 194 and
+// 176; 8190 x 1000: 8.8, 11.2, 19.6 and 32.4; 15728 x 3000: 39.8, 35.8, 60.1 and 83.5;
+// 12790 x 4099 fp32: 89.0, 78.3, 80.2 and 145).
 static int grad_threads(int64_t n) {
   return n <= 256 ? 64 : (n <= 1024 ? 256 : n <= 2560 ? 512 : 1024);
 }

@@ -277,7 +277,10 @@ __device__ __forceinline__ void put_column(const NormBwd& a, int64_t part, int s
 
 // Gradient of the rows and, over the rows a group takes, its column sums in
 // registers; at the end the groups of a workgroup join theirs (lanes of a wave
-// first, then the waves through LDS) and write one partial.  The weight stays in
+// first, then the waves through LDS) and write one partial.  These sums are fp32, as
+// 8 M of them a lane in fp64 are more registers than the rows themselves, and
+// only the fold is fp64: 32 rows a group at 16383 x 4096 leave an error of 1.2e-7
+// (5.8e-8 with every sum in fp64).  The weight stays in
 // registers (KEEP), except for four quads a lane in fp32, where there is no room
 // and it is read again.  With 64 MiB operands, fold included: bf16 51 us at 64
 // columns (70 with the weight read for every row and sums through ds_bpermute), 50
@@ -591,8 +594,11 @@ static int64_t even_rounds(int64_t need, int64_t most) {
 // threads per CU, which all run at once (so not evened out as above: 512 of them
 // take ViT-B's 1576 rounds in 19.8 us, 394 in 21.7), and half for fp32 rows of
 // three quads a lane, which have as many bytes in flight and are more columns to
-// fold (1500 columns 55 us instead of 62, 2500 52 and 61; bf16 64 and 67 the other
-// way about).  Few rows are one workgroup's, which writes the parameters'
+// fold (64 MiB operands, 512 and 1024 threads: 1200 columns 56.6 and 60.1 us, 1500
+// 54.7 and 61.8, 2500 52.6 and 59.2, 3000 53.9 and 61.6, 4200 57.7 and 57.0, 6144
+// 54.6 and 56.9; bf16 the other way about from 1200, 68.3 and 62.7, to 4200, 77.6 and
+// 60.1), except where a row takes 1024 lanes: half of the CUs would have none (10000
+// columns 73.9 and 60.1).  Few rows are one workgroup's, which writes the parameters'
 // gradients itself: up to NORM_ALONE rounds of it (GPU time of 1, 2 and 4 rounds
 // in one launch, and of as many rows in two: 768 columns 4.0, 5.2, 7.5 and 6.0 us;
 // 4096 4.4, 5.5, 7.6 and 6.7; the second launch costs the host 2.3 us).

@@ -648,7 +648,8 @@ def hlq_token_logprob_forward(logits, targets, scale=1.0, stream=None):
     fp32, stats being each row's maximum and sum of exponentials above it.
 
     Targets outside [0, V) (such as -100) are ignored: log probability 0, the
-    row not read.  The rows of logits may have any pitch (a slice of a padded
+    row not read; the losses below count such a token unless its weight is 0.
+    The rows of logits may have any pitch (a slice of a padded
     vocabulary).
     """
     return _native.token_logprob_forward(logits, targets, scale, stream)
@@ -671,7 +672,8 @@ def hlq_policy_loss(logprob, old_logprob, advantage, weight=None, ref_logprob=No
     """Clipped policy loss with a KL term from log probabilities [T]: returns
     (sums [3], g_logprob [T]), sums = (loss, weighted KL estimate, weight of
     the clipped tokens).  ``ref_logprob`` goes with a kl_coef other than 0; a
-    weight of 0 takes a token out (weight None: ones)."""
+    weight of 0 takes a token out (weight None: ones), which ignored targets
+    need: only :func:`hlq_policy_loss_logits` sees them."""
     return _native.policy_loss(logprob, old_logprob, advantage, weight, ref_logprob, clip_low,
                                clip_high, kl_coef, workspace, stream)
 
@@ -702,6 +704,7 @@ def hlq_preference_loss(logprob, start, beta, ref_logprob=None, weight=None, lab
     within 0 to T, the P chosen ones first (tokens outside every sequence get a
     gradient of zero); ``reduction`` HLQ_SUM scores a sequence by the
     sum of weight * (logprob - ref_logprob), HLQ_MEAN by its weighted mean.
+    Ignored targets need a weight of 0, or they count in the sequence's length.
     """
     return _native.preference_loss(logprob, start, beta, ref_logprob, weight, label_smoothing,
                                    reduction, workspace, stream)

@@ -421,6 +421,8 @@ hlq_status hlq_lqs_select(const double* stats, double threshold, int* gx_mode,
  *   h            [T][C] out, dtype: the sum, for the residual stream and the
  *                backward pass; NULL exactly when residual is.
  *   mean, rstd   [T] f32 out, for the backward pass.
+ * Statistics are fp32, the squares of the differences to the mean included: they
+ * pass its range where a row's values lie more than 2^63 apart.
  * One launch.  Errors: HLQ_ERR_NULL, HLQ_ERR_DTYPE, HLQ_ERR_SHAPE (T < 0,
  * C < 1, T or C >= 2^31), HLQ_ERR_VALUE (eps negative or not finite),
  * HLQ_ERR_ALIGN.
@@ -459,7 +461,9 @@ hlq_status hlq_layer_norm_backward(const void* g_y, const void* h, const void* g
  *   stats[t]   = (max_v logits[t][v], sum_v exp(z[t][v] - max_v z[t][v]))
  *   logits   T rows of V elements, dtype, row t at element t * ld (ld >= V).
  *   targets  [T] int64; one outside [0, V) is ignored: its row is not read,
- *            logprob is 0 and stats (0, 1).
+ *            logprob is 0 and stats (0, 1).  The losses on log probabilities do
+ *            not see targets: to them such a token is one of probability 1 until
+ *            its weight is 0.
  *   scale    the inverse temperature, 2^-64 to 2^64.
  *   logprob  [T] f32 out;  stats [T][2] f32 out, for the backward pass.
  * Logits of -inf have probability zero; a row of nothing else has logprob
@@ -519,7 +523,9 @@ hlq_status hlq_policy_loss(const float* logprob, const float* old_logprob,
 
 /*
  * hlq_token_logprob_forward, hlq_policy_loss and hlq_token_logprob_backward
- * in one pass over the logits.
+ * in one pass over the logits, with one difference: a token whose target is
+ * ignored does not count, as if its weight were 0 (the three calls need the
+ * weight for that).
  *   logprob  [T] f32 out; 0 where the weight is 0 or the target is ignored
  *            (such a token does not count in the loss, its row is not read).
  *   g_x      T rows of V elements out: the gradient of the loss; may be logits
@@ -543,6 +549,9 @@ hlq_status hlq_policy_loss_logits(const void* logits, int dtype, int64_t ld,
  * with e = label_smoothing.
  *   logprob  [T] f32; ref_logprob [T] f32 or NULL (no reference policy).
  *   weight   [T] f32 or NULL (ones); 0 takes a token out, whatever its values.
+ *            Ignored targets (log probability 0) have to be taken out that way:
+ *            they count in a sequence's length under HLQ_MEAN, and their
+ *            reference in its score.
  *            A token of logprob -inf (a banned target) makes the score of its
  *            sequence -inf and the margin -inf or +inf: the loss then has the
  *            limit's value (0 for a margin of +inf without smoothing), the
