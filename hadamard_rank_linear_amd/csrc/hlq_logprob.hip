@@ -347,7 +347,8 @@ __device__ __forceinline__ double policy_token(const PolicyArgs& p, const Policy
   const double r = exp(lp - (double)q.old);
   const double lo = 1.0 - p.clip_low, hi = 1.0 + p.clip_high;
   const double bounded = r < lo ? lo : (r > hi ? hi : r);
-  const double free_ = A == 0.0 ? 0.0 : r * A, clipped = bounded * A;  // r may overflow
+  // a ratio past the range counts as a finite one under an advantage of zero
+  const double free_ = A == 0.0 && r == __builtin_huge_val() ? 0.0 : r * A, clipped = bounded * A;
   const bool cut = clipped < free_;
   double kl = 0.0, g = cut ? 0.0 : -free_;
   if (p.ref_logprob) {

@@ -112,7 +112,7 @@ def policy_loss(logprob, old, advantage, weight=None, ref=None, clip_low=0.2, cl
             continue
         with np.errstate(over="ignore"):
             r = float(np.exp(logprob[t] - old[t]))
-        free = r * advantage[t] if advantage[t] else 0.0
+        free = 0.0 if advantage[t] == 0 and r == math.inf else r * advantage[t]
         held = min(max(r, 1.0 - clip_low), 1.0 + clip_high) * advantage[t]
         kl, slope = 0.0, 0.0
         if kl_coef:

@@ -151,6 +151,21 @@ def test_policy_loss_of_banned_targets(T, V, name):
         assert (_np(g_x2)[want == 0] == 0).all()
 
 
+def test_policy_loss_does_not_hide_nan():
+    # an advantage of zero takes out a ratio past the range, not one that is no number
+    import torch
+    import hadamard_rank_linear_amd as h
+    _say("policy: NaN logits under an advantage of zero")
+    x, t = torch.zeros(3, 40, device="cuda"), torch.zeros(3, dtype=torch.int64, device="cuda")
+    x[1, 7] = math.nan
+    old, adv = torch.zeros(3, device="cuda"), torch.zeros(3, device="cuda")
+    sums, lp, _ = h.hlq_policy_loss_logits(x, t, old, adv)
+    sums2, _ = h.hlq_policy_loss(lp, old, adv)
+    torch.cuda.synchronize()
+    assert torch.isnan(lp).tolist() == [False, True, False]
+    assert torch.isnan(sums[0]) and torch.isnan(sums2[0])
+
+
 # ------------------------------------------------------------ many pairs
 
 def test_preference_loss_of_more_pairs_than_a_launch_takes():

@@ -30,6 +30,8 @@ def test_policy_loss_of_banned_targets():
     assert sums.tolist() == [-1.0, 0.0, 0.0] and g.tolist() == [0.0, -1.0, 0.0]
     sums, g = o.policy_loss(lp, old, A, None, ref, kl_coef=0.5)
     assert sums.tolist() == [INF, INF, 0.0] and g.tolist() == [-INF, -0.5, 0.0]
+    sums, g = o.policy_loss(np.array([np.nan]), old[:1], np.zeros(1))    # NaN is not hidden
+    assert np.isnan(sums[0])
 
 
 def test_infinite_gradient_of_a_log_probability():
