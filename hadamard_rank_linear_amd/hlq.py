@@ -223,7 +223,9 @@ def _on_its_stream(f):
     one is current during the call, so that outputs and workspaces come from
     the pool of the stream that writes them (a block of the current stream's
     could be one that queued work there still uses).  Tensors that either
-    stream touches keep their memory, if they are dropped, until it has."""
+    stream touches keep their memory, if they are dropped, until it has.  For
+    an object that is no torch.cuda.Stream, and only names its handle, that is
+    left to the caller."""
     at = list(inspect.signature(f).parameters).index("stream")
 
     @functools.wraps(f)
@@ -232,6 +234,8 @@ def _on_its_stream(f):
         if stream is None:
             return f(*args, **kw)
         import torch
+        if not isinstance(stream, torch.cuda.Stream):
+            return f(*args, **kw)
         caller = torch.cuda.current_stream(stream.device)
         if stream == caller:
             return f(*args, **kw)

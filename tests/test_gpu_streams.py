@@ -215,3 +215,18 @@ def test_the_given_stream_is_current_and_no_longer():
     with pytest.raises(h.HLQError):            # a refused call leaves the stream as it was
         h.hlq_layer_norm_forward(x, w, eps=math.nan, stream=side)
     assert torch.cuda.current_stream() == before
+
+
+def test_streams_of_other_makes():
+    # an object that only names its handle, as the linear layer's entry points take it
+    torch = _torch()
+    import types
+
+    import hadamard_rank_linear_amd as h
+    _say("linear layer on a stream that is no torch object")
+    s = _linear_inputs()
+    want = h.hlq_compress_act(s["x"])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = h.hlq_compress_act(s["x"], stream=types.SimpleNamespace(cuda_stream=side.cuda_stream))
+    _same(got, want, "compress")
