@@ -25,7 +25,8 @@ _BINDING_NAMES = {
     "hlq_token_logprob_forward", "hlq_token_logprob_backward", "hlq_policy_loss",
     "hlq_policy_loss_logits", "hlq_policy_loss_workspace_size", "hlq_preference_loss",
     "hlq_preference_loss_workspace_size", "hlq_clip_grad_norm",
-    "hlq_clip_grad_norm_workspace_size",
+    "hlq_clip_grad_norm_workspace_size", "hlq_relative_bucket", "hlq_attention_forward",
+    "hlq_attention_backward", "hlq_dropout_forward", "hlq_dropout_backward",
 }
 
 

@@ -26,6 +26,10 @@ SOURCES = [("hlq_tr.hip", f"hlq_tr{n}", [f"-DHLQ_TR_N={n}"]) for n in (16, 32, 6
     ("hlq_ablation.hip", "hlq_ablation", []),
     ("hlq_norm.hip", "hlq_norm", []), ("hlq_logprob.hip", "hlq_logprob", []),
     ("hlq_clip.hip", "hlq_clip", []),
+    # the attention kernels build once per padded head size
+    *(("hlq_attention.hip", f"hlq_attention{d}", [f"-DHLQ_ATTN_D={d}"]) for d in (32, 64, 96, 128)),
+    ("hlq_attention_fold.hip", "hlq_attention_fold", []), ("hlq_dropout.hip", "hlq_dropout", []),
+    ("hlq_attention_api.cpp", "hlq_attention_api", []),
     ("hlq_api.cpp", "hlq_api", []), ("hlq_train_api.cpp", "hlq_train_api", [])]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1,0 +1,854 @@
+// Attention over packed sequences, forward and backward, for head sizes up to
+// HLQ_ATTN_D (built once per value).
+//
+// With S = scale q k^T + bias, P = exp(S - lse), delta_i = sum_d g_o o:
+//   o = P v,   g_v = P^T g_o,   dS = P (g_o v^T - delta),
+//   g_q = scale dS k,   g_k = scale dS^T q,   g_bias = sums of dS by bucket.
+// Scores and statistics are fp32, in powers of two (c = scale log2 e).
+//
+// Every product is written so that its result's columns (a lane each) are what
+// stays in a wave: a wave's 32 query rows in the forward pass and the gradient
+// of q, its 32 keys in the gradients of k and v.  Then P and dS leave the matrix
+// unit in the registers in which the next product takes them in, row statistics
+// are one value a lane, and nothing but the other operand's tiles goes through LDS.
+#include "hlq_attn.h"
+
+#ifndef HLQ_ATTN_D
+#error "HLQ_ATTN_D: the padded head size"
+#endif
+
+namespace hlq {
+namespace {
+
+constexpr float kInf = __builtin_inff();
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float max_halves(float v) {
+  return lanes_stage<32>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float sum_halves(float v) {
+  return lanes_stage<32>(v, [](float a, float b) { return a + b; });
+}
+
+template <int DT>
+__device__ __forceinline__ const char* row_at(const AttnRows& t, int64_t token, int head) {
+  return static_cast<const char*>(t.data) + (token * t.token + head * t.head) * (DT == 0 ? 4 : 2);
+}
+
+// Outputs of tokens that belong to no sequence: zeros.
+template <int DT>
+__device__ void clear_tokens(const AttnRows& t, int64_t from, int64_t to, int heads, int D,
+                             int64_t id, int64_t step) {
+  typedef typename Piece<DT>::Elem E;
+  const int64_t n = (to - from) * heads * D;
+  for (int64_t i = id; i < n; i += step) {
+    const int d = (int)(i % D);
+    const int64_t r = i / D;
+    const_cast<E*>(reinterpret_cast<const E*>(
+        row_at<DT>(t, from + r / heads, (int)(r % heads))))[d] = 0;
+  }
+}
+__device__ __forceinline__ int64_t bound(const int64_t* start, int64_t s, int64_t T) {
+  const int64_t a = start[s];
+  return a < 0 ? 0 : a > T ? T : a;
+}
+
+// What a wave knows of its 32 query rows: lane l has row l & 31.
+struct RowInfo {
+  bool valid;
+  int token, head;  // in the sequence; query head
+  int pos;          // position among the keys
+  int limit;        // keys before it are visible
+};
+__device__ __forceinline__ RowInfo row_info(const AttnShape& g, int row, int rows, int head0,
+                                            int off, int nk) {
+  RowInfo r;
+  r.valid = row < rows;
+  r.token = row;
+  r.head = head0;
+  if (g.pack > 1) {
+    r.token = (int)((unsigned)row / (unsigned)g.pack);
+    r.head = head0 + row - r.token * g.pack;
+  }
+  r.pos = r.token + off;
+  r.limit = nk;
+  if (g.causal) r.limit = max(0, min(nk, r.pos + 1));
+  return r;
+}
+
+__device__ __forceinline__ int wave_min(int v) {
+  return lanes_join<64>(v, [](int a, int b) { return a < b ? a : b; });
+}
+__device__ __forceinline__ int wave_max_int(int v) {
+  return lanes_join<64>(v, [](int a, int b) { return a > b ? a : b; });
+}
+
+// Scores of a 32 x 32 block with their bias, in powers of two; s holds q k^T,
+// rows are keys from key0 on, columns queries at pos (or the other way round:
+// step -1).  The distance of register r is base + step * acc_row(r).
+template <bool BIAS>
+__device__ __forceinline__ void add_bias(const AttnShape& g, const float* line, f32x16& s, int lo,
+                                         int hi, int base, bool down) {
+  if constexpr (!BIAS) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] *= g.c;
+    return;
+  }
+  const int reach = g.bias.reach;
+  if (lo >= reach || hi <= -reach) {
+    const float b = line[lo >= reach ? 2 * (reach + BIAS_MARGIN) : 0];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], g.c, b);
+    return;
+  }
+  const float* at = line + base + reach + BIAS_MARGIN;
+  if (down) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], g.c, at[-acc_row(r)]);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], g.c, at[acc_row(r)]);
+  }
+}
+
+// ------------------------------------------------------------ forward
+
+// A work item is a tile of query rows of one sequence and head group, and a
+// share of its keys.  FEW: the tile has 32 rows and each wave a quarter of the
+// keys, joined through LDS at the end; else 32 rows a wave and every key.
+template <int DT, int DP, bool FEW>
+struct FwdShape {
+  typedef Tile<DT, DP> T;
+  static constexpr int ROWS = FEW ? ATTN_FEW : ATTN_ROWS;
+  static constexpr int KEYS = FEW ? 128 : DT == 0 ? 32 : 64;  // of a tile
+  static constexpr int MINE = FEW ? 32 : KEYS;                // of them a wave's
+  static constexpr int TILE_BYTES = KEYS * T::ROW_BYTES;
+  static constexpr int JOIN_BYTES = FEW ? 4 * DP * 33 * 4 + 4 * 32 * 8 : 0;
+  static constexpr int LDS = 2 * TILE_BYTES > JOIN_BYTES ? 2 * TILE_BYTES : JOIN_BYTES;
+};
+
+template <int DT, int DP, bool BIAS, bool FEW>
+__global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(AttnFwd a) {
+  typedef FwdShape<DT, DP, FEW> F;
+  typedef Tile<DT, DP> T;
+  constexpr int DB = DP / 32, DC = DP / 16, SB = F::MINE / 32;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  char* const lk = lds;
+  char* const lv = lds + F::TILE_BYTES;
+  float* const line = reinterpret_cast<float*>(lds + F::LDS);
+  const AttnShape& g = a.g;
+  const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
+
+  if (blockIdx.x >= g.launched) {  // tokens of no sequence
+    const int64_t id = (int64_t)(blockIdx.x - g.launched) * 256 + threadIdx.x;
+    const int64_t step = (int64_t)(gridDim.x - g.launched) * 256;
+    const int64_t from = bound(g.start_q, 0, g.Tq), to = bound(g.start_q, g.S, g.Tq);
+    for (int part = 0; part < 2; ++part) {
+      const int64_t x = part ? max(from, to) : 0, y = part ? g.Tq : from;
+      if (a.po) {
+        for (int64_t i = id; i < (y - x) * g.heads * g.splits; i += step) {
+          const int64_t p = i / ((y - x) * g.heads), r = i % ((y - x) * g.heads);
+          float* ml = a.ml + ((p * g.Tq + x) * g.heads + r) * 2;
+          ml[0] = -kInf;
+          ml[1] = 0.f;
+        }
+        continue;
+      }
+      clear_tokens<DT>(a.o, x, y, g.heads, g.D, id, step);
+      for (int64_t i = id; i < (y - x) * g.heads; i += step)
+        a.lse[(i % g.heads) * g.Tq + x + i / g.heads] = -kInf;
+    }
+    return;
+  }
+
+  for (int64_t item = first_item(g.launched); item < g.items; item += g.launched) {
+    int64_t rest = item;
+    const int split = (int)(rest % g.splits);
+    rest /= g.splits;
+    const int64_t tile0 = g.tiles - 1 - rest % g.tiles;  // the longest first
+    rest /= g.tiles;
+    const int unit = (int)(rest % (g.kv_heads * g.groups));
+    const int64_t seq = rest / (g.kv_heads * g.groups);
+    const int head0 = unit * g.pack, kvh = unit / g.groups;
+    int q0, nq, k0, nk;
+    sequence(g.start_q, seq, g.Tq, q0, nq);
+    sequence(g.start_k, seq, g.Tk, k0, nk);
+    const int rows = nq * g.pack, off = nk - nq;
+    if constexpr (BIAS) {
+      __syncthreads();
+      load_bias_line(g.bias, head0, g.heads, line);
+    }
+
+    for (int64_t tile = tile0; tile * F::ROWS < rows; tile += g.tiles) {
+      const int row0 = (int)tile * F::ROWS + (FEW ? 0 : wave * 32);
+      const RowInfo me = row_info(g, row0 + (lane & 31), rows, head0, off, nk);
+      const int first = wave_min(me.valid ? me.limit : nk);
+      const int last = wave_max_int(me.valid ? me.limit : 0);
+      // keys of the tile's last row: every wave of the group goes that far
+      int end = nk;
+      if (g.causal) {
+        const int r = min(rows, (int)(tile + 1) * F::ROWS) - 1;
+        end = max(0, min(nk, (int)((unsigned)r / (unsigned)g.pack) + off + 1));
+      }
+      int from = 0;
+      if (g.splits > 1) {
+        const int share = ((end + F::KEYS - 1) / F::KEYS + g.splits - 1) / g.splits * F::KEYS;
+        from = min(end, split * share);
+        end = min(end, from + share);
+      }
+
+      Frag<DT> qf[DC];
+      {
+        const char* p = row_at<DT>(a.q, q0 + (me.valid ? me.token : 0), me.head);
+#pragma unroll
+        for (int c = 0; c < DC; ++c)
+          qf[c] = me.valid ? global_frag<DT>(p, 16 * c + 8 * half, g.D, a.q.vec) : zero_frag<DT>();
+      }
+      f32x16 o[DB];
+#pragma unroll
+      for (int d = 0; d < DB; ++d) o[d] = (f32x16)(0.f);
+      float m = -kInf, l = 0.f;
+
+      Stage<DT, DP, F::KEYS> sk, sv;
+      const auto krow = [&](const AttnRows& t, int key) -> const void* {
+        return key < end ? row_at<DT>(t, (int64_t)k0 + key, kvh) : nullptr;
+      };
+      sk.load([&](int r) { return krow(a.k, from + r); }, g.D, a.k.vec);
+      sv.load([&](int r) { return krow(a.v, from + r); }, g.D, a.v.vec);
+      for (int key = from; key < end; key += F::KEYS) {
+        __syncthreads();
+        sk.store(lk);
+        sv.store(lv);
+        __syncthreads();
+        if (key + F::KEYS < end) {
+          sk.load([&](int r) { return krow(a.k, key + F::KEYS + r); }, g.D, a.k.vec);
+          sv.load([&](int r) { return krow(a.v, key + F::KEYS + r); }, g.D, a.v.vec);
+        }
+        const int mine = FEW ? 32 * wave : 0, key0 = key + mine;
+        if (key0 >= min(last, end)) continue;
+
+        f32x16 s[SB];
+#pragma unroll
+        for (int b = 0; b < SB; ++b) {
+          s[b] = (f32x16)(0.f);
+#pragma unroll
+          for (int c = 0; c < DC; ++c)
+            s[b] = mma(T::row_frag(lk, mine + 32 * b + (lane & 31), 16 * c + 8 * half), qf[c], s[b]);
+          const int d = key0 + 32 * b - me.pos;
+          if constexpr (BIAS) {
+            const int dist = key0 + 32 * b - (row0 + off);  // of the first row; later ones less
+            add_bias<true>(g, line, s[b], dist - 31, dist + 31, d + 4 * half, false);
+          } else {
+            add_bias<false>(g, nullptr, s[b], 0, 0, 0, false);
+          }
+        }
+        const bool whole = key0 + F::MINE <= min(first, end);
+        if (!whole) {
+          const int limit = min(me.limit, end) - key0 - 4 * half;
+#pragma unroll
+          for (int b = 0; b < SB; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (32 * b + acc_row(r) >= limit) s[b][r] = -kInf;
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int b = 0; b < SB; ++b)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
+        top = fmaxf(m, max_halves(top));
+        const float base = top == -kInf ? 0.f : top;  // a row that has seen no key yet
+        if (__any(top != m)) {
+          const float keep = exp2_fast(m - base);
+          l *= keep;
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[d][r] *= keep;
+          m = top;
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int b = 0; b < SB; ++b)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            s[b][r] = exp2_fast(s[b][r] - base);
+            sum += s[b][r];
+          }
+        l += sum;
+        if (whole) {
+#pragma unroll
+          for (int b = 0; b < SB; ++b)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const Frag<DT> p = acc_frag<DT>(s[b], c);
+#pragma unroll
+              for (int d = 0; d < DB; ++d)
+                o[d] = mma(T::col_frag(lv, mine + 32 * b + 16 * c, 32 * d), p, o[d]);
+            }
+        } else {
+          const int limit = min(me.limit, end) - key0;
+#pragma unroll
+          for (int b = 0; b < SB; ++b)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const Frag<DT> p = acc_frag<DT>(s[b], c);
+#pragma unroll
+              for (int d = 0; d < DB; ++d)
+                o[d] = mma_seen<DT>(T::col_frag(lv, mine + 32 * b + 16 * c, 32 * d), p, o[d],
+                                    [&](int i) { return 32 * b + 16 * c + i < limit; });
+            }
+        }
+      }
+      l = sum_halves(l);
+
+      if constexpr (!FEW) {
+        if (!me.valid) continue;
+        const int64_t token = (int64_t)q0 + me.token;
+        if (a.po) {
+          const int64_t at = ((int64_t)split * g.Tq + token) * g.heads + me.head;
+          if (half == 0) {
+            a.ml[2 * at] = m;
+            a.ml[2 * at + 1] = l;
+          }
+          float* p = a.po + at * g.D;
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const int e = 32 * d + acc_row(r) + 4 * half;
+              if (e < g.D) p[e] = o[d][r];
+            }
+          continue;
+        }
+        if (half == 0)
+          a.lse[me.head * g.Tq + token] = l == 0.f ? -kInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        char* p = const_cast<char*>(row_at<DT>(a.o, token, me.head));
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; r += 4)
+            store4<DT>(p, 32 * d + acc_row(r) + 4 * half, g.D, a.o.vec, o[d][r] * inv,
+                       o[d][r + 1] * inv, o[d][r + 2] * inv, o[d][r + 3] * inv);
+      } else {
+        // the waves' shares of the keys: [wave][d][row], rows 33 apart
+        float* const jo = reinterpret_cast<float*>(lds);
+        float2* const jm = reinterpret_cast<float2*>(lds + 4 * DP * 33 * 4);
+        __syncthreads();
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            jo[(wave * DP + 32 * d + acc_row(r) + 4 * half) * 33 + (lane & 31)] = o[d][r];
+        if (half == 0) jm[wave * 32 + lane] = make_float2(m, l);
+        __syncthreads();
+        for (int i = threadIdx.x; i < 32 * DP; i += 256) {
+          const int r = i / DP, d = i % DP;
+          const RowInfo it = row_info(g, (int)tile * F::ROWS + r, rows, head0, off, nk);
+          if (!it.valid || d >= g.D) continue;
+          float top = -kInf, total = 0.f, v = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) top = fmaxf(top, jm[w * 32 + r].x);
+          const float base = top == -kInf ? 0.f : top;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float f = exp2_fast(jm[w * 32 + r].x - base);
+            total += f * jm[w * 32 + r].y;
+            v += f * jo[(w * DP + d) * 33 + r];
+          }
+          const int64_t token = (int64_t)q0 + it.token;
+          if (a.po) {
+            const int64_t at = ((int64_t)split * g.Tq + token) * g.heads + it.head;
+            a.po[at * g.D + d] = v;
+            if (d == 0) {
+              a.ml[2 * at] = top;
+              a.ml[2 * at + 1] = total;
+            }
+            continue;
+          }
+          if (d == 0)
+            a.lse[it.head * g.Tq + token] =
+                total == 0.f ? -kInf : (top + __builtin_amdgcn_logf(total)) * kLn2;
+          const float y = total == 0.f ? 0.f : v / total;
+          char* p = const_cast<char*>(row_at<DT>(a.o, token, it.head));
+          if constexpr (DT == 0) reinterpret_cast<float*>(p)[d] = y;
+          else reinterpret_cast<uint16_t*>(p)[d] = (uint16_t)pack_bf16(y, 0.f);
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------ gradient of q
+
+template <int DT, int DP>
+struct BwdShape {
+  typedef Tile<DT, DP> T;
+  static constexpr int KEYS = DT == 0 ? 32 : 64;  // keys, or rows, of a tile
+  static constexpr int TILE_BYTES = KEYS * T::ROW_BYTES;
+  static constexpr int LDS = 2 * TILE_BYTES;
+};
+
+// Waves as in the forward pass.  Writes delta for the gradients of k and v, and
+// with a bias the sums of dS by bucket over the item: each wave adds its blocks'
+// distances up in two lines of its own in LDS (one a half of the lanes, so that
+// no instruction meets an address twice and the order is the program's), blocks
+// beyond reach in registers.
+template <int DT, int DP, bool BIAS>
+__global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_backward_q(
+    AttnBwd a) {
+  typedef BwdShape<DT, DP> F;
+  typedef Tile<DT, DP> T;
+  constexpr int DB = DP / 32, DC = DP / 16, SB = F::KEYS / 32;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  char* const lk = lds;
+  char* const lv = lds + F::TILE_BYTES;
+  const AttnShape& g = a.g;
+  const int lines = BIAS ? bias_line_size(g.bias) : 0;
+  float* const line = reinterpret_cast<float*>(lds + F::LDS);
+  float* const sums = line + lines;  // [8][lines]
+  float* const far = sums + 8 * lines;  // [4][2]
+  const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
+
+  if (blockIdx.x >= g.launched) {
+    const int64_t id = (int64_t)(blockIdx.x - g.launched) * 256 + threadIdx.x;
+    const int64_t step = (int64_t)(gridDim.x - g.launched) * 256;
+    const int64_t from = bound(g.start_q, 0, g.Tq), to = bound(g.start_q, g.S, g.Tq);
+    clear_tokens<DT>(a.g_q, 0, from, g.heads, g.D, id, step);
+    clear_tokens<DT>(a.g_q, max(from, to), g.Tq, g.heads, g.D, id, step);
+    return;
+  }
+
+  for (int64_t item = first_item(g.launched); item < g.items; item += g.launched) {
+    int64_t rest = item;
+    const int64_t tile0 = g.tiles - 1 - rest % g.tiles;
+    rest /= g.tiles;
+    const int unit = (int)(rest % (g.kv_heads * g.groups));
+    const int64_t seq = rest / (g.kv_heads * g.groups);
+    const int head0 = unit * g.pack, kvh = unit / g.groups;
+    int q0, nq, k0, nk;
+    sequence(g.start_q, seq, g.Tq, q0, nq);
+    sequence(g.start_k, seq, g.Tk, k0, nk);
+    const int rows = nq * g.pack, off = nk - nq;
+    float far_low = 0.f, far_high = 0.f;
+    if constexpr (BIAS) {
+      __syncthreads();
+      load_bias_line(g.bias, head0, g.heads, line);
+      for (int i = threadIdx.x; i < 8 * lines; i += 256) sums[i] = 0.f;
+    }
+
+    for (int64_t tile = tile0; tile * ATTN_ROWS < rows; tile += g.tiles) {
+      const int row0 = (int)tile * ATTN_ROWS + wave * 32;
+      RowInfo me = row_info(g, row0 + (lane & 31), rows, head0, off, nk);
+      if (!me.valid) me.limit = 0;  // no key: such rows go through the masked form
+      const int first = wave_min(me.limit), last = wave_max_int(me.limit);
+      int end = nk;
+      if (g.causal) {
+        const int r = min(rows, (int)(tile + 1) * ATTN_ROWS) - 1;
+        end = max(0, min(nk, (int)((unsigned)r / (unsigned)g.pack) + off + 1));
+      }
+
+      Frag<DT> qf[DC], gf[DC];
+      float lse = kInf, delta = 0.f;
+      const int64_t token = (int64_t)q0 + (me.valid ? me.token : 0);
+      {
+        const char* pq = row_at<DT>(a.q, token, me.head);
+        const char* pg = row_at<DT>(a.g_o, token, me.head);
+        const char* po = row_at<DT>(a.o, token, me.head);
+#pragma unroll
+        for (int c = 0; c < DC; ++c) {
+          qf[c] = gf[c] = zero_frag<DT>();
+          if (me.valid) {
+            const int d = 16 * c + 8 * half;
+            qf[c] = global_frag<DT>(pq, d, g.D, a.q.vec);
+            gf[c] = global_frag<DT>(pg, d, g.D, a.g_o.vec);
+            const Frag<DT> of = global_frag<DT>(po, d, g.D, a.o.vec);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              delta = __builtin_fmaf((float)gf[c][e], (float)of[e], delta);
+          }
+        }
+        delta = sum_halves(delta);
+        if (me.valid) {
+          if (half == 0) a.delta[me.head * g.Tq + token] = delta;
+          lse = a.lse[me.head * g.Tq + token] * kLog2e;
+          if (lse == -kInf) lse = kInf;  // no key seen: probabilities of zero
+        }
+      }
+      f32x16 dq[DB];
+#pragma unroll
+      for (int d = 0; d < DB; ++d) dq[d] = (f32x16)(0.f);
+
+      Stage<DT, DP, F::KEYS> sk, sv;
+      const auto krow = [&](const AttnRows& t, int key) -> const void* {
+        return key < end ? row_at<DT>(t, (int64_t)k0 + key, kvh) : nullptr;
+      };
+      sk.load([&](int r) { return krow(a.k, r); }, g.D, a.k.vec);
+      sv.load([&](int r) { return krow(a.v, r); }, g.D, a.v.vec);
+      for (int key = 0; key < end; key += F::KEYS) {
+        __syncthreads();
+        sk.store(lk);
+        sv.store(lv);
+        __syncthreads();
+        if (key + F::KEYS < end) {
+          sk.load([&](int r) { return krow(a.k, key + F::KEYS + r); }, g.D, a.k.vec);
+          sv.load([&](int r) { return krow(a.v, key + F::KEYS + r); }, g.D, a.v.vec);
+        }
+        if (key >= last) continue;
+        const bool whole = key + F::KEYS <= first;
+#pragma unroll
+        for (int b = 0; b < SB; ++b) {
+          f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
+#pragma unroll
+          for (int c = 0; c < DC; ++c) {
+            const int r = 32 * b + (lane & 31), d = 16 * c + 8 * half;
+            s = mma(T::row_frag(lk, r, d), qf[c], s);
+            dp = mma(T::row_frag(lv, r, d), gf[c], dp);
+          }
+          const int base = key + 32 * b - me.pos + 4 * half;
+          const int dist = key + 32 * b - (row0 + off);
+          add_bias<BIAS>(g, line, s, dist - 31, dist + 31, base, false);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) s[r] = exp2_fast(s[r] - lse) * (dp[r] - delta);
+          const int limit = me.limit - key - 32 * b;
+          if (!whole) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (acc_row(r) + 4 * half >= limit) s[r] = 0.f;
+          }
+          if constexpr (BIAS) {
+            if (dist - 31 >= g.bias.reach || dist + 31 <= -g.bias.reach) {
+              float sum = 0.f;
+#pragma unroll
+              for (int r = 0; r < 16; ++r) sum += s[r];
+              if (dist > 0) far_high += sum;
+              else far_low += sum;
+            } else {
+              float* at = sums + (2 * wave + half) * lines + base + g.bias.reach + BIAS_MARGIN;
+#pragma unroll
+              for (int r = 0; r < 16; ++r)
+                __hip_atomic_fetch_add(at + acc_row(r), s[r], __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_WORKGROUP);
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const Frag<DT> ds = acc_frag<DT>(s, c);
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+              const Frag<DT> kf = T::col_frag(lk, 32 * b + 16 * c, 32 * d);
+              if (whole) dq[d] = mma(kf, ds, dq[d]);
+              else
+                dq[d] = mma_seen<DT>(kf, ds, dq[d], [&](int i) { return 16 * c + i < limit; });
+            }
+          }
+        }
+      }
+      if (me.valid) {
+        char* p = const_cast<char*>(row_at<DT>(a.g_q, token, me.head));
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; r += 4)
+            store4<DT>(p, 32 * d + acc_row(r) + 4 * half, g.D, a.g_q.vec, dq[d][r] * g.scale,
+                       dq[d][r + 1] * g.scale, dq[d][r + 2] * g.scale, dq[d][r + 3] * g.scale);
+      }
+    }
+
+    if constexpr (BIAS) {
+      far_low = lanes_sum<64>(far_low);
+      far_high = lanes_sum<64>(far_high);
+      if (lane == 0) {
+        far[2 * wave] = far_low;
+        far[2 * wave + 1] = far_high;
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < lines; i += 256) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v += sums[w * lines + i];
+        line[i] = v;
+      }
+      __syncthreads();
+      for (int b = threadIdx.x; b < g.bias.buckets; b += 256) {
+        float v = 0.f;
+        const int reach = g.bias.reach + BIAS_MARGIN;
+        for (int i = 0; i < lines; ++i)
+          if (bias_bucket(g.bias, i - reach) == b) v += line[i];
+        for (int w = 0; w < 4; ++w) {
+          if (bias_bucket(g.bias, -reach) == b) v += far[2 * w];
+          if (bias_bucket(g.bias, reach) == b) v += far[2 * w + 1];
+        }
+        a.g_line[item * g.bias.buckets + b] = v;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------ gradients of k and v
+
+// A work item is 128 keys of one sequence and key head, 32 a wave; it goes
+// through the query rows of the heads that share them.
+template <int DT, int DP, bool BIAS>
+__global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_backward_kv(
+    AttnBwd a) {
+  typedef BwdShape<DT, DP> F;
+  typedef Tile<DT, DP> T;
+  constexpr int DB = DP / 32, DC = DP / 16, SB = F::KEYS / 32;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  char* const lq = lds;
+  char* const lg = lds + F::TILE_BYTES;
+  float* const stat = reinterpret_cast<float*>(lds + F::LDS);  // lse, delta of the rows
+  float* const line = stat + 2 * F::KEYS;
+  const AttnShape& g = a.g;
+  const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
+
+  if (blockIdx.x >= g.launched) {
+    const int64_t id = (int64_t)(blockIdx.x - g.launched) * 256 + threadIdx.x;
+    const int64_t step = (int64_t)(gridDim.x - g.launched) * 256;
+    const int64_t from = bound(g.start_k, 0, g.Tk), to = bound(g.start_k, g.S, g.Tk);
+    for (int part = 0; part < 2; ++part) {
+      const int64_t x = part ? max(from, to) : 0, y = part ? g.Tk : from;
+      clear_tokens<DT>(a.g_k, x, y, g.kv_heads, g.D, id, step);
+      clear_tokens<DT>(a.g_v, x, y, g.kv_heads, g.D, id, step);
+    }
+    return;
+  }
+
+  for (int64_t item = first_item(g.launched); item < g.items; item += g.launched) {
+    int64_t rest = item;
+    const int64_t tile0 = rest % g.tiles;  // first keys are seen by most rows
+    rest /= g.tiles;
+    const int kvh = (int)(rest % g.kv_heads);
+    const int64_t seq = rest / g.kv_heads;
+    int q0, nq, k0, nk;
+    sequence(g.start_q, seq, g.Tq, q0, nq);
+    sequence(g.start_k, seq, g.Tk, k0, nk);
+    const int rows = nq * g.pack, off = nk - nq;
+
+    for (int64_t tile = tile0; tile * ATTN_ROWS < nk; tile += g.tiles) {
+      const int wkey = (int)tile * ATTN_ROWS + wave * 32, key = wkey + (lane & 31);
+      const bool valid = key < nk;
+      Frag<DT> kf[DC], vf[DC];
+      {
+        const int64_t token = (int64_t)k0 + (valid ? key : 0);
+        const char* pk = row_at<DT>(a.k, token, kvh);
+        const char* pv = row_at<DT>(a.v, token, kvh);
+#pragma unroll
+        for (int c = 0; c < DC; ++c) {
+          const int d = 16 * c + 8 * half;
+          kf[c] = valid ? global_frag<DT>(pk, d, g.D, a.k.vec) : zero_frag<DT>();
+          vf[c] = valid ? global_frag<DT>(pv, d, g.D, a.v.vec) : zero_frag<DT>();
+        }
+      }
+      f32x16 dk[DB], dv[DB];
+#pragma unroll
+      for (int d = 0; d < DB; ++d) dk[d] = dv[d] = (f32x16)(0.f);
+      // first row that sees the tile's first key; this wave's first key
+      int begin = 0, mine = 0;
+      if (g.causal) {
+        begin = max(0, (int)tile * ATTN_ROWS - off) * g.pack / F::KEYS * F::KEYS;
+        mine = max(0, wkey - off) * g.pack;
+      }
+      const int sees = g.causal ? max(0, key - off) * g.pack : 0;      // first row of this key
+      const int all = g.causal ? max(0, wkey + 31 - off) * g.pack : 0;  // of the wave's last
+
+      for (int group = 0; group < g.groups; ++group) {
+        const int head0 = (kvh * g.groups + group) * g.pack;
+        if constexpr (BIAS) {
+          __syncthreads();
+          load_bias_line(g.bias, head0, g.heads, line);
+        }
+        Stage<DT, DP, F::KEYS> sq, sg;
+        float st = 0.f;
+        const auto fetch = [&](int row) {
+          const auto at = [&](const AttnRows& t, int r) -> const void* {
+            if (r >= rows) return nullptr;
+            const int tok = g.pack == 1 ? r : (int)((unsigned)r / (unsigned)g.pack);
+            return row_at<DT>(t, (int64_t)q0 + tok, head0 + r - tok * g.pack);
+          };
+          sq.load([&](int r) { return at(a.q, row + r); }, g.D, a.q.vec);
+          sg.load([&](int r) { return at(a.g_o, row + r); }, g.D, a.g_o.vec);
+          if (threadIdx.x < 2 * F::KEYS) {
+            const int r = row + (int)threadIdx.x % F::KEYS;
+            const bool first = threadIdx.x < F::KEYS;
+            st = first ? kInf : 0.f;
+            if (r < rows) {
+              const int tok = g.pack == 1 ? r : (int)((unsigned)r / (unsigned)g.pack);
+              const int64_t i = (head0 + r - tok * g.pack) * g.Tq + q0 + tok;
+              st = first ? a.lse[i] * kLog2e : a.delta[i];
+              if (first && st == -kInf) st = kInf;
+            }
+          }
+        };
+        if (begin < rows) fetch(begin);
+        for (int row = begin; row < rows; row += F::KEYS) {
+          __syncthreads();
+          sq.store(lq);
+          sg.store(lg);
+          if (threadIdx.x < 2 * F::KEYS) stat[threadIdx.x] = st;
+          __syncthreads();
+          if (row + F::KEYS < rows) fetch(row + F::KEYS);
+          if (row + F::KEYS <= mine) continue;
+          const bool whole = row >= all && row + F::KEYS <= rows && wkey + 32 <= nk;
+#pragma unroll
+          for (int b = 0; b < SB; ++b) {
+            f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
+#pragma unroll
+            for (int c = 0; c < DC; ++c) {
+              const int r = 32 * b + (lane & 31), d = 16 * c + 8 * half;
+              s = mma(T::row_frag(lq, r, d), kf[c], s);
+              dp = mma(T::row_frag(lg, r, d), vf[c], dp);
+            }
+            const int r0 = row + 32 * b;
+            if constexpr (BIAS) {
+              const int dist = wkey - (r0 + off);
+              add_bias<true>(g, line, s, dist - 31, dist + 31, key - (r0 + off) - 4 * half, true);
+            } else {
+              add_bias<false>(g, nullptr, s, 0, 0, 0, false);
+            }
+            f32x16 ds;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float4 lse = *reinterpret_cast<const float4*>(stat + 32 * b + 8 * q + 4 * half);
+              const float4 del =
+                  *reinterpret_cast<const float4*>(stat + F::KEYS + 32 * b + 8 * q + 4 * half);
+              const float ls[4] = {lse.x, lse.y, lse.z, lse.w};
+              const float de[4] = {del.x, del.y, del.z, del.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = 4 * q + i;
+                s[r] = exp2_fast(s[r] - ls[i]);
+                ds[r] = s[r] * (dp[r] - de[i]);
+              }
+            }
+            const int low = sees - r0, high = valid ? rows - r0 : 0;
+            if (!whole) {
+#pragma unroll
+              for (int r = 0; r < 16; ++r) {
+                const int i = acc_row(r) + 4 * half;
+                if (i < low || i >= high) s[r] = ds[r] = 0.f;
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const Frag<DT> pf = acc_frag<DT>(s, c), df = acc_frag<DT>(ds, c);
+#pragma unroll
+              for (int d = 0; d < DB; ++d) {
+                const Frag<DT> gf = T::col_frag(lg, 32 * b + 16 * c, 32 * d);
+                const Frag<DT> qf = T::col_frag(lq, 32 * b + 16 * c, 32 * d);
+                if (whole) {
+                  dv[d] = mma(gf, pf, dv[d]);
+                  dk[d] = mma(qf, df, dk[d]);
+                } else {
+                  const auto seen = [&](int i) { return 16 * c + i >= low && 16 * c + i < high; };
+                  dv[d] = mma_seen<DT>(gf, pf, dv[d], seen);
+                  dk[d] = mma_seen<DT>(qf, df, dk[d], seen);
+                }
+              }
+            }
+          }
+        }
+      }
+      if (valid) {
+        char* pk = const_cast<char*>(row_at<DT>(a.g_k, (int64_t)k0 + key, kvh));
+        char* pv = const_cast<char*>(row_at<DT>(a.g_v, (int64_t)k0 + key, kvh));
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; r += 4) {
+            const int e = 32 * d + acc_row(r) + 4 * half;
+            store4<DT>(pv, e, g.D, a.g_v.vec, dv[d][r], dv[d][r + 1], dv[d][r + 2], dv[d][r + 3]);
+            store4<DT>(pk, e, g.D, a.g_k.vec, dk[d][r] * g.scale, dk[d][r + 1] * g.scale,
+                       dk[d][r + 2] * g.scale, dk[d][r + 3] * g.scale);
+          }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------ launches
+
+constexpr unsigned GAP_GROUPS = 8;  // workgroups for the tokens of no sequence
+
+// Workgroups for the items: at most 2^20 (a launch holds fewer than 2^32
+// threads; the rest go by the loop), in multiples of 8 for the XCDs.
+unsigned groups_for(int64_t items) {
+  const int64_t n = (items + 7) / 8 * 8;
+  return (unsigned)(n < (1 << 20) ? n : 1 << 20);
+}
+
+template <typename A>
+hipError_t launch_items(void (*kernel)(A), A a, int bytes, bool gaps, hipStream_t s) {
+  a.g.launched = groups_for(a.g.items);
+  if (bytes > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) {
+      (void)hipGetLastError();
+      return e;
+    }
+  }
+  void* at[] = {&a};
+  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel),
+                                       dim3(a.g.launched + (gaps ? GAP_GROUPS : 0)), dim3(256), at,
+                                       bytes, s);
+  if (e != hipSuccess) (void)hipGetLastError();
+  return e;
+}
+
+int line_bytes(const AttnShape& g, int lines) {
+  return g.bias.table ? 2 * (g.bias.reach + BIAS_MARGIN) * 4 * lines + 4 * lines : 0;
+}
+
+template <int DT, int DP, bool BIAS>
+hipError_t forward(const AttnFwd& a, bool few, hipStream_t s) {
+  const bool gaps = a.g.start_q != nullptr;
+  if (few)
+    return launch_items(k_attention_forward<DT, DP, BIAS, true>, a,
+                        FwdShape<DT, DP, true>::LDS + line_bytes(a.g, 1), gaps, s);
+  return launch_items(k_attention_forward<DT, DP, BIAS, false>, a,
+                      FwdShape<DT, DP, false>::LDS + line_bytes(a.g, 1), gaps, s);
+}
+
+}  // namespace
+
+template <>
+hipError_t launch_attention_forward<HLQ_ATTN_D>(const AttnFwd& a, int dtype, bool few,
+                                                hipStream_t s) {
+  constexpr int DP = HLQ_ATTN_D;
+  if (dtype == 0)
+    return a.g.bias.table ? forward<0, DP, true>(a, few, s) : forward<0, DP, false>(a, few, s);
+  return a.g.bias.table ? forward<1, DP, true>(a, few, s) : forward<1, DP, false>(a, few, s);
+}
+
+template <>
+hipError_t launch_attention_backward_q<HLQ_ATTN_D>(const AttnBwd& a, int dtype, hipStream_t s) {
+  constexpr int DP = HLQ_ATTN_D;
+  const bool gaps = a.g.start_q != nullptr;
+  const int lines = line_bytes(a.g, 9) + (a.g.bias.table ? 32 : 0);
+  if (dtype == 0)
+    return launch_items(a.g.bias.table ? k_attention_backward_q<0, DP, true>
+                                       : k_attention_backward_q<0, DP, false>,
+                        a, BwdShape<0, DP>::LDS + lines, gaps, s);
+  return launch_items(a.g.bias.table ? k_attention_backward_q<1, DP, true>
+                                     : k_attention_backward_q<1, DP, false>,
+                      a, BwdShape<1, DP>::LDS + lines, gaps, s);
+}
+
+template <>
+hipError_t launch_attention_backward_kv<HLQ_ATTN_D>(const AttnBwd& a, int dtype, hipStream_t s) {
+  constexpr int DP = HLQ_ATTN_D;
+  const bool gaps = a.g.start_k != nullptr;
+  const int lines = line_bytes(a.g, 1);
+  if (dtype == 0)
+    return launch_items(a.g.bias.table ? k_attention_backward_kv<0, DP, true>
+                                       : k_attention_backward_kv<0, DP, false>,
+                        a, BwdShape<0, DP>::LDS + 8 * BwdShape<0, DP>::KEYS + lines, gaps, s);
+  return launch_items(a.g.bias.table ? k_attention_backward_kv<1, DP, true>
+                                     : k_attention_backward_kv<1, DP, false>,
+                      a, BwdShape<1, DP>::LDS + 8 * BwdShape<1, DP>::KEYS + lines, gaps, s);
+}
+
+}  // namespace hlq

@@ -1,0 +1,339 @@
+// C ABI of the attention block's operators: attention over packed sequences,
+// forward and backward, with the relative position bias, and dropout.  Argument
+// validation, workspace sizes and launches; the arithmetic is in
+// hlq_attention.hip, hlq_attention_fold.hip and hlq_dropout.hip.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdlib>
+#include <stdint.h>
+
+#include "../../include/hlq.h"
+#include "hlq_internal.h"
+
+namespace {
+
+using hlq::AttnBwd;
+using hlq::AttnFwd;
+using hlq::AttnRows;
+using hlq::AttnShape;
+
+constexpr int64_t kRows = int64_t(1) << 30;    // queries times heads, and keys times heads
+constexpr int64_t kStride = int64_t(1) << 40;  // elements
+
+bool dtype_ok(int dt) { return dt == HLQ_F32 || dt == HLQ_BF16; }
+size_t esize(int dt) { return dt == HLQ_F32 ? 4 : 2; }
+bool aligned(const void* p, size_t bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
+// First distances of the buckets exact .. side - 1 of a side:
+//   exact + floor((side - exact) log(n / exact) / log(reach / exact)) = k.
+// The share of a distance that begins a bucket is a whole number up to rounding
+// (2^-50 or so); shares that are not differ from one by more than 2^-30 at the
+// sizes allowed here, so 2^-40 tells the two apart.
+void bucket_bounds(hlq::AttnBias& b) {
+  const double span = std::log((double)b.reach / b.exact);
+  int k = b.exact;
+  b.first[k] = (int16_t)b.exact;
+  for (int n = b.exact; n <= b.reach; ++n) {
+    const double share = (b.side - b.exact) * (std::log((double)n / b.exact) / span);
+    const int at = std::min(b.side - 1, b.exact + (int)std::floor(share + 0x1p-40));
+    while (k < at) b.first[++k] = (int16_t)n;
+  }
+}
+
+hlq_status check_shape(const hlq_attention* a) {
+  if (!a) return HLQ_ERR_NULL;
+  if (!dtype_ok(a->dtype) || (a->bias && !dtype_ok(a->bias_dtype))) return HLQ_ERR_DTYPE;
+  if (a->queries < 0 || a->keys < 0 || a->sequences < 1 || a->heads < 1 || a->kv_heads < 1 ||
+      a->heads % a->kv_heads || a->head_dim < 1 || a->head_dim > 128 || a->max_len < 0)
+    return HLQ_ERR_SHAPE;
+  if (a->heads >= (1 << 16) || a->sequences >= kRows || a->queries >= kRows / a->heads ||
+      a->keys >= kRows / a->heads)
+    return HLQ_ERR_SHAPE;
+  if (!a->start_q && (a->sequences != 1 || a->start_k)) return HLQ_ERR_SHAPE;
+  if (!a->start_k && a->start_q && a->queries != a->keys) return HLQ_ERR_SHAPE;
+  if (!(a->scale > 0.0) || !(a->scale <= 0x1p64) || a->scale < 0x1p-64) return HLQ_ERR_VALUE;
+  if (a->bias) {
+    const int side = a->bidirectional ? a->buckets / 2 : a->buckets;
+    if (a->buckets > 128 || (a->bidirectional && a->buckets % 2) || side < 2 ||
+        a->max_distance <= side / 2 || a->max_distance > 1024)
+      return HLQ_ERR_VALUE;
+    if (!aligned(a->bias, esize(a->bias_dtype))) return HLQ_ERR_ALIGN;
+  }
+  if (!aligned(a->start_q, 8) || !aligned(a->start_k, 8)) return HLQ_ERR_ALIGN;
+  return HLQ_OK;
+}
+
+// Pointer and strides of a tensor of `tokens` x `heads` rows; out: rows that do not
+// overlap.
+hlq_status check_rows(const hlq_attention* a, const hlq_tokens* t, int64_t tokens, int heads,
+                      bool out) {
+  if (!t) return HLQ_ERR_NULL;
+  if (tokens == 0) return HLQ_OK;
+  if (!t->data) return HLQ_ERR_NULL;
+  if (!aligned(t->data, esize(a->dtype))) return HLQ_ERR_ALIGN;
+  if (t->token_stride < 0 || t->head_stride < 0 || t->token_stride >= kStride ||
+      t->head_stride >= kStride)
+    return HLQ_ERR_SHAPE;
+  if (out) {
+    const int64_t D = a->head_dim, ts = t->token_stride, hs = t->head_stride;
+    const bool tokens_outside = heads == 1 ? ts >= D : hs >= D && ts >= (heads - 1) * hs + D;
+    const bool heads_outside = tokens == 1 ? hs >= D : ts >= D && hs >= (tokens - 1) * ts + D;
+    if (tokens > 1 && heads > 1 && !tokens_outside && !heads_outside) return HLQ_ERR_SHAPE;
+    if (tokens > 1 && heads == 1 && ts < D) return HLQ_ERR_SHAPE;
+    if (tokens == 1 && heads > 1 && hs < D) return HLQ_ERR_SHAPE;
+  }
+  return HLQ_OK;
+}
+
+AttnRows rows_of(const hlq_attention* a, const hlq_tokens* t) {
+  const int64_t es = (int64_t)esize(a->dtype);
+  AttnRows r = {t->data, t->token_stride, t->head_stride, 0};
+  r.vec = aligned(t->data, 16) && t->token_stride * es % 16 == 0 && t->head_stride * es % 16 == 0 &&
+          a->head_dim * es % 16 == 0;
+  return r;
+}
+
+AttnShape shape_of(const hlq_attention* a) {
+  AttnShape g = {};
+  g.start_q = a->start_q;
+  g.start_k = a->start_k ? a->start_k : a->start_q;
+  g.S = a->sequences;
+  g.Tq = a->queries;
+  g.Tk = a->keys;
+  g.heads = a->heads;
+  g.kv_heads = a->kv_heads;
+  g.D = a->head_dim;
+  g.causal = a->causal != 0;
+  g.scale = (float)a->scale;
+  g.c = (float)(a->scale * 1.4426950408889634074);
+  g.splits = 1;
+  const int shared = a->heads / a->kv_heads;
+  g.pack = a->bias ? 1 : shared;
+  g.groups = shared / g.pack;
+  if (a->bias) {
+    hlq::AttnBias& b = g.bias;
+    b.table = a->bias;
+    b.dtype = a->bias_dtype;
+    b.buckets = a->buckets;
+    b.reach = a->max_distance;
+    b.bidirectional = a->bidirectional != 0;
+    b.side = b.bidirectional ? a->buckets / 2 : a->buckets;
+    b.exact = b.side / 2;
+    bucket_bounds(b);
+  }
+  return g;
+}
+
+// How long the sequences are taken to be, where the launch needs a number: the
+// caller's longest one, or twice the mean.  Longer ones are looped over.
+int64_t expected(const hlq_attention* a, int64_t total) {
+  const int64_t mean = (total + a->sequences - 1) / a->sequences;
+  const int64_t guess = std::min(total, 2 * mean);
+  return std::max<int64_t>(1, a->max_len ? std::min(total, a->max_len) : guess);
+}
+
+struct FwdPlan {
+  bool few;
+  int64_t tiles, items;
+  int splits;
+};
+
+// Few rows leave most of the chip idle if a workgroup takes all keys of its rows;
+// their keys are shared out until there are about two workgroups a CU, with 256
+// keys each at least.
+FwdPlan plan_forward(const hlq_attention* a) {
+  const int shared = a->bias ? 1 : a->heads / a->kv_heads;
+  const int64_t rows = expected(a, a->queries) * shared;
+  FwdPlan p;
+  p.few = rows <= hlq::ATTN_FEW;
+  const int per = p.few ? hlq::ATTN_FEW : hlq::ATTN_ROWS;
+  p.tiles = (rows + per - 1) / per;
+  const int64_t units = p.tiles * a->sequences * (a->heads / shared);
+  const int64_t keys = a->keys / a->sequences;
+  int64_t splits = std::min<int64_t>((512 + units - 1) / units, keys / 256);
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(splits, 64));
+  p.items = units * p.splits;
+  return p;
+}
+
+size_t forward_bytes(const hlq_attention* a, const FwdPlan& p) {
+  if (p.splits == 1) return 0;
+  return (size_t)p.splits * a->queries * a->heads * (a->head_dim + 2) * 4;
+}
+
+int64_t backward_tiles(const hlq_attention* a) {
+  const int shared = a->bias ? 1 : a->heads / a->kv_heads;
+  return (expected(a, a->queries) * shared + hlq::ATTN_ROWS - 1) / hlq::ATTN_ROWS;
+}
+
+size_t delta_bytes(const hlq_attention* a) {
+  return ((size_t)a->queries * a->heads * 4 + 15) / 16 * 16;
+}
+
+template <typename F32, typename F64, typename F96, typename F128>
+hipError_t by_size(int D, F32 f32, F64 f64, F96 f96, F128 f128) {
+  return D <= 32 ? f32() : D <= 64 ? f64() : D <= 96 ? f96() : f128();
+}
+#define HLQ_BY_SIZE(D, f, ...)                                                             \
+  by_size(D, [&] { return hlq::f<32>(__VA_ARGS__); }, [&] { return hlq::f<64>(__VA_ARGS__); }, \
+          [&] { return hlq::f<96>(__VA_ARGS__); }, [&] { return hlq::f<128>(__VA_ARGS__); })
+
+}  // namespace
+
+#define HLQ_TRY(expr)                             \
+  do {                                            \
+    if ((expr) != hipSuccess) return HLQ_ERR_HIP; \
+  } while (0)
+#define HLQ_CHECK(expr)                  \
+  do {                                   \
+    const hlq_status st_ = (expr);       \
+    if (st_ != HLQ_OK) return st_;       \
+  } while (0)
+
+extern "C" {
+
+int hlq_relative_bucket(int distance, int buckets, int max_distance, int bidirectional) {
+  hlq::AttnBias b = {};
+  b.side = bidirectional ? buckets / 2 : buckets;
+  if (buckets > 128 || (bidirectional && buckets % 2) || b.side < 2 || max_distance <= b.side / 2 ||
+      max_distance > 1024)
+    return -1;
+  b.exact = b.side / 2;
+  b.reach = max_distance;
+  bucket_bounds(b);
+  const int64_t d = distance;
+  const int64_t n = bidirectional ? std::llabs(d) : std::max<int64_t>(-d, 0);
+  int k = (int)std::min<int64_t>(n, b.exact);
+  if (n >= b.exact)
+    for (int i = b.exact + 1; i < b.side; ++i) k += n >= b.first[i];
+  return k + (bidirectional && d > 0 ? b.side : 0);
+}
+
+size_t hlq_attention_forward_workspace_size(const hlq_attention* a) {
+  if (check_shape(a) != HLQ_OK) return 0;
+  return forward_bytes(a, plan_forward(a));
+}
+
+hlq_status hlq_attention_forward(const hlq_attention* a, const hlq_tokens* q, const hlq_tokens* k,
+                                 const hlq_tokens* v, const hlq_tokens* o, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  HLQ_CHECK(check_shape(a));
+  HLQ_CHECK(check_rows(a, q, a->queries, a->heads, false));
+  HLQ_CHECK(check_rows(a, k, a->keys, a->kv_heads, false));
+  HLQ_CHECK(check_rows(a, v, a->keys, a->kv_heads, false));
+  HLQ_CHECK(check_rows(a, o, a->queries, a->heads, true));
+  if (a->queries && !lse) return HLQ_ERR_NULL;
+  if (!aligned(lse, 4)) return HLQ_ERR_ALIGN;
+  const FwdPlan p = plan_forward(a);
+  const size_t need = forward_bytes(a, p);
+  if (need && (!workspace || workspace_bytes < need)) return HLQ_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return HLQ_ERR_ALIGN;
+  if (a->queries == 0) return HLQ_OK;
+  AttnFwd f = {};
+  f.g = shape_of(a);
+  f.q = rows_of(a, q);
+  f.k = rows_of(a, k);
+  f.v = rows_of(a, v);
+  f.o = rows_of(a, o);
+  f.lse = lse;
+  f.g.tiles = p.tiles;
+  f.g.items = p.items;
+  f.g.splits = p.splits;
+  if (need) {
+    f.ml = static_cast<float*>(workspace);
+    f.po = f.ml + (size_t)p.splits * a->queries * a->heads * 2;
+  }
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  HLQ_TRY(HLQ_BY_SIZE(a->head_dim, launch_attention_forward, f, a->dtype, p.few, s));
+  if (need) HLQ_TRY(hlq::launch_attention_join(f, a->dtype, s));
+  return HLQ_OK;
+}
+
+size_t hlq_attention_backward_workspace_size(const hlq_attention* a) {
+  if (check_shape(a) != HLQ_OK) return 0;
+  size_t bytes = delta_bytes(a);
+  if (a->bias)
+    bytes += (size_t)backward_tiles(a) * a->sequences * a->heads * a->buckets * 4;
+  return bytes;
+}
+
+hlq_status hlq_attention_backward(const hlq_attention* a, const hlq_tokens* g_o,
+                                  const hlq_tokens* q, const hlq_tokens* k, const hlq_tokens* v,
+                                  const hlq_tokens* o, const float* lse, const hlq_tokens* g_q,
+                                  const hlq_tokens* g_k, const hlq_tokens* g_v, void* g_bias,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  HLQ_CHECK(check_shape(a));
+  HLQ_CHECK(check_rows(a, g_o, a->queries, a->heads, false));
+  HLQ_CHECK(check_rows(a, q, a->queries, a->heads, false));
+  HLQ_CHECK(check_rows(a, k, a->keys, a->kv_heads, false));
+  HLQ_CHECK(check_rows(a, v, a->keys, a->kv_heads, false));
+  HLQ_CHECK(check_rows(a, o, a->queries, a->heads, false));
+  HLQ_CHECK(check_rows(a, g_q, a->queries, a->heads, true));
+  HLQ_CHECK(check_rows(a, g_k, a->keys, a->kv_heads, true));
+  HLQ_CHECK(check_rows(a, g_v, a->keys, a->kv_heads, true));
+  if ((a->queries && !lse) || (a->bias != nullptr) != (g_bias != nullptr)) return HLQ_ERR_NULL;
+  if (!aligned(lse, 4) || (g_bias && !aligned(g_bias, esize(a->bias_dtype)))) return HLQ_ERR_ALIGN;
+  const size_t need = hlq_attention_backward_workspace_size(a);
+  if (need && (!workspace || workspace_bytes < need)) return HLQ_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return HLQ_ERR_ALIGN;
+  AttnBwd b = {};
+  b.g = shape_of(a);
+  b.q = rows_of(a, q);
+  b.k = rows_of(a, k);
+  b.v = rows_of(a, v);
+  b.o = rows_of(a, o);
+  b.g_o = rows_of(a, g_o);
+  b.g_q = rows_of(a, g_q);
+  b.g_k = rows_of(a, g_k);
+  b.g_v = rows_of(a, g_v);
+  b.lse = lse;
+  b.delta = static_cast<float*>(workspace);
+  b.g_line = reinterpret_cast<float*>(static_cast<char*>(workspace) + delta_bytes(a));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  b.g.tiles = backward_tiles(a);
+  b.g.items = b.g.tiles * a->sequences * (a->heads / b.g.pack);
+  // with a bias also for no queries: the table's gradient is then zero
+  if (a->queries || a->bias)
+    HLQ_TRY(HLQ_BY_SIZE(a->head_dim, launch_attention_backward_q, b, a->dtype, s));
+  if (a->bias)
+    HLQ_TRY(hlq::launch_attention_bias(b.g_line, a->sequences, b.g.tiles, a->heads, a->buckets,
+                                       a->bias_dtype, g_bias, s));
+  if (a->keys) {
+    b.g.tiles = (expected(a, a->keys) + hlq::ATTN_ROWS - 1) / hlq::ATTN_ROWS;
+    b.g.items = b.g.tiles * a->sequences * a->kv_heads;
+    HLQ_TRY(HLQ_BY_SIZE(a->head_dim, launch_attention_backward_kv, b, a->dtype, s));
+  }
+  return HLQ_OK;
+}
+
+static hlq_status dropout(const void* x, const void* residual, int dtype, int64_t n, double p,
+                          const int64_t* seed, uint32_t site, void* y, void* stream) {
+  if (!seed || (n && (!x || !y))) return HLQ_ERR_NULL;
+  if (!dtype_ok(dtype)) return HLQ_ERR_DTYPE;
+  if (n < 0 || n >= (int64_t(1) << 35)) return HLQ_ERR_SHAPE;
+  if (!(p >= 0.0 && p <= 1.0)) return HLQ_ERR_VALUE;
+  if (!aligned(x, esize(dtype)) || !aligned(residual, esize(dtype)) || !aligned(y, esize(dtype)) ||
+      !aligned(seed, 8))
+    return HLQ_ERR_ALIGN;
+  hlq::DropArgs a = {x, residual, y, n, seed, site, 0, 0.f};
+  a.limit = (uint32_t)std::nearbyint(p * 65536.0);  // ties to even, as in the definition
+  a.scale = a.limit < 65536 ? (float)(65536.0 / (65536 - a.limit)) : 0.f;
+  HLQ_TRY(hlq::launch_dropout(a, dtype, static_cast<hipStream_t>(stream)));
+  return HLQ_OK;
+}
+
+hlq_status hlq_dropout_forward(const void* x, const void* residual, int dtype, int64_t n, double p,
+                               const int64_t* seed, uint32_t site, void* y, void* stream) {
+  return dropout(x, residual, dtype, n, p, seed, site, y, stream);
+}
+
+hlq_status hlq_dropout_backward(const void* g_y, int dtype, int64_t n, double p,
+                                const int64_t* seed, uint32_t site, void* g_x, void* stream) {
+  return dropout(g_y, nullptr, dtype, n, p, seed, site, g_x, stream);
+}
+
+}  // extern "C"

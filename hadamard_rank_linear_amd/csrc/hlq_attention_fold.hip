@@ -1,0 +1,88 @@
+// What follows the attention kernels: the join of the keys' shares of a row, and
+// the sums of the position bias's gradient over the work items.
+#include "hlq_rows.h"
+
+namespace hlq {
+namespace {
+
+// A wave a row of (token, head): with (m_p, l_p) of share p in powers of two and M
+// the largest m, o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.  Lane p holds
+// share p's factor (at most 64 shares).
+template <int DT>
+__global__ __launch_bounds__(256) void k_attention_join(AttnFwd a) {
+  typedef typename Piece<DT>::Elem E;
+  const AttnShape& g = a.g;
+  const int lane = threadIdx.x & 63;
+  const int64_t rows = g.Tq * g.heads;
+  for (int64_t r = blockIdx.x * 4ll + (threadIdx.x >> 6); r < rows; r += gridDim.x * 4ll) {
+    float m = -__builtin_inff(), l = 0.f;
+    if (lane < g.splits) {
+      const float2 v = *reinterpret_cast<const float2*>(a.ml + (lane * rows + r) * 2);
+      m = v.x;
+      l = v.y;
+    }
+    const float top = lanes_max(m), base = top == -__builtin_inff() ? 0.f : top;
+    const float f = __builtin_amdgcn_exp2f(m - base);
+    const float total = lanes_sum<64>(f * l);
+    const int64_t token = r / g.heads;
+    const int head = (int)(r % g.heads);
+    E* const o = static_cast<E*>(a.o.data) + token * a.o.token + head * a.o.head;
+    for (int d = lane; d - lane < g.D; d += 64) {
+      float v = 0.f;
+      for (int p = 0; p < g.splits; ++p) {
+        const float w = __shfl(f, p), k = __shfl(l, p);
+        // a share that has seen no key has written no sums
+        if (d < g.D && k != 0.f) v += w * a.po[(p * rows + r) * g.D + d];
+      }
+      v = total == 0.f ? 0.f : v / total;
+      if (d < g.D) {
+        if constexpr (DT == 0) o[d] = v;
+        else o[d] = (uint16_t)pack_bf16(v, 0.f);
+      }
+    }
+    if (lane == 0)
+      a.lse[head * g.Tq + token] = total == 0.f
+                                       ? -__builtin_inff()
+                                       : (top + __builtin_amdgcn_logf(total)) * 0.69314718055994530942f;
+  }
+}
+
+// g_bias[bucket][head]: a workgroup a head; thread t adds bucket t % buckets of
+// every 256 / buckets-th item, then one sum over the threads of a bucket.  fp64.
+__global__ __launch_bounds__(256) void k_attention_bias(const float* part, int64_t S, int64_t tiles,
+                                                        int heads, int buckets, int param_dt,
+                                                        void* g_bias) {
+  __shared__ double sm[256];
+  const int head = blockIdx.x, ways = 256 / buckets;
+  const int b = (int)threadIdx.x % buckets, way = (int)threadIdx.x / buckets;
+  double v = 0.0;
+  if (way < ways)
+    for (int64_t i = way; i < S * tiles; i += ways) {
+      const int64_t item = ((i / tiles) * heads + head) * tiles + i % tiles;
+      v += part[item * buckets + b];
+    }
+  sm[threadIdx.x] = v;
+  __syncthreads();
+  if (way == 0) {
+    for (int w = 1; w < ways; ++w) v += sm[w * buckets + b];
+    const int64_t at = (int64_t)b * heads + head;
+    if (param_dt == 0) static_cast<float*>(g_bias)[at] = (float)v;
+    else static_cast<uint16_t*>(g_bias)[at] = (uint16_t)pack_bf16((float)v, 0.f);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_attention_join(const AttnFwd& a, int dtype, hipStream_t s) {
+  const int64_t groups = (a.g.Tq * a.g.heads + 3) / 4;
+  const dim3 grid((unsigned)(groups < (1 << 20) ? groups : 1 << 20));
+  return launch(dtype == 0 ? k_attention_join<0> : k_attention_join<1>, grid, 256, s, a);
+}
+
+hipError_t launch_attention_bias(const float* part, int64_t S, int64_t tiles, int heads,
+                                 int buckets, int param_dt, void* g_bias, hipStream_t s) {
+  return launch(k_attention_bias, dim3((unsigned)heads), 256, s, part, S, tiles, heads, buckets,
+                param_dt, g_bias);
+}
+
+}  // namespace hlq

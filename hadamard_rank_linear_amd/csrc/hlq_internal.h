@@ -276,6 +276,71 @@ hipError_t launch_policy_logits(LogitArgs a, const PolicyArgs& p, int dtype, hip
 hipError_t launch_policy(const PolicyArgs& p, hipStream_t s);
 hipError_t launch_preference(PrefArgs p, hipStream_t s);
 
+// Attention over packed sequences (hlq_attention.hip, once per padded head size).
+// Rows of a sequence's queries in the kernels: row r is query r / pack, head
+// head0 + r % pack.  Without a bias the query heads that share a key head are
+// packed (pack = heads / kv_heads), with one each head goes by itself (pack = 1).
+struct AttnBias {
+  const void* table;  // [buckets][heads]; null: no bias
+  int dtype, buckets, reach, bidirectional;
+  int side, exact;    // buckets a side, those of one distance each
+  int16_t first[128];  // first distance of bucket exact .. side - 1 of a side
+};
+// A tensor [tokens][heads][D]; strides in elements.  vec: rows start at 16-byte
+// boundaries and hold whole 16-byte chunks.
+struct AttnRows {
+  void* data;
+  int64_t token, head;
+  int vec;
+};
+struct AttnShape {
+  const int64_t *start_q, *start_k;  // null: one sequence of all tokens
+  int64_t S, Tq, Tk;
+  int heads, kv_heads, D, causal;
+  int pack, groups;      // rows' heads; heads / kv_heads / pack
+  float scale, c;        // c = scale * log2(e)
+  int64_t tiles, items;  // row (or key) tiles a sequence is expected to have; all work items
+  int splits;            // of the keys (forward), of the rows (gradients of k and v)
+  unsigned launched;     // workgroups of the launch that take items
+  AttnBias bias;
+};
+struct AttnFwd {
+  AttnShape g;
+  AttnRows q, k, v, o;
+  float* lse;      // [heads][Tq]
+  float *po, *ml;  // splits > 1: [splits][Tq][heads][D] and [splits][Tq][heads][2]
+};
+struct AttnBwd {
+  AttnShape g;
+  AttnRows q, k, v, o, g_o, g_q, g_k, g_v;
+  const float* lse;
+  float *delta;   // [heads][Tq]: sum over d of g_o o
+  float *g_line;  // [items][buckets] partial sums of the bias's gradient
+};
+constexpr int ATTN_ROWS = 128;  // query rows, or keys, of a workgroup
+constexpr int ATTN_FEW = 32;    // rows of a workgroup whose waves share the keys
+template <int DP>
+hipError_t launch_attention_forward(const AttnFwd& a, int dtype, bool few, hipStream_t s);
+template <int DP>
+hipError_t launch_attention_backward_q(const AttnBwd& a, int dtype, hipStream_t s);
+template <int DP>
+hipError_t launch_attention_backward_kv(const AttnBwd& a, int dtype, hipStream_t s);
+hipError_t launch_attention_join(const AttnFwd& a, int dtype, hipStream_t s);
+// g_bias [buckets][heads] of param_dt from items' partial sums, `parts` a head
+hipError_t launch_attention_bias(const float* part, int64_t S, int64_t tiles, int heads,
+                                 int buckets, int param_dt, void* g_bias, hipStream_t s);
+
+// Dropout (hlq_dropout.hip): y = residual + keep * x * scale; residual may be null.
+struct DropArgs {
+  const void *x, *residual;
+  void* y;
+  int64_t n;
+  const int64_t* seed;
+  uint32_t site, limit;
+  float scale;
+};
+hipError_t launch_dropout(const DropArgs& a, int dtype, hipStream_t s);
+
 // Gradient clipping (hlq_clip.hip): part of a list of tensors, passed by value
 // (a kernel's arguments hold 4 KiB).  size: elements, at most 2^30, with bit 31
 // set for bf16.  Tensor i is chunks first[i] .. first[i + 1] - 1 of CLIP_BYTES;

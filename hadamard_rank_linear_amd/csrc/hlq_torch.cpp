@@ -1,4 +1,5 @@
-// Native half of the Python binding of the training step's operators: checks
+// Native half of the Python binding of the training step's operators, those of
+// the attention block among them: checks
 // of tensors, allocation of outputs and workspaces, the current stream and the
 // call of the C ABI, in one step per operator.
 //
@@ -19,6 +20,7 @@
 #include <c10/hip/HIPStream.h>
 #include <dlfcn.h>
 #include <limits.h>
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -41,7 +43,10 @@ PyObject* g_check = nullptr;  // hlq._check(name, status): raises HLQError
   F(hlq_layer_norm_backward) F(hlq_token_logprob_forward) F(hlq_token_logprob_backward)   \
   F(hlq_policy_loss_workspace_size) F(hlq_policy_loss) F(hlq_policy_loss_logits)          \
   F(hlq_preference_loss_workspace_size) F(hlq_preference_loss)                            \
-  F(hlq_clip_grad_norm_workspace_size) F(hlq_clip_grad_norm)
+  F(hlq_clip_grad_norm_workspace_size) F(hlq_clip_grad_norm)                              \
+  F(hlq_attention_forward_workspace_size) F(hlq_attention_forward)                        \
+  F(hlq_attention_backward_workspace_size) F(hlq_attention_backward)                      \
+  F(hlq_dropout_forward) F(hlq_dropout_backward)
 
 // The C ABI of the library that the Python binding has loaded.
 struct Library {
@@ -619,6 +624,217 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------------------------ attention
+
+int64_t integer64(const char* name, PyObject* o) {
+  int over = 0;
+  const long long v = PyLong_AsLongLongAndOverflow(o, &over);
+  if (v == -1 && PyErr_Occurred()) {
+    PyErr_Clear();
+    type_error("%s must be an integer, got %s", name, Py_TYPE(o)->tp_name);
+  }
+  if (over) value_error("%s is out of range", name);
+  return v;
+}
+
+// A tensor [tokens, heads, D] on the GPU of `like`, rows dense and any strides.
+void expect_rows(const char* name, const Tensor& like, const Tensor& t, ScalarType type,
+                 IntArrayRef shape) {
+  expect(name, t, type, shape);
+  on_gpu(t);
+  if (t.device() != like.device())
+    value_error("tensors on different devices: %s and %s", like.device().str().c_str(),
+                t.device().str().c_str());
+  if (t.size(2) > 1 && t.stride(2) != 1)
+    value_error("%s must be dense along its last dimension", name);
+}
+hlq_tokens view(const Tensor& t) { return {t.data_ptr(), t.stride(0), t.stride(1)}; }
+
+const Tensor* bounds(const char* name, const Tensor& like, PyObject* o) {
+  const Tensor* t = maybe(name, o);
+  if (!t) return nullptr;
+  if (t->dim() != 1 || t->numel() < 2)
+    value_error("%s must hold the sequences' bounds, [sequences + 1]", name);
+  expect(name, *t, ScalarType::Long, t->sizes());
+  same_gpu(like, {t});
+  return t;
+}
+
+// The arguments that the forward and the backward call share.
+struct Attention {
+  hlq_attention a = {};
+  const Tensor *start, *start_k, *bias;
+  // (start, start_k, causal, scale, bias, max_distance, bidirectional, max_len)
+  Attention(const Tensor& q, const Tensor& k, const Tensor& v, PyObject* const* o) {
+    if (q.dim() != 3 || k.dim() != 3)
+      value_error("q must be [queries, heads, D] and k [keys, kv_heads, D]");
+    on_gpu(q);
+    expect_rows("q", q, q, q.scalar_type(), q.sizes());
+    expect_rows("k", q, k, q.scalar_type(), {k.size(0), k.size(1), q.size(2)});
+    expect_rows("v", q, v, q.scalar_type(), k.sizes());
+    start = bounds("start", q, o[0]);
+    start_k = bounds("start_k", q, o[1]);
+    if (start_k && !start) value_error("start_k goes with start");
+    if (start_k && start_k->numel() != start->numel())
+      value_error("start_k must have as many bounds as start");
+    if (start && !start_k && q.size(0) != k.size(0))
+      value_error("without start_k there must be as many keys as queries");
+    a.dtype = code(q);
+    a.queries = q.size(0);
+    a.keys = k.size(0);
+    if (q.size(1) > INT_MAX || k.size(1) > INT_MAX || q.size(2) > INT_MAX)
+      value_error("q or k is out of range");
+    a.heads = (int)q.size(1);
+    a.kv_heads = (int)k.size(1);
+    a.head_dim = (int)q.size(2);
+    a.sequences = start ? start->numel() - 1 : 1;
+    a.start_q = ptr<const int64_t>(start);
+    a.start_k = ptr<const int64_t>(start_k);
+    a.causal = truth(o[2]);
+    a.scale = o[3] == Py_None ? 1.0 / sqrt((double)std::max(1, a.head_dim))
+                              : number("scale", o[3]);
+    bias = maybe("bias", o[4]);
+    a.max_distance = integer("max_distance", o[5]);
+    a.bidirectional = o[6] == Py_None ? !a.causal : truth(o[6]);
+    a.max_len = integer64("max_len", o[7]);
+    if (!bias) return;
+    if (bias->dim() != 2 || bias->size(0) > INT_MAX)
+      value_error("bias must be [buckets, heads]");
+    expect("bias", *bias, bias->scalar_type(), {bias->size(0), q.size(1)});
+    same_gpu(q, {bias});
+    a.bias = bias->data_ptr();
+    a.bias_dtype = code(*bias);
+    a.buckets = (int)bias->size(0);
+    // an empty table has no address
+    if (!a.bias) value_error("bias must be [buckets, heads]");
+  }
+};
+
+// (q, k, v, start, start_k, causal, scale, bias, max_distance, bidirectional, max_len, o,
+//  workspace, stream) -> (o, lse)
+PyObject* attention_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 14);
+  const Tensor &q = tensor("q", a[0]), &k = tensor("k", a[1]), &v = tensor("v", a[2]);
+  const Attention at(q, k, v, a + 3);
+  const Tensor* o_in = maybe("o", a[11]);
+  const Tensor* ws_in = maybe("workspace", a[12]);
+  if (o_in) expect_rows("o", q, *o_in, q.scalar_type(), q.sizes());
+  const Launch on(q, a[13]);
+  on.use({&q, &k, &v, at.start, at.start_k, at.bias, o_in, ws_in});
+  const Tensor o = o_in ? *o_in : make(q, q.scalar_type(), q.sizes());
+  const Tensor lse = make(q, ScalarType::Float, {q.size(1), q.size(0)});
+  const size_t need = lib.hlq_attention_forward_workspace_size(&at.a);
+  std::optional<Tensor> ws;
+  if (need || ws_in) ws = workspace(ws_in, need, q);
+  const hlq_tokens vq = view(q), vk = view(k), vv = view(v), vo = view(o);
+  check("hlq_attention_forward",
+        lib.hlq_attention_forward(&at.a, &vq, &vk, &vv, &vo, ptr<float>(lse),
+                                  ws ? ws->data_ptr() : nullptr, ws ? ws->numel() : 0, on.stream));
+  written({o_in});
+  on.give({&o, &lse});
+  return tuple(wrap(o), wrap(lse));
+  END_HANDLE_TH_ERRORS
+}
+
+// (g_o, q, k, v, o, lse, start, start_k, causal, scale, bias, max_distance, bidirectional,
+//  max_len, g_q, g_k, g_v, workspace, stream) -> (g_q, g_k, g_v, g_bias)
+PyObject* attention_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 19);
+  const Tensor& g_o = tensor("g_o", a[0]);
+  const Tensor &q = tensor("q", a[1]), &k = tensor("k", a[2]), &v = tensor("v", a[3]);
+  const Tensor &o = tensor("o", a[4]), &lse = tensor("lse", a[5]);
+  const Attention at(q, k, v, a + 6);
+  const Tensor* gq_in = maybe("g_q", a[14]);
+  const Tensor* gk_in = maybe("g_k", a[15]);
+  const Tensor* gv_in = maybe("g_v", a[16]);
+  const Tensor* ws_in = maybe("workspace", a[17]);
+  expect_rows("g_o", q, g_o, q.scalar_type(), q.sizes());
+  expect_rows("o", q, o, q.scalar_type(), q.sizes());
+  expect("lse", lse, ScalarType::Float, {q.size(1), q.size(0)});
+  same_gpu(q, {&lse});
+  if (gq_in) expect_rows("g_q", q, *gq_in, q.scalar_type(), q.sizes());
+  if (gk_in) expect_rows("g_k", q, *gk_in, q.scalar_type(), k.sizes());
+  if (gv_in) expect_rows("g_v", q, *gv_in, q.scalar_type(), k.sizes());
+  const Launch on(q, a[18]);
+  on.use({&g_o, &q, &k, &v, &o, &lse, at.start, at.start_k, at.bias, gq_in, gk_in, gv_in, ws_in});
+  const Tensor g_q = gq_in ? *gq_in : make(q, q.scalar_type(), q.sizes());
+  const Tensor g_k = gk_in ? *gk_in : make(q, q.scalar_type(), k.sizes());
+  const Tensor g_v = gv_in ? *gv_in : make(q, q.scalar_type(), k.sizes());
+  std::optional<Tensor> g_bias;
+  if (at.bias) g_bias = make(q, at.bias->scalar_type(), at.bias->sizes());
+  const Tensor ws = workspace(ws_in, lib.hlq_attention_backward_workspace_size(&at.a), q);
+  const hlq_tokens vgo = view(g_o), vq = view(q), vk = view(k), vv = view(v), vo = view(o);
+  const hlq_tokens vgq = view(g_q), vgk = view(g_k), vgv = view(g_v);
+  check("hlq_attention_backward",
+        lib.hlq_attention_backward(&at.a, &vgo, &vq, &vk, &vv, &vo, ptr<float>(lse), &vgq, &vgk,
+                                   &vgv, g_bias ? g_bias->data_ptr() : nullptr, ptr(ws), ws.numel(),
+                                   on.stream));
+  written({gq_in, gk_in, gv_in});
+  on.give({&g_q, &g_k, &g_v, g_bias ? &*g_bias : nullptr});
+  return tuple(wrap(g_q), wrap(g_k), wrap(g_v), g_bias ? wrap(*g_bias) : none());
+  END_HANDLE_TH_ERRORS
+}
+
+// ------------------------------------------------------------ dropout
+
+uint32_t site_of(PyObject* o) {
+  const int64_t v = integer64("site", o);
+  if (v < 0 || v > UINT32_MAX) value_error("site is out of range");
+  return (uint32_t)v;
+}
+
+// (x, p, seed, site, residual, y, stream) -> y
+PyObject* dropout_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 7);
+  const Tensor& x = tensor("x", a[0]);
+  const double p = number("p", a[1]);
+  const Tensor& seed = tensor("seed", a[2]);
+  const uint32_t site = site_of(a[3]);
+  const Tensor* residual = maybe("residual", a[4]);
+  const Tensor* y_in = maybe("y", a[5]);
+  expect("seed", seed, ScalarType::Long, {2});
+  if (residual) expect("residual", *residual, x.scalar_type(), x.sizes());
+  if (y_in) expect("y", *y_in, x.scalar_type(), x.sizes());
+  same_gpu(x, {&x, &seed, residual, y_in});
+  const Launch on(x, a[6]);
+  on.use({&x, &seed, residual, y_in});
+  const Tensor y = y_in ? *y_in : make(x, x.scalar_type(), x.sizes());
+  check("hlq_dropout_forward",
+        lib.hlq_dropout_forward(ptr(x), ptr(residual), code(x), x.numel(), p,
+                                ptr<const int64_t>(seed), site, ptr(y), on.stream));
+  written({y_in});
+  on.give({&y});
+  return wrap(y);
+  END_HANDLE_TH_ERRORS
+}
+
+// (g_y, p, seed, site, g_x, stream) -> g_x
+PyObject* dropout_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 6);
+  const Tensor& g_y = tensor("g_y", a[0]);
+  const double p = number("p", a[1]);
+  const Tensor& seed = tensor("seed", a[2]);
+  const uint32_t site = site_of(a[3]);
+  const Tensor* gx_in = maybe("g_x", a[4]);
+  expect("seed", seed, ScalarType::Long, {2});
+  if (gx_in) expect("g_x", *gx_in, g_y.scalar_type(), g_y.sizes());
+  same_gpu(g_y, {&g_y, &seed, gx_in});
+  const Launch on(g_y, a[5]);
+  on.use({&g_y, &seed, gx_in});
+  const Tensor g_x = gx_in ? *gx_in : make(g_y, g_y.scalar_type(), g_y.sizes());
+  check("hlq_dropout_backward",
+        lib.hlq_dropout_backward(ptr(g_y), code(g_y), g_y.numel(), p, ptr<const int64_t>(seed),
+                                 site, ptr(g_x), on.stream));
+  written({gx_in});
+  on.give({&g_x});
+  return wrap(g_x);
+  END_HANDLE_TH_ERRORS
+}
+
 // (handle of the loaded library, hlq._check)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -647,6 +863,10 @@ PyMethodDef methods[] = {HLQ_METHOD(bind),
                          HLQ_METHOD(policy_loss_logits),
                          HLQ_METHOD(preference_loss),
                          HLQ_METHOD(clip_grad_norm),
+                         HLQ_METHOD(attention_forward),
+                         HLQ_METHOD(attention_backward),
+                         HLQ_METHOD(dropout_forward),
+                         HLQ_METHOD(dropout_backward),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_hlq_torch", nullptr, -1, methods,
                       nullptr,               nullptr,      nullptr, nullptr};

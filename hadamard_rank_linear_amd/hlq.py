@@ -57,6 +57,13 @@ EXPORTED = (
     "hlq_preference_loss",
     "hlq_clip_grad_norm_workspace_size",
     "hlq_clip_grad_norm",
+    "hlq_relative_bucket",
+    "hlq_attention_forward_workspace_size",
+    "hlq_attention_forward",
+    "hlq_attention_backward_workspace_size",
+    "hlq_attention_backward",
+    "hlq_dropout_forward",
+    "hlq_dropout_backward",
     "hlq_status_string",
     "hlq_version",
 )
@@ -75,6 +82,21 @@ class WorkspaceLayout(ctypes.Structure):
         ("t_low", ctypes.c_int64), ("total", ctypes.c_size_t),
         ("partial", ctypes.c_size_t), ("partial_bytes", ctypes.c_size_t),
         ("gx_splits", ctypes.c_int32), ("gw_splits", ctypes.c_int32)]
+
+
+class Tokens(ctypes.Structure):
+    """hlq_tokens: a tensor [tokens][heads][head_dim] by its strides."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class Attention(ctypes.Structure):
+    """hlq_attention: what one attention call deals with."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("queries", "keys", "sequences", "max_len")] + [
+        (n, ctypes.c_void_p) for n in ("start_q", "start_k", "bias")] + [
+        ("scale", ctypes.c_double)] + [
+        (n, ctypes.c_int32) for n in ("dtype", "heads", "kv_heads", "head_dim", "causal",
+                                      "bias_dtype", "buckets", "max_distance", "bidirectional")]
 
 
 def _load():
@@ -157,6 +179,22 @@ def _load():
     lib.hlq_clip_grad_norm_workspace_size.restype = SZ
     lib.hlq_clip_grad_norm.argtypes = [P, P, P, P, I64, F64, I32, P, P, SZ, P]
     lib.hlq_clip_grad_norm.restype = I32
+    A, R = ctypes.POINTER(Attention), ctypes.POINTER(Tokens)
+    lib.hlq_relative_bucket.argtypes = [I32, I32, I32, I32]
+    lib.hlq_relative_bucket.restype = I32
+    lib.hlq_attention_forward_workspace_size.argtypes = [A]
+    lib.hlq_attention_forward_workspace_size.restype = SZ
+    lib.hlq_attention_forward.argtypes = [A, R, R, R, R, P, P, SZ, P]
+    lib.hlq_attention_forward.restype = I32
+    lib.hlq_attention_backward_workspace_size.argtypes = [A]
+    lib.hlq_attention_backward_workspace_size.restype = SZ
+    lib.hlq_attention_backward.argtypes = [A, R, R, R, R, R, P, R, R, R, P, P, SZ, P]
+    lib.hlq_attention_backward.restype = I32
+    U32 = ctypes.c_uint32
+    lib.hlq_dropout_forward.argtypes = [P, P, I32, I64, F64, P, U32, P, P]
+    lib.hlq_dropout_forward.restype = I32
+    lib.hlq_dropout_backward.argtypes = [P, I32, I64, F64, P, U32, P, P]
+    lib.hlq_dropout_backward.restype = I32
     lib.hlq_status_string.argtypes = [I32]
     lib.hlq_status_string.restype = ctypes.c_char_p
     lib.hlq_version.argtypes = []
@@ -735,6 +773,71 @@ def hlq_clip_grad_norm(grads, max_norm, norm_kind=HLQ_NORM_L2, out=None, workspa
         import torch
         device = torch.cuda.current_device()
     return _native.clip_grad_norm(grads, max_norm, norm_kind, out, workspace, stream, device)
+
+
+# ---------------------------------------------------------- attention block
+
+def hlq_relative_bucket(distance, buckets, max_distance=128, bidirectional=True) -> int:
+    """Row of a bias table for key position - query position = ``distance``:
+    near distances by themselves, farther ones by their logarithm up to
+    ``max_distance``; ``bidirectional`` gives keys behind the query the table's
+    second half, else they share bucket 0."""
+    b = int(_lib.hlq_relative_bucket(distance, buckets, max_distance, bool(bidirectional)))
+    if b < 0:
+        raise ValueError(f"{buckets} buckets up to a distance of {max_distance}: out of range")
+    return b
+
+
+def hlq_attention_forward(q, k, v, start=None, start_k=None, causal=False, scale=None, bias=None,
+                          max_distance=128, bidirectional=None, max_len=0, o=None, workspace=None,
+                          stream=None):
+    """Attention over packed sequences: returns (o [queries, heads, D],
+    lse [heads, queries] fp32).
+
+    q [queries, heads, D], k and v [keys, kv_heads, D] are fp32 or bf16, dense
+    along D (up to 128) with any other strides (slices of the qkv layer's
+    output); query head h reads key head h // (heads / kv_heads).  ``start``
+    [sequences + 1] (int64, on the GPU) holds the sequences' bounds among the
+    queries, ``start_k`` among the keys (None: the same); without ``start`` there
+    is one sequence.  The last query stands at the last key's position; with
+    ``causal`` a query sees the keys up to its own.  ``scale`` None: 1/sqrt(D).
+    ``bias`` [buckets, heads] is added to the scores by
+    :func:`hlq_relative_bucket` of ``max_distance`` and ``bidirectional`` (None:
+    not causal).  ``max_len``: the longest sequence's queries, if known, makes the
+    launch fit; the result does not depend on it beyond rounding.  A query that
+    sees no key, and tokens outside every sequence, get o = 0 and lse = -inf.
+    """
+    return _native.attention_forward(q, k, v, start, start_k, causal, scale, bias, max_distance,
+                                     bidirectional, max_len, o, workspace, stream)
+
+
+def hlq_attention_backward(g_o, q, k, v, o, lse, start=None, start_k=None, causal=False, scale=None,
+                           bias=None, max_distance=128, bidirectional=None, max_len=0, g_q=None,
+                           g_k=None, g_v=None, workspace=None, stream=None):
+    """Backward of :func:`hlq_attention_forward`, the probabilities computed
+    again from ``lse``: returns (g_q, g_k, g_v, g_bias), g_bias None without a
+    bias.  The gradients may be given as slices of one tensor, the gradient of
+    the qkv layer's output."""
+    return _native.attention_backward(g_o, q, k, v, o, lse, start, start_k, causal, scale, bias,
+                                      max_distance, bidirectional, max_len, g_q, g_k, g_v,
+                                      workspace, stream)
+
+
+def hlq_dropout_forward(x, p, seed, site=0, residual=None, y=None, stream=None):
+    """residual + dropout(x): an element is kept, times 1 / (1 - p), with
+    probability 1 - p (p in steps of 2^-16).
+
+    ``seed`` (int64 [2], on the GPU) is a key and a step that the caller moves on
+    between training steps, ``site`` a number that tells the places of a model
+    apart.  The mask is a function of these and of the element's index; it is not
+    stored.  ``y`` may be x or the residual."""
+    return _native.dropout_forward(x, p, seed, site, residual, y, stream)
+
+
+def hlq_dropout_backward(g_y, p, seed, site=0, g_x=None, stream=None):
+    """Gradient of x in :func:`hlq_dropout_forward` of the same p, seed and
+    site (the residual's is g_y itself).  ``g_x`` may be g_y."""
+    return _native.dropout_backward(g_y, p, seed, site, g_x, stream)
 
 
 def lib_handle():

@@ -600,6 +600,122 @@ hlq_status hlq_clip_grad_norm(const void* const* grads, void* const* outs, const
                               double* norm, void* workspace, size_t workspace_bytes,
                               void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of an attention block between its linear layers: attention over
+ * packed sequences with a learned relative position bias, and dropout in front
+ * of the residual addition.  Conventions as for the operators above: data
+ * pointers need the alignment of their elements, counts of tokens may be zero,
+ * results are reproducible.
+ * ------------------------------------------------------------------------ */
+
+/* A tensor [tokens][heads][head_dim], head_dim elements dense, strides in
+   elements (below 2^40, not negative): a slice of what the qkv layer wrote, or of
+   the gradient it will read.  Outputs must not overlap themselves. */
+typedef struct hlq_tokens {
+  void* data;
+  int64_t token_stride, head_stride;
+} hlq_tokens;
+
+/*
+ * What one attention call deals with.  Sequence s has the queries start_q[s] ..
+ * start_q[s+1] - 1 and the keys start_k[s] .. start_k[s+1] - 1 of the packed
+ * tensors (the bounds [sequences + 1] int64, non-decreasing, read on the device and
+ * limited there to the tokens there are; tokens before the first and behind the
+ * last sequence get zeros).  start_q NULL: one sequence of all tokens; start_k
+ * NULL: start_q, for as many keys as queries.  Query i of Lq stands at position
+ * i + Lk - Lq of its sequence's Lk keys, so that new tokens follow those of a
+ * cache.  Lengths may be zero.
+ *   max_len   the longest sequence's queries, for the launch alone (0: unknown);
+ *             longer ones are dealt with all the same.
+ *   heads     query heads; head h reads key head h / (heads / kv_heads).
+ *   head_dim  1 to 128.
+ *   causal    a query sees the keys up to its own position.
+ *   scale     2^-64 to 2^64.
+ *   bias      [buckets][heads] of bias_dtype or NULL: added to scale * q k, by the
+ *             bucket of d = key position - query position (hlq_relative_bucket).
+ * Fewer than 2^30 queries times heads and keys times heads, 2^16 heads.
+ */
+typedef struct hlq_attention {
+  int64_t queries, keys, sequences, max_len;
+  const int64_t *start_q, *start_k;
+  const void* bias;
+  double scale;
+  int32_t dtype, heads, kv_heads, head_dim, causal;
+  int32_t bias_dtype, buckets, max_distance, bidirectional;
+} hlq_attention;
+
+/*
+ * Bucket of a distance d (a host function; -1 for sizes out of range).  A side has
+ * n = buckets distances (bidirectional: buckets / 2, and those of d > 0 come after
+ * the others), e = n / 2 of them by themselves:
+ *   a = |d| (one side: max(-d, 0));   bucket = a for a < e, else
+ *   min(n - 1, e + floor((n - e) log(a / e) / log(max_distance / e)))
+ * 2 <= n, buckets <= 128 and even if bidirectional, e < max_distance <= 1024.
+ */
+int hlq_relative_bucket(int distance, int buckets, int max_distance, int bidirectional);
+
+/*
+ * Attention:  S_ij = scale q_i k_j + bias,  lse_i = log sum_j exp(S_ij),
+ *   o_i = sum_j exp(S_ij - lse_i) v_j      over the keys j that query i sees.
+ *   q, o     [queries][heads][head_dim], k, v [keys][kv_heads][head_dim], dtype.
+ *   lse      [heads][queries] f32 out, for the backward pass.
+ *   workspace at least hlq_attention_forward_workspace_size(a) bytes (0 unless
+ *            there are too few queries to fill the GPU: then the keys are shared out).
+ * A query that sees no key, or none with a score above -inf, gets o = 0 and lse =
+ * -inf.  Keys and values that a query does not see do not reach it, infinities and
+ * NaN among them included.  Scores, sums and statistics are fp32; for bf16 the
+ * probabilities are rounded to bf16 in the product with v.
+ * One launch, two with a workspace.  Errors: HLQ_ERR_NULL, HLQ_ERR_DTYPE,
+ * HLQ_ERR_SHAPE, HLQ_ERR_VALUE (scale, buckets), HLQ_ERR_ALIGN,
+ * HLQ_ERR_WORKSPACE.
+ */
+size_t hlq_attention_forward_workspace_size(const hlq_attention* a);
+hlq_status hlq_attention_forward(const hlq_attention* a, const hlq_tokens* q, const hlq_tokens* k,
+                                 const hlq_tokens* v, const hlq_tokens* o, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its backward pass.  The probabilities P_ij = exp(S_ij - lse_i) are computed
+ * again:  D_i = sum_d g_o o (o as stored),  G_ij = P_ij (g_o_i v_j - D_i),
+ *   g_q_i = scale sum_j G_ij k_j,  g_k_j = scale sum_i G_ij q_i,
+ *   g_v_j = sum_i P_ij g_o_i (the last two over the query heads that share a key
+ *   head),  g_bias[b][h] = sum of G over the pairs of head h in bucket b.
+ *   g_o      [queries][heads][head_dim]; q, k, v, o, lse of the forward call.
+ *   g_q, g_k, g_v  out, dtype;  g_bias [buckets][heads] out, bias_dtype, NULL
+ *            exactly when there is no bias.
+ * For bf16 P and G are rounded to bf16 in the products; g_bias sums them unrounded.
+ * Two launches, three with a bias.  No atomics: a call repeats bit for bit.
+ * Errors as above.
+ */
+size_t hlq_attention_backward_workspace_size(const hlq_attention* a);
+hlq_status hlq_attention_backward(const hlq_attention* a, const hlq_tokens* g_o,
+                                  const hlq_tokens* q, const hlq_tokens* k, const hlq_tokens* v,
+                                  const hlq_tokens* o, const float* lse, const hlq_tokens* g_q,
+                                  const hlq_tokens* g_k, const hlq_tokens* g_v, void* g_bias,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Dropout with the residual addition:
+ *   y_i = residual_i + (r_i >= t ? x_i * 65536 / (65536 - t) : 0)
+ * with t = p * 65536 rounded to nearest (ties to even) and r_i 16 random bits of element i; p = 1
+ * leaves the residual.  The mask is not stored: r_i is half i % 2 (the lower
+ * first) of word i % 8 / 2 of Philox 4x32 with seven rounds (Salmon, Moraes,
+ * Dror, Shaw 2011) for the counter (i / 8, site, seed[1] low, seed[1] high)
+ * and the key seed[0] (low, high), so that the backward pass draws it again.
+ *   x, residual, y [n] dtype, n < 2^35; residual NULL: none.  y may be x or residual.
+ *   seed     [2] int64 on the device: a key and a step, which the caller moves on
+ *            between training steps (in a captured graph too).
+ *   site     tells the places of a model apart that share a seed.
+ *   p        0 to 1 (HLQ_ERR_VALUE).
+ * An element that is dropped contributes zero whatever it is.  One launch.
+ */
+hlq_status hlq_dropout_forward(const void* x, const void* residual, int dtype, int64_t n, double p,
+                               const int64_t* seed, uint32_t site, void* y, void* stream);
+/* The gradient of x: g_x_i = (r_i >= t ? g_y_i * 65536 / (65536 - t) : 0).  g_x may
+   be g_y.  The residual's gradient is g_y itself. */
+hlq_status hlq_dropout_backward(const void* g_y, int dtype, int64_t n, double p,
+                                const int64_t* seed, uint32_t site, void* g_x, void* stream);
+
 /* Static text for a status code (never NULL). */
 const char* hlq_status_string(int status);
 
