@@ -30,9 +30,9 @@ __device__ __forceinline__ float sum_halves(float v) {
   return lanes_stage<32>(v, [](float a, float b) { return a + b; });
 }
 
-template <int DT>
-__device__ __forceinline__ const char* row_at(const AttnRows& t, int64_t token, int head) {
-  return static_cast<const char*>(t.data) + (token * t.token + head * t.head) * (DT == 0 ? 4 : 2);
+template <int DT, typename R>
+__device__ __forceinline__ char* row_at(const R& t, int64_t token, int64_t head) {
+  return static_cast<char*>(t.data) + (token * t.token + head * t.head) * (DT == 0 ? 4 : 2);
 }
 
 // Outputs of tokens that belong to no sequence: zeros.
@@ -42,10 +42,8 @@ __device__ void clear_tokens(const AttnRows& t, int64_t from, int64_t to, int he
   typedef typename Piece<DT>::Elem E;
   const int64_t n = (to - from) * heads * D;
   for (int64_t i = id; i < n; i += step) {
-    const int d = (int)(i % D);
     const int64_t r = i / D;
-    const_cast<E*>(reinterpret_cast<const E*>(
-        row_at<DT>(t, from + r / heads, (int)(r % heads))))[d] = 0;
+    reinterpret_cast<E*>(row_at<DT>(t, from + r / heads, r % heads))[i % D] = 0;
   }
 }
 __device__ __forceinline__ int64_t bound(const int64_t* start, int64_t s, int64_t T) {
@@ -83,17 +81,13 @@ __device__ __forceinline__ int wave_max_int(int v) {
   return lanes_join<64>(v, [](int a, int b) { return a > b ? a : b; });
 }
 
-// Scores of a 32 x 32 block with their bias, in powers of two; s holds q k^T,
-// rows are keys from key0 on, columns queries at pos (or the other way round:
-// step -1).  The distance of register r is base + step * acc_row(r).
-template <bool BIAS>
+// Scores of a 32 x 32 block plus their bias, in powers of two (s holds q k^T).  lo
+// .. hi: the block's distances (key position - query position); base: the lane's
+// of row 0, from which row r of the block is r up, or down where its rows are
+// queries.
+template <bool DOWN>
 __device__ __forceinline__ void add_bias(const AttnShape& g, const float* line, f32x16& s, int lo,
-                                         int hi, int base, bool down) {
-  if constexpr (!BIAS) {
-#pragma unroll
-    for (int r = 0; r < 16; ++r) s[r] *= g.c;
-    return;
-  }
+                                         int hi, int base) {
   const int reach = g.bias.reach;
   if (lo >= reach || hi <= -reach) {
     const float b = line[lo >= reach ? 2 * (reach + BIAS_MARGIN) : 0];
@@ -102,14 +96,18 @@ __device__ __forceinline__ void add_bias(const AttnShape& g, const float* line, 
     return;
   }
   const float* at = line + base + reach + BIAS_MARGIN;
-  if (down) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], g.c, at[-acc_row(r)]);
-  } else {
-#pragma unroll
-    for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], g.c, at[acc_row(r)]);
-  }
+  for (int r = 0; r < 16; ++r)
+    s[r] = __builtin_fmaf(s[r], g.c, DOWN ? at[-acc_row(r)] : at[acc_row(r)]);
 }
+
+// Address of the kernel's dynamic LDS.
+__device__ __forceinline__ uint32_t lds_place(char* lds) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+}
+
+typedef std::integral_constant<bool, true> Whole;
+typedef std::integral_constant<bool, false> Masked;
 
 // ------------------------------------------------------------ forward
 
@@ -122,20 +120,21 @@ struct FwdShape {
   static constexpr int ROWS = FEW ? ATTN_FEW : ATTN_ROWS;
   static constexpr int KEYS = FEW ? 128 : DT == 0 ? 32 : 64;  // of a tile
   static constexpr int MINE = FEW ? 32 : KEYS;                // of them a wave's
+  static constexpr int BUFS = FEW ? 1 : 2;  // tiles of keys and of values in LDS
   static constexpr int TILE_BYTES = KEYS * T::ROW_BYTES;
   static constexpr int JOIN_BYTES = FEW ? 4 * DP * 33 * 4 + 4 * 32 * 8 : 0;
-  static constexpr int LDS = 2 * TILE_BYTES > JOIN_BYTES ? 2 * TILE_BYTES : JOIN_BYTES;
+  static constexpr int LDS =
+      2 * BUFS * TILE_BYTES > JOIN_BYTES ? 2 * BUFS * TILE_BYTES : JOIN_BYTES;
 };
 
 template <int DT, int DP, bool BIAS, bool FEW>
 __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(AttnFwd a) {
   typedef FwdShape<DT, DP, FEW> F;
   typedef Tile<DT, DP> T;
-  constexpr int DB = DP / 32, DC = DP / 16, SB = F::MINE / 32;
+  constexpr int DB = DP / 32, DC = DP / 16, SB = F::MINE / 32, ES = DT == 0 ? 4 : 2;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  char* const lk = lds;
-  char* const lv = lds + F::TILE_BYTES;
   float* const line = reinterpret_cast<float*>(lds + F::LDS);
+  const uint32_t row_lane = lds_place(lds) + T::row_lane(), col_lane = lds_place(lds) + T::col_lane();
   const AttnShape& g = a.g;
   const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
 
@@ -174,16 +173,21 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
     sequence(g.start_q, seq, g.Tq, q0, nq);
     sequence(g.start_k, seq, g.Tk, k0, nk);
     const int rows = nq * g.pack, off = nk - nq;
+    if (tile0 * F::ROWS >= rows) continue;
     if constexpr (BIAS) {
       __syncthreads();
       load_bias_line(g.bias, head0, g.heads, line);
     }
+    const char* const kb = row_at<DT>(a.k, k0, kvh);
+    const char* const vb = row_at<DT>(a.v, k0, kvh);
+    const int64_t kt = a.k.token * ES, vt = a.v.token * ES;
+    Stage<DT, DP, F::KEYS> sk, sv;
+    sk.init((uint32_t)kt, 0, 1);
+    sv.init((uint32_t)vt, 0, 1);
 
     for (int64_t tile = tile0; tile * F::ROWS < rows; tile += g.tiles) {
       const int row0 = (int)tile * F::ROWS + (FEW ? 0 : wave * 32);
       const RowInfo me = row_info(g, row0 + (lane & 31), rows, head0, off, nk);
-      const int first = wave_min(me.valid ? me.limit : nk);
-      const int last = wave_max_int(me.valid ? me.limit : 0);
       // keys of the tile's last row: every wave of the group goes that far
       int end = nk;
       if (g.causal) {
@@ -196,6 +200,9 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
         from = min(end, split * share);
         end = min(end, from + share);
       }
+      const int limit = min(me.limit, end);
+      const int first = wave_min(me.valid ? limit : end);     // keys that all rows see
+      const int last = wave_max_int(me.valid ? limit : from);  // and that any does
 
       Frag<DT> qf[DC];
       {
@@ -209,54 +216,35 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
       for (int d = 0; d < DB; ++d) o[d] = (f32x16)(0.f);
       float m = -kInf, l = 0.f;
 
-      Stage<DT, DP, F::KEYS> sk, sv;
-      const auto krow = [&](const AttnRows& t, int key) -> const void* {
-        return key < end ? row_at<DT>(t, (int64_t)k0 + key, kvh) : nullptr;
-      };
-      sk.load([&](int r) { return krow(a.k, from + r); }, g.D, a.k.vec);
-      sv.load([&](int r) { return krow(a.v, from + r); }, g.D, a.v.vec);
-      for (int key = from; key < end; key += F::KEYS) {
-        __syncthreads();
-        sk.store(lk);
-        sv.store(lv);
-        __syncthreads();
-        if (key + F::KEYS < end) {
-          sk.load([&](int r) { return krow(a.k, key + F::KEYS + r); }, g.D, a.k.vec);
-          sv.load([&](int r) { return krow(a.v, key + F::KEYS + r); }, g.D, a.v.vec);
-        }
-        const int mine = FEW ? 32 * wave : 0, key0 = key + mine;
-        if (key0 >= min(last, end)) continue;
-
+      // One tile of keys, from key0 on in this wave.
+      // tile: its place in LDS, the values' tile after the keys'.
+      const auto attend = [&](auto all, int key0, int tile) {
+        constexpr bool WHOLE = decltype(all)::value;
+        const uint32_t rl = row_lane + tile, cl = col_lane + tile;
         f32x16 s[SB];
+        float top = -kInf;
 #pragma unroll
         for (int b = 0; b < SB; ++b) {
+          if (!WHOLE && key0 + 32 * b >= last) continue;
           s[b] = (f32x16)(0.f);
 #pragma unroll
           for (int c = 0; c < DC; ++c)
-            s[b] = mma(T::row_frag(lk, mine + 32 * b + (lane & 31), 16 * c + 8 * half), qf[c], s[b]);
-          const int d = key0 + 32 * b - me.pos;
+            s[b] = mma(T::row_frag(rl, 32 * b, c), qf[c], s[b]);
           if constexpr (BIAS) {
             const int dist = key0 + 32 * b - (row0 + off);  // of the first row; later ones less
-            add_bias<true>(g, line, s[b], dist - 31, dist + 31, d + 4 * half, false);
-          } else {
-            add_bias<false>(g, nullptr, s[b], 0, 0, 0, false);
+            add_bias<false>(g, line, s[b], dist - 31, dist + 31, key0 + 32 * b - me.pos + 4 * half);
           }
-        }
-        const bool whole = key0 + F::MINE <= min(first, end);
-        if (!whole) {
-          const int limit = min(me.limit, end) - key0 - 4 * half;
-#pragma unroll
-          for (int b = 0; b < SB; ++b)
+          if (!WHOLE) {
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-              if (32 * b + acc_row(r) >= limit) s[b][r] = -kInf;
-        }
-        float top = s[0][0];
-#pragma unroll
-        for (int b = 0; b < SB; ++b)
+              if (key0 + 32 * b + acc_row(r) + 4 * half >= limit) s[b][r] = -kInf;
+          }
 #pragma unroll
           for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
-        top = fmaxf(m, max_halves(top));
+        }
+        top = max_halves(top);
+        if constexpr (!BIAS) top *= g.c;
+        top = fmaxf(m, top);
         const float base = top == -kInf ? 0.f : top;  // a row that has seen no key yet
         if (__any(top != m)) {
           const float keep = exp2_fast(m - base);
@@ -269,68 +257,95 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
         }
         float sum = 0.f;
 #pragma unroll
-        for (int b = 0; b < SB; ++b)
+        for (int b = 0; b < SB; ++b) {
+          if (!WHOLE && key0 + 32 * b >= last) continue;
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
-            s[b][r] = exp2_fast(s[b][r] - base);
+            s[b][r] = exp2_fast(BIAS ? s[b][r] - base : __builtin_fmaf(s[b][r], g.c, -base));
             sum += s[b][r];
           }
-        l += sum;
-        if (whole) {
-#pragma unroll
-          for (int b = 0; b < SB; ++b)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const Frag<DT> p = acc_frag<DT>(s[b], c);
-#pragma unroll
-              for (int d = 0; d < DB; ++d)
-                o[d] = mma(T::col_frag(lv, mine + 32 * b + 16 * c, 32 * d), p, o[d]);
-            }
-        } else {
-          const int limit = min(me.limit, end) - key0;
-#pragma unroll
-          for (int b = 0; b < SB; ++b)
+          const uint32_t bad =
+              !WHOLE && g.causal ? rows_not_finite<DT, DP>(rl, F::KEYS + 32 * b) : 0;
+          if (!WHOLE && bad) {
+            if (bad & bit_range(0, limit - key0 - 32 * b)) sum = __builtin_nanf("");
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const Frag<DT> p = acc_frag<DT>(s[b], c);
 #pragma unroll
               for (int d = 0; d < DB; ++d)
-                o[d] = mma_seen<DT>(T::col_frag(lv, mine + 32 * b + 16 * c, 32 * d), p, o[d],
-                                    [&](int i) { return 32 * b + 16 * c + i < limit; });
+                o[d] = mma(finite<DT>(T::col_frag(cl, F::KEYS + 32 * b + 16 * c, d)), p, o[d]);
             }
+            continue;
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const Frag<DT> p = acc_frag<DT>(s[b], c);
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+              o[d] = mma(T::col_frag(cl, F::KEYS + 32 * b + 16 * c, d), p, o[d]);
+          }
         }
+        l += sum;
+      };
+
+      sk.load(kb + from * kt, end - from, g.D, a.k.vec);
+      sv.load(vb + from * vt, end - from, g.D, a.v.vec);
+      int buf = 0;
+      if (F::BUFS == 2) __syncthreads();  // the previous tile's reads are done
+      for (int key = from; key < end; key += F::KEYS) {
+        char* const lk = lds + buf * 2 * F::TILE_BYTES;
+        char* const lv = lk + F::TILE_BYTES;
+        if (F::BUFS == 1) __syncthreads();
+        sk.store(lk);
+        sv.store(lv);
+        __syncthreads();
+        const int next = key + F::KEYS;
+        if (next < end) {
+          sk.load(kb + next * kt, end - next, g.D, a.k.vec);
+          sv.load(vb + next * vt, end - next, g.D, a.v.vec);
+        }
+        if (F::BUFS == 2) buf ^= 1;
+        const int mine = FEW ? 32 * wave : 0, key0 = key + mine;
+        if (key0 >= last) continue;
+        const int at = (int)(lk - lds) + mine * T::ROW_BYTES;
+        if (key0 + F::MINE <= first) attend(Whole(), key0, at);
+        else attend(Masked(), key0, at);
       }
       l = sum_halves(l);
 
+      const auto& z = *again<AttnFwd>();
       if constexpr (!FEW) {
         if (!me.valid) continue;
         const int64_t token = (int64_t)q0 + me.token;
-        if (a.po) {
-          const int64_t at = ((int64_t)split * g.Tq + token) * g.heads + me.head;
+        if (z.po) {
+          const int64_t at = ((int64_t)split * z.g.Tq + token) * z.g.heads + me.head;
           if (half == 0) {
-            a.ml[2 * at] = m;
-            a.ml[2 * at + 1] = l;
+            z.ml[2 * at] = m;
+            z.ml[2 * at + 1] = l;
           }
-          float* p = a.po + at * g.D;
+          float* p = z.po + at * z.g.D;
 #pragma unroll
           for (int d = 0; d < DB; ++d)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
               const int e = 32 * d + acc_row(r) + 4 * half;
-              if (e < g.D) p[e] = o[d][r];
+              if (e < z.g.D) p[e] = o[d][r];
             }
           continue;
         }
         if (half == 0)
-          a.lse[me.head * g.Tq + token] = l == 0.f ? -kInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
+          z.lse[me.head * z.g.Tq + token] =
+              l == 0.f ? -kInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        char* p = const_cast<char*>(row_at<DT>(a.o, token, me.head));
+        char* p = row_at<DT>(z.o, token, me.head);
+        const int D = z.g.D;
+        const bool vec = z.o.vec;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
           for (int r = 0; r < 16; r += 4)
-            store4<DT>(p, 32 * d + acc_row(r) + 4 * half, g.D, a.o.vec, o[d][r] * inv,
-                       o[d][r + 1] * inv, o[d][r + 2] * inv, o[d][r + 3] * inv);
+            store4<DT>(p, 32 * d + acc_row(r) + 4 * half, D, vec, o[d][r] * inv, o[d][r + 1] * inv,
+                       o[d][r + 2] * inv, o[d][r + 3] * inv);
       } else {
         // the waves' shares of the keys: [wave][d][row], rows 33 apart
         float* const jo = reinterpret_cast<float*>(lds);
@@ -346,7 +361,7 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
         for (int i = threadIdx.x; i < 32 * DP; i += 256) {
           const int r = i / DP, d = i % DP;
           const RowInfo it = row_info(g, (int)tile * F::ROWS + r, rows, head0, off, nk);
-          if (!it.valid || d >= g.D) continue;
+          if (!it.valid || d >= z.g.D) continue;
           float top = -kInf, total = 0.f, v = 0.f;
 #pragma unroll
           for (int w = 0; w < 4; ++w) top = fmaxf(top, jm[w * 32 + r].x);
@@ -358,23 +373,24 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
             v += f * jo[(w * DP + d) * 33 + r];
           }
           const int64_t token = (int64_t)q0 + it.token;
-          if (a.po) {
-            const int64_t at = ((int64_t)split * g.Tq + token) * g.heads + it.head;
-            a.po[at * g.D + d] = v;
+          if (z.po) {
+            const int64_t at = ((int64_t)split * z.g.Tq + token) * z.g.heads + it.head;
+            z.po[at * z.g.D + d] = v;
             if (d == 0) {
-              a.ml[2 * at] = top;
-              a.ml[2 * at + 1] = total;
+              z.ml[2 * at] = top;
+              z.ml[2 * at + 1] = total;
             }
             continue;
           }
           if (d == 0)
-            a.lse[it.head * g.Tq + token] =
+            z.lse[it.head * z.g.Tq + token] =
                 total == 0.f ? -kInf : (top + __builtin_amdgcn_logf(total)) * kLn2;
           const float y = total == 0.f ? 0.f : v / total;
-          char* p = const_cast<char*>(row_at<DT>(a.o, token, it.head));
+          char* p = row_at<DT>(z.o, token, it.head);
           if constexpr (DT == 0) reinterpret_cast<float*>(p)[d] = y;
           else reinterpret_cast<uint16_t*>(p)[d] = (uint16_t)pack_bf16(y, 0.f);
         }
+        __syncthreads();
       }
     }
   }
@@ -387,7 +403,7 @@ struct BwdShape {
   typedef Tile<DT, DP> T;
   static constexpr int KEYS = DT == 0 ? 32 : 64;  // keys, or rows, of a tile
   static constexpr int TILE_BYTES = KEYS * T::ROW_BYTES;
-  static constexpr int LDS = 2 * TILE_BYTES;
+  static constexpr int LDS = 4 * TILE_BYTES;  // two tensors, two buffers
 };
 
 // Waves as in the forward pass.  Writes delta for the gradients of k and v, and
@@ -396,18 +412,16 @@ struct BwdShape {
 // no instruction meets an address twice and the order is the program's), blocks
 // beyond reach in registers.
 template <int DT, int DP, bool BIAS>
-__global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_backward_q(
-    AttnBwd a) {
+__global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(AttnBwd a) {
   typedef BwdShape<DT, DP> F;
   typedef Tile<DT, DP> T;
-  constexpr int DB = DP / 32, DC = DP / 16, SB = F::KEYS / 32;
+  constexpr int DB = DP / 32, DC = DP / 16, SB = F::KEYS / 32, ES = DT == 0 ? 4 : 2;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  char* const lk = lds;
-  char* const lv = lds + F::TILE_BYTES;
+  const uint32_t row_lane = lds_place(lds) + T::row_lane(), col_lane = lds_place(lds) + T::col_lane();
   const AttnShape& g = a.g;
   const int lines = BIAS ? bias_line_size(g.bias) : 0;
   float* const line = reinterpret_cast<float*>(lds + F::LDS);
-  float* const sums = line + lines;  // [8][lines]
+  float* const sums = line + lines;     // [8][lines]
   float* const far = sums + 8 * lines;  // [4][2]
   const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
 
@@ -431,12 +445,24 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
     sequence(g.start_q, seq, g.Tq, q0, nq);
     sequence(g.start_k, seq, g.Tk, k0, nk);
     const int rows = nq * g.pack, off = nk - nq;
+    if (tile0 * ATTN_ROWS >= rows) {
+      if constexpr (BIAS)
+        for (int b = threadIdx.x; b < g.bias.buckets; b += 256)
+          a.g_line[item * g.bias.buckets + b] = 0.f;
+      continue;
+    }
     float far_low = 0.f, far_high = 0.f;
     if constexpr (BIAS) {
       __syncthreads();
       load_bias_line(g.bias, head0, g.heads, line);
       for (int i = threadIdx.x; i < 8 * lines; i += 256) sums[i] = 0.f;
     }
+    const char* const kb = row_at<DT>(a.k, k0, kvh);
+    const char* const vb = row_at<DT>(a.v, k0, kvh);
+    const int64_t kt = a.k.token * ES, vt = a.v.token * ES;
+    Stage<DT, DP, F::KEYS> sk, sv;
+    sk.init((uint32_t)kt, 0, 1);
+    sv.init((uint32_t)vt, 0, 1);
 
     for (int64_t tile = tile0; tile * ATTN_ROWS < rows; tile += g.tiles) {
       const int row0 = (int)tile * ATTN_ROWS + wave * 32;
@@ -453,17 +479,20 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
       float lse = kInf, delta = 0.f;
       const int64_t token = (int64_t)q0 + (me.valid ? me.token : 0);
       {
-        const char* pq = row_at<DT>(a.q, token, me.head);
-        const char* pg = row_at<DT>(a.g_o, token, me.head);
-        const char* po = row_at<DT>(a.o, token, me.head);
+        const auto& z = *again<AttnBwd>();
+        const char* pq = row_at<DT>(z.q, token, me.head);
+        const char* pg = row_at<DT>(z.g_o, token, me.head);
+        const char* po = row_at<DT>(z.o, token, me.head);
+        const int D = z.g.D;
+        const bool qv = z.q.vec, gv = z.g_o.vec, ov = z.o.vec;
 #pragma unroll
         for (int c = 0; c < DC; ++c) {
           qf[c] = gf[c] = zero_frag<DT>();
           if (me.valid) {
             const int d = 16 * c + 8 * half;
-            qf[c] = global_frag<DT>(pq, d, g.D, a.q.vec);
-            gf[c] = global_frag<DT>(pg, d, g.D, a.g_o.vec);
-            const Frag<DT> of = global_frag<DT>(po, d, g.D, a.o.vec);
+            qf[c] = global_frag<DT>(pq, d, D, qv);
+            gf[c] = global_frag<DT>(pg, d, D, gv);
+            const Frag<DT> of = global_frag<DT>(po, d, D, ov);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               delta = __builtin_fmaf((float)gf[c][e], (float)of[e], delta);
@@ -471,48 +500,37 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
         }
         delta = sum_halves(delta);
         if (me.valid) {
-          if (half == 0) a.delta[me.head * g.Tq + token] = delta;
-          lse = a.lse[me.head * g.Tq + token] * kLog2e;
+          if (half == 0) z.delta[me.head * z.g.Tq + token] = delta;
+          lse = z.lse[me.head * z.g.Tq + token] * kLog2e;
           if (lse == -kInf) lse = kInf;  // no key seen: probabilities of zero
         }
       }
       f32x16 dq[DB];
 #pragma unroll
       for (int d = 0; d < DB; ++d) dq[d] = (f32x16)(0.f);
+      float poison = 0.f;
 
-      Stage<DT, DP, F::KEYS> sk, sv;
-      const auto krow = [&](const AttnRows& t, int key) -> const void* {
-        return key < end ? row_at<DT>(t, (int64_t)k0 + key, kvh) : nullptr;
-      };
-      sk.load([&](int r) { return krow(a.k, r); }, g.D, a.k.vec);
-      sv.load([&](int r) { return krow(a.v, r); }, g.D, a.v.vec);
-      for (int key = 0; key < end; key += F::KEYS) {
-        __syncthreads();
-        sk.store(lk);
-        sv.store(lv);
-        __syncthreads();
-        if (key + F::KEYS < end) {
-          sk.load([&](int r) { return krow(a.k, key + F::KEYS + r); }, g.D, a.k.vec);
-          sv.load([&](int r) { return krow(a.v, key + F::KEYS + r); }, g.D, a.v.vec);
-        }
-        if (key >= last) continue;
-        const bool whole = key + F::KEYS <= first;
-#pragma unroll
+      const auto attend = [&](auto all, int key, int tile) {
+        constexpr bool WHOLE = decltype(all)::value;
+#pragma unroll 1
         for (int b = 0; b < SB; ++b) {
+          const uint32_t rl = row_lane + tile + 32 * b * T::ROW_BYTES;
+          const uint32_t cl = col_lane + tile + 32 * b * T::ROW_BYTES;
+          if (!WHOLE && key + 32 * b >= last) continue;
           f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
 #pragma unroll
           for (int c = 0; c < DC; ++c) {
-            const int r = 32 * b + (lane & 31), d = 16 * c + 8 * half;
-            s = mma(T::row_frag(lk, r, d), qf[c], s);
-            dp = mma(T::row_frag(lv, r, d), gf[c], dp);
+            s = mma(T::row_frag(rl, 0, c), qf[c], s);
+            dp = mma(T::row_frag(rl, F::KEYS, c), gf[c], dp);
           }
           const int base = key + 32 * b - me.pos + 4 * half;
           const int dist = key + 32 * b - (row0 + off);
-          add_bias<BIAS>(g, line, s, dist - 31, dist + 31, base, false);
+          if constexpr (BIAS) add_bias<false>(g, line, s, dist - 31, dist + 31, base);
 #pragma unroll
-          for (int r = 0; r < 16; ++r) s[r] = exp2_fast(s[r] - lse) * (dp[r] - delta);
+          for (int r = 0; r < 16; ++r)
+            s[r] = exp2_fast(BIAS ? s[r] - lse : __builtin_fmaf(s[r], g.c, -lse)) * (dp[r] - delta);
           const int limit = me.limit - key - 32 * b;
-          if (!whole) {
+          if (!WHOLE) {
 #pragma unroll
             for (int r = 0; r < 16; ++r)
               if (acc_row(r) + 4 * half >= limit) s[r] = 0.f;
@@ -532,27 +550,60 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
                                        __HIP_MEMORY_SCOPE_WORKGROUP);
             }
           }
+          const uint32_t bad = !WHOLE && g.causal ? rows_not_finite<DT, DP>(rl, 0) : 0;
+          if (!WHOLE && bad) {
+            if (bad & bit_range(0, limit)) poison = __builtin_nanf("");
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const Frag<DT> ds = acc_frag<DT>(s, c);
+#pragma unroll
+              for (int d = 0; d < DB; ++d)
+                dq[d] = mma(finite<DT>(T::col_frag(cl, 16 * c, d)), ds, dq[d]);
+            }
+            continue;
+          }
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const Frag<DT> ds = acc_frag<DT>(s, c);
 #pragma unroll
-            for (int d = 0; d < DB; ++d) {
-              const Frag<DT> kf = T::col_frag(lk, 32 * b + 16 * c, 32 * d);
-              if (whole) dq[d] = mma(kf, ds, dq[d]);
-              else
-                dq[d] = mma_seen<DT>(kf, ds, dq[d], [&](int i) { return 16 * c + i < limit; });
-            }
+            for (int d = 0; d < DB; ++d) dq[d] = mma(T::col_frag(cl, 16 * c, d), ds, dq[d]);
           }
         }
+      };
+
+      sk.load(kb, end, g.D, a.k.vec);
+      sv.load(vb, end, g.D, a.v.vec);
+      int buf = 0;
+      __syncthreads();  // the previous tile's reads are done
+      for (int key = 0; key < end; key += F::KEYS) {
+        char* const lk = lds + buf * 2 * F::TILE_BYTES;
+        char* const lv = lk + F::TILE_BYTES;
+        sk.store(lk);
+        sv.store(lv);
+        __syncthreads();
+        const int next = key + F::KEYS;
+        if (next < end) {
+          sk.load(kb + next * kt, end - next, g.D, a.k.vec);
+          sv.load(vb + next * vt, end - next, g.D, a.v.vec);
+        }
+        buf ^= 1;
+        if (key >= last) continue;
+        const int at = (int)(lk - lds);
+        if (key + F::KEYS <= first) attend(Whole(), key, at);
+        else attend(Masked(), key, at);
       }
       if (me.valid) {
-        char* p = const_cast<char*>(row_at<DT>(a.g_q, token, me.head));
+        const auto& z = *again<AttnBwd>();
+        char* p = row_at<DT>(z.g_q, token, me.head);
+        const int D = z.g.D;
+        const bool vec = z.g_q.vec;
+        const float scale = z.g.scale + poison;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
           for (int r = 0; r < 16; r += 4)
-            store4<DT>(p, 32 * d + acc_row(r) + 4 * half, g.D, a.g_q.vec, dq[d][r] * g.scale,
-                       dq[d][r + 1] * g.scale, dq[d][r + 2] * g.scale, dq[d][r + 3] * g.scale);
+            store4<DT>(p, 32 * d + acc_row(r) + 4 * half, D, vec, dq[d][r] * scale,
+                       dq[d][r + 1] * scale, dq[d][r + 2] * scale, dq[d][r + 3] * scale);
       }
     }
 
@@ -564,6 +615,8 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
         far[2 * wave + 1] = far_high;
       }
       __syncthreads();
+      // the eight lines added up, and each distance's bucket
+      int* const which = reinterpret_cast<int*>(sums) + lines;
       for (int i = threadIdx.x; i < lines; i += 256) {
         float v = 0.f;
 #pragma unroll
@@ -571,14 +624,16 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
         line[i] = v;
       }
       __syncthreads();
+      for (int i = threadIdx.x; i < lines; i += 256)
+        which[i] = bias_bucket(g.bias, i - g.bias.reach - BIAS_MARGIN);
+      __syncthreads();
       for (int b = threadIdx.x; b < g.bias.buckets; b += 256) {
         float v = 0.f;
-        const int reach = g.bias.reach + BIAS_MARGIN;
         for (int i = 0; i < lines; ++i)
-          if (bias_bucket(g.bias, i - reach) == b) v += line[i];
+          if (which[i] == b) v += line[i];
         for (int w = 0; w < 4; ++w) {
-          if (bias_bucket(g.bias, -reach) == b) v += far[2 * w];
-          if (bias_bucket(g.bias, reach) == b) v += far[2 * w + 1];
+          if (which[0] == b) v += far[2 * w];
+          if (which[lines - 1] == b) v += far[2 * w + 1];
         }
         a.g_line[item * g.bias.buckets + b] = v;
       }
@@ -595,12 +650,11 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
     AttnBwd a) {
   typedef BwdShape<DT, DP> F;
   typedef Tile<DT, DP> T;
-  constexpr int DB = DP / 32, DC = DP / 16, SB = F::KEYS / 32;
+  constexpr int DB = DP / 32, DC = DP / 16, SB = F::KEYS / 32, ES = DT == 0 ? 4 : 2;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  char* const lq = lds;
-  char* const lg = lds + F::TILE_BYTES;
-  float* const stat = reinterpret_cast<float*>(lds + F::LDS);  // lse, delta of the rows
-  float* const line = stat + 2 * F::KEYS;
+  float* const stats = reinterpret_cast<float*>(lds + F::LDS);  // lse, delta of the rows, twice
+  float* const line = stats + 4 * F::KEYS;
+  const uint32_t row_lane = lds_place(lds) + T::row_lane(), col_lane = lds_place(lds) + T::col_lane();
   const AttnShape& g = a.g;
   const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
 
@@ -626,142 +680,173 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
     sequence(g.start_q, seq, g.Tq, q0, nq);
     sequence(g.start_k, seq, g.Tk, k0, nk);
     const int rows = nq * g.pack, off = nk - nq;
+    const int64_t qt = a.q.token * ES, gt = a.g_o.token * ES;
+    Stage<DT, DP, F::KEYS> sq, sg;
+    sq.init((uint32_t)qt, (uint32_t)(a.q.head * ES), g.pack);
+    sg.init((uint32_t)gt, (uint32_t)(a.g_o.head * ES), g.pack);
 
     for (int64_t tile = tile0; tile * ATTN_ROWS < nk; tile += g.tiles) {
       const int wkey = (int)tile * ATTN_ROWS + wave * 32, key = wkey + (lane & 31);
       const bool valid = key < nk;
       Frag<DT> kf[DC], vf[DC];
       {
+        const auto& z = *again<AttnBwd>();
         const int64_t token = (int64_t)k0 + (valid ? key : 0);
-        const char* pk = row_at<DT>(a.k, token, kvh);
-        const char* pv = row_at<DT>(a.v, token, kvh);
+        const char* pk = row_at<DT>(z.k, token, kvh);
+        const char* pv = row_at<DT>(z.v, token, kvh);
+        const int D = z.g.D;
+        const bool kvec = z.k.vec, vvec = z.v.vec;
 #pragma unroll
         for (int c = 0; c < DC; ++c) {
           const int d = 16 * c + 8 * half;
-          kf[c] = valid ? global_frag<DT>(pk, d, g.D, a.k.vec) : zero_frag<DT>();
-          vf[c] = valid ? global_frag<DT>(pv, d, g.D, a.v.vec) : zero_frag<DT>();
+          kf[c] = valid ? global_frag<DT>(pk, d, D, kvec) : zero_frag<DT>();
+          vf[c] = valid ? global_frag<DT>(pv, d, D, vvec) : zero_frag<DT>();
         }
       }
       f32x16 dk[DB], dv[DB];
 #pragma unroll
       for (int d = 0; d < DB; ++d) dk[d] = dv[d] = (f32x16)(0.f);
-      // first row that sees the tile's first key; this wave's first key
+      float poison_k = 0.f, poison_v = 0.f;
+      // first row that sees the tile's first key, in whole tiles; this wave's first key
       int begin = 0, mine = 0;
       if (g.causal) {
         begin = max(0, (int)tile * ATTN_ROWS - off) * g.pack / F::KEYS * F::KEYS;
         mine = max(0, wkey - off) * g.pack;
       }
-      const int sees = g.causal ? max(0, key - off) * g.pack : 0;      // first row of this key
-      const int all = g.causal ? max(0, wkey + 31 - off) * g.pack : 0;  // of the wave's last
+      const int sees = g.causal ? max(0, key - off) * g.pack : 0;       // first row of this key
+      const int most = g.causal ? max(0, wkey + 31 - off) * g.pack : 0;  // of the wave's last
+
+      const auto attend = [&](auto all, int row, int tile, const float* stat) {
+        constexpr bool WHOLE = decltype(all)::value;
+#pragma unroll 1
+        for (int b = 0; b < SB; ++b) {
+          const uint32_t rl = row_lane + tile + 32 * b * T::ROW_BYTES;
+          const uint32_t cl = col_lane + tile + 32 * b * T::ROW_BYTES;
+          const int r0 = row + 32 * b;
+          if (!WHOLE && (r0 + 32 <= mine || r0 >= rows)) continue;
+          f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
+#pragma unroll
+          for (int c = 0; c < DC; ++c) {
+            s = mma(T::row_frag(rl, 0, c), kf[c], s);
+            dp = mma(T::row_frag(rl, F::KEYS, c), vf[c], dp);
+          }
+          if constexpr (BIAS) {
+            const int dist = wkey - (r0 + off);
+            add_bias<true>(g, line, s, dist - 31, dist + 31, key - (r0 + off) - 4 * half);
+          }
+          f32x16 ds;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 lse = *reinterpret_cast<const float4*>(stat + 32 * b + 8 * q + 4 * half);
+            const float4 del =
+                *reinterpret_cast<const float4*>(stat + F::KEYS + 32 * b + 8 * q + 4 * half);
+            const float ls[4] = {lse.x, lse.y, lse.z, lse.w};
+            const float de[4] = {del.x, del.y, del.z, del.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 4 * q + i;
+              s[r] = exp2_fast(BIAS ? s[r] - ls[i] : __builtin_fmaf(s[r], g.c, -ls[i]));
+              ds[r] = s[r] * (dp[r] - de[i]);
+            }
+          }
+          const int low = sees - r0, high = valid ? rows - r0 : 0;
+          if (!WHOLE) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const int i = acc_row(r) + 4 * half;
+              if (i < low || i >= high) s[r] = ds[r] = 0.f;
+            }
+          }
+          uint32_t bad_q = 0, bad_g = 0;
+          if (!WHOLE && g.causal) {
+            bad_q = rows_not_finite<DT, DP>(rl, 0);
+            bad_g = rows_not_finite<DT, DP>(rl, F::KEYS);
+          }
+          if (!WHOLE && (bad_q | bad_g)) {
+            const uint32_t seen = bit_range(low, high);
+            if (bad_q & seen) poison_k = __builtin_nanf("");
+            if (bad_g & seen) poison_v = __builtin_nanf("");
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const Frag<DT> pf = acc_frag<DT>(s, c), df = acc_frag<DT>(ds, c);
+#pragma unroll
+              for (int d = 0; d < DB; ++d) {
+                dv[d] = mma(finite<DT>(T::col_frag(cl, F::KEYS + 16 * c, d)), pf, dv[d]);
+                dk[d] = mma(finite<DT>(T::col_frag(cl, 16 * c, d)), df, dk[d]);
+              }
+            }
+            continue;
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const Frag<DT> pf = acc_frag<DT>(s, c), df = acc_frag<DT>(ds, c);
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+              dv[d] = mma(T::col_frag(cl, F::KEYS + 16 * c, d), pf, dv[d]);
+              dk[d] = mma(T::col_frag(cl, 16 * c, d), df, dk[d]);
+            }
+          }
+        }
+      };
 
       for (int group = 0; group < g.groups; ++group) {
         const int head0 = (kvh * g.groups + group) * g.pack;
-        if constexpr (BIAS) {
-          __syncthreads();
-          load_bias_line(g.bias, head0, g.heads, line);
-        }
-        Stage<DT, DP, F::KEYS> sq, sg;
+        __syncthreads();  // the previous rows' reads are done
+        if constexpr (BIAS) load_bias_line(g.bias, head0, g.heads, line);
+        const char* const qb = row_at<DT>(a.q, q0, head0);
+        const char* const gb = row_at<DT>(a.g_o, q0, head0);
         float st = 0.f;
         const auto fetch = [&](int row) {
-          const auto at = [&](const AttnRows& t, int r) -> const void* {
-            if (r >= rows) return nullptr;
-            const int tok = g.pack == 1 ? r : (int)((unsigned)r / (unsigned)g.pack);
-            return row_at<DT>(t, (int64_t)q0 + tok, head0 + r - tok * g.pack);
-          };
-          sq.load([&](int r) { return at(a.q, row + r); }, g.D, a.q.vec);
-          sg.load([&](int r) { return at(a.g_o, row + r); }, g.D, a.g_o.vec);
+          const int64_t tok = row / g.pack;  // KEYS is a multiple of pack
+          sq.load(qb + tok * qt, rows - row, g.D, a.q.vec);
+          sg.load(gb + tok * gt, rows - row, g.D, a.g_o.vec);
           if (threadIdx.x < 2 * F::KEYS) {
             const int r = row + (int)threadIdx.x % F::KEYS;
             const bool first = threadIdx.x < F::KEYS;
             st = first ? kInf : 0.f;
             if (r < rows) {
-              const int tok = g.pack == 1 ? r : (int)((unsigned)r / (unsigned)g.pack);
-              const int64_t i = (head0 + r - tok * g.pack) * g.Tq + q0 + tok;
+              const int t = (int)((unsigned)r / (unsigned)g.pack);
+              const int64_t i = (head0 + r - t * g.pack) * g.Tq + q0 + t;
               st = first ? a.lse[i] * kLog2e : a.delta[i];
               if (first && st == -kInf) st = kInf;
             }
           }
         };
         if (begin < rows) fetch(begin);
+        int buf = 0;
         for (int row = begin; row < rows; row += F::KEYS) {
-          __syncthreads();
+          char* const lq = lds + buf * 2 * F::TILE_BYTES;
+          char* const lg = lq + F::TILE_BYTES;
+          float* const stat = stats + buf * 2 * F::KEYS;
           sq.store(lq);
           sg.store(lg);
           if (threadIdx.x < 2 * F::KEYS) stat[threadIdx.x] = st;
           __syncthreads();
           if (row + F::KEYS < rows) fetch(row + F::KEYS);
+          buf ^= 1;
           if (row + F::KEYS <= mine) continue;
-          const bool whole = row >= all && row + F::KEYS <= rows && wkey + 32 <= nk;
-#pragma unroll
-          for (int b = 0; b < SB; ++b) {
-            f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
-#pragma unroll
-            for (int c = 0; c < DC; ++c) {
-              const int r = 32 * b + (lane & 31), d = 16 * c + 8 * half;
-              s = mma(T::row_frag(lq, r, d), kf[c], s);
-              dp = mma(T::row_frag(lg, r, d), vf[c], dp);
-            }
-            const int r0 = row + 32 * b;
-            if constexpr (BIAS) {
-              const int dist = wkey - (r0 + off);
-              add_bias<true>(g, line, s, dist - 31, dist + 31, key - (r0 + off) - 4 * half, true);
-            } else {
-              add_bias<false>(g, nullptr, s, 0, 0, 0, false);
-            }
-            f32x16 ds;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float4 lse = *reinterpret_cast<const float4*>(stat + 32 * b + 8 * q + 4 * half);
-              const float4 del =
-                  *reinterpret_cast<const float4*>(stat + F::KEYS + 32 * b + 8 * q + 4 * half);
-              const float ls[4] = {lse.x, lse.y, lse.z, lse.w};
-              const float de[4] = {del.x, del.y, del.z, del.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int r = 4 * q + i;
-                s[r] = exp2_fast(s[r] - ls[i]);
-                ds[r] = s[r] * (dp[r] - de[i]);
-              }
-            }
-            const int low = sees - r0, high = valid ? rows - r0 : 0;
-            if (!whole) {
-#pragma unroll
-              for (int r = 0; r < 16; ++r) {
-                const int i = acc_row(r) + 4 * half;
-                if (i < low || i >= high) s[r] = ds[r] = 0.f;
-              }
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const Frag<DT> pf = acc_frag<DT>(s, c), df = acc_frag<DT>(ds, c);
-#pragma unroll
-              for (int d = 0; d < DB; ++d) {
-                const Frag<DT> gf = T::col_frag(lg, 32 * b + 16 * c, 32 * d);
-                const Frag<DT> qf = T::col_frag(lq, 32 * b + 16 * c, 32 * d);
-                if (whole) {
-                  dv[d] = mma(gf, pf, dv[d]);
-                  dk[d] = mma(qf, df, dk[d]);
-                } else {
-                  const auto seen = [&](int i) { return 16 * c + i >= low && 16 * c + i < high; };
-                  dv[d] = mma_seen<DT>(gf, pf, dv[d], seen);
-                  dk[d] = mma_seen<DT>(qf, df, dk[d], seen);
-                }
-              }
-            }
-          }
+          if (row >= most && row + F::KEYS <= rows && wkey + 32 <= nk)
+            attend(Whole(), row, (int)(lq - lds), stat);
+          else
+            attend(Masked(), row, (int)(lq - lds), stat);
         }
       }
       if (valid) {
-        char* pk = const_cast<char*>(row_at<DT>(a.g_k, (int64_t)k0 + key, kvh));
-        char* pv = const_cast<char*>(row_at<DT>(a.g_v, (int64_t)k0 + key, kvh));
+        const auto& z = *again<AttnBwd>();
+        char* pk = row_at<DT>(z.g_k, (int64_t)k0 + key, kvh);
+        char* pv = row_at<DT>(z.g_v, (int64_t)k0 + key, kvh);
+        const int D = z.g.D;
+        const bool kvec = z.g_k.vec, vvec = z.g_v.vec;
+        const float scale = z.g.scale + poison_k, one = 1.f + poison_v;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
           for (int r = 0; r < 16; r += 4) {
             const int e = 32 * d + acc_row(r) + 4 * half;
-            store4<DT>(pv, e, g.D, a.g_v.vec, dv[d][r], dv[d][r + 1], dv[d][r + 2], dv[d][r + 3]);
-            store4<DT>(pk, e, g.D, a.g_k.vec, dk[d][r] * g.scale, dk[d][r + 1] * g.scale,
-                       dk[d][r + 2] * g.scale, dk[d][r + 3] * g.scale);
+            store4<DT>(pv, e, D, vvec, dv[d][r] * one, dv[d][r + 1] * one, dv[d][r + 2] * one,
+                       dv[d][r + 3] * one);
+            store4<DT>(pk, e, D, kvec, dk[d][r] * scale, dk[d][r + 1] * scale, dk[d][r + 2] * scale,
+                       dk[d][r + 3] * scale);
           }
       }
     }
@@ -845,10 +930,10 @@ hipError_t launch_attention_backward_kv<HLQ_ATTN_D>(const AttnBwd& a, int dtype,
   if (dtype == 0)
     return launch_items(a.g.bias.table ? k_attention_backward_kv<0, DP, true>
                                        : k_attention_backward_kv<0, DP, false>,
-                        a, BwdShape<0, DP>::LDS + 8 * BwdShape<0, DP>::KEYS + lines, gaps, s);
+                        a, BwdShape<0, DP>::LDS + 16 * BwdShape<0, DP>::KEYS + lines, gaps, s);
   return launch_items(a.g.bias.table ? k_attention_backward_kv<1, DP, true>
                                      : k_attention_backward_kv<1, DP, false>,
-                      a, BwdShape<1, DP>::LDS + 8 * BwdShape<1, DP>::KEYS + lines, gaps, s);
+                      a, BwdShape<1, DP>::LDS + 16 * BwdShape<1, DP>::KEYS + lines, gaps, s);
 }
 
 }  // namespace hlq

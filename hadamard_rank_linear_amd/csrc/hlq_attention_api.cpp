@@ -21,6 +21,8 @@ using hlq::AttnShape;
 
 constexpr int64_t kRows = int64_t(1) << 30;    // queries times heads, and keys times heads
 constexpr int64_t kStride = int64_t(1) << 40;  // elements
+// Tokens: a tile's 128 rows at this distance are within 32-bit offsets.
+constexpr int64_t kTokenStride = int64_t(1) << 22;
 
 bool dtype_ok(int dt) { return dt == HLQ_F32 || dt == HLQ_BF16; }
 size_t esize(int dt) { return dt == HLQ_F32 ? 4 : 2; }
@@ -75,7 +77,7 @@ hlq_status check_rows(const hlq_attention* a, const hlq_tokens* t, int64_t token
   if (tokens == 0) return HLQ_OK;
   if (!t->data) return HLQ_ERR_NULL;
   if (!aligned(t->data, esize(a->dtype))) return HLQ_ERR_ALIGN;
-  if (t->token_stride < 0 || t->head_stride < 0 || t->token_stride >= kStride ||
+  if (t->token_stride < 0 || t->head_stride < 0 || t->token_stride >= kTokenStride ||
       t->head_stride >= kStride)
     return HLQ_ERR_SHAPE;
   if (out) {
@@ -303,6 +305,12 @@ hlq_status hlq_attention_backward(const hlq_attention* a, const hlq_tokens* g_o,
     HLQ_TRY(hlq::launch_attention_bias(b.g_line, a->sequences, b.g.tiles, a->heads, a->buckets,
                                        a->bias_dtype, g_bias, s));
   if (a->keys) {
+    // Rows that are read through LDS are packed where the heads are a power of two
+    // that divides the rows a thread steps over, and near enough for 32-bit offsets.
+    const int shared = a->heads / a->kv_heads;
+    const int64_t far = std::max(b.q.head, b.g_o.head) * (int64_t)esize(a->dtype) * shared;
+    if ((shared & (shared - 1)) || shared > hlq::ATTN_PACK || far >= (int64_t(1) << 30)) b.g.pack = 1;
+    b.g.groups = shared / b.g.pack;
     b.g.tiles = (expected(a, a->keys) + hlq::ATTN_ROWS - 1) / hlq::ATTN_ROWS;
     b.g.items = b.g.tiles * a->sequences * a->kv_heads;
     HLQ_TRY(HLQ_BY_SIZE(a->head_dim, launch_attention_backward_kv, b, a->dtype, s));

@@ -12,6 +12,7 @@
 namespace hlq {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -74,45 +75,38 @@ __device__ __forceinline__ Frag<DT> acc_frag(const f32x16& s, int c) {
   return f;
 }
 
-// Nonzero if one of the fragment's values is not finite (all exponent bits set).
-__device__ __forceinline__ uint32_t not_finite(const bf16x8& f) {
-  u32x4 w;
-  __builtin_memcpy(&w, &f, 16);
-  uint32_t bad = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) bad |= ((w[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-  return bad;
-}
-__device__ __forceinline__ uint32_t not_finite(const f32x8& f) {
-  uint32_t bad = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    bad |= ((__float_as_uint(f[i]) & 0x7F800000u) + 0x00800000u) & 0x80000000u;
-  return bad;
-}
+// Where hidden pairs have probability zero, an infinity or NaN in the other operand
+// would reach the columns that do not see it (0 * NaN).  Blocks of which some
+// columns see a part are looked through for such values first.  If there are any,
+// the product goes without them, and a column that sees one becomes NaN as a whole.
 
-// acc += A B where the probabilities B of hidden pairs are zero but A may hold
-// infinities or NaN in rows that some columns do not see (0 * NaN would reach
-// them).  sees(i): whether this lane's column sees place i (0 .. 15) of the sum.
-// Finite operands, the usual case, cost the test alone; else one product for
-// each of the 16 places, kept by the columns that see it.
-template <int DT, typename F>
-__device__ __forceinline__ f32x16 mma_seen(const Frag<DT>& a, const Frag<DT>& b, f32x16 acc,
-                                           F sees) {
-  if (__builtin_expect(!__any(not_finite(a) != 0), 1)) return mma(a, b, acc);
-  const int half = (threadIdx.x >> 5) & 1;
-  for (int i = 0; i < 16; ++i) {
-    const int h = (i >> 2) & 1, e = 4 * (i >> 3) + (i & 3);
-    Frag<DT> one = zero_frag<DT>();
+// The high bits of the halves (bf16) or words (fp32) whose value is not finite.
+template <int DT>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  if constexpr (DT == 1) return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+  else return ((w & 0x7F800000u) + 0x00800000u) & 0x80000000u;
+}
+template <int DT>
+__device__ __forceinline__ uint32_t not_finite(const Frag<DT>& f) {
+  uint32_t w[sizeof f / 4], bad = 0;
+  __builtin_memcpy(w, &f, sizeof f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j == e && half == h) one[j] = a[j];
-    const f32x16 next = mma(one, b, acc);
-    const bool s = sees(i);
+  for (unsigned i = 0; i < sizeof f / 4; ++i) bad |= not_finite<DT>(w[i]);
+  return bad;
+}
+// Those values set to zero.
+template <int DT>
+__device__ __forceinline__ Frag<DT> finite(const Frag<DT>& f) {
+  uint32_t w[sizeof f / 4];
+  __builtin_memcpy(w, &f, sizeof f);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] = s ? next[r] : acc[r];
+  for (unsigned i = 0; i < sizeof f / 4; ++i) {
+    const uint32_t t = not_finite<DT>(w[i]);
+    w[i] &= DT == 1 ? ~((t - (t >> 15)) | t) : t ? 0u : ~0u;
   }
-  return acc;
+  Frag<DT> r;
+  __builtin_memcpy(&r, w, sizeof f);
+  return r;
 }
 
 // ------------------------------------------------------------ tiles in LDS
@@ -127,45 +121,67 @@ struct Tile {
   static constexpr int PITCH = CHUNKS <= 8 ? 8 : CHUNKS <= 16 ? 16 : 32;
   static constexpr int ROW_BYTES = PITCH * 16;
 
+  typedef __attribute__((address_space(3))) const char L;
+
   __device__ static __forceinline__ int mix(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
   __device__ static __forceinline__ int at(int r, int c) { return (r * PITCH + (c ^ mix(r))) * 16; }
 
-  // Row r, elements d .. d + 7 (d a multiple of 8).
-  __device__ static __forceinline__ Frag<DT> row_frag(const char* lds, int r, int d) {
+  // A lane's place in a tile read by rows (row lane & 31, the first of its half's
+  // chunks) and by columns (see col_frag): what at() gives without the constant
+  // parts of row and chunk.  mix() depends on the lane alone, since blocks begin at
+  // multiples of 16 rows, and a constant's bits below the mix's are put in by an
+  // exclusive or, those above by addition.
+  __device__ static __forceinline__ uint32_t row_lane() {
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    return at(lane & 31, DT == 1 ? half : 2 * half);
+  }
+  __device__ static __forceinline__ uint32_t col_lane() {
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    if constexpr (DT == 1) {
+      const int col = (lane & 16) + 4 * (lane & 3);
+      return at(4 * half + ((lane & 15) >> 2), col >> 3) + (col & 4) * 2;
+    } else {
+      return at(4 * half, (lane & 31) >> 2) + (lane & 3) * 4;
+    }
+  }
+  __device__ static __forceinline__ L* place(uint32_t lane, int row, int chunk) {
+    return (L*)(uintptr_t)((lane ^ ((chunk & 7) * 16)) + (chunk & ~7) * 16 + row * ROW_BYTES);
+  }
+
+  // Rows r .. r + 31 (one a lane), elements 16 c + 8 half .. + 7.  tile: row_lane()
+  // plus the tile's place in LDS.
+  __device__ static __forceinline__ Frag<DT> row_frag(uint32_t tile, int r, int c) {
     Frag<DT> f;
     if constexpr (DT == 1) {
-      f = *reinterpret_cast<const bf16x8*>(lds + at(r, d / 8));
+      f = *(__attribute__((address_space(3))) const bf16x8*)place(tile, r, 2 * c);
     } else {
-      const float4 a = *reinterpret_cast<const float4*>(lds + at(r, d / 4));
-      const float4 b = *reinterpret_cast<const float4*>(lds + at(r, d / 4 + 1));
-      f = (f32x8){a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      typedef __attribute__((address_space(3))) const f32x4 V;
+      const f32x4 a = *(V*)place(tile, r, 4 * c), b = *(V*)place(tile, r, 4 * c + 1);
+      f = (f32x8){a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     }
     return f;
   }
 
-  // Column d + (lane & 31), rows r + 8 (e >> 2) + 4 half + (e & 3): the operand
-  // whose sum runs over rows.  bf16: two transposing reads, in which lane j of 16
-  // points at row j / 4, columns 4 (j % 4) of a 4 x 16 block and gets column j.
-  __device__ static __forceinline__ Frag<DT> col_frag(const char* lds, int r, int d) {
-    const int lane = threadIdx.x & 63, half = lane >> 5;
+  // Columns 32 d .. 32 d + 31 (one a lane), rows r + 8 (e >> 2) + 4 half + (e & 3):
+  // the operand whose sum runs over rows.  bf16: two transposing reads, in which
+  // lane j of 16 points at row j / 4, columns 4 (j % 4) of a 4 x 16 block and gets
+  // column j.  tile: col_lane() plus the tile's place.
+  __device__ static __forceinline__ Frag<DT> col_frag(uint32_t tile, int r, int d) {
     Frag<DT> f;
     if constexpr (DT == 1) {
-      const int row = r + 4 * half + ((lane & 15) >> 2);
-      const int col = d + (lane & 16) + 4 * (lane & 3);
-      const int sub = (col & 4) * 2;
-      typedef __attribute__((address_space(3))) s16x4 L;
+      typedef __attribute__((address_space(3))) s16x4 V;
       s16x4 v[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        v[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (L*)(lds + at(row + 8 * i, col >> 3) + sub));
+        v[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((V*)place(tile, r + 8 * i, 4 * d));
       __builtin_memcpy(&f, v, 16);
     } else {
-      const int col = d + (lane & 31);
+      typedef __attribute__((address_space(3))) const float V;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int row = r + 8 * (e >> 2) + 4 * half + (e & 3);
-        f[e] = *reinterpret_cast<const float*>(lds + at(row, col >> 2) + (col & 3) * 4);
+        // rows 4 half + (e & 3): the mix of e & 3 on top of the lane's
+        const int row = r + 8 * (e >> 2) + (e & 3);
+        f[e] = *(V*)place(tile ^ (mix(e & 3) * 16), row, 8 * d);
       }
     }
     return f;
@@ -224,34 +240,79 @@ __device__ __forceinline__ void store4(void* row, int d, int n, bool vec, float 
   }
 }
 
-// A tile's global loads, a chunk a time per thread of 256, held until the LDS
-// is free.  row(r) is row r's address, null past the end (read as zeros).
+// Bit i: row r + i of a tile holds a value that is not finite.  The same in every lane.
+template <int DT, int DP>
+__device__ __forceinline__ uint32_t rows_not_finite(uint32_t tile, int r) {
+  uint32_t bad = 0;
+#pragma unroll
+  for (int c = 0; c < DP / 16; ++c) bad |= not_finite<DT>(Tile<DT, DP>::row_frag(tile, r, c));
+  const uint64_t lanes = __ballot(bad != 0);
+  return (uint32_t)lanes | (uint32_t)(lanes >> 32);
+}
+// Bits low .. high - 1 of 32.
+__device__ __forceinline__ uint32_t bit_range(int low, int high) {
+  const uint32_t below = high >= 32 ? ~0u : high <= 0 ? 0u : (1u << high) - 1u;
+  return low >= 32 ? 0u : low <= 0 ? below : below & ~((1u << low) - 1u);
+}
+
+// A tile's global loads by 256 threads, held in registers until its place in LDS
+// is free.  A thread has the same chunk of every RS-th row; its bytes from the
+// tile's first row on are 32-bit offsets (token strides are limited for that).
 template <int DT, int DP, int ROWS>
 struct Stage {
   typedef Tile<DT, DP> T;
-  static constexpr int N = (ROWS * T::CHUNKS + 255) / 256;
+  // rows at a time: a power of two
+  static constexpr int RS = 256 / (T::CHUNKS == 12 ? 16 : T::CHUNKS == 24 ? 32 : T::CHUNKS);
+  static constexpr int N = (ROWS + RS - 1) / RS;
   u32x4 v[N];
+  uint32_t off, step;
+  int r0, c;
 
-  template <typename F>
-  __device__ __forceinline__ void load(F row, int D, bool vec) {
+  // Strides in bytes; pack heads of a token make neighbouring rows (pack divides RS).
+  __device__ __forceinline__ void init(uint32_t token, uint32_t head, int pack) {
+    r0 = threadIdx.x / T::CHUNKS;
+    c = threadIdx.x % T::CHUNKS;
+    step = RS / pack * token;
+    off = (uint32_t)(r0 / pack) * token + (uint32_t)(r0 % pack) * head + c * 16;
+    if (r0 >= RS) r0 = ROWS;  // threads beyond the last whole row
+  }
+  // base: the tile's first row; n: how many rows there are from it on; past them, and
+  // past D, zeros.
+  __device__ __forceinline__ void load(const char* base, int n, int D, bool vec) {
+    if (vec && n >= ROWS && D == DP && N * RS == ROWS && RS * T::CHUNKS == 256) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        v[i] = *reinterpret_cast<const u32x4*>(base + (size_t)(off + i * step));
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int at = i * 256 + threadIdx.x, r = at / T::CHUNKS, c = at % T::CHUNKS;
+      const int r = r0 + i * RS;
       v[i] = (u32x4){0u, 0u, 0u, 0u};
-      if (at < ROWS * T::CHUNKS) {
-        const void* p = row(r);
-        if (p) v[i] = row_chunk<DT>(p, c * T::CE, D, vec);
+      if (r < n && r < ROWS && c * T::CE < D) {
+        const char* p = base + (size_t)(off + i * step);
+        if (vec) v[i] = *reinterpret_cast<const u32x4*>(p);
+        else v[i] = load_piece<DT>(p, 0, D - c * T::CE);
       }
     }
   }
   __device__ __forceinline__ void store(char* lds) const {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int at = i * 256 + threadIdx.x, r = at / T::CHUNKS, c = at % T::CHUNKS;
-      if (at < ROWS * T::CHUNKS) *reinterpret_cast<u32x4*>(lds + T::at(r, c)) = v[i];
-    }
+    for (int i = 0; i < N; ++i)
+      if (r0 + i * RS < ROWS) *reinterpret_cast<u32x4*>(lds + T::at(r0 + i * RS, c)) = v[i];
   }
 };
+
+// The kernel's argument (its only one) to be read where it is needed: the compiler
+// loads what it knows to be constant at the start, and has no registers to keep it
+// in until the end.
+template <typename A>
+__device__ __forceinline__ const __attribute__((address_space(4))) A* again() {
+  typedef const __attribute__((address_space(4))) A C;
+  uint64_t p = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return (C*)p;
+}
 
 // ------------------------------------------------------------ sequences
 

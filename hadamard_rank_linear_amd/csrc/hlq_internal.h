@@ -319,6 +319,7 @@ struct AttnBwd {
 };
 constexpr int ATTN_ROWS = 128;  // query rows, or keys, of a workgroup
 constexpr int ATTN_FEW = 32;    // rows of a workgroup whose waves share the keys
+constexpr int ATTN_PACK = 8;    // heads packed into the rows that go through LDS (a power of two)
 template <int DP>
 hipError_t launch_attention_forward(const AttnFwd& a, int dtype, bool few, hipStream_t s);
 template <int DP>
