@@ -120,9 +120,10 @@ struct FwdShape {
   static constexpr int ROWS = FEW ? ATTN_FEW : ATTN_ROWS;
   static constexpr int KEYS = FEW ? 128 : DT == 0 ? 32 : 64;  // of a tile
   static constexpr int MINE = FEW ? 32 : KEYS;                // of them a wave's
-  static constexpr int BUFS = FEW ? 1 : 2;  // tiles of keys and of values in LDS
   static constexpr int TILE_BYTES = KEYS * T::ROW_BYTES;
   static constexpr int JOIN_BYTES = FEW ? 4 * DP * 33 * 4 + 4 * 32 * 8 : 0;
+  // buffers of a tile of keys and of values: one where two do not fit the LDS
+  static constexpr int BUFS = TILE_BYTES > 32768 ? 1 : 2;
   static constexpr int LDS =
       2 * BUFS * TILE_BYTES > JOIN_BYTES ? 2 * BUFS * TILE_BYTES : JOIN_BYTES;
 };
@@ -160,20 +161,19 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
     return;
   }
 
-  for (int64_t item = first_item(g.launched); item < g.items; item += g.launched) {
-    int64_t rest = item;
-    const int split = (int)(rest % g.splits);
-    rest /= g.splits;
-    const int64_t tile0 = g.tiles - 1 - rest % g.tiles;  // the longest first
-    rest /= g.tiles;
-    const int unit = (int)(rest % (g.kv_heads * g.groups));
-    const int64_t seq = rest / (g.kv_heads * g.groups);
-    const int head0 = unit * g.pack, kvh = unit / g.groups;
+  for (unsigned item = blockIdx.x; item < g.items; item += g.launched) {
+    unsigned u, t;
+    if (!item_of(g, item, u, t)) continue;
+    const int split = (int)(t % g.splits);
+    const unsigned tile0 = g.tiles - 1 - t / g.splits;  // the longest first
+    const unsigned per = g.kv_heads * g.groups;
+    const int64_t seq = u / per;
+    const int unit = (int)(u % per), head0 = unit * g.pack, kvh = unit / g.groups;
     int q0, nq, k0, nk;
     sequence(g.start_q, seq, g.Tq, q0, nq);
     sequence(g.start_k, seq, g.Tk, k0, nk);
     const int rows = nq * g.pack, off = nk - nq;
-    if (tile0 * F::ROWS >= rows) continue;
+    if ((int64_t)tile0 * F::ROWS >= rows) continue;
     if constexpr (BIAS) {
       __syncthreads();
       load_bias_line(g.bias, head0, g.heads, line);
@@ -181,7 +181,7 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
     const char* const kb = row_at<DT>(a.k, k0, kvh);
     const char* const vb = row_at<DT>(a.v, k0, kvh);
     const int64_t kt = a.k.token * ES, vt = a.v.token * ES;
-    Stage<DT, DP, F::KEYS> sk, sv;
+    Feed<DT, DP, F::KEYS> sk, sv;
     sk.init((uint32_t)kt, 0, 1);
     sv.init((uint32_t)vt, 0, 1);
 
@@ -288,26 +288,24 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
         l += sum;
       };
 
-      sk.load(kb + from * kt, end - from, g.D, a.k.vec);
-      sv.load(vb + from * vt, end - from, g.D, a.v.vec);
+      const auto feed = [&](int key, int buf) {
+        char* const at = lds + buf * 2 * F::TILE_BYTES;
+        sk.issue(kb + key * kt, end - key, g.D, a.k.vec, at);
+        sv.issue(vb + key * vt, end - key, g.D, a.v.vec, at + F::TILE_BYTES);
+      };
+      __syncthreads();  // the previous tile's reads are done
+      if (F::BUFS == 2 && from < end) feed(from, 0);
       int buf = 0;
-      if (F::BUFS == 2) __syncthreads();  // the previous tile's reads are done
-      for (int key = from; key < end; key += F::KEYS) {
-        char* const lk = lds + buf * 2 * F::TILE_BYTES;
-        char* const lv = lk + F::TILE_BYTES;
-        if (F::BUFS == 1) __syncthreads();
-        sk.store(lk);
-        sv.store(lv);
-        __syncthreads();
-        const int next = key + F::KEYS;
-        if (next < end) {
-          sk.load(kb + next * kt, end - next, g.D, a.k.vec);
-          sv.load(vb + next * vt, end - next, g.D, a.v.vec);
+      for (int key = from; key < end; key += F::KEYS, buf ^= F::BUFS - 1) {
+        if (F::BUFS == 1) {
+          __syncthreads();
+          feed(key, 0);
         }
-        if (F::BUFS == 2) buf ^= 1;
+        feed_wait();
+        if (F::BUFS == 2 && key + F::KEYS < end) feed(key + F::KEYS, buf ^ 1);
         const int mine = FEW ? 32 * wave : 0, key0 = key + mine;
         if (key0 >= last) continue;
-        const int at = (int)(lk - lds) + mine * T::ROW_BYTES;
+        const int at = buf * 2 * F::TILE_BYTES + mine * T::ROW_BYTES;
         if (key0 + F::MINE <= first) attend(Whole(), key0, at);
         else attend(Masked(), key0, at);
       }
@@ -434,21 +432,21 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
     return;
   }
 
-  for (int64_t item = first_item(g.launched); item < g.items; item += g.launched) {
-    int64_t rest = item;
-    const int64_t tile0 = g.tiles - 1 - rest % g.tiles;
-    rest /= g.tiles;
-    const int unit = (int)(rest % (g.kv_heads * g.groups));
-    const int64_t seq = rest / (g.kv_heads * g.groups);
-    const int head0 = unit * g.pack, kvh = unit / g.groups;
+  for (unsigned item = blockIdx.x; item < g.items; item += g.launched) {
+    unsigned u, t;
+    if (!item_of(g, item, u, t)) continue;
+    const unsigned tile0 = g.tiles - 1 - t, per = g.kv_heads * g.groups;
+    const int64_t seq = u / per;
+    const int unit = (int)(u % per), head0 = unit * g.pack, kvh = unit / g.groups;
+    float* const bucket_sums = a.g_line + ((int64_t)u * g.tiles + tile0) * g.bias.buckets;
     int q0, nq, k0, nk;
     sequence(g.start_q, seq, g.Tq, q0, nq);
     sequence(g.start_k, seq, g.Tk, k0, nk);
     const int rows = nq * g.pack, off = nk - nq;
-    if (tile0 * ATTN_ROWS >= rows) {
+    if ((int64_t)tile0 * ATTN_ROWS >= rows) {
       if constexpr (BIAS)
         for (int b = threadIdx.x; b < g.bias.buckets; b += 256)
-          a.g_line[item * g.bias.buckets + b] = 0.f;
+          bucket_sums[b] = 0.f;
       continue;
     }
     float far_low = 0.f, far_high = 0.f;
@@ -460,7 +458,7 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
     const char* const kb = row_at<DT>(a.k, k0, kvh);
     const char* const vb = row_at<DT>(a.v, k0, kvh);
     const int64_t kt = a.k.token * ES, vt = a.v.token * ES;
-    Stage<DT, DP, F::KEYS> sk, sv;
+    Feed<DT, DP, F::KEYS> sk, sv;
     sk.init((uint32_t)kt, 0, 1);
     sv.init((uint32_t)vt, 0, 1);
 
@@ -571,24 +569,19 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
         }
       };
 
-      sk.load(kb, end, g.D, a.k.vec);
-      sv.load(vb, end, g.D, a.v.vec);
-      int buf = 0;
+      const auto feed = [&](int key, int buf) {
+        char* const at = lds + buf * 2 * F::TILE_BYTES;
+        sk.issue(kb + key * kt, end - key, g.D, a.k.vec, at);
+        sv.issue(vb + key * vt, end - key, g.D, a.v.vec, at + F::TILE_BYTES);
+      };
       __syncthreads();  // the previous tile's reads are done
-      for (int key = 0; key < end; key += F::KEYS) {
-        char* const lk = lds + buf * 2 * F::TILE_BYTES;
-        char* const lv = lk + F::TILE_BYTES;
-        sk.store(lk);
-        sv.store(lv);
-        __syncthreads();
-        const int next = key + F::KEYS;
-        if (next < end) {
-          sk.load(kb + next * kt, end - next, g.D, a.k.vec);
-          sv.load(vb + next * vt, end - next, g.D, a.v.vec);
-        }
-        buf ^= 1;
+      if (end > 0) feed(0, 0);
+      int buf = 0;
+      for (int key = 0; key < end; key += F::KEYS, buf ^= 1) {
+        feed_wait();
+        if (key + F::KEYS < end) feed(key + F::KEYS, buf ^ 1);
         if (key >= last) continue;
-        const int at = (int)(lk - lds);
+        const int at = buf * 2 * F::TILE_BYTES;
         if (key + F::KEYS <= first) attend(Whole(), key, at);
         else attend(Masked(), key, at);
       }
@@ -635,7 +628,7 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
           if (which[0] == b) v += far[2 * w];
           if (which[lines - 1] == b) v += far[2 * w + 1];
         }
-        a.g_line[item * g.bias.buckets + b] = v;
+        bucket_sums[b] = v;
       }
     }
   }
@@ -670,18 +663,18 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
     return;
   }
 
-  for (int64_t item = first_item(g.launched); item < g.items; item += g.launched) {
-    int64_t rest = item;
-    const int64_t tile0 = rest % g.tiles;  // first keys are seen by most rows
-    rest /= g.tiles;
-    const int kvh = (int)(rest % g.kv_heads);
-    const int64_t seq = rest / g.kv_heads;
+  for (unsigned item = blockIdx.x; item < g.items; item += g.launched) {
+    unsigned u, tile0;  // first keys are seen by most rows
+    if (!item_of(g, item, u, tile0)) continue;
+    const int64_t seq = u / (unsigned)g.kv_heads;
+    const int kvh = (int)(u % (unsigned)g.kv_heads);
     int q0, nq, k0, nk;
     sequence(g.start_q, seq, g.Tq, q0, nq);
     sequence(g.start_k, seq, g.Tk, k0, nk);
     const int rows = nq * g.pack, off = nk - nq;
+    if ((int64_t)tile0 * ATTN_ROWS >= nk) continue;
     const int64_t qt = a.q.token * ES, gt = a.g_o.token * ES;
-    Stage<DT, DP, F::KEYS> sq, sg;
+    Feed<DT, DP, F::KEYS> sq, sg;
     sq.init((uint32_t)qt, (uint32_t)(a.q.head * ES), g.pack);
     sg.init((uint32_t)gt, (uint32_t)(a.g_o.head * ES), g.pack);
 
@@ -796,10 +789,12 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
         const char* const qb = row_at<DT>(a.q, q0, head0);
         const char* const gb = row_at<DT>(a.g_o, q0, head0);
         float st = 0.f;
-        const auto fetch = [&](int row) {
+        // The rows' statistics go through a register, into the buffer at the next turn.
+        const auto fetch = [&](int row, int buf) {
           const int64_t tok = row / g.pack;  // KEYS is a multiple of pack
-          sq.load(qb + tok * qt, rows - row, g.D, a.q.vec);
-          sg.load(gb + tok * gt, rows - row, g.D, a.g_o.vec);
+          char* const at = lds + buf * 2 * F::TILE_BYTES;
+          sq.issue(qb + tok * qt, rows - row, g.D, a.q.vec, at);
+          sg.issue(gb + tok * gt, rows - row, g.D, a.g_o.vec, at + F::TILE_BYTES);
           if (threadIdx.x < 2 * F::KEYS) {
             const int r = row + (int)threadIdx.x % F::KEYS;
             const bool first = threadIdx.x < F::KEYS;
@@ -812,23 +807,18 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
             }
           }
         };
-        if (begin < rows) fetch(begin);
+        if (begin < rows) fetch(begin, 0);
         int buf = 0;
-        for (int row = begin; row < rows; row += F::KEYS) {
-          char* const lq = lds + buf * 2 * F::TILE_BYTES;
-          char* const lg = lq + F::TILE_BYTES;
+        for (int row = begin; row < rows; row += F::KEYS, buf ^= 1) {
           float* const stat = stats + buf * 2 * F::KEYS;
-          sq.store(lq);
-          sg.store(lg);
           if (threadIdx.x < 2 * F::KEYS) stat[threadIdx.x] = st;
-          __syncthreads();
-          if (row + F::KEYS < rows) fetch(row + F::KEYS);
-          buf ^= 1;
+          feed_wait();
+          if (row + F::KEYS < rows) fetch(row + F::KEYS, buf ^ 1);
           if (row + F::KEYS <= mine) continue;
           if (row >= most && row + F::KEYS <= rows && wkey + 32 <= nk)
-            attend(Whole(), row, (int)(lq - lds), stat);
+            attend(Whole(), row, buf * 2 * F::TILE_BYTES, stat);
           else
-            attend(Masked(), row, (int)(lq - lds), stat);
+            attend(Masked(), row, buf * 2 * F::TILE_BYTES, stat);
         }
       }
       if (valid) {
@@ -858,11 +848,8 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
 constexpr unsigned GAP_GROUPS = 8;  // workgroups for the tokens of no sequence
 
 // Workgroups for the items: at most 2^20 (a launch holds fewer than 2^32
-// threads; the rest go by the loop), in multiples of 8 for the XCDs.
-unsigned groups_for(int64_t items) {
-  const int64_t n = (items + 7) / 8 * 8;
-  return (unsigned)(n < (1 << 20) ? n : 1 << 20);
-}
+// threads; the rest go by the loop), a multiple of 8 so that the loop keeps to an XCD.
+unsigned groups_for(unsigned items) { return items < (1u << 20) ? items : 1u << 20; }
 
 template <typename A>
 hipError_t launch_items(void (*kernel)(A), A a, int bytes, bool gaps, hipStream_t s) {

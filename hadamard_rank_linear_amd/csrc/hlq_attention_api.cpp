@@ -52,7 +52,7 @@ hlq_status check_shape(const hlq_attention* a) {
   if (a->queries < 0 || a->keys < 0 || a->sequences < 1 || a->heads < 1 || a->kv_heads < 1 ||
       a->heads % a->kv_heads || a->head_dim < 1 || a->head_dim > 128 || a->max_len < 0)
     return HLQ_ERR_SHAPE;
-  if (a->heads >= (1 << 16) || a->sequences >= kRows || a->queries >= kRows / a->heads ||
+  if (a->heads >= (1 << 16) || a->sequences >= kRows / a->heads || a->queries >= kRows / a->heads ||
       a->keys >= kRows / a->heads)
     return HLQ_ERR_SHAPE;
   if (!a->start_q && (a->sequences != 1 || a->start_k)) return HLQ_ERR_SHAPE;
@@ -138,10 +138,22 @@ int64_t expected(const hlq_attention* a, int64_t total) {
   return std::max<int64_t>(1, a->max_len ? std::min(total, a->max_len) : guess);
 }
 
+// Numbers a launch's work items.  Tiles beyond 2^30 items are looped over.  A unit's
+// items (which read the same keys and values, or rows) go to one XCD, where they meet
+// in its L2, if that leaves the eight equally busy.  With a causal mask long tiles come
+// first, of all units, so that the last to end are short.
+void number(AttnShape& g, int64_t tiles, int64_t units, int64_t splits) {
+  g.splits = (unsigned)splits;
+  g.units = (unsigned)units;
+  g.tiles = (unsigned)std::max<int64_t>(1, std::min(tiles, (int64_t(1) << 30) / (units * splits)));
+  g.by_xcd = units % 8 == 0 || units >= 64;
+  g.by_tile = g.causal;
+  g.items = g.tiles * g.splits * (g.by_xcd ? (g.units + 7) / 8 * 8 : g.units);
+}
+
 struct FwdPlan {
   bool few;
-  int64_t tiles, items;
-  int splits;
+  int64_t tiles, units, splits;
 };
 
 // Few rows leave most of the chip idle if a workgroup takes all keys of its rows;
@@ -154,11 +166,10 @@ FwdPlan plan_forward(const hlq_attention* a) {
   p.few = rows <= hlq::ATTN_FEW;
   const int per = p.few ? hlq::ATTN_FEW : hlq::ATTN_ROWS;
   p.tiles = (rows + per - 1) / per;
-  const int64_t units = p.tiles * a->sequences * (a->heads / shared);
-  const int64_t keys = a->keys / a->sequences;
-  int64_t splits = std::min<int64_t>((512 + units - 1) / units, keys / 256);
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(splits, 64));
-  p.items = units * p.splits;
+  p.units = a->sequences * (a->heads / shared);
+  const int64_t keys = a->keys / a->sequences, groups = p.tiles * p.units;
+  const int64_t splits = std::min<int64_t>((512 + groups - 1) / groups, keys / 256);
+  p.splits = std::max<int64_t>(1, std::min<int64_t>(splits, 64));
   return p;
 }
 
@@ -167,9 +178,14 @@ size_t forward_bytes(const hlq_attention* a, const FwdPlan& p) {
   return (size_t)p.splits * a->queries * a->heads * (a->head_dim + 2) * 4;
 }
 
-int64_t backward_tiles(const hlq_attention* a) {
+// The gradient of q's items, by which a bias's partial sums are laid out.
+AttnShape backward_q_shape(const hlq_attention* a) {
+  AttnShape g = {};
   const int shared = a->bias ? 1 : a->heads / a->kv_heads;
-  return (expected(a, a->queries) * shared + hlq::ATTN_ROWS - 1) / hlq::ATTN_ROWS;
+  g.causal = a->causal != 0;
+  const int64_t rows = expected(a, a->queries) * shared;
+  number(g, (rows + hlq::ATTN_ROWS - 1) / hlq::ATTN_ROWS, a->sequences * (a->heads / shared), 1);
+  return g;
 }
 
 size_t delta_bytes(const hlq_attention* a) {
@@ -242,9 +258,7 @@ hlq_status hlq_attention_forward(const hlq_attention* a, const hlq_tokens* q, co
   f.v = rows_of(a, v);
   f.o = rows_of(a, o);
   f.lse = lse;
-  f.g.tiles = p.tiles;
-  f.g.items = p.items;
-  f.g.splits = p.splits;
+  number(f.g, p.tiles, p.units, p.splits);
   if (need) {
     f.ml = static_cast<float*>(workspace);
     f.po = f.ml + (size_t)p.splits * a->queries * a->heads * 2;
@@ -259,7 +273,7 @@ size_t hlq_attention_backward_workspace_size(const hlq_attention* a) {
   if (check_shape(a) != HLQ_OK) return 0;
   size_t bytes = delta_bytes(a);
   if (a->bias)
-    bytes += (size_t)backward_tiles(a) * a->sequences * a->heads * a->buckets * 4;
+    bytes += (size_t)backward_q_shape(a).tiles * a->sequences * a->heads * a->buckets * 4;
   return bytes;
 }
 
@@ -296,8 +310,8 @@ hlq_status hlq_attention_backward(const hlq_attention* a, const hlq_tokens* g_o,
   b.delta = static_cast<float*>(workspace);
   b.g_line = reinterpret_cast<float*>(static_cast<char*>(workspace) + delta_bytes(a));
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  b.g.tiles = backward_tiles(a);
-  b.g.items = b.g.tiles * a->sequences * (a->heads / b.g.pack);
+  const AttnShape n = backward_q_shape(a);
+  number(b.g, n.tiles, n.units, 1);
   // with a bias also for no queries: the table's gradient is then zero
   if (a->queries || a->bias)
     HLQ_TRY(HLQ_BY_SIZE(a->head_dim, launch_attention_backward_q, b, a->dtype, s));
@@ -311,8 +325,8 @@ hlq_status hlq_attention_backward(const hlq_attention* a, const hlq_tokens* g_o,
     const int64_t far = std::max(b.q.head, b.g_o.head) * (int64_t)esize(a->dtype) * shared;
     if ((shared & (shared - 1)) || shared > hlq::ATTN_PACK || far >= (int64_t(1) << 30)) b.g.pack = 1;
     b.g.groups = shared / b.g.pack;
-    b.g.tiles = (expected(a, a->keys) + hlq::ATTN_ROWS - 1) / hlq::ATTN_ROWS;
-    b.g.items = b.g.tiles * a->sequences * a->kv_heads;
+    number(b.g, (expected(a, a->keys) + hlq::ATTN_ROWS - 1) / hlq::ATTN_ROWS,
+           a->sequences * a->kv_heads, 1);
     HLQ_TRY(HLQ_BY_SIZE(a->head_dim, launch_attention_backward_kv, b, a->dtype, s));
   }
   return HLQ_OK;

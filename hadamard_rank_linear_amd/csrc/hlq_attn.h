@@ -255,53 +255,65 @@ __device__ __forceinline__ uint32_t bit_range(int low, int high) {
   return low >= 32 ? 0u : low <= 0 ? below : below & ~((1u << low) - 1u);
 }
 
-// A tile's global loads by 256 threads, held in registers until its place in LDS
-// is free.  A thread has the same chunk of every RS-th row; its bytes from the
-// tile's first row on are 32-bit offsets (token strides are limited for that).
+// A tile's way from global memory straight into LDS, by 256 threads.  A load writes
+// 16 bytes of each lane of a wave behind one another, so the mix of a row's chunks
+// is made by the lanes' addresses; chunks that do not exist come from a page of
+// zeros.  A thread has the same chunk of every RS-th row; its bytes from the tile's
+// first row on are 32-bit offsets (token strides are limited for that).
+__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
+
 template <int DT, int DP, int ROWS>
-struct Stage {
+struct Feed {
   typedef Tile<DT, DP> T;
-  // rows at a time: a power of two
-  static constexpr int RS = 256 / (T::CHUNKS == 12 ? 16 : T::CHUNKS == 24 ? 32 : T::CHUNKS);
-  static constexpr int N = (ROWS + RS - 1) / RS;
-  u32x4 v[N];
+  static constexpr int RS = 256 / T::PITCH, N = ROWS / RS;
+  static_assert(RS % 8 == 0 && ROWS % RS == 0, "a thread's rows have one mix");
   uint32_t off, step;
   int r0, c;
 
   // Strides in bytes; pack heads of a token make neighbouring rows (pack divides RS).
   __device__ __forceinline__ void init(uint32_t token, uint32_t head, int pack) {
-    r0 = threadIdx.x / T::CHUNKS;
-    c = threadIdx.x % T::CHUNKS;
+    r0 = threadIdx.x / T::PITCH;
+    c = (int)(threadIdx.x % T::PITCH) ^ T::mix(r0);
     step = RS / pack * token;
     off = (uint32_t)(r0 / pack) * token + (uint32_t)(r0 % pack) * head + c * 16;
-    if (r0 >= RS) r0 = ROWS;  // threads beyond the last whole row
   }
-  // base: the tile's first row; n: how many rows there are from it on; past them, and
-  // past D, zeros.
-  __device__ __forceinline__ void load(const char* base, int n, int D, bool vec) {
-    if (vec && n >= ROWS && D == DP && N * RS == ROWS && RS * T::CHUNKS == 256) {
+  // base: the tile's first row; n: how many rows there are from it on.  The tile is in
+  // place for a thread when its vmcnt is 0, and for the others after a barrier.
+  __device__ __forceinline__ void issue(const char* base, int n, int D, bool vec, char* tile) const {
+    typedef const __attribute__((address_space(1))) void G;
+    typedef __attribute__((address_space(3))) void S;
+    char* const mine = tile + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+    if (vec && n >= ROWS && D == DP && T::PITCH == T::CHUNKS) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        v[i] = *reinterpret_cast<const u32x4*>(base + (size_t)(off + i * step));
+        __builtin_amdgcn_global_load_lds((G*)(base + (size_t)(off + i * step)),
+                                         (S*)(mine + i * 4096), 16, 0, 0);
       return;
     }
+    if (vec) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int r = r0 + i * RS;
-      v[i] = (u32x4){0u, 0u, 0u, 0u};
-      if (r < n && r < ROWS && c * T::CE < D) {
-        const char* p = base + (size_t)(off + i * step);
-        if (vec) v[i] = *reinterpret_cast<const u32x4*>(p);
-        else v[i] = load_piece<DT>(p, 0, D - c * T::CE);
+      for (int i = 0; i < N; ++i) {
+        const bool in = r0 + i * RS < n && c * T::CE < D;
+        const char* p = in ? base + (size_t)(off + i * step) : (const char*)kZeros;
+        __builtin_amdgcn_global_load_lds((G*)p, (S*)(mine + i * 4096), 16, 0, 0);
       }
+      return;
+    }
+#pragma unroll 1
+    for (int i = 0; i < N; ++i) {
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (r0 + i * RS < n && c * T::CE < D)
+        v = load_piece<DT>(base + (size_t)(off + i * step), 0, D - c * T::CE);
+      *reinterpret_cast<u32x4*>(tile + (i * 256 + threadIdx.x) * 16) = v;
     }
   }
-  __device__ __forceinline__ void store(char* lds) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (r0 + i * RS < ROWS) *reinterpret_cast<u32x4*>(lds + T::at(r0 + i * RS, c)) = v[i];
-  }
 };
+
+// Every load into LDS of this thread has arrived, and, after the barrier, the group's.
+__device__ __forceinline__ void feed_wait() {
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  __syncthreads();
+}
 
 // The kernel's argument (its only one) to be read where it is needed: the compiler
 // loads what it knows to be constant at the start, and has no registers to keep it
@@ -330,11 +342,25 @@ __device__ __forceinline__ void sequence(const int64_t* start, int64_t s, int64_
   n = b > a ? (int)(b - a) : 0;
 }
 
-// Work items are numbered so that an XCD (workgroups go to the eight in turn)
-// takes neighbouring ones, which share keys and values in its L2.
-__device__ __forceinline__ int64_t first_item(unsigned groups) {
-  const unsigned b = blockIdx.x, per = groups / 8;
-  return groups % 8 ? b : (int64_t)(b % 8) * per + b / 8;
+// Unit and tile of a work item (see AttnShape); false for the items that fill the
+// last round of the XCDs.  A workgroup's XCD is its number modulo 8.
+__device__ __forceinline__ bool item_of(const AttnShape& g, unsigned item, unsigned& unit,
+                                        unsigned& tile) {
+  const unsigned n = g.tiles * g.splits;
+  unsigned i = item, units = g.units;
+  if (g.by_xcd) {
+    i = item / 8;
+    units = (g.units + 7) / 8;
+  }
+  if (g.by_tile) {
+    tile = i / units;
+    unit = i % units;
+  } else {
+    unit = i / n;
+    tile = i % n;
+  }
+  if (g.by_xcd) unit = unit * 8 + item % 8;
+  return unit < g.units;
 }
 
 // ------------------------------------------------------------ position bias

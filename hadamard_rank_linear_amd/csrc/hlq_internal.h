@@ -299,9 +299,13 @@ struct AttnShape {
   int heads, kv_heads, D, causal;
   int pack, groups;      // rows' heads; heads / kv_heads / pack
   float scale, c;        // c = scale * log2(e)
-  int64_t tiles, items;  // row (or key) tiles a sequence is expected to have; all work items
-  int splits;            // of the keys (forward), of the rows (gradients of k and v)
-  unsigned launched;     // workgroups of the launch that take items
+  // Work items: row (or key) tiles a sequence is expected to have, times shares of
+  // the keys (forward); units: sequences times heads (groups of heads).  by_xcd: a
+  // unit's items go to one of the eight XCDs; by_tile: the first tile of every unit
+  // comes before the second.
+  unsigned tiles, splits, units, items;
+  int by_xcd, by_tile;
+  unsigned launched;  // workgroups of the launch that take items
   AttnBias bias;
 };
 struct AttnFwd {
@@ -315,7 +319,7 @@ struct AttnBwd {
   AttnRows q, k, v, o, g_o, g_q, g_k, g_v;
   const float* lse;
   float *delta;   // [heads][Tq]: sum over d of g_o o
-  float *g_line;  // [items][buckets] partial sums of the bias's gradient
+  float* g_line;  // [units][tiles][buckets] partial sums of the bias's gradient
 };
 constexpr int ATTN_ROWS = 128;  // query rows, or keys, of a workgroup
 constexpr int ATTN_FEW = 32;    // rows of a workgroup whose waves share the keys
@@ -327,7 +331,7 @@ hipError_t launch_attention_backward_q(const AttnBwd& a, int dtype, hipStream_t 
 template <int DP>
 hipError_t launch_attention_backward_kv(const AttnBwd& a, int dtype, hipStream_t s);
 hipError_t launch_attention_join(const AttnFwd& a, int dtype, hipStream_t s);
-// g_bias [buckets][heads] of param_dt from items' partial sums, `parts` a head
+// g_bias [buckets][heads] of param_dt from the partial sums
 hipError_t launch_attention_bias(const float* part, int64_t S, int64_t tiles, int heads,
                                  int buckets, int param_dt, void* g_bias, hipStream_t s);
 
