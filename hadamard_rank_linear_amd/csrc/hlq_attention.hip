@@ -109,6 +109,32 @@ __device__ __forceinline__ uint32_t lds_place(char* lds) {
 typedef std::integral_constant<bool, true> Whole;
 typedef std::integral_constant<bool, false> Masked;
 
+// A chain of matrix products whose fragments come from LDS, in steps whose order the
+// compiler keeps: fragment i + AHEAD is read, product i starts, and what the matrix
+// unit does not need runs beside it.  Left alone the compiler reads a fragment, waits
+// and multiplies: with one or two waves a SIMD the backward pass of 8192 tokens then
+// has the matrix units idle for three quarters of the time.
+constexpr int AHEAD = 4;
+template <int DT, int N, typename Read, typename Use>
+__device__ __forceinline__ void steps(Frag<DT> (&ring)[AHEAD + 1], Read read, Use use) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i + AHEAD < N) ring[(i + AHEAD) % (AHEAD + 1)] = read(i + AHEAD);
+    use(i, ring[i % (AHEAD + 1)]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+template <int DT, int N, typename Read>
+__device__ __forceinline__ void first_reads(Frag<DT> (&ring)[AHEAD + 1], Read read) {
+#pragma unroll
+  for (int i = 0; i < AHEAD && i < N; ++i) ring[i] = read(i);
+}
+// Of `all` pieces of work beside steps 1 .. n - 1 (the step before has the results
+// they need still under way), the first that belongs to step i.
+__device__ __forceinline__ constexpr int beside(int i, int n, int all) {
+  return i <= 0 ? 0 : i >= n ? all : all * (i - 1) / (n - 1);
+}
+
 // ------------------------------------------------------------ forward
 
 // A work item is a tile of query rows of one sequence and head group, and a
@@ -128,7 +154,7 @@ struct FwdShape {
       2 * BUFS * TILE_BYTES > JOIN_BYTES ? 2 * BUFS * TILE_BYTES : JOIN_BYTES;
 };
 
-template <int DT, int DP, bool BIAS, bool FEW>
+template <int DT, int DP, bool BIAS, bool FEW, bool VEC>
 __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(AttnFwd a) {
   typedef FwdShape<DT, DP, FEW> F;
   typedef Tile<DT, DP> T;
@@ -181,7 +207,7 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
     const char* const kb = row_at<DT>(a.k, k0, kvh);
     const char* const vb = row_at<DT>(a.v, k0, kvh);
     const int64_t kt = a.k.token * ES, vt = a.v.token * ES;
-    Feed<DT, DP, F::KEYS> sk, sv;
+    Feed<DT, DP, F::KEYS, VEC> sk, sv;
     sk.init((uint32_t)kt, 0, 1);
     sv.init((uint32_t)vt, 0, 1);
 
@@ -209,7 +235,7 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
         const char* p = row_at<DT>(a.q, q0 + (me.valid ? me.token : 0), me.head);
 #pragma unroll
         for (int c = 0; c < DC; ++c)
-          qf[c] = me.valid ? global_frag<DT>(p, 16 * c + 8 * half, g.D, a.q.vec) : zero_frag<DT>();
+          qf[c] = me.valid ? global_frag<DT, VEC>(p, 16 * c + 8 * half, g.D) : zero_frag<DT>();
       }
       f32x16 o[DB];
 #pragma unroll
@@ -289,9 +315,9 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
       };
 
       const auto feed = [&](int key, int buf) {
-        char* const at = lds + buf * 2 * F::TILE_BYTES;
-        sk.issue(kb + key * kt, end - key, g.D, a.k.vec, at);
-        sv.issue(vb + key * vt, end - key, g.D, a.v.vec, at + F::TILE_BYTES);
+        const uint32_t at = lds_place(lds) + buf * 2 * F::TILE_BYTES;
+        sk.issue(kb + key * kt, end - key, g.D, at);
+        sv.issue(vb + key * vt, end - key, g.D, at + F::TILE_BYTES);
       };
       __syncthreads();  // the previous tile's reads are done
       if (F::BUFS == 2 && from < end) feed(from, 0);
@@ -409,7 +435,7 @@ struct BwdShape {
 // distances up in two lines of its own in LDS (one a half of the lanes, so that
 // no instruction meets an address twice and the order is the program's), blocks
 // beyond reach in registers.
-template <int DT, int DP, bool BIAS>
+template <int DT, int DP, bool BIAS, bool VEC>
 __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(AttnBwd a) {
   typedef BwdShape<DT, DP> F;
   typedef Tile<DT, DP> T;
@@ -458,7 +484,7 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
     const char* const kb = row_at<DT>(a.k, k0, kvh);
     const char* const vb = row_at<DT>(a.v, k0, kvh);
     const int64_t kt = a.k.token * ES, vt = a.v.token * ES;
-    Feed<DT, DP, F::KEYS> sk, sv;
+    Feed<DT, DP, F::KEYS, VEC> sk, sv;
     sk.init((uint32_t)kt, 0, 1);
     sv.init((uint32_t)vt, 0, 1);
 
@@ -482,15 +508,14 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
         const char* pg = row_at<DT>(z.g_o, token, me.head);
         const char* po = row_at<DT>(z.o, token, me.head);
         const int D = z.g.D;
-        const bool qv = z.q.vec, gv = z.g_o.vec, ov = z.o.vec;
 #pragma unroll
         for (int c = 0; c < DC; ++c) {
           qf[c] = gf[c] = zero_frag<DT>();
           if (me.valid) {
             const int d = 16 * c + 8 * half;
-            qf[c] = global_frag<DT>(pq, d, D, qv);
-            gf[c] = global_frag<DT>(pg, d, D, gv);
-            const Frag<DT> of = global_frag<DT>(po, d, D, ov);
+            qf[c] = global_frag<DT, VEC>(pq, d, D);
+            gf[c] = global_frag<DT, VEC>(pg, d, D);
+            const Frag<DT> of = global_frag<DT, VEC>(po, d, D);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               delta = __builtin_fmaf((float)gf[c][e], (float)of[e], delta);
@@ -515,14 +540,63 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
           const uint32_t rl = row_lane + tile + 32 * b * T::ROW_BYTES;
           const uint32_t cl = col_lane + tile + 32 * b * T::ROW_BYTES;
           if (!WHOLE && key + 32 * b >= last) continue;
+          const int base = key + 32 * b - me.pos + 4 * half;
+          const int dist = key + 32 * b - (row0 + off);
+          const auto add_up = [&](const f32x16& ds) {  // the bias's gradient
+            if (dist - 31 >= g.bias.reach || dist + 31 <= -g.bias.reach) {
+              float sum = 0.f;
+#pragma unroll
+              for (int r = 0; r < 16; ++r) sum += ds[r];
+              if (dist > 0) far_high += sum;
+              else far_low += sum;
+              return;
+            }
+            float* at = sums + (2 * wave + half) * lines + base + g.bias.reach + BIAS_MARGIN;
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              __hip_atomic_fetch_add(at + acc_row(r), ds[r], __ATOMIC_RELAXED,
+                                     __HIP_MEMORY_SCOPE_WORKGROUP);
+          };
+          if constexpr (WHOLE) {
+            // fragments in the order of use: rows of k, rows of v, columns of k
+            const auto read = [&](int i) {
+              if (i < 2 * DC) return T::row_frag(rl, i < DC ? 0 : F::KEYS, i % DC);
+              return T::col_frag(cl, 16 * ((i - 2 * DC) / DB), (i - 2 * DC) % DB);
+            };
+            Frag<DT> ring[AHEAD + 1], df[2];
+            f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
+            first_reads<DT, 2 * DC + 2 * DB>(ring, read);
+            steps<DT, 2 * DC + 2 * DB>(ring, read, [&](int i, const Frag<DT>& f) {
+              if (i < DC) {
+                s = mma(f, qf[i], s);
+                if constexpr (BIAS)
+                  if (i == DC - 1) add_bias<false>(g, line, s, dist - 31, dist + 31, base);
+              } else if (i < 2 * DC) {
+                dp = mma(f, gf[i - DC], dp);
+                const int j = i - DC;
+#pragma unroll
+                for (int r = beside(j, DC, 16); r < beside(j + 1, DC, 16); ++r)
+                  s[r] = exp2_fast(BIAS ? s[r] - lse : __builtin_fmaf(s[r], g.c, -lse));
+                if (j == DC - 1) {
+#pragma unroll
+                  for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
+                  if constexpr (BIAS) add_up(s);
+                  df[0] = acc_frag<DT>(s, 0);
+                  df[1] = acc_frag<DT>(s, 1);
+                }
+              } else {
+                const int j = i - 2 * DC;
+                dq[j % DB] = mma(f, df[j / DB], dq[j % DB]);
+              }
+            });
+            continue;
+          }
           f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
 #pragma unroll
           for (int c = 0; c < DC; ++c) {
             s = mma(T::row_frag(rl, 0, c), qf[c], s);
             dp = mma(T::row_frag(rl, F::KEYS, c), gf[c], dp);
           }
-          const int base = key + 32 * b - me.pos + 4 * half;
-          const int dist = key + 32 * b - (row0 + off);
           if constexpr (BIAS) add_bias<false>(g, line, s, dist - 31, dist + 31, base);
 #pragma unroll
           for (int r = 0; r < 16; ++r)
@@ -533,21 +607,7 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
             for (int r = 0; r < 16; ++r)
               if (acc_row(r) + 4 * half >= limit) s[r] = 0.f;
           }
-          if constexpr (BIAS) {
-            if (dist - 31 >= g.bias.reach || dist + 31 <= -g.bias.reach) {
-              float sum = 0.f;
-#pragma unroll
-              for (int r = 0; r < 16; ++r) sum += s[r];
-              if (dist > 0) far_high += sum;
-              else far_low += sum;
-            } else {
-              float* at = sums + (2 * wave + half) * lines + base + g.bias.reach + BIAS_MARGIN;
-#pragma unroll
-              for (int r = 0; r < 16; ++r)
-                __hip_atomic_fetch_add(at + acc_row(r), s[r], __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_WORKGROUP);
-            }
-          }
+          if constexpr (BIAS) add_up(s);
           const uint32_t bad = !WHOLE && g.causal ? rows_not_finite<DT, DP>(rl, 0) : 0;
           if (!WHOLE && bad) {
             if (bad & bit_range(0, limit)) poison = __builtin_nanf("");
@@ -570,9 +630,9 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
       };
 
       const auto feed = [&](int key, int buf) {
-        char* const at = lds + buf * 2 * F::TILE_BYTES;
-        sk.issue(kb + key * kt, end - key, g.D, a.k.vec, at);
-        sv.issue(vb + key * vt, end - key, g.D, a.v.vec, at + F::TILE_BYTES);
+        const uint32_t at = lds_place(lds) + buf * 2 * F::TILE_BYTES;
+        sk.issue(kb + key * kt, end - key, g.D, at);
+        sv.issue(vb + key * vt, end - key, g.D, at + F::TILE_BYTES);
       };
       __syncthreads();  // the previous tile's reads are done
       if (end > 0) feed(0, 0);
@@ -638,7 +698,7 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
 
 // A work item is 128 keys of one sequence and key head, 32 a wave; it goes
 // through the query rows of the heads that share them.
-template <int DT, int DP, bool BIAS>
+template <int DT, int DP, bool BIAS, bool VEC>
 __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_backward_kv(
     AttnBwd a) {
   typedef BwdShape<DT, DP> F;
@@ -674,7 +734,7 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
     const int rows = nq * g.pack, off = nk - nq;
     if ((int64_t)tile0 * ATTN_ROWS >= nk) continue;
     const int64_t qt = a.q.token * ES, gt = a.g_o.token * ES;
-    Feed<DT, DP, F::KEYS> sq, sg;
+    Feed<DT, DP, F::KEYS, VEC> sq, sg;
     sq.init((uint32_t)qt, (uint32_t)(a.q.head * ES), g.pack);
     sg.init((uint32_t)gt, (uint32_t)(a.g_o.head * ES), g.pack);
 
@@ -688,12 +748,11 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
         const char* pk = row_at<DT>(z.k, token, kvh);
         const char* pv = row_at<DT>(z.v, token, kvh);
         const int D = z.g.D;
-        const bool kvec = z.k.vec, vvec = z.v.vec;
 #pragma unroll
         for (int c = 0; c < DC; ++c) {
           const int d = 16 * c + 8 * half;
-          kf[c] = valid ? global_frag<DT>(pk, d, D, kvec) : zero_frag<DT>();
-          vf[c] = valid ? global_frag<DT>(pv, d, D, vvec) : zero_frag<DT>();
+          kf[c] = valid ? global_frag<DT, VEC>(pk, d, D) : zero_frag<DT>();
+          vf[c] = valid ? global_frag<DT, VEC>(pv, d, D) : zero_frag<DT>();
         }
       }
       f32x16 dk[DB], dv[DB];
@@ -717,6 +776,62 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
           const uint32_t cl = col_lane + tile + 32 * b * T::ROW_BYTES;
           const int r0 = row + 32 * b;
           if (!WHOLE && (r0 + 32 <= mine || r0 >= rows)) continue;
+          if constexpr (WHOLE) {
+            constexpr int ND = 2 * DB;
+            // fragments in the order of use: rows of q, rows of g_o, columns of g_o, of q
+            const auto read = [&](int i) {
+              if (i < 2 * DC) return T::row_frag(rl, i < DC ? 0 : F::KEYS, i % DC);
+              const int j = (i - 2 * DC) % ND;
+              return T::col_frag(cl, (i < 2 * DC + ND ? F::KEYS : 0) + 16 * (j / DB), j % DB);
+            };
+            Frag<DT> ring[AHEAD + 1], pf[2], df[2];
+            f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
+            f32x4 lse[4], del[4];
+            first_reads<DT, 2 * (DC + ND)>(ring, read);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float* p = stat + 32 * b + 8 * q + 4 * half;
+              lse[q] = *reinterpret_cast<const f32x4*>(p);
+              del[q] = *reinterpret_cast<const f32x4*>(p + F::KEYS);
+            }
+            steps<DT, 2 * (DC + ND)>(ring, read, [&](int i, const Frag<DT>& f) {
+              if (i < DC) {
+                s = mma(f, kf[i], s);
+                if constexpr (BIAS) {
+                  if (i == DC - 1) {
+                    const int dist = wkey - (r0 + off);
+                    add_bias<true>(g, line, s, dist - 31, dist + 31, key - (r0 + off) - 4 * half);
+                  }
+                }
+              } else if (i < 2 * DC) {
+                dp = mma(f, vf[i - DC], dp);
+                const int j = i - DC;
+#pragma unroll
+                for (int r = beside(j, DC, 16); r < beside(j + 1, DC, 16); ++r) {
+                  const float ls = lse[r / 4][r % 4];
+                  s[r] = exp2_fast(BIAS ? s[r] - ls : __builtin_fmaf(s[r], g.c, -ls));
+                }
+                if (j == DC - 1) {
+                  pf[0] = acc_frag<DT>(s, 0);
+                  pf[1] = acc_frag<DT>(s, 1);
+                }
+              } else if (i < 2 * DC + ND) {
+                const int j = i - 2 * DC;
+                dv[j % DB] = mma(f, pf[j / DB], dv[j % DB]);
+#pragma unroll
+                for (int r = beside(j, ND, 16); r < beside(j + 1, ND, 16); ++r)
+                  s[r] *= dp[r] - del[r / 4][r % 4];
+                if (j == ND - 1) {
+                  df[0] = acc_frag<DT>(s, 0);
+                  df[1] = acc_frag<DT>(s, 1);
+                }
+              } else {
+                const int j = i - 2 * DC - ND;
+                dk[j % DB] = mma(f, df[j / DB], dk[j % DB]);
+              }
+            });
+            continue;
+          }
           f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
 #pragma unroll
           for (int c = 0; c < DC; ++c) {
@@ -791,26 +906,26 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
         float st = 0.f;
         // The rows' statistics go through a register, into the buffer at the next turn.
         const auto fetch = [&](int row, int buf) {
-          const int64_t tok = row / g.pack;  // KEYS is a multiple of pack
-          char* const at = lds + buf * 2 * F::TILE_BYTES;
-          sq.issue(qb + tok * qt, rows - row, g.D, a.q.vec, at);
-          sg.issue(gb + tok * gt, rows - row, g.D, a.g_o.vec, at + F::TILE_BYTES);
           if (threadIdx.x < 2 * F::KEYS) {
             const int r = row + (int)threadIdx.x % F::KEYS;
             const bool first = threadIdx.x < F::KEYS;
-            st = first ? kInf : 0.f;
+            st = first ? -kInf : 0.f;
             if (r < rows) {
               const int t = (int)((unsigned)r / (unsigned)g.pack);
               const int64_t i = (head0 + r - t * g.pack) * g.Tq + q0 + t;
-              st = first ? a.lse[i] * kLog2e : a.delta[i];
-              if (first && st == -kInf) st = kInf;
+              st = first ? a.lse[i] : a.delta[i];
             }
           }
+          const int64_t tok = row / g.pack;  // KEYS is a multiple of pack
+          const uint32_t at = lds_place(lds) + buf * 2 * F::TILE_BYTES;
+          sq.issue(qb + tok * qt, rows - row, g.D, at);
+          sg.issue(gb + tok * gt, rows - row, g.D, at + F::TILE_BYTES);
         };
         if (begin < rows) fetch(begin, 0);
         int buf = 0;
         for (int row = begin; row < rows; row += F::KEYS, buf ^= 1) {
           float* const stat = stats + buf * 2 * F::KEYS;
+          if (threadIdx.x < F::KEYS) st = st == -kInf ? kInf : st * kLog2e;  // no key: P = 0
           if (threadIdx.x < 2 * F::KEYS) stat[threadIdx.x] = st;
           feed_wait();
           if (row + F::KEYS < rows) fetch(row + F::KEYS, buf ^ 1);
@@ -874,14 +989,19 @@ int line_bytes(const AttnShape& g, int lines) {
   return g.bias.table ? 2 * (g.bias.reach + BIAS_MARGIN) * 4 * lines + 4 * lines : 0;
 }
 
-template <int DT, int DP, bool BIAS>
-hipError_t forward(const AttnFwd& a, bool few, hipStream_t s) {
-  const bool gaps = a.g.start_q != nullptr;
-  if (few)
-    return launch_items(k_attention_forward<DT, DP, BIAS, true>, a,
-                        FwdShape<DT, DP, true>::LDS + line_bytes(a.g, 1), gaps, s);
-  return launch_items(k_attention_forward<DT, DP, BIAS, false>, a,
-                      FwdShape<DT, DP, false>::LDS + line_bytes(a.g, 1), gaps, s);
+// The variant for what the call needs: type, bias, and whether every row consists of
+// whole 16-byte chunks.
+template <typename F>
+hipError_t choose(int dtype, bool bias, bool vec, F f) {
+  typedef std::integral_constant<int, 0> F32;
+  typedef std::integral_constant<int, 1> Bf16;
+  const auto pick = [&](auto t) {
+    if (bias) return vec ? f(t, std::true_type(), std::true_type())
+                         : f(t, std::true_type(), std::false_type());
+    return vec ? f(t, std::false_type(), std::true_type())
+               : f(t, std::false_type(), std::false_type());
+  };
+  return dtype == 0 ? pick(F32()) : pick(Bf16());
 }
 
 }  // namespace
@@ -889,38 +1009,37 @@ hipError_t forward(const AttnFwd& a, bool few, hipStream_t s) {
 template <>
 hipError_t launch_attention_forward<HLQ_ATTN_D>(const AttnFwd& a, int dtype, bool few,
                                                 hipStream_t s) {
-  constexpr int DP = HLQ_ATTN_D;
-  if (dtype == 0)
-    return a.g.bias.table ? forward<0, DP, true>(a, few, s) : forward<0, DP, false>(a, few, s);
-  return a.g.bias.table ? forward<1, DP, true>(a, few, s) : forward<1, DP, false>(a, few, s);
+  const bool gaps = a.g.start_q != nullptr;
+  return choose(dtype, a.g.bias.table, a.q.vec && a.k.vec && a.v.vec, [&](auto t, auto b, auto v) {
+    constexpr int DT = decltype(t)::value, DP = HLQ_ATTN_D;
+    constexpr bool BIAS = decltype(b)::value, VEC = decltype(v)::value;
+    if (few)
+      return launch_items(k_attention_forward<DT, DP, BIAS, true, VEC>, a,
+                          FwdShape<DT, DP, true>::LDS + line_bytes(a.g, 1), gaps, s);
+    return launch_items(k_attention_forward<DT, DP, BIAS, false, VEC>, a,
+                        FwdShape<DT, DP, false>::LDS + line_bytes(a.g, 1), gaps, s);
+  });
 }
 
 template <>
 hipError_t launch_attention_backward_q<HLQ_ATTN_D>(const AttnBwd& a, int dtype, hipStream_t s) {
-  constexpr int DP = HLQ_ATTN_D;
-  const bool gaps = a.g.start_q != nullptr;
-  const int lines = line_bytes(a.g, 9) + (a.g.bias.table ? 32 : 0);
-  if (dtype == 0)
-    return launch_items(a.g.bias.table ? k_attention_backward_q<0, DP, true>
-                                       : k_attention_backward_q<0, DP, false>,
-                        a, BwdShape<0, DP>::LDS + lines, gaps, s);
-  return launch_items(a.g.bias.table ? k_attention_backward_q<1, DP, true>
-                                     : k_attention_backward_q<1, DP, false>,
-                      a, BwdShape<1, DP>::LDS + lines, gaps, s);
+  const bool vec = a.q.vec && a.k.vec && a.v.vec && a.o.vec && a.g_o.vec;
+  return choose(dtype, a.g.bias.table, vec, [&](auto t, auto b, auto v) {
+    constexpr int DT = decltype(t)::value, DP = HLQ_ATTN_D;
+    return launch_items(k_attention_backward_q<DT, DP, decltype(b)::value, decltype(v)::value>, a,
+                        BwdShape<DT, DP>::LDS + line_bytes(a.g, 9) + 32, a.g.start_q != nullptr, s);
+  });
 }
 
 template <>
 hipError_t launch_attention_backward_kv<HLQ_ATTN_D>(const AttnBwd& a, int dtype, hipStream_t s) {
-  constexpr int DP = HLQ_ATTN_D;
-  const bool gaps = a.g.start_k != nullptr;
-  const int lines = line_bytes(a.g, 1);
-  if (dtype == 0)
-    return launch_items(a.g.bias.table ? k_attention_backward_kv<0, DP, true>
-                                       : k_attention_backward_kv<0, DP, false>,
-                        a, BwdShape<0, DP>::LDS + 16 * BwdShape<0, DP>::KEYS + lines, gaps, s);
-  return launch_items(a.g.bias.table ? k_attention_backward_kv<1, DP, true>
-                                     : k_attention_backward_kv<1, DP, false>,
-                      a, BwdShape<1, DP>::LDS + 16 * BwdShape<1, DP>::KEYS + lines, gaps, s);
+  const bool vec = a.q.vec && a.k.vec && a.v.vec && a.g_o.vec;
+  return choose(dtype, a.g.bias.table, vec, [&](auto t, auto b, auto v) {
+    constexpr int DT = decltype(t)::value, DP = HLQ_ATTN_D;
+    return launch_items(k_attention_backward_kv<DT, DP, decltype(b)::value, decltype(v)::value>, a,
+                        BwdShape<DT, DP>::LDS + 16 * BwdShape<DT, DP>::KEYS + line_bytes(a.g, 1),
+                        a.g.start_k != nullptr, s);
+  });
 }
 
 }  // namespace hlq

@@ -111,26 +111,32 @@ __device__ __forceinline__ Frag<DT> finite(const Frag<DT>& f) {
 
 // ------------------------------------------------------------ tiles in LDS
 
-// Rows of DP elements in 16-byte chunks.  Chunk c of row r lies at c ^ mix(r):
-// eight consecutive rows put one chunk into eight different bank groups (reads
-// by rows), and four consecutive rows two neighbouring chunks (reads by columns).
+// Rows of DP elements in 16-byte chunks, chunk c of row r at c ^ mix(r).  The 64
+// banks give 256 bytes a cycle: 16 lanes of a read by rows (one chunk of 16
+// consecutive rows), 32 of a transposing read (four chunks of four rows), 64 of a
+// read of single words (eight chunks of two rows, four apart).  The mix puts each of
+// these into banks of its own; it is linear over exclusive or.  (No conflicts are
+// counted; with a mix for 32 banks they were as many cycles as the reads.)
 template <int DT, int DP>
 struct Tile {
   static constexpr int CE = DT == 0 ? 4 : 8;          // elements a chunk
   static constexpr int CHUNKS = DP / CE;              // of a row
   static constexpr int PITCH = CHUNKS <= 8 ? 8 : CHUNKS <= 16 ? 16 : 32;
   static constexpr int ROW_BYTES = PITCH * 16;
-
+  static constexpr int MIXED = PITCH == 8 ? 7 : 15;   // chunk bits that take part
   typedef __attribute__((address_space(3))) const char L;
 
-  __device__ static __forceinline__ int mix(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
+  __device__ static __forceinline__ constexpr int mix(int r) {
+    if (PITCH == 8) return ((r & 2) << 1) | ((r >> 2) & 3);  // two rows fill the banks
+    if (DT == 0) return ((r & 4) << 1) | ((r & 3) << 1) | ((r >> 3) & 1);
+    return ((r & 3) << 2) | ((r >> 2) & 3);
+  }
   __device__ static __forceinline__ int at(int r, int c) { return (r * PITCH + (c ^ mix(r))) * 16; }
 
   // A lane's place in a tile read by rows (row lane & 31, the first of its half's
   // chunks) and by columns (see col_frag): what at() gives without the constant
-  // parts of row and chunk.  mix() depends on the lane alone, since blocks begin at
-  // multiples of 16 rows, and a constant's bits below the mix's are put in by an
-  // exclusive or, those above by addition.
+  // parts of row and chunk, which are put in by an exclusive or where they meet the
+  // mix and by addition above.
   __device__ static __forceinline__ uint32_t row_lane() {
     const int lane = threadIdx.x & 63, half = lane >> 5;
     return at(lane & 31, DT == 1 ? half : 2 * half);
@@ -144,8 +150,10 @@ struct Tile {
       return at(4 * half, (lane & 31) >> 2) + (lane & 3) * 4;
     }
   }
-  __device__ static __forceinline__ L* place(uint32_t lane, int row, int chunk) {
-    return (L*)(uintptr_t)((lane ^ ((chunk & 7) * 16)) + (chunk & ~7) * 16 + row * ROW_BYTES);
+  // row: a multiple of 32, and low rows of the 16 that share no bit with the lane's
+  __device__ static __forceinline__ L* place(uint32_t lane, int row, int low, int chunk) {
+    return (L*)(uintptr_t)((lane ^ (((chunk & MIXED) ^ mix(low)) * 16)) + (chunk & ~MIXED) * 16 +
+                           (row + low) * ROW_BYTES);
   }
 
   // Rows r .. r + 31 (one a lane), elements 16 c + 8 half .. + 7.  tile: row_lane()
@@ -153,19 +161,19 @@ struct Tile {
   __device__ static __forceinline__ Frag<DT> row_frag(uint32_t tile, int r, int c) {
     Frag<DT> f;
     if constexpr (DT == 1) {
-      f = *(__attribute__((address_space(3))) const bf16x8*)place(tile, r, 2 * c);
+      f = *(__attribute__((address_space(3))) const bf16x8*)place(tile, r, 0, 2 * c);
     } else {
       typedef __attribute__((address_space(3))) const f32x4 V;
-      const f32x4 a = *(V*)place(tile, r, 4 * c), b = *(V*)place(tile, r, 4 * c + 1);
+      const f32x4 a = *(V*)place(tile, r, 0, 4 * c), b = *(V*)place(tile, r, 0, 4 * c + 1);
       f = (f32x8){a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     }
     return f;
   }
 
-  // Columns 32 d .. 32 d + 31 (one a lane), rows r + 8 (e >> 2) + 4 half + (e & 3):
-  // the operand whose sum runs over rows.  bf16: two transposing reads, in which
-  // lane j of 16 points at row j / 4, columns 4 (j % 4) of a 4 x 16 block and gets
-  // column j.  tile: col_lane() plus the tile's place.
+  // Columns 32 d .. 32 d + 31 (one a lane), rows r + 8 (e >> 2) + 4 half + (e & 3)
+  // (r a multiple of 16): the operand whose sum runs over rows.  bf16: two transposing
+  // reads, in which lane j of 16 points at row j / 4, columns 4 (j % 4) of a 4 x 16
+  // block and gets column j.  tile: col_lane() plus the tile's place.
   __device__ static __forceinline__ Frag<DT> col_frag(uint32_t tile, int r, int d) {
     Frag<DT> f;
     if constexpr (DT == 1) {
@@ -173,40 +181,36 @@ struct Tile {
       s16x4 v[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        v[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((V*)place(tile, r + 8 * i, 4 * d));
+        v[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((V*)place(tile, r, 8 * i, 4 * d));
       __builtin_memcpy(&f, v, 16);
     } else {
       typedef __attribute__((address_space(3))) const float V;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // rows 4 half + (e & 3): the mix of e & 3 on top of the lane's
-        const int row = r + 8 * (e >> 2) + (e & 3);
-        f[e] = *(V*)place(tile ^ (mix(e & 3) * 16), row, 8 * d);
-      }
+      for (int e = 0; e < 8; ++e)
+        f[e] = *(V*)place(tile, r, 8 * (e >> 2) + (e & 3), 8 * d);
     }
     return f;
   }
 };
 
 // Elements d .. of a row of n as a chunk of 16 bytes; past the row: zero.
-// vec: rows start at 16-byte boundaries and hold whole chunks.
-template <int DT>
-__device__ __forceinline__ u32x4 row_chunk(const void* row, int d, int n, bool vec) {
+// VEC: rows start at 16-byte boundaries and hold whole chunks.
+template <int DT, bool VEC>
+__device__ __forceinline__ u32x4 row_chunk(const void* row, int d, int n) {
   typedef typename Piece<DT>::Elem E;
-  const E* p = static_cast<const E*>(row) + d;
-  if (vec) {
-    if (d < n) return *reinterpret_cast<const u32x4*>(p);
+  if constexpr (VEC) {
+    if (d < n) return *reinterpret_cast<const u32x4*>(static_cast<const E*>(row) + d);
     return (u32x4){0u, 0u, 0u, 0u};
   }
   return load_piece<DT>(row, d, n - d);
 }
 
-template <int DT>
-__device__ __forceinline__ Frag<DT> global_frag(const void* row, int d, int n, bool vec) {
+template <int DT, bool VEC>
+__device__ __forceinline__ Frag<DT> global_frag(const void* row, int d, int n) {
   Frag<DT> f;
   u32x4 w[DT == 0 ? 2 : 1];
-  w[0] = row_chunk<DT>(row, d, n, vec);
-  if constexpr (DT == 0) w[1] = row_chunk<DT>(row, d + 4, n, vec);
+  w[0] = row_chunk<DT, VEC>(row, d, n);
+  if constexpr (DT == 0) w[1] = row_chunk<DT, VEC>(row, d + 4, n);
   __builtin_memcpy(&f, w, sizeof f);
   return f;
 }
@@ -255,65 +259,85 @@ __device__ __forceinline__ uint32_t bit_range(int low, int high) {
   return low >= 32 ? 0u : low <= 0 ? below : below & ~((1u << low) - 1u);
 }
 
-// A tile's way from global memory straight into LDS, by 256 threads.  A load writes
-// 16 bytes of each lane of a wave behind one another, so the mix of a row's chunks
-// is made by the lanes' addresses; chunks that do not exist come from a page of
-// zeros.  A thread has the same chunk of every RS-th row; its bytes from the tile's
-// first row on are 32-bit offsets (token strides are limited for that).
+// A tile's way from global memory into LDS, by 256 threads: straight, without
+// registers, where rows are whole 16-byte chunks (VEC).  A load writes 16 bytes of
+// each lane of a wave behind one another, so the mix of a row's chunks is made by the
+// lanes' addresses; chunks that do not exist come from a page of zeros.  A thread has
+// the same chunk of every RS-th row; its bytes from the tile's first row on are
+// 32-bit offsets (token strides are limited for that).
 __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
 
-template <int DT, int DP, int ROWS>
+// v, which the compiler takes for unknown: what is made of it is not kept in
+// registers from before the loop.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// The loads are written out: the compiler would wait for all of them before the
+// first transposing read of any tile, also of those that are there.  They have no
+// result in a register; feed_wait() is what waits for them.
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void load_to_lds(const char* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :: "s"(lds), "v"(p) : "memory", "m0");
+}
+// Every load into LDS of this thread has arrived, and, after the barrier, the group's.
+__device__ __forceinline__ void feed_wait() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+}
+
+template <int DT, int DP, int ROWS, bool VEC>
 struct Feed {
   typedef Tile<DT, DP> T;
   static constexpr int RS = 256 / T::PITCH, N = ROWS / RS;
-  static_assert(RS % 8 == 0 && ROWS % RS == 0, "a thread's rows have one mix");
+  static_assert(RS % 8 == 0 && ROWS % RS == 0, "whole turns of a thread");
   uint32_t off, step;
-  int r0, c;
 
+  __device__ static __forceinline__ int row() { return threadIdx.x / T::PITCH; }
+  // The thread's chunk at turn i: where rows step by 8 every other one has another mix.
+  __device__ static __forceinline__ int chunk(int i) {
+    return (int)(threadIdx.x % T::PITCH) ^ T::mix(row()) ^ (RS == 8 && (i & 1) ? T::mix(8) : 0);
+  }
   // Strides in bytes; pack heads of a token make neighbouring rows (pack divides RS).
   __device__ __forceinline__ void init(uint32_t token, uint32_t head, int pack) {
-    r0 = threadIdx.x / T::PITCH;
-    c = (int)(threadIdx.x % T::PITCH) ^ T::mix(r0);
     step = RS / pack * token;
-    off = (uint32_t)(r0 / pack) * token + (uint32_t)(r0 % pack) * head + c * 16;
+    off = (uint32_t)(row() / pack) * token + (uint32_t)(row() % pack) * head + chunk(0) * 16;
   }
-  // base: the tile's first row; n: how many rows there are from it on.  The tile is in
-  // place for a thread when its vmcnt is 0, and for the others after a barrier.
-  __device__ __forceinline__ void issue(const char* base, int n, int D, bool vec, char* tile) const {
-    typedef const __attribute__((address_space(1))) void G;
-    typedef __attribute__((address_space(3))) void S;
-    char* const mine = tile + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
-    if (vec && n >= ROWS && D == DP && T::PITCH == T::CHUNKS) {
+  // base: the tile's first row; n: how many rows there are from it on; lds: the tile's
+  // place.  For the others of the group the tile is there after feed_wait().
+  __device__ __forceinline__ void issue(const char* base, int n, int D, uint32_t lds) const {
+    const int flip = RS == 8 ? (chunk(1) - chunk(0)) * 16 : 0;
+    if constexpr (VEC) {
+      const uint32_t mine = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+      if (n >= ROWS && D == DP && T::PITCH == T::CHUNKS) {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        __builtin_amdgcn_global_load_lds((G*)(base + (size_t)(off + i * step)),
-                                         (S*)(mine + i * 4096), 16, 0, 0);
-      return;
-    }
-    if (vec) {
+        for (int i = 0; i < N; ++i)
+          load_to_lds(base + (size_t)(i * step), off + (i & 1 ? flip : 0), mine + i * 4096);
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const bool in = r0 + i * RS < n && c * T::CE < D;
-        const char* p = in ? base + (size_t)(off + i * step) : (const char*)kZeros;
-        __builtin_amdgcn_global_load_lds((G*)p, (S*)(mine + i * 4096), 16, 0, 0);
+        const int r = opaque(row()) + i * RS;
+        const char* p = base + (size_t)(off + (i & 1 ? flip : 0) + i * step);
+        load_to_lds(r < n && chunk(i) * T::CE < D ? p : (const char*)kZeros, mine + i * 4096);
       }
       return;
     }
 #pragma unroll 1
     for (int i = 0; i < N; ++i) {
+      const int c = chunk(i);
       u32x4 v = {0u, 0u, 0u, 0u};
-      if (r0 + i * RS < n && c * T::CE < D)
-        v = load_piece<DT>(base + (size_t)(off + i * step), 0, D - c * T::CE);
-      *reinterpret_cast<u32x4*>(tile + (i * 256 + threadIdx.x) * 16) = v;
+      if (row() + i * RS < n && c * T::CE < D)
+        v = load_piece<DT>(base + (size_t)(off + (i & 1 ? flip : 0) + i * step), 0, D - c * T::CE);
+      *(__attribute__((address_space(3))) u32x4*)(uintptr_t)(lds + (i * 256 + threadIdx.x) * 16) = v;
     }
   }
 };
-
-// Every load into LDS of this thread has arrived, and, after the barrier, the group's.
-__device__ __forceinline__ void feed_wait() {
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-  __syncthreads();
-}
 
 // The kernel's argument (its only one) to be read where it is needed: the compiler
 // loads what it knows to be constant at the start, and has no registers to keep it
