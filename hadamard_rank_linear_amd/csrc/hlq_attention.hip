@@ -11,6 +11,8 @@
 // of q, its 32 keys in the gradients of k and v.  Then P and dS leave the matrix
 // unit in the registers in which the next product takes them in, row statistics
 // are one value a lane, and nothing but the other operand's tiles goes through LDS.
+#include <utility>
+
 #include "hlq_attn.h"
 
 #ifndef HLQ_ATTN_D
@@ -114,20 +116,31 @@ typedef std::integral_constant<bool, false> Masked;
 // unit does not need runs beside it.  Left alone the compiler reads a fragment, waits
 // and multiplies: with one or two waves a SIMD the backward pass of 8192 tokens then
 // has the matrix units idle for three quarters of the time.
+// read and use get the step's number as a constant.
 constexpr int AHEAD = 4;
-template <int DT, int N, typename Read, typename Use>
-__device__ __forceinline__ void steps(Frag<DT> (&ring)[AHEAD + 1], Read read, Use use) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (i + AHEAD < N) ring[(i + AHEAD) % (AHEAD + 1)] = read(i + AHEAD);
-    use(i, ring[i % (AHEAD + 1)]);
+template <int I>
+using Step = std::integral_constant<int, I>;
+template <int DT, int N, typename Read, typename Use, int... I>
+__device__ __forceinline__ void steps(std::integer_sequence<int, I...>, Read read, Use use) {
+  Frag<DT> ring[AHEAD + 1];
+  const auto one = [&](auto step) {
+    constexpr int i = decltype(step)::value;
+    if constexpr (i == 0) {
+      ring[0] = read(Step<0>());
+      if constexpr (N > 1 && AHEAD > 1) ring[1] = read(Step<1>());
+      if constexpr (N > 2 && AHEAD > 2) ring[2] = read(Step<2>());
+      if constexpr (N > 3 && AHEAD > 3) ring[3] = read(Step<3>());
+    }
+    if constexpr (i + AHEAD < N) ring[(i + AHEAD) % (AHEAD + 1)] = read(Step<i + AHEAD>());
+    use(step, ring[i % (AHEAD + 1)]);
     __builtin_amdgcn_sched_barrier(0);
-  }
+  };
+  (one(Step<I>()), ...);
 }
-template <int DT, int N, typename Read>
-__device__ __forceinline__ void first_reads(Frag<DT> (&ring)[AHEAD + 1], Read read) {
-#pragma unroll
-  for (int i = 0; i < AHEAD && i < N; ++i) ring[i] = read(i);
+template <int DT, int N, typename Read, typename Use>
+__device__ __forceinline__ void steps(Read read, Use use) {
+  static_assert(AHEAD <= 4, "the first reads are written out");
+  steps<DT, N>(std::make_integer_sequence<int, N>(), read, use);
 }
 // Of `all` pieces of work beside steps 1 .. n - 1 (the step before has the results
 // they need still under way), the first that belongs to step i.
@@ -247,6 +260,102 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
       const auto attend = [&](auto all, int key0, int tile) {
         constexpr bool WHOLE = decltype(all)::value;
         const uint32_t rl = row_lane + tile, cl = col_lane + tile;
+        if constexpr (WHOLE) {
+          constexpr int ND = 2 * DB;
+          // fragments in the order of use: rows of k by blocks, columns of v by blocks
+          const auto read = [&](auto step) {
+            constexpr int i = decltype(step)::value;
+            if constexpr (i < SB * DC) {
+              return T::row_frag(rl, 32 * (i / DC), i % DC);
+            } else {
+              constexpr int j = i - SB * DC;
+              return T::col_frag(cl, F::KEYS + 32 * (j / ND) + 16 * (j % ND / DB), j % DB);
+            }
+          };
+          Frag<DT> pf[2];
+          f32x16 s[SB];
+          float base = 0.f, keep = 1.f, sum = 0.f;
+          bool moved = false;  // the maximum; uniform
+          // The running maximum with block b's scores, and the factor that the sums so
+          // far then need.
+          const auto enter = [&](int b) {
+            float top = s[b][0];
+#pragma unroll
+            for (int r = 1; r < 16; ++r) top = fmaxf(top, s[b][r]);
+            top = max_halves(top);
+            if constexpr (!BIAS) top *= g.c;
+            top = fmaxf(m, top);
+            base = top == -kInf ? 0.f : top;  // a row that has seen no key yet
+            moved = __any(top != m);
+            if (moved) {
+              keep = exp2_fast(m - base);
+              l *= keep;
+              m = top;
+            }
+          };
+          const auto rescale = [&] {
+            if (!moved) return;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+              for (int r = 0; r < 16; ++r) o[d][r] *= keep;
+          };
+          const auto probability = [&](int b, int r) {
+            s[b][r] = exp2_fast(BIAS ? s[b][r] - base : __builtin_fmaf(s[b][r], g.c, -base));
+            sum += s[b][r];
+          };
+          const auto leave = [&](int b) {
+            l += sum;
+            sum = 0.f;
+            pf[0] = acc_frag<DT>(s[b], 0);
+            pf[1] = acc_frag<DT>(s[b], 1);
+          };
+          constexpr int PV = SB * DC;  // first product with v
+          steps<DT, PV + SB * ND>(read, [&](auto step, const Frag<DT>& f) {
+              constexpr int i = decltype(step)::value;
+            if constexpr (i < PV) {
+              constexpr int b = i / DC, j = i % DC;
+              if constexpr (j == 0) s[b] = (f32x16)(0.f);
+              s[b] = mma(f, qf[j], s[b]);
+              if constexpr (BIAS && j == DC - 1) {
+                const int dist = key0 + 32 * b - (row0 + off);  // of the first row; later ones less
+                add_bias<false>(g, line, s[b], dist - 31, dist + 31,
+                                key0 + 32 * b - me.pos + 4 * half);
+              }
+              if constexpr (SB == 1 && j == DC - 1) {
+                enter(0);
+                rescale();
+#pragma unroll
+                for (int r = 0; r < 16; ++r) probability(0, r);
+                leave(0);
+              }
+              if constexpr (b > 0) {
+                // beside the second block's scores: the first one's probabilities
+                if constexpr (j == 1) {
+                  enter(0);
+                  rescale();
+                }
+#pragma unroll
+                for (int r = beside(j, DC, 16); r < beside(j + 1, DC, 16); ++r) probability(0, r);
+                if constexpr (j == DC - 1) leave(0);
+              }
+            } else {
+              constexpr int b = (i - PV) / ND, j = (i - PV) % ND;
+              o[j % DB] = mma(f, pf[j / DB], o[j % DB]);
+              if constexpr (b + 1 < SB) {
+                // beside the first block's values: the second one's probabilities
+                if constexpr (j == 1) enter(1);
+#pragma unroll
+                for (int r = beside(j, ND, 16); r < beside(j + 1, ND, 16); ++r) probability(1, r);
+                if constexpr (j == ND - 1) {
+                  rescale();
+                  leave(1);
+                }
+              }
+            }
+          });
+          return;
+        }
         f32x16 s[SB];
         float top = -kInf;
 #pragma unroll
@@ -559,25 +668,26 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
           };
           if constexpr (WHOLE) {
             // fragments in the order of use: rows of k, rows of v, columns of k
-            const auto read = [&](int i) {
-              if (i < 2 * DC) return T::row_frag(rl, i < DC ? 0 : F::KEYS, i % DC);
-              return T::col_frag(cl, 16 * ((i - 2 * DC) / DB), (i - 2 * DC) % DB);
+            const auto read = [&](auto step) {
+            constexpr int i = decltype(step)::value;
+              if constexpr (i < 2 * DC) return T::row_frag(rl, i < DC ? 0 : F::KEYS, i % DC);
+              else return T::col_frag(cl, 16 * ((i - 2 * DC) / DB), (i - 2 * DC) % DB);
             };
-            Frag<DT> ring[AHEAD + 1], df[2];
+            Frag<DT> df[2];
             f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
-            first_reads<DT, 2 * DC + 2 * DB>(ring, read);
-            steps<DT, 2 * DC + 2 * DB>(ring, read, [&](int i, const Frag<DT>& f) {
-              if (i < DC) {
+            steps<DT, 2 * DC + 2 * DB>(read, [&](auto step, const Frag<DT>& f) {
+              constexpr int i = decltype(step)::value;
+              if constexpr (i < DC) {
                 s = mma(f, qf[i], s);
                 if constexpr (BIAS)
-                  if (i == DC - 1) add_bias<false>(g, line, s, dist - 31, dist + 31, base);
-              } else if (i < 2 * DC) {
+                  if constexpr (i == DC - 1) add_bias<false>(g, line, s, dist - 31, dist + 31, base);
+              } else if constexpr (i < 2 * DC) {
                 dp = mma(f, gf[i - DC], dp);
-                const int j = i - DC;
+                constexpr int j = i - DC;
 #pragma unroll
                 for (int r = beside(j, DC, 16); r < beside(j + 1, DC, 16); ++r)
                   s[r] = exp2_fast(BIAS ? s[r] - lse : __builtin_fmaf(s[r], g.c, -lse));
-                if (j == DC - 1) {
+                if constexpr (j == DC - 1) {
 #pragma unroll
                   for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
                   if constexpr (BIAS) add_up(s);
@@ -585,7 +695,7 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
                   df[1] = acc_frag<DT>(s, 1);
                 }
               } else {
-                const int j = i - 2 * DC;
+                constexpr int j = i - 2 * DC;
                 dq[j % DB] = mma(f, df[j / DB], dq[j % DB]);
               }
             });
@@ -779,54 +889,58 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
           if constexpr (WHOLE) {
             constexpr int ND = 2 * DB;
             // fragments in the order of use: rows of q, rows of g_o, columns of g_o, of q
-            const auto read = [&](int i) {
-              if (i < 2 * DC) return T::row_frag(rl, i < DC ? 0 : F::KEYS, i % DC);
-              const int j = (i - 2 * DC) % ND;
-              return T::col_frag(cl, (i < 2 * DC + ND ? F::KEYS : 0) + 16 * (j / DB), j % DB);
+            const auto read = [&](auto step) {
+            constexpr int i = decltype(step)::value;
+              if constexpr (i < 2 * DC) {
+                return T::row_frag(rl, i < DC ? 0 : F::KEYS, i % DC);
+              } else {
+                constexpr int j = (i - 2 * DC) % ND;
+                return T::col_frag(cl, (i < 2 * DC + ND ? F::KEYS : 0) + 16 * (j / DB), j % DB);
+              }
             };
-            Frag<DT> ring[AHEAD + 1], pf[2], df[2];
+            Frag<DT> pf[2], df[2];
             f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
             f32x4 lse[4], del[4];
-            first_reads<DT, 2 * (DC + ND)>(ring, read);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const float* p = stat + 32 * b + 8 * q + 4 * half;
               lse[q] = *reinterpret_cast<const f32x4*>(p);
               del[q] = *reinterpret_cast<const f32x4*>(p + F::KEYS);
             }
-            steps<DT, 2 * (DC + ND)>(ring, read, [&](int i, const Frag<DT>& f) {
-              if (i < DC) {
+            steps<DT, 2 * (DC + ND)>(read, [&](auto step, const Frag<DT>& f) {
+              constexpr int i = decltype(step)::value;
+              if constexpr (i < DC) {
                 s = mma(f, kf[i], s);
                 if constexpr (BIAS) {
-                  if (i == DC - 1) {
+                  if constexpr (i == DC - 1) {
                     const int dist = wkey - (r0 + off);
                     add_bias<true>(g, line, s, dist - 31, dist + 31, key - (r0 + off) - 4 * half);
                   }
                 }
-              } else if (i < 2 * DC) {
+              } else if constexpr (i < 2 * DC) {
                 dp = mma(f, vf[i - DC], dp);
-                const int j = i - DC;
+                constexpr int j = i - DC;
 #pragma unroll
                 for (int r = beside(j, DC, 16); r < beside(j + 1, DC, 16); ++r) {
                   const float ls = lse[r / 4][r % 4];
                   s[r] = exp2_fast(BIAS ? s[r] - ls : __builtin_fmaf(s[r], g.c, -ls));
                 }
-                if (j == DC - 1) {
+                if constexpr (j == DC - 1) {
                   pf[0] = acc_frag<DT>(s, 0);
                   pf[1] = acc_frag<DT>(s, 1);
                 }
-              } else if (i < 2 * DC + ND) {
-                const int j = i - 2 * DC;
+              } else if constexpr (i < 2 * DC + ND) {
+                constexpr int j = i - 2 * DC;
                 dv[j % DB] = mma(f, pf[j / DB], dv[j % DB]);
 #pragma unroll
                 for (int r = beside(j, ND, 16); r < beside(j + 1, ND, 16); ++r)
                   s[r] *= dp[r] - del[r / 4][r % 4];
-                if (j == ND - 1) {
+                if constexpr (j == ND - 1) {
                   df[0] = acc_frag<DT>(s, 0);
                   df[1] = acc_frag<DT>(s, 1);
                 }
               } else {
-                const int j = i - 2 * DC - ND;
+                constexpr int j = i - 2 * DC - ND;
                 dk[j % DB] = mma(f, df[j / DB], dk[j % DB]);
               }
             });
