@@ -173,7 +173,8 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
   typedef Tile<DT, DP> T;
   constexpr int DB = DP / 32, DC = DP / 16, SB = F::MINE / 32, ES = DT == 0 ? 4 : 2;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  float* const line = reinterpret_cast<float*>(lds + F::LDS);
+  int16_t* const first_of = reinterpret_cast<int16_t*>(lds + F::LDS);
+  float* const line = reinterpret_cast<float*>(first_of + BIAS_FIRST);
   const uint32_t row_lane = lds_place(lds) + T::row_lane(), col_lane = lds_place(lds) + T::col_lane();
   const AttnShape& g = a.g;
   const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
@@ -215,7 +216,8 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
     if ((int64_t)tile0 * F::ROWS >= rows) continue;
     if constexpr (BIAS) {
       __syncthreads();
-      load_bias_line(g.bias, head0, g.heads, line);
+      load_bias_first(g.bias, first_of);
+      load_bias_line(g.bias, first_of, head0, g.heads, line);
     }
     const char* const kb = row_at<DT>(a.k, k0, kvh);
     const char* const vb = row_at<DT>(a.v, k0, kvh);
@@ -541,9 +543,8 @@ struct BwdShape {
 
 // Waves as in the forward pass.  Writes delta for the gradients of k and v, and
 // with a bias the sums of dS by bucket over the item: each wave adds its blocks'
-// distances up in two lines of its own in LDS (one a half of the lanes, so that
-// no instruction meets an address twice and the order is the program's), blocks
-// beyond reach in registers.
+// diagonals to a line of distances of its own in LDS, blocks beyond reach in
+// registers.
 template <int DT, int DP, bool BIAS, bool VEC>
 __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(AttnBwd a) {
   typedef BwdShape<DT, DP> F;
@@ -553,9 +554,11 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
   const uint32_t row_lane = lds_place(lds) + T::row_lane(), col_lane = lds_place(lds) + T::col_lane();
   const AttnShape& g = a.g;
   const int lines = BIAS ? bias_line_size(g.bias) : 0;
-  float* const line = reinterpret_cast<float*>(lds + F::LDS);
-  float* const sums = line + lines;     // [8][lines]
-  float* const far = sums + 8 * lines;  // [4][2]
+  int16_t* const first_of = reinterpret_cast<int16_t*>(lds + F::LDS);
+  float* const skew = reinterpret_cast<float*>(first_of + BIAS_FIRST);  // [4][SKEW_SIZE]
+  float* const far = skew + (BIAS ? 4 * SKEW_SIZE : 0);                 // [4][2]
+  float* const sums = far + 8;                                          // [4][lines]
+  float* const line = sums + 4 * lines;
   const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
 
   if (blockIdx.x >= g.launched) {
@@ -587,8 +590,10 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
     float far_low = 0.f, far_high = 0.f;
     if constexpr (BIAS) {
       __syncthreads();
-      load_bias_line(g.bias, head0, g.heads, line);
-      for (int i = threadIdx.x; i < 8 * lines; i += 256) sums[i] = 0.f;
+      load_bias_first(g.bias, first_of);
+      load_bias_line(g.bias, first_of, head0, g.heads, line);
+      for (int i = threadIdx.x; i < 4 * lines; i += 256) sums[i] = 0.f;
+      for (int i = threadIdx.x; i < 4 * SKEW_SIZE; i += 256) skew[i] = 0.f;
     }
     const char* const kb = row_at<DT>(a.k, k0, kvh);
     const char* const vb = row_at<DT>(a.v, k0, kvh);
@@ -660,11 +665,10 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
               else far_low += sum;
               return;
             }
-            float* at = sums + (2 * wave + half) * lines + base + g.bias.reach + BIAS_MARGIN;
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-              __hip_atomic_fetch_add(at + acc_row(r), ds[r], __ATOMIC_RELAXED,
-                                     __HIP_MEMORY_SCOPE_WORKGROUP);
+            const float sum = diagonal_sum(skew + wave * SKEW_SIZE, ds);
+            // lane i: distance i - 31 from the block's first row and column
+            if (lane < 63)
+              sums[wave * lines + dist - 31 + lane + g.bias.reach + BIAS_MARGIN] += sum;
           };
           if constexpr (WHOLE) {
             // fragments in the order of use: rows of k, rows of v, columns of k
@@ -778,25 +782,18 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
         far[2 * wave + 1] = far_high;
       }
       __syncthreads();
-      // the eight lines added up, and each distance's bucket
-      int* const which = reinterpret_cast<int*>(sums) + lines;
-      for (int i = threadIdx.x; i < lines; i += 256) {
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) v += sums[w * lines + i];
-        line[i] = v;
-      }
-      __syncthreads();
       for (int i = threadIdx.x; i < lines; i += 256)
-        which[i] = bias_bucket(g.bias, i - g.bias.reach - BIAS_MARGIN);
+        line[i] = (sums[i] + sums[lines + i]) + (sums[2 * lines + i] + sums[3 * lines + i]);
       __syncthreads();
+      const int end = g.bias.reach + BIAS_MARGIN;
       for (int b = threadIdx.x; b < g.bias.buckets; b += 256) {
+        int from, to;
+        bucket_range(g.bias, first_of, b, from, to);
         float v = 0.f;
-        for (int i = 0; i < lines; ++i)
-          if (which[i] == b) v += line[i];
+        for (int i = from; i <= to; ++i) v += line[i + end];
         for (int w = 0; w < 4; ++w) {
-          if (which[0] == b) v += far[2 * w];
-          if (which[lines - 1] == b) v += far[2 * w + 1];
+          if (from <= -end && -end <= to) v += far[2 * w];
+          if (from <= end && end <= to) v += far[2 * w + 1];
         }
         bucket_sums[b] = v;
       }
@@ -816,7 +813,8 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
   constexpr int DB = DP / 32, DC = DP / 16, SB = F::KEYS / 32, ES = DT == 0 ? 4 : 2;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   float* const stats = reinterpret_cast<float*>(lds + F::LDS);  // lse, delta of the rows, twice
-  float* const line = stats + 4 * F::KEYS;
+  int16_t* const first_of = reinterpret_cast<int16_t*>(stats + 4 * F::KEYS);
+  float* const line = reinterpret_cast<float*>(first_of + BIAS_FIRST);
   const uint32_t row_lane = lds_place(lds) + T::row_lane(), col_lane = lds_place(lds) + T::col_lane();
   const AttnShape& g = a.g;
   const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
@@ -1014,7 +1012,10 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
       for (int group = 0; group < g.groups; ++group) {
         const int head0 = (kvh * g.groups + group) * g.pack;
         __syncthreads();  // the previous rows' reads are done
-        if constexpr (BIAS) load_bias_line(g.bias, head0, g.heads, line);
+        if constexpr (BIAS) {
+          load_bias_first(g.bias, first_of);
+          load_bias_line(g.bias, first_of, head0, g.heads, line);
+        }
         const char* const qb = row_at<DT>(a.q, q0, head0);
         const char* const gb = row_at<DT>(a.g_o, q0, head0);
         float st = 0.f;
@@ -1099,8 +1100,9 @@ hipError_t launch_items(void (*kernel)(A), A a, int bytes, bool gaps, hipStream_
   return e;
 }
 
-int line_bytes(const AttnShape& g, int lines) {
-  return g.bias.table ? 2 * (g.bias.reach + BIAS_MARGIN) * 4 * lines + 4 * lines : 0;
+// LDS for a bias: the buckets' first distances and `lines` lines.
+int bias_bytes(const AttnShape& g, int lines) {
+  return g.bias.table ? 2 * BIAS_FIRST + (2 * (g.bias.reach + BIAS_MARGIN) + 1) * 4 * lines : 0;
 }
 
 // The variant for what the call needs: type, bias, and whether every row consists of
@@ -1129,9 +1131,9 @@ hipError_t launch_attention_forward<HLQ_ATTN_D>(const AttnFwd& a, int dtype, boo
     constexpr bool BIAS = decltype(b)::value, VEC = decltype(v)::value;
     if (few)
       return launch_items(k_attention_forward<DT, DP, BIAS, true, VEC>, a,
-                          FwdShape<DT, DP, true>::LDS + line_bytes(a.g, 1), gaps, s);
+                          FwdShape<DT, DP, true>::LDS + bias_bytes(a.g, 1), gaps, s);
     return launch_items(k_attention_forward<DT, DP, BIAS, false, VEC>, a,
-                        FwdShape<DT, DP, false>::LDS + line_bytes(a.g, 1), gaps, s);
+                        FwdShape<DT, DP, false>::LDS + bias_bytes(a.g, 1), gaps, s);
   });
 }
 
@@ -1141,7 +1143,8 @@ hipError_t launch_attention_backward_q<HLQ_ATTN_D>(const AttnBwd& a, int dtype, 
   return choose(dtype, a.g.bias.table, vec, [&](auto t, auto b, auto v) {
     constexpr int DT = decltype(t)::value, DP = HLQ_ATTN_D;
     return launch_items(k_attention_backward_q<DT, DP, decltype(b)::value, decltype(v)::value>, a,
-                        BwdShape<DT, DP>::LDS + line_bytes(a.g, 9) + 32, a.g.start_q != nullptr, s);
+                        BwdShape<DT, DP>::LDS + bias_bytes(a.g, 5) +
+                            (a.g.bias.table ? (4 * SKEW_SIZE + 8) * 4 : 0), a.g.start_q != nullptr, s);
   });
 }
 
@@ -1151,7 +1154,7 @@ hipError_t launch_attention_backward_kv<HLQ_ATTN_D>(const AttnBwd& a, int dtype,
   return choose(dtype, a.g.bias.table, vec, [&](auto t, auto b, auto v) {
     constexpr int DT = decltype(t)::value, DP = HLQ_ATTN_D;
     return launch_items(k_attention_backward_kv<DT, DP, decltype(b)::value, decltype(v)::value>, a,
-                        BwdShape<DT, DP>::LDS + 16 * BwdShape<DT, DP>::KEYS + line_bytes(a.g, 1),
+                        BwdShape<DT, DP>::LDS + 16 * BwdShape<DT, DP>::KEYS + bias_bytes(a.g, 1),
                         a.g.start_k != nullptr, s);
   });
 }

@@ -389,17 +389,6 @@ __device__ __forceinline__ bool item_of(const AttnShape& g, unsigned item, unsig
 
 // ------------------------------------------------------------ position bias
 
-// Bucket of a distance d = key position - query position.
-__device__ __forceinline__ int bias_bucket(const AttnBias& b, int d) {
-  int n = b.bidirectional ? (d < 0 ? -d : d) : (d < 0 ? -d : 0);
-  if (n >= b.exact) {
-    int k = b.exact;
-    for (int i = b.exact + 1; i < b.side; ++i) k += n >= b.first[i];
-    n = k;
-  }
-  return n + (b.bidirectional && d > 0 ? b.side : 0);
-}
-
 // The biases of one head, times log2(e), over the distances -(reach + 64) ..
 // reach + 64: a 32 x 32 block of scores that is not beyond reach as a whole
 // reads its line without limits.
@@ -407,15 +396,71 @@ constexpr int BIAS_MARGIN = 64;
 __device__ __forceinline__ int bias_line_size(const AttnBias& b) {
   return 2 * (b.reach + BIAS_MARGIN) + 1;
 }
-__device__ __forceinline__ float bias_value(const AttnBias& b, int bucket, int head, int heads) {
-  const int64_t at = (int64_t)bucket * heads + head;
-  return b.dtype == 0 ? static_cast<const float*>(b.table)[at]
-                      : bf16_lo(static_cast<const uint16_t*>(b.table)[at]);
+
+// Bucket of a distance d = key position - query position; first: the first distance
+// of each bucket of a side, in LDS.
+__device__ __forceinline__ int bias_bucket(const AttnBias& b, const int16_t* first, int d) {
+  const int n = b.bidirectional ? (d < 0 ? -d : d) : (d < 0 ? -d : 0);
+  int low = 0, high = b.side;  // first[low] <= n < first[high]
+  while (high - low > 1) {
+    const int mid = (low + high) / 2;
+    if (n >= first[mid]) low = mid;
+    else high = mid;
+  }
+  return low + (b.bidirectional && d > 0 ? b.side : 0);
 }
-__device__ __forceinline__ void load_bias_line(const AttnBias& b, int head, int heads, float* line) {
+
+// Call by all threads; ends with first in place (BIAS_FIRST entries) but the line
+// needing a barrier.
+constexpr int BIAS_FIRST = 128;
+__device__ __forceinline__ void load_bias_first(const AttnBias& b, int16_t* first) {
+  for (int i = threadIdx.x; i < b.side; i += blockDim.x)
+    first[i] = (int16_t)(i < b.exact ? i : b.first[i]);
+  __syncthreads();
+}
+__device__ __forceinline__ void load_bias_line(const AttnBias& b, const int16_t* first, int head,
+                                               int heads, float* line) {
   const int n = bias_line_size(b);
-  for (int i = threadIdx.x; i < n; i += blockDim.x)
-    line[i] = bias_value(b, bias_bucket(b, i - b.reach - BIAS_MARGIN), head, heads) * kLog2e;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int64_t at = (int64_t)bias_bucket(b, first, i - b.reach - BIAS_MARGIN) * heads + head;
+    line[i] = kLog2e * (b.dtype == 0 ? static_cast<const float*>(b.table)[at]
+                                     : bf16_lo(static_cast<const uint16_t*>(b.table)[at]));
+  }
+}
+
+// The line's distances of bucket k: from .. to, none if from > to.
+__device__ __forceinline__ void bucket_range(const AttnBias& b, const int16_t* first, int k, int& from,
+                                             int& to) {
+  const int j = k >= b.side ? k - b.side : k, end = b.reach + BIAS_MARGIN;
+  const int near = first[j], far = j + 1 < b.side ? first[j + 1] - 1 : end;
+  if (k >= b.side) {
+    from = near > 1 ? near : 1;
+    to = far;
+  } else {
+    from = -far;
+    to = j == 0 && !b.bidirectional ? end : -near;
+  }
+}
+
+// Sums along the diagonals of a wave's 32 x 32 block (rows of the accumulator at acc_row
+// + 4 half, columns lanes): element (i, l) is written to place i of line i - l + 31, so
+// that a line's 32 places, of which those without an element stay zero, are one lane's.
+// 16 writes and 8 reads; adding to LDS with the unit's own fp32 additions takes 193
+// cycles an instruction, 16 times as long, and the order of the additions is not ours.
+constexpr int SKEW = 36;  // a line's pitch: 16-byte pieces, no bank conflicts
+constexpr int SKEW_SIZE = 63 * SKEW;
+__device__ __forceinline__ float diagonal_sum(float* skew, const f32x16& v) {
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  float* const at = skew + (31 - (lane & 31)) * SKEW + 4 * half * (SKEW + 1);
+#pragma unroll
+  for (int r = 0; r < 16; ++r) at[acc_row(r) * (SKEW + 1)] = v[r];
+  __builtin_amdgcn_wave_barrier();
+  const f32x4* const mine = reinterpret_cast<const f32x4*>(skew + min(lane, 62) * SKEW);
+  f32x4 sum = mine[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) sum += mine[i];
+  __builtin_amdgcn_wave_barrier();
+  return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
 }  // namespace hlq
