@@ -108,8 +108,8 @@ __device__ __forceinline__ uint32_t lds_place(char* lds) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
 }
 
-typedef std::integral_constant<bool, true> Whole;
-typedef std::integral_constant<bool, false> Masked;
+typedef std::true_type Yes;
+typedef std::false_type No;
 
 // A chain of matrix products whose fragments come from LDS, in steps whose order the
 // compiler keeps: fragment i + AHEAD is read, product i starts, and what the matrix
@@ -168,7 +168,7 @@ struct FwdShape {
 };
 
 template <int DT, int DP, bool BIAS, bool FEW, bool VEC>
-__global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(AttnFwd a) {
+__global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !FEW ? 3 : 2) void k_attention_forward(AttnFwd a) {
   typedef FwdShape<DT, DP, FEW> F;
   typedef Tile<DT, DP> T;
   constexpr int DB = DP / 32, DC = DP / 16, SB = F::MINE / 32, ES = DT == 0 ? 4 : 2;
@@ -258,171 +258,124 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
       float m = -kInf, l = 0.f;
 
       // One tile of keys, from key0 on in this wave.
-      // tile: its place in LDS, the values' tile after the keys'.
-      const auto attend = [&](auto all, int key0, int tile) {
-        constexpr bool WHOLE = decltype(all)::value;
-        const uint32_t rl = row_lane + tile, cl = col_lane + tile;
-        if constexpr (WHOLE) {
-          constexpr int ND = 2 * DB;
-          // fragments in the order of use: rows of k by blocks, columns of v by blocks
-          const auto read = [&](auto step) {
-            constexpr int i = decltype(step)::value;
-            if constexpr (i < SB * DC) {
-              return T::row_frag(rl, 32 * (i / DC), i % DC);
-            } else {
-              constexpr int j = i - SB * DC;
-              return T::col_frag(cl, F::KEYS + 32 * (j / ND) + 16 * (j % ND / DB), j % DB);
-            }
-          };
-          Frag<DT> pf[2];
-          f32x16 s[SB];
-          float base = 0.f, keep = 1.f, sum = 0.f;
-          bool moved = false;  // the maximum; uniform
-          // The running maximum with block b's scores, and the factor that the sums so
-          // far then need.
-          const auto enter = [&](int b) {
-            float top = s[b][0];
-#pragma unroll
-            for (int r = 1; r < 16; ++r) top = fmaxf(top, s[b][r]);
-            top = max_halves(top);
-            if constexpr (!BIAS) top *= g.c;
-            top = fmaxf(m, top);
-            base = top == -kInf ? 0.f : top;  // a row that has seen no key yet
-            moved = __any(top != m);
-            if (moved) {
-              keep = exp2_fast(m - base);
-              l *= keep;
-              m = top;
-            }
-          };
-          const auto rescale = [&] {
-            if (!moved) return;
-#pragma unroll
-            for (int d = 0; d < DB; ++d)
-#pragma unroll
-              for (int r = 0; r < 16; ++r) o[d][r] *= keep;
-          };
-          const auto probability = [&](int b, int r) {
-            s[b][r] = exp2_fast(BIAS ? s[b][r] - base : __builtin_fmaf(s[b][r], g.c, -base));
-            sum += s[b][r];
-          };
-          const auto leave = [&](int b) {
-            l += sum;
-            sum = 0.f;
-            pf[0] = acc_frag<DT>(s[b], 0);
-            pf[1] = acc_frag<DT>(s[b], 1);
-          };
-          constexpr int PV = SB * DC;  // first product with v
-          steps<DT, PV + SB * ND>(read, [&](auto step, const Frag<DT>& f) {
-              constexpr int i = decltype(step)::value;
-            if constexpr (i < PV) {
-              constexpr int b = i / DC, j = i % DC;
-              if constexpr (j == 0) s[b] = (f32x16)(0.f);
-              s[b] = mma(f, qf[j], s[b]);
-              if constexpr (BIAS && j == DC - 1) {
-                const int dist = key0 + 32 * b - (row0 + off);  // of the first row; later ones less
-                add_bias<false>(g, line, s[b], dist - 31, dist + 31,
-                                key0 + 32 * b - me.pos + 4 * half);
-              }
-              if constexpr (SB == 1 && j == DC - 1) {
-                enter(0);
-                rescale();
-#pragma unroll
-                for (int r = 0; r < 16; ++r) probability(0, r);
-                leave(0);
-              }
-              if constexpr (b > 0) {
-                // beside the second block's scores: the first one's probabilities
-                if constexpr (j == 1) {
-                  enter(0);
-                  rescale();
-                }
-#pragma unroll
-                for (int r = beside(j, DC, 16); r < beside(j + 1, DC, 16); ++r) probability(0, r);
-                if constexpr (j == DC - 1) leave(0);
-              }
-            } else {
-              constexpr int b = (i - PV) / ND, j = (i - PV) % ND;
-              o[j % DB] = mma(f, pf[j / DB], o[j % DB]);
-              if constexpr (b + 1 < SB) {
-                // beside the first block's values: the second one's probabilities
-                if constexpr (j == 1) enter(1);
-#pragma unroll
-                for (int r = beside(j, ND, 16); r < beside(j + 1, ND, 16); ++r) probability(1, r);
-                if constexpr (j == ND - 1) {
-                  rescale();
-                  leave(1);
-                }
-              }
-            }
-          });
-          return;
-        }
-        f32x16 s[SB];
-        float top = -kInf;
-#pragma unroll
-        for (int b = 0; b < SB; ++b) {
-          if (!WHOLE && key0 + 32 * b >= last) continue;
-          s[b] = (f32x16)(0.f);
-#pragma unroll
-          for (int c = 0; c < DC; ++c)
-            s[b] = mma(T::row_frag(rl, 32 * b, c), qf[c], s[b]);
-          if constexpr (BIAS) {
-            const int dist = key0 + 32 * b - (row0 + off);  // of the first row; later ones less
-            add_bias<false>(g, line, s[b], dist - 31, dist + 31, key0 + 32 * b - me.pos + 4 * half);
+      // COUNT blocks of 32 keys from key0 on; rl, cl: the lane's place in the keys'
+      // tile, by rows and by columns, the values' follow.  MASK: some rows do not see
+      // some of the keys; bad: those of them whose values are not finite.
+      const auto blocks = [&](auto count, auto mask, int key0, uint32_t rl, uint32_t cl,
+                              uint32_t bad) {
+        constexpr int COUNT = decltype(count)::value, ND = 2 * DB, PV = COUNT * DC;
+        constexpr bool MASK = decltype(mask)::value;
+        // fragments in the order of use: rows of k by blocks, columns of v by blocks
+        const auto read = [&](auto step) {
+          constexpr int i = decltype(step)::value;
+          if constexpr (i < PV) {
+            return T::row_frag(rl, 32 * (i / DC), i % DC);
+          } else {
+            constexpr int j = i - PV;
+            return T::col_frag(cl, F::KEYS + 32 * (j / ND) + 16 * (j % ND / DB), j % DB);
           }
-          if (!WHOLE) {
+        };
+        Frag<DT> pf[2];
+        f32x16 s[COUNT];
+        float base = 0.f, keep = 1.f, sum = 0.f;
+        bool moved = false;  // the maximum; uniform
+        // A block's scores are there: bias, mask, the running maximum, and the factor
+        // that the sums so far then need.
+        const auto enter = [&](int b) {
+          if constexpr (MASK) {
 #pragma unroll
             for (int r = 0; r < 16; ++r)
               if (key0 + 32 * b + acc_row(r) + 4 * half >= limit) s[b][r] = -kInf;
           }
+          float top = s[b][0];
 #pragma unroll
-          for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
-        }
-        top = max_halves(top);
-        if constexpr (!BIAS) top *= g.c;
-        top = fmaxf(m, top);
-        const float base = top == -kInf ? 0.f : top;  // a row that has seen no key yet
-        if (__any(top != m)) {
-          const float keep = exp2_fast(m - base);
-          l *= keep;
+          for (int r = 1; r < 16; ++r) top = fmaxf(top, s[b][r]);
+          top = max_halves(top);
+          if constexpr (!BIAS) top *= g.c;
+          top = fmaxf(m, top);
+          base = top == -kInf ? 0.f : top;  // a row that has seen no key yet
+          moved = __any(top != m);
+          if (moved) {
+            keep = exp2_fast(m - base);
+            l *= keep;
+            m = top;
+          }
+        };
+        const auto rescale = [&] {
+          if (!moved) return;
 #pragma unroll
           for (int d = 0; d < DB; ++d)
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[d][r] *= keep;
-          m = top;
-        }
-        float sum = 0.f;
-#pragma unroll
-        for (int b = 0; b < SB; ++b) {
-          if (!WHOLE && key0 + 32 * b >= last) continue;
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            s[b][r] = exp2_fast(BIAS ? s[b][r] - base : __builtin_fmaf(s[b][r], g.c, -base));
-            sum += s[b][r];
-          }
-          const uint32_t bad =
-              !WHOLE && g.causal ? rows_not_finite<DT, DP>(rl, F::KEYS + 32 * b) : 0;
-          if (!WHOLE && bad) {
-            if (bad & bit_range(0, limit - key0 - 32 * b)) sum = __builtin_nanf("");
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const Frag<DT> p = acc_frag<DT>(s[b], c);
-#pragma unroll
-              for (int d = 0; d < DB; ++d)
-                o[d] = mma(finite<DT>(T::col_frag(cl, F::KEYS + 32 * b + 16 * c, d)), p, o[d]);
+        };
+        const auto probability = [&](int b, int r) {
+          s[b][r] = exp2_fast(BIAS ? s[b][r] - base : __builtin_fmaf(s[b][r], g.c, -base));
+          sum += s[b][r];
+        };
+        const auto leave = [&](int b) {
+          if (MASK && (bad & bit_range(0, limit - key0 - 32 * b))) sum = __builtin_nanf("");
+          l += sum;
+          sum = 0.f;
+          pf[0] = acc_frag<DT>(s[b], 0);
+          pf[1] = acc_frag<DT>(s[b], 1);
+        };
+        steps<DT, PV + COUNT * ND>(read, [&](auto step, const Frag<DT>& f) {
+          constexpr int i = decltype(step)::value;
+          if constexpr (i < PV) {
+            constexpr int b = i / DC, j = i % DC;
+            if constexpr (j == 0) s[b] = (f32x16)(0.f);
+            s[b] = mma(f, qf[j], s[b]);
+            if constexpr (BIAS && j == DC - 1) {
+              const int dist = key0 + 32 * b - (row0 + off);  // of the first row; later ones less
+              add_bias<false>(g, line, s[b], dist - 31, dist + 31, key0 + 32 * b - me.pos + 4 * half);
             }
-            continue;
-          }
+            if constexpr (COUNT == 1 && j == DC - 1) {
+              enter(0);
+              rescale();
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const Frag<DT> p = acc_frag<DT>(s[b], c);
+              for (int r = 0; r < 16; ++r) probability(0, r);
+              leave(0);
+            }
+            if constexpr (b > 0) {
+              // beside the second block's scores: the first one's probabilities
+              if constexpr (j == 1) {
+                enter(0);
+                rescale();
+              }
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
-              o[d] = mma(T::col_frag(cl, F::KEYS + 32 * b + 16 * c, d), p, o[d]);
+              for (int r = beside(j, DC, 16); r < beside(j + 1, DC, 16); ++r) probability(0, r);
+              if constexpr (j == DC - 1) leave(0);
+            }
+          } else {
+            constexpr int b = (i - PV) / ND, j = (i - PV) % ND;
+            o[j % DB] = mma(only_finite<DT>(f, MASK && bad), pf[j / DB], o[j % DB]);
+            if constexpr (b + 1 < COUNT) {
+              // beside the first block's values: the second one's probabilities
+              if constexpr (j == 1) enter(1);
+#pragma unroll
+              for (int r = beside(j, ND, 16); r < beside(j + 1, ND, 16); ++r) probability(1, r);
+              if constexpr (j == ND - 1) {
+                rescale();
+                leave(1);
+              }
+            }
           }
+        });
+      };
+      // A tile of keys, of which this wave's begin at key0 and in LDS at `tile`.
+      const auto attend = [&](int key0, int tile) {
+        uint32_t rl = row_lane + tile, cl = col_lane + tile;
+        if (key0 + F::MINE <= first) {
+          blocks(Step<SB>(), No(), key0, rl, cl, 0);
+          return;
         }
-        l += sum;
+#pragma unroll 1
+        for (int b = 0; b < SB && key0 < last; ++b, key0 += 32) {
+          blocks(Step<1>(), Yes(), key0, rl, cl,
+                 g.causal ? rows_not_finite<DT, DP>(rl, F::KEYS) : 0);
+          rl += 32 * T::ROW_BYTES;
+          cl += 32 * T::ROW_BYTES;
+        }
       };
 
       const auto feed = [&](int key, int buf) {
@@ -443,8 +396,7 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
         const int mine = FEW ? 32 * wave : 0, key0 = key + mine;
         if (key0 >= last) continue;
         const int at = buf * 2 * F::TILE_BYTES + mine * T::ROW_BYTES;
-        if (key0 + F::MINE <= first) attend(Whole(), key0, at);
-        else attend(Masked(), key0, at);
+        attend(key0, at);
       }
       l = sum_halves(l);
 
@@ -533,23 +485,60 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_forward(Attn
 
 // ------------------------------------------------------------ gradient of q
 
-template <int DT, int DP>
+// FEW: a tile of 32 rows (keys), of which each wave takes a quarter of the keys
+// (rows); the waves' sums are joined through LDS.
+template <int DT, int DP, bool FEW, bool SKEWED = false>
 struct BwdShape {
   typedef Tile<DT, DP> T;
-  static constexpr int KEYS = DT == 0 ? 32 : 64;  // keys, or rows, of a tile
+  static constexpr int OWN = FEW ? ATTN_FEW : ATTN_ROWS;      // rows (keys) of a workgroup
+  static constexpr int KEYS = FEW ? 128 : DT == 0 ? 32 : 64;  // keys, or rows, of a tile
+  static constexpr int BLOCKS = FEW ? 1 : KEYS / 32;          // of them a wave's
   static constexpr int TILE_BYTES = KEYS * T::ROW_BYTES;
-  static constexpr int LDS = 4 * TILE_BYTES;  // two tensors, two buffers
+  // SKEWED: the sums of a bias's gradient need room too
+  static constexpr int BUFS = TILE_BYTES > (SKEWED ? 16384 : 32768) ? 1 : 2;
+  static constexpr int JOIN_BYTES = FEW ? 4 * DP * 33 * 4 : 0;
+  static constexpr int LDS =
+      2 * BUFS * TILE_BYTES > JOIN_BYTES ? 2 * BUFS * TILE_BYTES : JOIN_BYTES;
 };
+
+// Sums of the four waves, each [d][lane] in `mine` (plus poison, 0 or NaN), times scale
+// into the lanes' rows: row(i) is the address of lane i's output or null.  All
+// threads; LDS is free before and after.
+template <int DT, int DP, typename Row>
+__device__ __forceinline__ void join_waves(char* lds, const f32x16 (&mine)[DP / 32], float poison,
+                                           float scale, int D, Row row) {
+  typedef typename Piece<DT>::Elem E;
+  float* const sums = reinterpret_cast<float*>(lds);
+  const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
+  __syncthreads();
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      sums[(wave * DP + 32 * d + acc_row(r) + 4 * half) * 33 + (lane & 31)] =
+          mine[d][r] + poison;
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * DP; i += 256) {
+    const int d = i % DP, at = d * 33 + i / DP;
+    char* const p = row(i / DP);
+    if (!p || d >= D) continue;
+    const float v = ((sums[at] + sums[DP * 33 + at]) +
+                     (sums[2 * DP * 33 + at] + sums[3 * DP * 33 + at])) * scale;
+    if constexpr (DT == 0) reinterpret_cast<E*>(p)[d] = v;
+    else reinterpret_cast<E*>(p)[d] = (uint16_t)pack_bf16(v, 0.f);
+  }
+  __syncthreads();
+}
 
 // Waves as in the forward pass.  Writes delta for the gradients of k and v, and
 // with a bias the sums of dS by bucket over the item: each wave adds its blocks'
 // diagonals to a line of distances of its own in LDS, blocks beyond reach in
 // registers.
-template <int DT, int DP, bool BIAS, bool VEC>
-__global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(AttnBwd a) {
-  typedef BwdShape<DT, DP> F;
+template <int DT, int DP, bool BIAS, bool FEW, bool VEC>
+__global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !BIAS && !FEW ? 3 : 2) void k_attention_backward_q(AttnBwd a) {
+  typedef BwdShape<DT, DP, FEW, BIAS> F;
   typedef Tile<DT, DP> T;
-  constexpr int DB = DP / 32, DC = DP / 16, SB = F::KEYS / 32, ES = DT == 0 ? 4 : 2;
+  constexpr int DB = DP / 32, DC = DP / 16, ES = DT == 0 ? 4 : 2;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const uint32_t row_lane = lds_place(lds) + T::row_lane(), col_lane = lds_place(lds) + T::col_lane();
   const AttnShape& g = a.g;
@@ -581,7 +570,7 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
     sequence(g.start_q, seq, g.Tq, q0, nq);
     sequence(g.start_k, seq, g.Tk, k0, nk);
     const int rows = nq * g.pack, off = nk - nq;
-    if ((int64_t)tile0 * ATTN_ROWS >= rows) {
+    if ((int64_t)tile0 * F::OWN >= rows) {
       if constexpr (BIAS)
         for (int b = threadIdx.x; b < g.bias.buckets; b += 256)
           bucket_sums[b] = 0.f;
@@ -602,14 +591,16 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
     sk.init((uint32_t)kt, 0, 1);
     sv.init((uint32_t)vt, 0, 1);
 
-    for (int64_t tile = tile0; tile * ATTN_ROWS < rows; tile += g.tiles) {
-      const int row0 = (int)tile * ATTN_ROWS + wave * 32;
+    for (int64_t tile = tile0; tile * F::OWN < rows; tile += g.tiles) {
+      const int row0 = (int)tile * F::OWN + (FEW ? 0 : wave * 32);
       RowInfo me = row_info(g, row0 + (lane & 31), rows, head0, off, nk);
-      if (!me.valid) me.limit = 0;  // no key: such rows go through the masked form
-      const int first = wave_min(me.limit), last = wave_max_int(me.limit);
+      // Rows past the end are computed for nothing, but not for the bias's gradient.
+      if (BIAS && !me.valid) me.limit = 0;
+      const int first = wave_min(BIAS || me.valid ? me.limit : nk);
+      const int last = wave_max_int(me.valid ? me.limit : 0);
       int end = nk;
       if (g.causal) {
-        const int r = min(rows, (int)(tile + 1) * ATTN_ROWS) - 1;
+        const int r = min(rows, (int)(tile + 1) * F::OWN) - 1;
         end = max(0, min(nk, (int)((unsigned)r / (unsigned)g.pack) + off + 1));
       }
 
@@ -647,99 +638,69 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
       for (int d = 0; d < DB; ++d) dq[d] = (f32x16)(0.f);
       float poison = 0.f;
 
-      const auto attend = [&](auto all, int key, int tile) {
-        constexpr bool WHOLE = decltype(all)::value;
-#pragma unroll 1
-        for (int b = 0; b < SB; ++b) {
-          const uint32_t rl = row_lane + tile + 32 * b * T::ROW_BYTES;
-          const uint32_t cl = col_lane + tile + 32 * b * T::ROW_BYTES;
-          if (!WHOLE && key + 32 * b >= last) continue;
-          const int base = key + 32 * b - me.pos + 4 * half;
-          const int dist = key + 32 * b - (row0 + off);
-          const auto add_up = [&](const f32x16& ds) {  // the bias's gradient
-            if (dist - 31 >= g.bias.reach || dist + 31 <= -g.bias.reach) {
-              float sum = 0.f;
+      // A block of 32 keys from key on; see the forward pass.
+      const auto block = [&](auto mask, int key, uint32_t rl, uint32_t cl, uint32_t bad) {
+        constexpr bool MASK = decltype(mask)::value;
+        const int dist = key - (row0 + off), limit = me.limit - key;
+        // fragments in the order of use: rows of k, rows of v, columns of k
+        const auto read = [&](auto step) {
+          constexpr int i = decltype(step)::value;
+          if constexpr (i < 2 * DC) return T::row_frag(rl, i < DC ? 0 : F::KEYS, i % DC);
+          else return T::col_frag(cl, 16 * ((i - 2 * DC) / DB), (i - 2 * DC) % DB);
+        };
+        Frag<DT> df[2];
+        f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
+        steps<DT, 2 * DC + 2 * DB>(read, [&](auto step, const Frag<DT>& f) {
+          constexpr int i = decltype(step)::value;
+          if constexpr (i < DC) {
+            s = mma(f, qf[i], s);
+            if constexpr (BIAS && i == DC - 1)
+              add_bias<false>(g, line, s, dist - 31, dist + 31, key - me.pos + 4 * half);
+          } else if constexpr (i < 2 * DC) {
+            dp = mma(f, gf[i - DC], dp);
+            constexpr int j = i - DC;
 #pragma unroll
-              for (int r = 0; r < 16; ++r) sum += ds[r];
-              if (dist > 0) far_high += sum;
-              else far_low += sum;
-              return;
-            }
-            const float sum = diagonal_sum(skew + wave * SKEW_SIZE, ds);
-            // lane i: distance i - 31 from the block's first row and column
-            if (lane < 63)
-              sums[wave * lines + dist - 31 + lane + g.bias.reach + BIAS_MARGIN] += sum;
-          };
-          if constexpr (WHOLE) {
-            // fragments in the order of use: rows of k, rows of v, columns of k
-            const auto read = [&](auto step) {
-            constexpr int i = decltype(step)::value;
-              if constexpr (i < 2 * DC) return T::row_frag(rl, i < DC ? 0 : F::KEYS, i % DC);
-              else return T::col_frag(cl, 16 * ((i - 2 * DC) / DB), (i - 2 * DC) % DB);
-            };
-            Frag<DT> df[2];
-            f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
-            steps<DT, 2 * DC + 2 * DB>(read, [&](auto step, const Frag<DT>& f) {
-              constexpr int i = decltype(step)::value;
-              if constexpr (i < DC) {
-                s = mma(f, qf[i], s);
-                if constexpr (BIAS)
-                  if constexpr (i == DC - 1) add_bias<false>(g, line, s, dist - 31, dist + 31, base);
-              } else if constexpr (i < 2 * DC) {
-                dp = mma(f, gf[i - DC], dp);
-                constexpr int j = i - DC;
+            for (int r = beside(j, DC, 16); r < beside(j + 1, DC, 16); ++r)
+              s[r] = exp2_fast(BIAS ? s[r] - lse : __builtin_fmaf(s[r], g.c, -lse));
+            if constexpr (j == DC - 1) {
 #pragma unroll
-                for (int r = beside(j, DC, 16); r < beside(j + 1, DC, 16); ++r)
-                  s[r] = exp2_fast(BIAS ? s[r] - lse : __builtin_fmaf(s[r], g.c, -lse));
-                if constexpr (j == DC - 1) {
-#pragma unroll
-                  for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
-                  if constexpr (BIAS) add_up(s);
-                  df[0] = acc_frag<DT>(s, 0);
-                  df[1] = acc_frag<DT>(s, 1);
-                }
-              } else {
-                constexpr int j = i - 2 * DC;
-                dq[j % DB] = mma(f, df[j / DB], dq[j % DB]);
+              for (int r = 0; r < 16; ++r) {
+                s[r] *= dp[r] - delta;
+                if (MASK && acc_row(r) + 4 * half >= limit) s[r] = 0.f;
               }
-            });
-            continue;
-          }
-          f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
+              if constexpr (BIAS) {  // its gradient
+                if (dist - 31 >= g.bias.reach || dist + 31 <= -g.bias.reach) {
+                  float sum = 0.f;
 #pragma unroll
-          for (int c = 0; c < DC; ++c) {
-            s = mma(T::row_frag(rl, 0, c), qf[c], s);
-            dp = mma(T::row_frag(rl, F::KEYS, c), gf[c], dp);
-          }
-          if constexpr (BIAS) add_bias<false>(g, line, s, dist - 31, dist + 31, base);
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            s[r] = exp2_fast(BIAS ? s[r] - lse : __builtin_fmaf(s[r], g.c, -lse)) * (dp[r] - delta);
-          const int limit = me.limit - key - 32 * b;
-          if (!WHOLE) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-              if (acc_row(r) + 4 * half >= limit) s[r] = 0.f;
-          }
-          if constexpr (BIAS) add_up(s);
-          const uint32_t bad = !WHOLE && g.causal ? rows_not_finite<DT, DP>(rl, 0) : 0;
-          if (!WHOLE && bad) {
-            if (bad & bit_range(0, limit)) poison = __builtin_nanf("");
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const Frag<DT> ds = acc_frag<DT>(s, c);
-#pragma unroll
-              for (int d = 0; d < DB; ++d)
-                dq[d] = mma(finite<DT>(T::col_frag(cl, 16 * c, d)), ds, dq[d]);
+                  for (int r = 0; r < 16; ++r) sum += s[r];
+                  if (dist > 0) far_high += sum;
+                  else far_low += sum;
+                } else {
+                  const float sum = diagonal_sum(skew + wave * SKEW_SIZE, s);
+                  // lane i: distance i - 31 from the block's first row and column
+                  if (lane < 63)
+                    sums[wave * lines + dist - 31 + lane + g.bias.reach + BIAS_MARGIN] += sum;
+                }
+              }
+              if (MASK && (bad & bit_range(0, limit))) poison = __builtin_nanf("");
+              df[0] = acc_frag<DT>(s, 0);
+              df[1] = acc_frag<DT>(s, 1);
             }
-            continue;
+          } else {
+            constexpr int j = i - 2 * DC;
+            dq[j % DB] = mma(only_finite<DT>(f, MASK && bad), df[j / DB], dq[j % DB]);
           }
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const Frag<DT> ds = acc_frag<DT>(s, c);
-#pragma unroll
-            for (int d = 0; d < DB; ++d) dq[d] = mma(T::col_frag(cl, 16 * c, d), ds, dq[d]);
-          }
+        });
+      };
+      // A tile of keys, of which this wave's begin at key and in LDS at `tile`.
+      const auto attend = [&](int key, int tile) {
+        uint32_t rl = row_lane + tile, cl = col_lane + tile;
+#pragma unroll 1
+        for (int b = 0; b < F::BLOCKS && key < last; ++b, key += 32) {
+          if (key + 32 <= first) block(No(), key, rl, cl, 0);
+          else block(Yes(), key, rl, cl, g.causal ? rows_not_finite<DT, DP>(rl, 0) : 0);
+          rl += 32 * T::ROW_BYTES;
+          cl += 32 * T::ROW_BYTES;
         }
       };
 
@@ -749,15 +710,25 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
         sv.issue(vb + key * vt, end - key, g.D, at + F::TILE_BYTES);
       };
       __syncthreads();  // the previous tile's reads are done
-      if (end > 0) feed(0, 0);
+      if (F::BUFS == 2 && end > 0) feed(0, 0);
       int buf = 0;
-      for (int key = 0; key < end; key += F::KEYS, buf ^= 1) {
+      for (int key = 0; key < end; key += F::KEYS, buf ^= F::BUFS - 1) {
+        if (F::BUFS == 1) {
+          __syncthreads();
+          feed(key, 0);
+        }
         feed_wait();
-        if (key + F::KEYS < end) feed(key + F::KEYS, buf ^ 1);
-        if (key >= last) continue;
-        const int at = buf * 2 * F::TILE_BYTES;
-        if (key + F::KEYS <= first) attend(Whole(), key, at);
-        else attend(Masked(), key, at);
+        if (F::BUFS == 2 && key + F::KEYS < end) feed(key + F::KEYS, buf ^ 1);
+        const int mine = FEW ? 32 * wave : 0;
+        attend(key + mine, buf * 2 * F::TILE_BYTES + mine * T::ROW_BYTES);
+      }
+      if constexpr (FEW) {
+        const auto& z = *again<AttnBwd>();
+        join_waves<DT, DP>(lds, dq, poison, z.g.scale, z.g.D, [&](int i) -> char* {
+          const RowInfo it = row_info(g, row0 + i, rows, head0, off, nk);
+          return it.valid ? row_at<DT>(z.g_q, (int64_t)q0 + it.token, it.head) : nullptr;
+        });
+        continue;
       }
       if (me.valid) {
         const auto& z = *again<AttnBwd>();
@@ -805,12 +776,12 @@ __global__ __launch_bounds__(256, DT == 1 ? 2 : 1) void k_attention_backward_q(A
 
 // A work item is 128 keys of one sequence and key head, 32 a wave; it goes
 // through the query rows of the heads that share them.
-template <int DT, int DP, bool BIAS, bool VEC>
+template <int DT, int DP, bool BIAS, bool FEW, bool VEC>
 __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_backward_kv(
     AttnBwd a) {
-  typedef BwdShape<DT, DP> F;
+  typedef BwdShape<DT, DP, FEW> F;
   typedef Tile<DT, DP> T;
-  constexpr int DB = DP / 32, DC = DP / 16, SB = F::KEYS / 32, ES = DT == 0 ? 4 : 2;
+  constexpr int DB = DP / 32, DC = DP / 16, ES = DT == 0 ? 4 : 2;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   float* const stats = reinterpret_cast<float*>(lds + F::LDS);  // lse, delta of the rows, twice
   int16_t* const first_of = reinterpret_cast<int16_t*>(stats + 4 * F::KEYS);
@@ -840,14 +811,14 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
     sequence(g.start_q, seq, g.Tq, q0, nq);
     sequence(g.start_k, seq, g.Tk, k0, nk);
     const int rows = nq * g.pack, off = nk - nq;
-    if ((int64_t)tile0 * ATTN_ROWS >= nk) continue;
+    if ((int64_t)tile0 * F::OWN >= nk) continue;
     const int64_t qt = a.q.token * ES, gt = a.g_o.token * ES;
     Feed<DT, DP, F::KEYS, VEC> sq, sg;
     sq.init((uint32_t)qt, (uint32_t)(a.q.head * ES), g.pack);
     sg.init((uint32_t)gt, (uint32_t)(a.g_o.head * ES), g.pack);
 
-    for (int64_t tile = tile0; tile * ATTN_ROWS < nk; tile += g.tiles) {
-      const int wkey = (int)tile * ATTN_ROWS + wave * 32, key = wkey + (lane & 31);
+    for (int64_t tile = tile0; tile * F::OWN < nk; tile += g.tiles) {
+      const int wkey = (int)tile * F::OWN + (FEW ? 0 : wave * 32), key = wkey + (lane & 31);
       const bool valid = key < nk;
       Frag<DT> kf[DC], vf[DC];
       {
@@ -870,142 +841,106 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
       // first row that sees the tile's first key, in whole tiles; this wave's first key
       int begin = 0, mine = 0;
       if (g.causal) {
-        begin = max(0, (int)tile * ATTN_ROWS - off) * g.pack / F::KEYS * F::KEYS;
+        begin = max(0, (int)tile * F::OWN - off) * g.pack / F::KEYS * F::KEYS;
         mine = max(0, wkey - off) * g.pack;
       }
       const int sees = g.causal ? max(0, key - off) * g.pack : 0;       // first row of this key
       const int most = g.causal ? max(0, wkey + 31 - off) * g.pack : 0;  // of the wave's last
 
-      const auto attend = [&](auto all, int row, int tile, const float* stat) {
-        constexpr bool WHOLE = decltype(all)::value;
+      // A block of 32 rows from row on; stat: their lse, and delta after a tile's.
+      const auto block = [&](auto mask, int row, uint32_t rl, uint32_t cl, const float* stat,
+                             uint32_t bad_q, uint32_t bad_g) {
+        constexpr bool MASK = decltype(mask)::value;
+        constexpr int ND = 2 * DB;
+        const int low = sees - row, high = rows - row;
+        // fragments in the order of use: rows of q, rows of g_o, columns of g_o, of q
+        const auto read = [&](auto step) {
+          constexpr int i = decltype(step)::value;
+          if constexpr (i < 2 * DC) {
+            return T::row_frag(rl, i < DC ? 0 : F::KEYS, i % DC);
+          } else {
+            constexpr int j = (i - 2 * DC) % ND;
+            return T::col_frag(cl, (i < 2 * DC + ND ? F::KEYS : 0) + 16 * (j / DB), j % DB);
+          }
+        };
+        Frag<DT> pf[2], df[2];
+        f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
+        f32x4 lse[4], del[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float* p = stat + 8 * q + 4 * half;
+          lse[q] = *reinterpret_cast<const f32x4*>(p);
+          del[q] = *reinterpret_cast<const f32x4*>(p + F::KEYS);
+        }
+        const auto hidden = [&](int r) {
+          const int i = acc_row(r) + 4 * half;
+          return MASK && (i < low || i >= high);
+        };
+        steps<DT, 2 * (DC + ND)>(read, [&](auto step, const Frag<DT>& f) {
+          constexpr int i = decltype(step)::value;
+          if constexpr (i < DC) {
+            s = mma(f, kf[i], s);
+            if constexpr (BIAS && i == DC - 1) {
+              const int dist = wkey - (row + off);
+              add_bias<true>(g, line, s, dist - 31, dist + 31, key - (row + off) - 4 * half);
+            }
+          } else if constexpr (i < 2 * DC) {
+            dp = mma(f, vf[i - DC], dp);
+            constexpr int j = i - DC;
+#pragma unroll
+            for (int r = beside(j, DC, 16); r < beside(j + 1, DC, 16); ++r) {
+              const float ls = lse[r / 4][r % 4];
+              s[r] = exp2_fast(BIAS ? s[r] - ls : __builtin_fmaf(s[r], g.c, -ls));
+              if (hidden(r)) s[r] = 0.f;
+            }
+            if constexpr (j == DC - 1) {
+              if (MASK && (bad_q | bad_g)) {
+                const uint32_t seen = bit_range(low, high);
+                if (bad_q & seen) poison_k = __builtin_nanf("");
+                if (bad_g & seen) poison_v = __builtin_nanf("");
+              }
+              pf[0] = acc_frag<DT>(s, 0);
+              pf[1] = acc_frag<DT>(s, 1);
+            }
+          } else if constexpr (i < 2 * DC + ND) {
+            constexpr int j = i - 2 * DC;
+            dv[j % DB] = mma(only_finite<DT>(f, MASK && bad_g), pf[j / DB], dv[j % DB]);
+#pragma unroll
+            for (int r = beside(j, ND, 16); r < beside(j + 1, ND, 16); ++r) {
+              s[r] *= dp[r] - del[r / 4][r % 4];
+              if (hidden(r)) s[r] = 0.f;
+            }
+            if constexpr (j == ND - 1) {
+              df[0] = acc_frag<DT>(s, 0);
+              df[1] = acc_frag<DT>(s, 1);
+            }
+          } else {
+            constexpr int j = i - 2 * DC - ND;
+            dk[j % DB] = mma(only_finite<DT>(f, MASK && bad_q), df[j / DB], dk[j % DB]);
+          }
+        });
+      };
+      // A tile of rows, of which this wave's begin at row and in LDS at `tile`.  Rows past
+      // the end are zeros with a probability of zero; with a bias they are masked (a
+      // table may hold infinities that no pair needs).
+      const auto attend = [&](int row, int tile, const float* stat) {
+        uint32_t rl = row_lane + tile, cl = col_lane + tile;
 #pragma unroll 1
-        for (int b = 0; b < SB; ++b) {
-          const uint32_t rl = row_lane + tile + 32 * b * T::ROW_BYTES;
-          const uint32_t cl = col_lane + tile + 32 * b * T::ROW_BYTES;
-          const int r0 = row + 32 * b;
-          if (!WHOLE && (r0 + 32 <= mine || r0 >= rows)) continue;
-          if constexpr (WHOLE) {
-            constexpr int ND = 2 * DB;
-            // fragments in the order of use: rows of q, rows of g_o, columns of g_o, of q
-            const auto read = [&](auto step) {
-            constexpr int i = decltype(step)::value;
-              if constexpr (i < 2 * DC) {
-                return T::row_frag(rl, i < DC ? 0 : F::KEYS, i % DC);
-              } else {
-                constexpr int j = (i - 2 * DC) % ND;
-                return T::col_frag(cl, (i < 2 * DC + ND ? F::KEYS : 0) + 16 * (j / DB), j % DB);
-              }
-            };
-            Frag<DT> pf[2], df[2];
-            f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
-            f32x4 lse[4], del[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float* p = stat + 32 * b + 8 * q + 4 * half;
-              lse[q] = *reinterpret_cast<const f32x4*>(p);
-              del[q] = *reinterpret_cast<const f32x4*>(p + F::KEYS);
+        for (int b = 0; b < F::BLOCKS && row < rows; ++b) {
+          if (row >= most && (!BIAS || row + 32 <= rows)) {
+            block(No(), row, rl, cl, stat, 0, 0);
+          } else if (row + 32 > mine) {
+            uint32_t bad_q = 0, bad_g = 0;
+            if (g.causal) {
+              bad_q = rows_not_finite<DT, DP>(rl, 0);
+              bad_g = rows_not_finite<DT, DP>(rl, F::KEYS);
             }
-            steps<DT, 2 * (DC + ND)>(read, [&](auto step, const Frag<DT>& f) {
-              constexpr int i = decltype(step)::value;
-              if constexpr (i < DC) {
-                s = mma(f, kf[i], s);
-                if constexpr (BIAS) {
-                  if constexpr (i == DC - 1) {
-                    const int dist = wkey - (r0 + off);
-                    add_bias<true>(g, line, s, dist - 31, dist + 31, key - (r0 + off) - 4 * half);
-                  }
-                }
-              } else if constexpr (i < 2 * DC) {
-                dp = mma(f, vf[i - DC], dp);
-                constexpr int j = i - DC;
-#pragma unroll
-                for (int r = beside(j, DC, 16); r < beside(j + 1, DC, 16); ++r) {
-                  const float ls = lse[r / 4][r % 4];
-                  s[r] = exp2_fast(BIAS ? s[r] - ls : __builtin_fmaf(s[r], g.c, -ls));
-                }
-                if constexpr (j == DC - 1) {
-                  pf[0] = acc_frag<DT>(s, 0);
-                  pf[1] = acc_frag<DT>(s, 1);
-                }
-              } else if constexpr (i < 2 * DC + ND) {
-                constexpr int j = i - 2 * DC;
-                dv[j % DB] = mma(f, pf[j / DB], dv[j % DB]);
-#pragma unroll
-                for (int r = beside(j, ND, 16); r < beside(j + 1, ND, 16); ++r)
-                  s[r] *= dp[r] - del[r / 4][r % 4];
-                if constexpr (j == ND - 1) {
-                  df[0] = acc_frag<DT>(s, 0);
-                  df[1] = acc_frag<DT>(s, 1);
-                }
-              } else {
-                constexpr int j = i - 2 * DC - ND;
-                dk[j % DB] = mma(f, df[j / DB], dk[j % DB]);
-              }
-            });
-            continue;
+            block(Yes(), row, rl, cl, stat, bad_q, bad_g);
           }
-          f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
-#pragma unroll
-          for (int c = 0; c < DC; ++c) {
-            s = mma(T::row_frag(rl, 0, c), kf[c], s);
-            dp = mma(T::row_frag(rl, F::KEYS, c), vf[c], dp);
-          }
-          if constexpr (BIAS) {
-            const int dist = wkey - (r0 + off);
-            add_bias<true>(g, line, s, dist - 31, dist + 31, key - (r0 + off) - 4 * half);
-          }
-          f32x16 ds;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float4 lse = *reinterpret_cast<const float4*>(stat + 32 * b + 8 * q + 4 * half);
-            const float4 del =
-                *reinterpret_cast<const float4*>(stat + F::KEYS + 32 * b + 8 * q + 4 * half);
-            const float ls[4] = {lse.x, lse.y, lse.z, lse.w};
-            const float de[4] = {del.x, del.y, del.z, del.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = 4 * q + i;
-              s[r] = exp2_fast(BIAS ? s[r] - ls[i] : __builtin_fmaf(s[r], g.c, -ls[i]));
-              ds[r] = s[r] * (dp[r] - de[i]);
-            }
-          }
-          const int low = sees - r0, high = valid ? rows - r0 : 0;
-          if (!WHOLE) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const int i = acc_row(r) + 4 * half;
-              if (i < low || i >= high) s[r] = ds[r] = 0.f;
-            }
-          }
-          uint32_t bad_q = 0, bad_g = 0;
-          if (!WHOLE && g.causal) {
-            bad_q = rows_not_finite<DT, DP>(rl, 0);
-            bad_g = rows_not_finite<DT, DP>(rl, F::KEYS);
-          }
-          if (!WHOLE && (bad_q | bad_g)) {
-            const uint32_t seen = bit_range(low, high);
-            if (bad_q & seen) poison_k = __builtin_nanf("");
-            if (bad_g & seen) poison_v = __builtin_nanf("");
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const Frag<DT> pf = acc_frag<DT>(s, c), df = acc_frag<DT>(ds, c);
-#pragma unroll
-              for (int d = 0; d < DB; ++d) {
-                dv[d] = mma(finite<DT>(T::col_frag(cl, F::KEYS + 16 * c, d)), pf, dv[d]);
-                dk[d] = mma(finite<DT>(T::col_frag(cl, 16 * c, d)), df, dk[d]);
-              }
-            }
-            continue;
-          }
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const Frag<DT> pf = acc_frag<DT>(s, c), df = acc_frag<DT>(ds, c);
-#pragma unroll
-            for (int d = 0; d < DB; ++d) {
-              dv[d] = mma(T::col_frag(cl, F::KEYS + 16 * c, d), pf, dv[d]);
-              dk[d] = mma(T::col_frag(cl, 16 * c, d), df, dk[d]);
-            }
-          }
+          rl += 32 * T::ROW_BYTES;
+          cl += 32 * T::ROW_BYTES;
+          stat += 32;
+          row += 32;
         }
       };
 
@@ -1036,20 +971,31 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
           sq.issue(qb + tok * qt, rows - row, g.D, at);
           sg.issue(gb + tok * gt, rows - row, g.D, at + F::TILE_BYTES);
         };
-        if (begin < rows) fetch(begin, 0);
+        if (F::BUFS == 2 && begin < rows) fetch(begin, 0);
         int buf = 0;
-        for (int row = begin; row < rows; row += F::KEYS, buf ^= 1) {
+        for (int row = begin; row < rows; row += F::KEYS, buf ^= F::BUFS - 1) {
+          if (F::BUFS == 1) {
+            __syncthreads();
+            fetch(row, 0);
+          }
           float* const stat = stats + buf * 2 * F::KEYS;
           if (threadIdx.x < F::KEYS) st = st == -kInf ? kInf : st * kLog2e;  // no key: P = 0
           if (threadIdx.x < 2 * F::KEYS) stat[threadIdx.x] = st;
           feed_wait();
-          if (row + F::KEYS < rows) fetch(row + F::KEYS, buf ^ 1);
-          if (row + F::KEYS <= mine) continue;
-          if (row >= most && row + F::KEYS <= rows && wkey + 32 <= nk)
-            attend(Whole(), row, buf * 2 * F::TILE_BYTES, stat);
-          else
-            attend(Masked(), row, buf * 2 * F::TILE_BYTES, stat);
+          if (F::BUFS == 2 && row + F::KEYS < rows) fetch(row + F::KEYS, buf ^ 1);
+          const int skip = FEW ? 32 * wave : 0;
+          attend(row + skip, buf * 2 * F::TILE_BYTES + skip * T::ROW_BYTES, stat + skip);
         }
+      }
+      if constexpr (FEW) {
+        const auto& z = *again<AttnBwd>();
+        const auto out = [&](const auto& t, int i) -> char* {
+          const int k = (int)tile * F::OWN + i;
+          return k < nk ? row_at<DT>(t, (int64_t)k0 + k, kvh) : nullptr;
+        };
+        join_waves<DT, DP>(lds, dv, poison_v, 1.f, z.g.D, [&](int i) { return out(z.g_v, i); });
+        join_waves<DT, DP>(lds, dk, poison_k, z.g.scale, z.g.D, [&](int i) { return out(z.g_k, i); });
+        continue;
       }
       if (valid) {
         const auto& z = *again<AttnBwd>();
@@ -1138,24 +1084,38 @@ hipError_t launch_attention_forward<HLQ_ATTN_D>(const AttnFwd& a, int dtype, boo
 }
 
 template <>
-hipError_t launch_attention_backward_q<HLQ_ATTN_D>(const AttnBwd& a, int dtype, hipStream_t s) {
+hipError_t launch_attention_backward_q<HLQ_ATTN_D>(const AttnBwd& a, int dtype, bool few,
+                                                   hipStream_t s) {
   const bool vec = a.q.vec && a.k.vec && a.v.vec && a.o.vec && a.g_o.vec;
+  const int extra = bias_bytes(a.g, 5) + (a.g.bias.table ? (4 * SKEW_SIZE + 8) * 4 : 0);
   return choose(dtype, a.g.bias.table, vec, [&](auto t, auto b, auto v) {
     constexpr int DT = decltype(t)::value, DP = HLQ_ATTN_D;
-    return launch_items(k_attention_backward_q<DT, DP, decltype(b)::value, decltype(v)::value>, a,
-                        BwdShape<DT, DP>::LDS + bias_bytes(a.g, 5) +
-                            (a.g.bias.table ? (4 * SKEW_SIZE + 8) * 4 : 0), a.g.start_q != nullptr, s);
+    constexpr bool BIAS = decltype(b)::value, VEC = decltype(v)::value;
+    const bool gaps = a.g.start_q != nullptr;
+    if (few)
+      return launch_items(k_attention_backward_q<DT, DP, BIAS, true, VEC>, a,
+                          BwdShape<DT, DP, true, BIAS>::LDS + extra, gaps, s);
+    return launch_items(k_attention_backward_q<DT, DP, BIAS, false, VEC>, a,
+                        BwdShape<DT, DP, false, BIAS>::LDS + extra, gaps, s);
   });
 }
 
 template <>
-hipError_t launch_attention_backward_kv<HLQ_ATTN_D>(const AttnBwd& a, int dtype, hipStream_t s) {
+hipError_t launch_attention_backward_kv<HLQ_ATTN_D>(const AttnBwd& a, int dtype, bool few,
+                                                    hipStream_t s) {
   const bool vec = a.q.vec && a.k.vec && a.v.vec && a.g_o.vec;
   return choose(dtype, a.g.bias.table, vec, [&](auto t, auto b, auto v) {
     constexpr int DT = decltype(t)::value, DP = HLQ_ATTN_D;
-    return launch_items(k_attention_backward_kv<DT, DP, decltype(b)::value, decltype(v)::value>, a,
-                        BwdShape<DT, DP>::LDS + 16 * BwdShape<DT, DP>::KEYS + bias_bytes(a.g, 1),
-                        a.g.start_k != nullptr, s);
+    constexpr bool BIAS = decltype(b)::value, VEC = decltype(v)::value;
+    const bool gaps = a.g.start_k != nullptr;
+    const int extra = bias_bytes(a.g, 1);
+    if (few)
+      return launch_items(
+          k_attention_backward_kv<DT, DP, BIAS, true, VEC>, a,
+          BwdShape<DT, DP, true>::LDS + 16 * BwdShape<DT, DP, true>::KEYS + extra, gaps, s);
+    return launch_items(
+        k_attention_backward_kv<DT, DP, BIAS, false, VEC>, a,
+        BwdShape<DT, DP, false>::LDS + 16 * BwdShape<DT, DP, false>::KEYS + extra, gaps, s);
   });
 }
 

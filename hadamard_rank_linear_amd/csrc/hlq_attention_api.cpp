@@ -156,17 +156,26 @@ struct FwdPlan {
   int64_t tiles, units, splits;
 };
 
-// Few rows leave most of the chip idle if a workgroup takes all keys of its rows;
-// their keys are shared out until there are about two workgroups a CU, with 256
-// keys each at least.
+// Tiles of 128 rows (or keys) that leave compute units without work are cut into
+// four, the waves of a workgroup sharing the other side.
+constexpr int64_t kUnits = 256;
+bool few_tiles(int64_t rows, int64_t units) {
+  return rows <= hlq::ATTN_FEW || (rows + hlq::ATTN_ROWS - 1) / hlq::ATTN_ROWS * units < kUnits;
+}
+int64_t tiles_of(int64_t rows, bool few) {
+  const int per = few ? hlq::ATTN_FEW : hlq::ATTN_ROWS;
+  return (rows + per - 1) / per;
+}
+
+// If that is too few still, the keys are shared out until there are about two
+// workgroups a CU, with 256 keys each at least.
 FwdPlan plan_forward(const hlq_attention* a) {
   const int shared = a->bias ? 1 : a->heads / a->kv_heads;
   const int64_t rows = expected(a, a->queries) * shared;
   FwdPlan p;
-  p.few = rows <= hlq::ATTN_FEW;
-  const int per = p.few ? hlq::ATTN_FEW : hlq::ATTN_ROWS;
-  p.tiles = (rows + per - 1) / per;
   p.units = a->sequences * (a->heads / shared);
+  p.few = few_tiles(rows, p.units);
+  p.tiles = tiles_of(rows, p.few);
   const int64_t keys = a->keys / a->sequences, groups = p.tiles * p.units;
   const int64_t splits = std::min<int64_t>((512 + groups - 1) / groups, keys / 256);
   p.splits = std::max<int64_t>(1, std::min<int64_t>(splits, 64));
@@ -179,12 +188,15 @@ size_t forward_bytes(const hlq_attention* a, const FwdPlan& p) {
 }
 
 // The gradient of q's items, by which a bias's partial sums are laid out.
-AttnShape backward_q_shape(const hlq_attention* a) {
+AttnShape backward_q_shape(const hlq_attention* a, bool* few) {
   AttnShape g = {};
   const int shared = a->bias ? 1 : a->heads / a->kv_heads;
   g.causal = a->causal != 0;
   const int64_t rows = expected(a, a->queries) * shared;
-  number(g, (rows + hlq::ATTN_ROWS - 1) / hlq::ATTN_ROWS, a->sequences * (a->heads / shared), 1);
+  const int64_t units = a->sequences * (a->heads / shared);
+  // the sums of a bias's gradient leave no room for 128 rows of 512 bytes
+  *few = few_tiles(rows, units) && !(a->bias && a->dtype == HLQ_F32 && a->head_dim > 64);
+  number(g, tiles_of(rows, *few), units, 1);
   return g;
 }
 
@@ -272,8 +284,9 @@ hlq_status hlq_attention_forward(const hlq_attention* a, const hlq_tokens* q, co
 size_t hlq_attention_backward_workspace_size(const hlq_attention* a) {
   if (check_shape(a) != HLQ_OK) return 0;
   size_t bytes = delta_bytes(a);
+  bool few;
   if (a->bias)
-    bytes += (size_t)backward_q_shape(a).tiles * a->sequences * a->heads * a->buckets * 4;
+    bytes += (size_t)backward_q_shape(a, &few).tiles * a->sequences * a->heads * a->buckets * 4;
   return bytes;
 }
 
@@ -310,11 +323,12 @@ hlq_status hlq_attention_backward(const hlq_attention* a, const hlq_tokens* g_o,
   b.delta = static_cast<float*>(workspace);
   b.g_line = reinterpret_cast<float*>(static_cast<char*>(workspace) + delta_bytes(a));
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const AttnShape n = backward_q_shape(a);
+  bool few;
+  const AttnShape n = backward_q_shape(a, &few);
   number(b.g, n.tiles, n.units, 1);
   // with a bias also for no queries: the table's gradient is then zero
   if (a->queries || a->bias)
-    HLQ_TRY(HLQ_BY_SIZE(a->head_dim, launch_attention_backward_q, b, a->dtype, s));
+    HLQ_TRY(HLQ_BY_SIZE(a->head_dim, launch_attention_backward_q, b, a->dtype, few, s));
   if (a->bias)
     HLQ_TRY(hlq::launch_attention_bias(b.g_line, a->sequences, b.g.tiles, a->heads, a->buckets,
                                        a->bias_dtype, g_bias, s));
@@ -325,9 +339,10 @@ hlq_status hlq_attention_backward(const hlq_attention* a, const hlq_tokens* g_o,
     const int64_t far = std::max(b.q.head, b.g_o.head) * (int64_t)esize(a->dtype) * shared;
     if ((shared & (shared - 1)) || shared > hlq::ATTN_PACK || far >= (int64_t(1) << 30)) b.g.pack = 1;
     b.g.groups = shared / b.g.pack;
-    number(b.g, (expected(a, a->keys) + hlq::ATTN_ROWS - 1) / hlq::ATTN_ROWS,
-           a->sequences * a->kv_heads, 1);
-    HLQ_TRY(HLQ_BY_SIZE(a->head_dim, launch_attention_backward_kv, b, a->dtype, s));
+    const int64_t keys = expected(a, a->keys), units = a->sequences * a->kv_heads;
+    few = few_tiles(keys, units);
+    number(b.g, tiles_of(keys, few), units, 1);
+    HLQ_TRY(HLQ_BY_SIZE(a->head_dim, launch_attention_backward_kv, b, a->dtype, few, s));
   }
   return HLQ_OK;
 }

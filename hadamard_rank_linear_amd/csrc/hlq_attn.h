@@ -94,9 +94,10 @@ __device__ __forceinline__ uint32_t not_finite(const Frag<DT>& f) {
   for (unsigned i = 0; i < sizeof f / 4; ++i) bad |= not_finite<DT>(w[i]);
   return bad;
 }
-// Those values set to zero.
+// f with those values set to zero if `clean`, the same in all lanes.
 template <int DT>
-__device__ __forceinline__ Frag<DT> finite(const Frag<DT>& f) {
+__device__ __forceinline__ Frag<DT> only_finite(const Frag<DT>& f, bool clean) {
+  if (!clean) return f;
   uint32_t w[sizeof f / 4];
   __builtin_memcpy(w, &f, sizeof f);
 #pragma unroll

@@ -327,9 +327,9 @@ constexpr int ATTN_PACK = 8;    // heads packed into the rows that go through LD
 template <int DP>
 hipError_t launch_attention_forward(const AttnFwd& a, int dtype, bool few, hipStream_t s);
 template <int DP>
-hipError_t launch_attention_backward_q(const AttnBwd& a, int dtype, hipStream_t s);
+hipError_t launch_attention_backward_q(const AttnBwd& a, int dtype, bool few, hipStream_t s);
 template <int DP>
-hipError_t launch_attention_backward_kv(const AttnBwd& a, int dtype, hipStream_t s);
+hipError_t launch_attention_backward_kv(const AttnBwd& a, int dtype, bool few, hipStream_t s);
 hipError_t launch_attention_join(const AttnFwd& a, int dtype, hipStream_t s);
 // g_bias [buckets][heads] of param_dt from the partial sums
 hipError_t launch_attention_bias(const float* part, int64_t S, int64_t tiles, int heads,
