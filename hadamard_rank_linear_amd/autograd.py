@@ -15,7 +15,10 @@ flattened into tokens.  No bias (its gradient is not part of the method).
 
 Around it, the operators of a training step in the same form: the layer norm
 with its residual addition (:class:`HLQLayerNorm`), token log probabilities,
-the policy and preference losses on them, and the clipping of gradients.
+the policy and preference losses on them, and the clipping of gradients; and
+those of an attention block: attention over packed sequences with a relative
+position bias (:class:`HLQSelfAttention` between two HLQ linear layers), and
+dropout with the residual addition (:class:`HLQDropout`).
 """
 from __future__ import annotations
 
@@ -219,3 +222,150 @@ def hlq_clip_grad_norm_(parameters, max_norm, norm_kind=hlq.HLQ_NORM_L2):
         parameters = [parameters]
     return hlq.hlq_clip_grad_norm([p.grad for p in parameters if p.grad is not None], max_norm,
                                   norm_kind)
+
+
+def _rows_dense(t):
+    return t if t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
+
+
+class HLQAttentionFunction(torch.autograd.Function):
+    """Attention over packed sequences; gradients of q, k, v and the bias table."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, start, start_k, bias, causal, scale, max_distance, bidirectional,
+                max_len):
+        q, k, v = _rows_dense(q), _rows_dense(k), _rows_dense(v)
+        bias = None if bias is None else bias.contiguous()
+        ctx.kw = dict(causal=causal, scale=scale, max_distance=max_distance,
+                      bidirectional=bidirectional, max_len=max_len)
+        o, lse = hlq.hlq_attention_forward(q, k, v, start, start_k, bias=bias, **ctx.kw)
+        ctx.save_for_backward(q, k, v, o, lse, start, start_k, bias)
+        return o
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_o):
+        q, k, v, o, lse, start, start_k, bias = ctx.saved_tensors
+        g_q, g_k, g_v, g_bias = hlq.hlq_attention_backward(
+            _rows_dense(g_o), q, k, v, o, lse, start, start_k, bias=bias, **ctx.kw)
+        return g_q, g_k, g_v, None, None, g_bias, *(None,) * 5
+
+
+def hlq_attention(q, k, v, start=None, start_k=None, causal=False, scale=None, bias=None,
+                  max_distance=128, bidirectional=None, max_len=0):
+    """Differentiable :func:`hlq.hlq_attention_forward`: o [queries, heads, D]."""
+    return HLQAttentionFunction.apply(q, k, v, start, start_k, bias, causal, scale, max_distance,
+                                      bidirectional, max_len)
+
+
+class HLQPackedAttentionFunction(torch.autograd.Function):
+    """Self-attention on what a qkv layer writes, [tokens, heads + 2 kv_heads, D];
+    the gradient comes as one tensor, no sum of slices' gradients."""
+
+    @staticmethod
+    def forward(ctx, qkv, heads, start, bias, causal, scale, max_distance, bidirectional, max_len):
+        kv = (qkv.shape[1] - heads) // 2
+        if qkv.dim() != 3 or kv < 1 or qkv.shape[1] != heads + 2 * kv:
+            raise ValueError("qkv must be [tokens, heads + 2 kv_heads, D]")
+        qkv = _rows_dense(qkv)
+        bias = None if bias is None else bias.contiguous()
+        ctx.cuts = (heads, kv, kv)
+        ctx.kw = dict(causal=causal, scale=scale, max_distance=max_distance,
+                      bidirectional=bidirectional, max_len=max_len)
+        o, lse = hlq.hlq_attention_forward(*qkv.split(ctx.cuts, 1), start, bias=bias, **ctx.kw)
+        ctx.save_for_backward(qkv, o, lse, start, bias)
+        return o
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_o):
+        qkv, o, lse, start, bias = ctx.saved_tensors
+        g_qkv = torch.empty(qkv.shape, dtype=qkv.dtype, device=qkv.device)
+        g_q, g_k, g_v = g_qkv.split(ctx.cuts, 1)
+        g_bias = hlq.hlq_attention_backward(
+            _rows_dense(g_o), *qkv.split(ctx.cuts, 1), o, lse, start, bias=bias, **ctx.kw, g_q=g_q,
+            g_k=g_k, g_v=g_v)[3]
+        return g_qkv, None, None, g_bias, *(None,) * 5
+
+
+def hlq_packed_attention(qkv, heads, start=None, causal=False, scale=None, bias=None,
+                         max_distance=128, bidirectional=None, max_len=0):
+    """Differentiable self-attention on the slices of ``qkv`` [tokens, heads + 2
+    kv_heads, D]: o [tokens, heads, D]."""
+    return HLQPackedAttentionFunction.apply(qkv, heads, start, bias, causal, scale, max_distance,
+                                            bidirectional, max_len)
+
+
+class HLQSelfAttention(torch.nn.Module):
+    """Self-attention over packed sequences between two :class:`HLQLinear` layers:
+    x [tokens, features] -> [tokens, features].  ``buckets`` of a learned
+    relative position bias (0: none).  The token count has to suit the linear
+    layers (a multiple of ``block``); sequences end where ``start`` says."""
+
+    def __init__(self, features, heads, kv_heads=None, causal=False, buckets=0, max_distance=128,
+                 block=16, rank=8, device=None, dtype=None):
+        super().__init__()
+        kv_heads = heads if kv_heads is None else kv_heads
+        if features % heads or heads % kv_heads:
+            raise ValueError("features must be a multiple of heads, heads of kv_heads")
+        self.heads, self.kv_heads, self.dim = heads, kv_heads, features // heads
+        self.causal, self.max_distance = causal, max_distance
+        self.qkv = HLQLinear(features, (heads + 2 * kv_heads) * self.dim, block, rank, device=device,
+                             dtype=dtype)
+        self.out = HLQLinear(features, features, block, rank, device=device, dtype=dtype)
+        self.bias = torch.nn.Parameter(torch.zeros((buckets, heads), device=device)) \
+            if buckets else None
+
+    def forward(self, x, start=None, max_len=0):
+        qkv = self.qkv(x).view(x.shape[0], self.heads + 2 * self.kv_heads, self.dim)
+        o = hlq_packed_attention(qkv, self.heads, start, self.causal, bias=self.bias,
+                                 max_distance=self.max_distance, max_len=max_len)
+        return self.out(o.view(x.shape[0], -1))
+
+    def extra_repr(self):
+        return (f"heads={self.heads}, kv_heads={self.kv_heads}, dim={self.dim}, "
+                f"causal={self.causal}, buckets={0 if self.bias is None else len(self.bias)}")
+
+
+class HLQDropoutFunction(torch.autograd.Function):
+    """residual + dropout(x); the backward pass draws the mask again."""
+
+    @staticmethod
+    def forward(ctx, x, residual, p, seed, site):
+        ctx.p, ctx.site, ctx.with_residual = p, site, residual is not None
+        ctx.save_for_backward(seed)
+        return hlq.hlq_dropout_forward(x.contiguous(), p, seed, site,
+                                       None if residual is None else residual.contiguous())
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_y):
+        seed, = ctx.saved_tensors
+        g_x = hlq.hlq_dropout_backward(g_y.contiguous(), ctx.p, seed, ctx.site) \
+            if ctx.needs_input_grad[0] else None
+        return g_x, (g_y if ctx.with_residual else None), None, None, None
+
+
+def hlq_dropout(x, p, seed, site=0, residual=None):
+    """residual + dropout(x).  ``seed`` (int64 [2] on the GPU) must not move on
+    before the backward pass has drawn the mask again: autograd raises if it was
+    changed in place."""
+    return HLQDropoutFunction.apply(x, residual, p, seed, site)
+
+
+class HLQDropout(torch.nn.Module):
+    """Dropout in front of a residual addition: called with (x, seed, residual).
+    ``site`` tells the places of a model apart that share a seed.  In evaluation
+    nothing is dropped."""
+
+    def __init__(self, p=0.1, site=0):
+        super().__init__()
+        self.p, self.site = p, site
+
+    def forward(self, x, seed, residual=None):
+        if self.training:
+            return hlq_dropout(x, self.p, seed, self.site, residual)
+        return x if residual is None else residual + x
+
+    def extra_repr(self):
+        return f"p={self.p}, site={self.site}"

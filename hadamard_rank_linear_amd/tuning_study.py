@@ -3,8 +3,10 @@ train with the HLQ/HOT backward, with every operator of the step from this
 library: ``python -m hadamard_rank_linear_amd.tuning_study``.
 
 The model predicts a token from the one before it: embedding, one MLP block
-with its layer norm and residual addition, a last norm and a head.  Synthetic
-tasks with a known direction:
+with its layer norm and residual addition, a last norm and a head.  With
+``--heads`` an attention block comes before the MLP's: causal attention within
+each sequence with a relative position bias, and dropout in front of the residual
+addition.  Synthetic tasks with a known direction:
 
 - preference: in each pair the chosen sequence counts up by one, the rejected
   one is random; the mean margin over the reference model has to grow;
@@ -18,14 +20,17 @@ import argparse
 import torch
 
 from . import hlq
-from .autograd import (HLQLayerNorm, HLQLinear, hlq_clip_grad_norm_, hlq_preference_loss,
-                       hlq_token_logprob)
+from .autograd import (HLQDropout, HLQLayerNorm, HLQLinear, HLQSelfAttention, hlq_clip_grad_norm_,
+                       hlq_preference_loss, hlq_token_logprob)
 
 
 class TokenModel(torch.nn.Module):
-    """Logits [T, vocab] of the next token for tokens [T] (T a multiple of 16)."""
+    """Logits [T, vocab] of the next token for tokens [T] (T a multiple of 16).
+    With ``heads``, packed sequences of the bounds ``start``; ``seed`` moves on by
+    one step after each training step."""
 
-    def __init__(self, vocab=512, width=256, inner=512, device="cuda", dtype=torch.bfloat16):
+    def __init__(self, vocab=512, width=256, inner=512, device="cuda", dtype=torch.bfloat16,
+                 heads=0, dropout=0.1):
         super().__init__()
         self.embed = torch.nn.Parameter(
             torch.randn(vocab, width, device=device).mul_(0.5).to(dtype))
@@ -34,9 +39,18 @@ class TokenModel(torch.nn.Module):
         self.down = HLQLinear(inner, width, device=device, dtype=dtype)
         self.last = HLQLayerNorm(width, device=device)
         self.head = HLQLinear(width, vocab, device=device, dtype=dtype)
+        self.attention = None
+        if heads:
+            self.first = HLQLayerNorm(width, device=device)
+            self.attention = HLQSelfAttention(width, heads, max(1, heads // 2), causal=True,
+                                              buckets=16, max_distance=64, device=device, dtype=dtype)
+            self.drop = HLQDropout(dropout, site=1)
+            self.register_buffer("seed", torch.tensor([1234, 0], device=device))
 
-    def forward(self, tokens):
+    def forward(self, tokens, start=None):
         x = self.embed[tokens]
+        if self.attention is not None:
+            x = self.drop(self.attention(self.first(x), start), self.seed, residual=x)
         f = self.down(torch.nn.functional.gelu(self.up(self.norm(x))))
         y, _ = self.last(f, residual=x)
         return self.head(y)
@@ -69,17 +83,20 @@ def _update(model, lr, max_norm):
             if p.grad is not None:
                 p.add_(p.grad, alpha=-lr)
                 p.grad = None
+        if model.attention is not None:
+            model.seed[1] += 1
     return norm
 
 
-def tune_preferences(steps=20, pairs=16, length=32, vocab=512, lr=0.2, beta=0.1, seed=0, log=None):
+def tune_preferences(steps=20, pairs=16, length=32, vocab=512, lr=0.2, beta=0.1, seed=0, log=None,
+                     heads=0):
     """Mean margin before and after ``steps`` steps of preference tuning."""
     torch.manual_seed(seed)
-    model = TokenModel(vocab)
+    model = TokenModel(vocab, heads=heads)
     margins = []
     for step in range(steps):
         inputs, targets, start = preference_pairs(pairs, length, vocab, seed)
-        logits = model(inputs)
+        logits = model(inputs, start)
         logprob = hlq_token_logprob(logits, targets)
         if step == 0:
             ref = logprob.detach().clone()
@@ -94,23 +111,25 @@ def tune_preferences(steps=20, pairs=16, length=32, vocab=512, lr=0.2, beta=0.1,
     return margins[0].item(), margins[-1].item()
 
 
-def tune_policy(steps=20, tokens=1024, vocab=512, lr=0.5, updates=2, seed=0, log=None):
-    """Mean reward of the first and of the last batch of ``steps``."""
+def tune_policy(steps=20, tokens=1024, vocab=512, lr=0.5, updates=2, seed=0, log=None, heads=0):
+    """Mean reward of the first and of the last batch of ``steps``.  With
+    ``heads`` the tokens are sequences of 16."""
     torch.manual_seed(seed)
     g = _generator(seed)
-    model = TokenModel(vocab)
+    model = TokenModel(vocab, heads=heads)
+    start = torch.arange(tokens // 16 + 1, device="cuda") * 16
     rewards = []
     for step in range(steps):
         inputs = torch.randint(0, vocab, (tokens,), generator=g, device="cuda")
         with torch.no_grad():
-            logits = model(inputs)
+            logits = model(inputs, start)
             actions = torch.multinomial(torch.softmax(logits.float(), -1), 1, generator=g)[:, 0]
             old = hlq.hlq_token_logprob_forward(logits, actions)[0]
         reward = (actions % 2 == 0).float()
         advantage = (reward - reward.mean()) / (reward.std() + 1e-6)
         weight = torch.full_like(reward, 1.0 / tokens)
         for _ in range(updates):
-            logits = model(inputs)
+            logits = model(inputs, start)
             sums, _, g_x = hlq.hlq_policy_loss_logits(logits.detach(), actions, old, advantage,
                                                       weight, ref_logprob=old, clip_high=0.28,
                                                       kl_coef=0.01)
@@ -128,10 +147,11 @@ def main():
     p = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     p.add_argument("--steps", type=int, default=20)
     p.add_argument("--seed", type=int, default=0)
+    p.add_argument("--heads", type=int, default=0, help="query heads of an attention block (0: none)")
     args = p.parse_args()
     say = lambda m: print(m, flush=True)
-    a, b = tune_preferences(args.steps, seed=args.seed, log=say)
-    c, d = tune_policy(args.steps, seed=args.seed, log=say)
+    a, b = tune_preferences(args.steps, seed=args.seed, log=say, heads=args.heads)
+    c, d = tune_policy(args.steps, seed=args.seed, log=say, heads=args.heads)
     say(f"mean margin {a:+.4f} -> {b:+.4f}, mean reward {c:.3f} -> {d:.3f}")
 
 
