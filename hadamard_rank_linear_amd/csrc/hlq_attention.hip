@@ -161,8 +161,9 @@ struct FwdShape {
   static constexpr int MINE = FEW ? 32 : KEYS;                // of them a wave's
   static constexpr int TILE_BYTES = KEYS * T::ROW_BYTES;
   static constexpr int JOIN_BYTES = FEW ? 4 * DP * 33 * 4 + 4 * 32 * 8 : 0;
-  // buffers of a tile of keys and of values: one where two do not fit the LDS
-  static constexpr int BUFS = TILE_BYTES > 32768 ? 1 : 2;
+  // buffers of a tile of keys and of values: one where two leave no room for a second
+  // workgroup (or do not fit the LDS)
+  static constexpr int BUFS = TILE_BYTES > 16384 ? 1 : 2;
   static constexpr int LDS =
       2 * BUFS * TILE_BYTES > JOIN_BYTES ? 2 * BUFS * TILE_BYTES : JOIN_BYTES;
 };
@@ -237,8 +238,9 @@ __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !FEW ? 3 : 2) void k
       }
       int from = 0;
       if (g.splits > 1) {
-        const int share = ((end + F::KEYS - 1) / F::KEYS + g.splits - 1) / g.splits * F::KEYS;
-        from = min(end, split * share);
+        const int share =
+            max(g.share, (int)(((end + F::KEYS - 1) / F::KEYS + g.splits - 1) / g.splits) * F::KEYS);
+        from = (int)min((int64_t)end, (int64_t)split * share);
         end = min(end, from + share);
       }
       const int limit = min(me.limit, end);

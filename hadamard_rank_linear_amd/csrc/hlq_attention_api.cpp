@@ -153,7 +153,7 @@ void number(AttnShape& g, int64_t tiles, int64_t units, int64_t splits) {
 
 struct FwdPlan {
   bool few;
-  int64_t tiles, units, splits;
+  int64_t tiles, units, splits, share;
 };
 
 // Tiles of 128 rows (or keys) that leave compute units without work are cut into
@@ -167,8 +167,9 @@ int64_t tiles_of(int64_t rows, bool few) {
   return (rows + per - 1) / per;
 }
 
-// If that is too few still, the keys are shared out until there are about two
-// workgroups a CU, with 256 keys each at least.
+// If that is too few still, the keys are shared out: in shares of equal length, of
+// which all sequences together have about two a CU, 256 keys each at least.  As many
+// as the longest sequence is expected to need (at most 64); a longer one's are longer.
 FwdPlan plan_forward(const hlq_attention* a) {
   const int shared = a->bias ? 1 : a->heads / a->kv_heads;
   const int64_t rows = expected(a, a->queries) * shared;
@@ -176,9 +177,15 @@ FwdPlan plan_forward(const hlq_attention* a) {
   p.units = a->sequences * (a->heads / shared);
   p.few = few_tiles(rows, p.units);
   p.tiles = tiles_of(rows, p.few);
-  const int64_t keys = a->keys / a->sequences, groups = p.tiles * p.units;
-  const int64_t splits = std::min<int64_t>((512 + groups - 1) / groups, keys / 256);
-  p.splits = std::max<int64_t>(1, std::min<int64_t>(splits, 64));
+  p.splits = 1;
+  p.share = 0;
+  const int64_t slots = 2 * kUnits, groups = p.tiles * p.units;
+  const int64_t mean = a->keys / a->sequences, longest = std::min(a->keys, 2 * mean);
+  if (groups >= slots || mean < 512) return p;
+  // groups < slots, so that the product of a 40-bit number is in range
+  const int64_t share = std::max<int64_t>(256, (mean * groups + slots - 1) / slots);
+  p.splits = std::min<int64_t>(64, (longest + share - 1) / share);
+  p.share = ((longest + p.splits - 1) / p.splits + 127) / 128 * 128;
   return p;
 }
 
@@ -271,6 +278,7 @@ hlq_status hlq_attention_forward(const hlq_attention* a, const hlq_tokens* q, co
   f.o = rows_of(a, o);
   f.lse = lse;
   number(f.g, p.tiles, p.units, p.splits);
+  f.g.share = (int)p.share;
   if (need) {
     f.ml = static_cast<float*>(workspace);
     f.po = f.ml + (size_t)p.splits * a->queries * a->heads * 2;

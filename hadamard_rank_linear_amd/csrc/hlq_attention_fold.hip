@@ -7,10 +7,12 @@ namespace {
 
 // A wave a row of (token, head): with (m_p, l_p) of share p in powers of two and M
 // the largest m, o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.  Lane p holds
-// share p's factor (at most 64 shares).
+// share p's factor (at most 64 shares).  The shares' sums are loaded AHEAD at a time,
+// also those that no share has written, and are not used then.
 template <int DT>
 __global__ __launch_bounds__(256) void k_attention_join(AttnFwd a) {
   typedef typename Piece<DT>::Elem E;
+  constexpr int AHEAD = 8;
   const AttnShape& g = a.g;
   const int lane = threadIdx.x & 63;
   const int64_t rows = g.Tq * g.heads;
@@ -28,11 +30,20 @@ __global__ __launch_bounds__(256) void k_attention_join(AttnFwd a) {
     const int head = (int)(r % g.heads);
     E* const o = static_cast<E*>(a.o.data) + token * a.o.token + head * a.o.head;
     for (int d = lane; d - lane < g.D; d += 64) {
+      const float* const part = a.po + r * g.D + min(d, g.D - 1);
       float v = 0.f;
-      for (int p = 0; p < g.splits; ++p) {
-        const float w = __shfl(f, p), k = __shfl(l, p);
-        // a share that has seen no key has written no sums
-        if (d < g.D && k != 0.f) v += w * a.po[(p * rows + r) * g.D + d];
+      for (int p0 = 0; p0 < g.splits; p0 += AHEAD) {
+        float x[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+          x[i] = part[min(p0 + i, (int)g.splits - 1) * rows * g.D];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          const int p = min(p0 + i, 63);
+          const float w = __shfl(f, p), k = __shfl(l, p);
+          // a share that has seen no key (or is none) has written no sums
+          if (k != 0.f) v += w * x[i];
+        }
       }
       v = total == 0.f ? 0.f : v / total;
       if (d < g.D) {

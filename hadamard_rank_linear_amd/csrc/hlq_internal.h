@@ -304,6 +304,7 @@ struct AttnShape {
   // unit's items go to one of the eight XCDs; by_tile: the first tile of every unit
   // comes before the second.
   unsigned tiles, splits, units, items;
+  int share;  // keys of a share at least, a multiple of 128
   int by_xcd, by_tile;
   unsigned launched;  // workgroups of the launch that take items
   AttnBias bias;
