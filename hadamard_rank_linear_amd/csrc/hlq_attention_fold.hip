@@ -59,19 +59,41 @@ __global__ __launch_bounds__(256) void k_attention_join(AttnFwd a) {
 }
 
 // g_bias[bucket][head]: a workgroup a head; thread t adds bucket t % buckets of
-// every 256 / buckets-th item, then one sum over the threads of a bucket.  fp64.
-__global__ __launch_bounds__(256) void k_attention_bias(const float* part, int64_t S, int64_t tiles,
-                                                        int heads, int buckets, int param_dt,
-                                                        void* g_bias) {
-  __shared__ double sm[256];
-  const int head = blockIdx.x, ways = 256 / buckets;
+// every 1024 / buckets-th item, four at a time, then one sum over the threads of a
+// bucket.  fp64, always in the same order.  A sequence's items lie together, those of
+// two sequences heads * tiles apart.
+__global__ __launch_bounds__(1024) void k_attention_bias(const float* part, int64_t S, unsigned tiles,
+                                                         int heads, int buckets, int param_dt,
+                                                         void* g_bias) {
+  __shared__ double sm[1024];
+  const int head = blockIdx.x, ways = 1024 / buckets;
   const int b = (int)threadIdx.x % buckets, way = (int)threadIdx.x / buckets;
   double v = 0.0;
-  if (way < ways)
-    for (int64_t i = way; i < S * tiles; i += ways) {
-      const int64_t item = ((i / tiles) * heads + head) * tiles + i % tiles;
-      v += part[item * buckets + b];
+  if (way < ways) {
+    const float* const mine = part + (int64_t)head * tiles * buckets + b;
+    const int64_t next = (int64_t)heads * tiles * buckets;
+    const auto at = [&](int64_t s, unsigned t) {
+      return s < S ? mine[s * next + (int64_t)t * buckets] : 0.f;
+    };
+    int64_t s = way / tiles;
+    unsigned t = way % tiles;
+    const unsigned ds = ways / tiles, dt = ways % tiles;
+    while (s < S) {
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = at(s, t);
+        s += ds;
+        t += dt;
+        if (t >= tiles) {
+          t -= tiles;
+          ++s;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v += x[i];
     }
+  }
   sm[threadIdx.x] = v;
   __syncthreads();
   if (way == 0) {
@@ -92,7 +114,7 @@ hipError_t launch_attention_join(const AttnFwd& a, int dtype, hipStream_t s) {
 
 hipError_t launch_attention_bias(const float* part, int64_t S, int64_t tiles, int heads,
                                  int buckets, int param_dt, void* g_bias, hipStream_t s) {
-  return launch(k_attention_bias, dim3((unsigned)heads), 256, s, part, S, tiles, heads, buckets,
+  return launch(k_attention_bias, dim3((unsigned)heads), 1024, s, part, S, (unsigned)tiles, heads, buckets,
                 param_dt, g_bias);
 }
 
