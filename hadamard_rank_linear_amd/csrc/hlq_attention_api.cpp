@@ -21,7 +21,7 @@ using hlq::AttnShape;
 
 constexpr int64_t kRows = int64_t(1) << 30;    // queries times heads, and keys times heads
 constexpr int64_t kStride = int64_t(1) << 40;  // elements
-// Tokens: a tile's 128 rows at this distance are within 32-bit offsets.
+// Tokens (fewer elements than this apart): a tile's 128 rows are within 32-bit offsets.
 constexpr int64_t kTokenStride = int64_t(1) << 22;
 
 bool dtype_ok(int dt) { return dt == HLQ_F32 || dt == HLQ_BF16; }
@@ -77,8 +77,8 @@ hlq_status check_rows(const hlq_attention* a, const hlq_tokens* t, int64_t token
   if (tokens == 0) return HLQ_OK;
   if (!t->data) return HLQ_ERR_NULL;
   if (!aligned(t->data, esize(a->dtype))) return HLQ_ERR_ALIGN;
-  if (t->token_stride < 0 || t->head_stride < 0 || t->token_stride >= kTokenStride ||
-      t->head_stride >= kStride)
+  if (t->token_stride < 0 || t->head_stride < 0 || (tokens > 1 && t->token_stride >= kTokenStride) ||
+      (heads > 1 && t->head_stride >= kStride))
     return HLQ_ERR_SHAPE;
   if (out) {
     const int64_t D = a->head_dim, ts = t->token_stride, hs = t->head_stride;
@@ -91,10 +91,11 @@ hlq_status check_rows(const hlq_attention* a, const hlq_tokens* t, int64_t token
   return HLQ_OK;
 }
 
-AttnRows rows_of(const hlq_attention* a, const hlq_tokens* t) {
+// The kernels' form of them: the stride of a single token, or head, is not looked at.
+AttnRows rows_of(const hlq_attention* a, const hlq_tokens* t, int64_t tokens, int heads) {
   const int64_t es = (int64_t)esize(a->dtype);
-  AttnRows r = {t->data, t->token_stride, t->head_stride, 0};
-  r.vec = aligned(t->data, 16) && t->token_stride * es % 16 == 0 && t->head_stride * es % 16 == 0 &&
+  AttnRows r = {t->data, tokens > 1 ? t->token_stride : 0, heads > 1 ? t->head_stride : 0, 0};
+  r.vec = aligned(t->data, 16) && r.token * es % 16 == 0 && r.head * es % 16 == 0 &&
           a->head_dim * es % 16 == 0;
   return r;
 }
@@ -272,10 +273,10 @@ hlq_status hlq_attention_forward(const hlq_attention* a, const hlq_tokens* q, co
   if (a->queries == 0) return HLQ_OK;
   AttnFwd f = {};
   f.g = shape_of(a);
-  f.q = rows_of(a, q);
-  f.k = rows_of(a, k);
-  f.v = rows_of(a, v);
-  f.o = rows_of(a, o);
+  f.q = rows_of(a, q, a->queries, a->heads);
+  f.k = rows_of(a, k, a->keys, a->kv_heads);
+  f.v = rows_of(a, v, a->keys, a->kv_heads);
+  f.o = rows_of(a, o, a->queries, a->heads);
   f.lse = lse;
   number(f.g, p.tiles, p.units, p.splits);
   f.g.share = (int)p.share;
@@ -319,14 +320,14 @@ hlq_status hlq_attention_backward(const hlq_attention* a, const hlq_tokens* g_o,
   if (!aligned(workspace, 16)) return HLQ_ERR_ALIGN;
   AttnBwd b = {};
   b.g = shape_of(a);
-  b.q = rows_of(a, q);
-  b.k = rows_of(a, k);
-  b.v = rows_of(a, v);
-  b.o = rows_of(a, o);
-  b.g_o = rows_of(a, g_o);
-  b.g_q = rows_of(a, g_q);
-  b.g_k = rows_of(a, g_k);
-  b.g_v = rows_of(a, g_v);
+  b.q = rows_of(a, q, a->queries, a->heads);
+  b.k = rows_of(a, k, a->keys, a->kv_heads);
+  b.v = rows_of(a, v, a->keys, a->kv_heads);
+  b.o = rows_of(a, o, a->queries, a->heads);
+  b.g_o = rows_of(a, g_o, a->queries, a->heads);
+  b.g_q = rows_of(a, g_q, a->queries, a->heads);
+  b.g_k = rows_of(a, g_k, a->keys, a->kv_heads);
+  b.g_v = rows_of(a, g_v, a->keys, a->kv_heads);
   b.lse = lse;
   b.delta = static_cast<float*>(workspace);
   b.g_line = reinterpret_cast<float*>(static_cast<char*>(workspace) + delta_bytes(a));

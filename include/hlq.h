@@ -609,8 +609,10 @@ hlq_status hlq_clip_grad_norm(const void* const* grads, void* const* outs, const
  * ------------------------------------------------------------------------ */
 
 /* A tensor [tokens][heads][head_dim], head_dim elements dense, strides in
-   elements (below 2^40, not negative): a slice of what the qkv layer wrote, or of
-   the gradient it will read.  Outputs must not overlap themselves. */
+   elements and not negative: a slice of what the qkv layer wrote, or of the
+   gradient it will read.  Tokens are less than 2^22 elements apart, heads less than
+   2^40 (a single token's or head's stride may be anything).  An input's strides may
+   be 0; outputs must not overlap themselves. */
 typedef struct hlq_tokens {
   void* data;
   int64_t token_stride, head_stride;
@@ -663,7 +665,9 @@ int hlq_relative_bucket(int distance, int buckets, int max_distance, int bidirec
  *            there are too few queries to fill the GPU: then the keys are shared out).
  * A query that sees no key, or none with a score above -inf, gets o = 0 and lse =
  * -inf.  Keys and values that a query does not see do not reach it, infinities and
- * NaN among them included.  Scores, sums and statistics are fp32; for bf16 the
+ * NaN among them included; one that it does see makes its row infinite or NaN,
+ * in elements that are not specified (none of them, if only scores of -inf come of
+ * it).  Scores, sums and statistics are fp32; for bf16 the
  * probabilities are rounded to bf16 in the product with v.
  * One launch, two with a workspace.  Errors: HLQ_ERR_NULL, HLQ_ERR_DTYPE,
  * HLQ_ERR_SHAPE, HLQ_ERR_VALUE (scale, buckets), HLQ_ERR_ALIGN,
@@ -684,6 +688,8 @@ hlq_status hlq_attention_forward(const hlq_attention* a, const hlq_tokens* q, co
  *   g_q, g_k, g_v  out, dtype;  g_bias [buckets][heads] out, bias_dtype, NULL
  *            exactly when there is no bias.
  * For bf16 P and G are rounded to bf16 in the products; g_bias sums them unrounded.
+ * Infinities and NaN reach the gradients of what they meet in a pair that is seen,
+ * in elements that are not specified, and no others.
  * Two launches, three with a bias.  No atomics: a call repeats bit for bit.
  * Errors as above.
  */

@@ -85,6 +85,24 @@ def test_attention_backward_refuses(kw, status):
     assert _backward(**kw) == status
 
 
+@pytest.mark.parametrize("name", ["q", "k", "v", "g_o"])
+def test_attention_refuses_tokens_too_far_apart(name):
+    for far in (1 << 22, 1 << 40):
+        assert _backward(**{name + "_t": far}) == SHAPE
+        if name != "g_o":
+            assert _forward(**{name + "_t": far}) == SHAPE
+    # just near enough: the next thing to refuse is the workspace
+    assert _backward(ws=None, **{name + "_t": (1 << 22) - 1}) == WORKSPACE
+
+
+def test_attention_stride_of_a_single_token_or_head_is_not_looked_at():
+    one = dict(queries=1, keys=1, sequences=1, start_k=None, ws=None)
+    far = {n + "_t": 1 << 45 for n in ("g_o", "q", "k", "v", "o", "g_q", "g_k", "g_v")}
+    assert _backward(**one, **far) == WORKSPACE
+    far = {n + "_h": 1 << 45 for n in ("g_o", "q", "k", "v", "o", "g_q", "g_k", "g_v")}
+    assert _backward(**{**one, "heads": 1, "kv_heads": 1}, **far) == WORKSPACE
+
+
 def test_attention_workspace_sizes():
     fwd = lambda **kw: h.lib_handle().hlq_attention_forward_workspace_size(ctypes.byref(_shape(**kw)))
     bwd = lambda **kw: h.lib_handle().hlq_attention_backward_workspace_size(ctypes.byref(_shape(**kw)))
