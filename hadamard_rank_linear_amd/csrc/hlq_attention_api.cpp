@@ -132,11 +132,13 @@ AttnShape shape_of(const hlq_attention* a) {
 }
 
 // How long the sequences are taken to be, where the launch needs a number: the
-// caller's longest one, or twice the mean.  Longer ones are looped over.
-int64_t expected(const hlq_attention* a, int64_t total) {
+// caller's longest one (of queries, and of keys with the same bounds), or twice the
+// mean.  Longer ones are looped over.
+int64_t expected(const hlq_attention* a, int64_t total, bool keys = false) {
   const int64_t mean = (total + a->sequences - 1) / a->sequences;
   const int64_t guess = std::min(total, 2 * mean);
-  return std::max<int64_t>(1, a->max_len ? std::min(total, a->max_len) : guess);
+  return std::max<int64_t>(
+      1, a->max_len && !(keys && a->start_k) ? std::min(total, a->max_len) : guess);
 }
 
 // Numbers a launch's work items.  Tiles beyond 2^30 items are looped over.  A unit's
@@ -348,7 +350,7 @@ hlq_status hlq_attention_backward(const hlq_attention* a, const hlq_tokens* g_o,
     const int64_t far = std::max(b.q.head, b.g_o.head) * (int64_t)esize(a->dtype) * shared;
     if ((shared & (shared - 1)) || shared > hlq::ATTN_PACK || far >= (int64_t(1) << 30)) b.g.pack = 1;
     b.g.groups = shared / b.g.pack;
-    const int64_t keys = expected(a, a->keys), units = a->sequences * a->kv_heads;
+    const int64_t keys = expected(a, a->keys, true), units = a->sequences * a->kv_heads;
     few = few_tiles(keys, units);
     number(b.g, tiles_of(keys, few), units, 1);
     HLQ_TRY(HLQ_BY_SIZE(a->head_dim, launch_attention_backward_kv, b, a->dtype, few, s));
