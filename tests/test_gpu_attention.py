@@ -299,6 +299,32 @@ def test_shares_of_the_keys(dtype, heads, D):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("klens", [[9000, 1, 0, 2, 300, 129, 40, 128, 127, 1, 1, 65], [70001]])
+def test_shares_of_unequal_sequences(dtype, klens):
+    """Sequences far longer than the shares are made for, many shares without a key
+    (whose part of the workspace holds NaN), more keys than 64 of the least shares."""
+    torch, h = _torch(), _h()
+    _say(f"attention shares of {len(klens)} sequences {dtype}")
+    case = Case([1] * len(klens), 4, 2, 64, dtype, True, klens=klens)
+    _check(case, max_len=1, backward=False)
+    d, kw = case.device()
+    want = h.hlq_attention_forward(**d, **kw, max_len=1)
+    rows = case.H * sum(case.lens) * (case.D + 2) * 4      # one share's bytes
+    ws = torch.full((64 * rows,), 255, dtype=torch.uint8, device="cuda")
+    got = h.hlq_attention_forward(**d, **kw, max_len=1, workspace=ws)
+    assert not bool((ws == 255).all())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_hint_with_keys_of_their_own(dtype):
+    """The longest sequence's queries say nothing of its keys."""
+    _say(f"attention hint, keys of their own {dtype}")
+    _check(Case([3, 5, 1], 4, 2, 64, dtype, True, klens=[700, 30, 300]), max_len=5)
+    _check(Case([40, 2], 2, 2, 40, dtype, False, klens=[9, 290], buckets=8, reach=20), max_len=40)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("max_len", [1, 33, 1 << 20])
 def test_hint_does_not_matter(dtype, max_len):
     """A longest length that is wrong either way: sequences beyond it are looped
