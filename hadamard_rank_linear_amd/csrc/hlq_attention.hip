@@ -247,6 +247,14 @@ __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !FEW ? 3 : 2) void k
       const int first = wave_min(me.valid ? limit : end);     // keys that all rows see
       const int last = wave_max_int(me.valid ? limit : from);  // and that any does
 
+      const auto feed = [&](int key, int buf) {
+        const uint32_t at = lds_place(lds) + buf * 2 * F::TILE_BYTES;
+        sk.issue(kb + key * kt, end - key, g.D, at);
+        sv.issue(vb + key * vt, end - key, g.D, at + F::TILE_BYTES);
+      };
+      __syncthreads();  // the previous tile's reads are done
+      if (F::BUFS == 2 && from < end) feed(from, 0);
+
       Frag<DT> qf[DC];
       {
         const char* p = row_at<DT>(a.q, q0 + (me.valid ? me.token : 0), me.head);
@@ -380,13 +388,6 @@ __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !FEW ? 3 : 2) void k
         }
       };
 
-      const auto feed = [&](int key, int buf) {
-        const uint32_t at = lds_place(lds) + buf * 2 * F::TILE_BYTES;
-        sk.issue(kb + key * kt, end - key, g.D, at);
-        sv.issue(vb + key * vt, end - key, g.D, at + F::TILE_BYTES);
-      };
-      __syncthreads();  // the previous tile's reads are done
-      if (F::BUFS == 2 && from < end) feed(from, 0);
       int buf = 0;
       for (int key = from; key < end; key += F::KEYS, buf ^= F::BUFS - 1) {
         if (F::BUFS == 1) {
@@ -606,6 +607,14 @@ __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !BIAS && !FEW ? 3 : 
         end = max(0, min(nk, (int)((unsigned)r / (unsigned)g.pack) + off + 1));
       }
 
+      const auto feed = [&](int key, int buf) {
+        const uint32_t at = lds_place(lds) + buf * 2 * F::TILE_BYTES;
+        sk.issue(kb + key * kt, end - key, g.D, at);
+        sv.issue(vb + key * vt, end - key, g.D, at + F::TILE_BYTES);
+      };
+      __syncthreads();  // the previous tile's reads are done
+      if (F::BUFS == 2 && end > 0) feed(0, 0);
+
       Frag<DT> qf[DC], gf[DC];
       float lse = kInf, delta = 0.f;
       const int64_t token = (int64_t)q0 + (me.valid ? me.token : 0);
@@ -650,7 +659,7 @@ __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !BIAS && !FEW ? 3 : 
           if constexpr (i < 2 * DC) return T::row_frag(rl, i < DC ? 0 : F::KEYS, i % DC);
           else return T::col_frag(cl, 16 * ((i - 2 * DC) / DB), (i - 2 * DC) % DB);
         };
-        Frag<DT> df[2];
+        Frag<DT> df[2], rest[2];
         f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
         steps<DT, 2 * DC + 2 * DB>(read, [&](auto step, const Frag<DT>& f) {
           constexpr int i = decltype(step)::value;
@@ -685,12 +694,17 @@ __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !BIAS && !FEW ? 3 : 
                 }
               }
               if (MASK && (bad & bit_range(0, limit))) poison = __builtin_nanf("");
-              df[0] = acc_frag<DT>(s, 0);
-              df[1] = acc_frag<DT>(s, 1);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                df[c] = acc_frag<DT>(s, c);
+                if constexpr (DT == 1) rest[c] = acc_rest(s, c, df[c]);
+              }
             }
           } else {
             constexpr int j = i - 2 * DC;
-            dq[j % DB] = mma(only_finite<DT>(f, MASK && bad), df[j / DB], dq[j % DB]);
+            const Frag<DT> k = only_finite<DT>(f, MASK && bad);
+            dq[j % DB] = mma(k, df[j / DB], dq[j % DB]);
+            if constexpr (DT == 1) dq[j % DB] = mma(k, rest[j / DB], dq[j % DB]);
           }
         });
       };
@@ -705,14 +719,6 @@ __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !BIAS && !FEW ? 3 : 
           cl += 32 * T::ROW_BYTES;
         }
       };
-
-      const auto feed = [&](int key, int buf) {
-        const uint32_t at = lds_place(lds) + buf * 2 * F::TILE_BYTES;
-        sk.issue(kb + key * kt, end - key, g.D, at);
-        sv.issue(vb + key * vt, end - key, g.D, at + F::TILE_BYTES);
-      };
-      __syncthreads();  // the previous tile's reads are done
-      if (F::BUFS == 2 && end > 0) feed(0, 0);
       int buf = 0;
       for (int key = 0; key < end; key += F::KEYS, buf ^= F::BUFS - 1) {
         if (F::BUFS == 1) {
@@ -925,10 +931,11 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
       // A tile of rows, of which this wave's begin at row and in LDS at `tile`.  Rows past
       // the end are zeros with a probability of zero; with a bias they are masked (a
       // table may hold infinities that no pair needs).
+      const int stop = wkey < nk ? rows : 0;  // a wave without keys has nothing to do
       const auto attend = [&](int row, int tile, const float* stat) {
         uint32_t rl = row_lane + tile, cl = col_lane + tile;
 #pragma unroll 1
-        for (int b = 0; b < F::BLOCKS && row < rows; ++b) {
+        for (int b = 0; b < F::BLOCKS && row < stop; ++b) {
           if (row >= most && (!BIAS || row + 32 <= rows)) {
             block(No(), row, rl, cl, stat, 0, 0);
           } else if (row + 32 > mine) {

@@ -58,8 +58,10 @@ __device__ __forceinline__ Frag<DT> zero_frag() {
 // Registers 8 c .. 8 c + 7 of a result as the fragment of a following product
 // that sums over its rows: rows 16 c + 8 (e >> 2) + 4 half + (e & 3), which is
 // the order col_frag reads in.  In bf16 this rounds probabilities and score
-// gradients to nearest even (2^-9 of each at most): the matrix instructions take
-// no other type, and the sums of a row average it out.
+// gradients to nearest even (2^-8 of each at most): the matrix instructions take
+// bf16 only with bf16.  In o the error averages out (0.0017 of it in all, 0.0016 of
+// that o's own rounding), in the gradients of k and v it is as large as their own
+// rounding (0.0023 in all); see acc_rest for that of q.
 template <int DT>
 __device__ __forceinline__ Frag<DT> acc_frag(const f32x16& s, int c) {
   Frag<DT> f;
@@ -73,6 +75,24 @@ __device__ __forceinline__ Frag<DT> acc_frag(const f32x16& s, int c) {
     __builtin_memcpy(&f, &w, 16);
   }
   return f;
+}
+
+// What acc_frag(s, c) = f has rounded off, as a fragment of its own: the product with
+// it makes up for the rounding.  A row's score gradients sum to zero, so that the part
+// that keys have in common cancels in the gradient of q, but not in their rounding
+// errors: without this they are twice the gradient's own rounding where 0.7 of the keys'
+// size is common (ViT-B 0.0034 of g_q in all, with it 0.0017), and grow with that share.
+// It costs 2 of 46 us there, 62 of 297 on 8192 ragged tokens with heads of 128.
+__device__ __forceinline__ bf16x8 acc_rest(const f32x16& s, int c, const bf16x8& f) {
+  u32x4 w;
+  __builtin_memcpy(&w, &f, 16);
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    w[e] = pack_bf16(s[8 * c + 2 * e] - __uint_as_float(w[e] << 16),
+                     s[8 * c + 2 * e + 1] - __uint_as_float(w[e] & 0xFFFF0000u));
+  bf16x8 r;
+  __builtin_memcpy(&r, &w, 16);
+  return r;
 }
 
 // Where hidden pairs have probability zero, an infinity or NaN in the other operand

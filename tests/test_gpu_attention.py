@@ -9,7 +9,9 @@ relative for bf16, 0 for fp32, whose half step counts among the u):
  - a probability: relative, that of its score and of the row's maximum or lse,
    and 4 u for the exponential and the sum's factors;
  - each product's sum of n terms: n u sum|terms|, and e sum|terms| for the
-   rounding of the probabilities or score gradients to the type;
+   rounding of the probabilities or score gradients to the type; in the gradient of
+   q, 2 n terms and e^2: what the rounding takes off is a second product, and only
+   its rounding is lost;
  - an output: e of itself.
 fp32 has nothing below TINY = 2^-126 (an exponential under it is zero, where the
 definition in 64 bits still has 10^-73 at scores of hundreds): each probability and
@@ -176,7 +178,7 @@ class Case:
                 + TINY * (1 + dp + de)
             G = fin(G)
             n, m = len(k), len(q) * (self.H // self.K)
-            tol[0][rows, h] += sc * ((gerr + (e + (n + 4) * U) * G) @ fin(k))
+            tol[0][rows, h] += sc * ((gerr + (e * e + (2 * n + 4) * U) * G) @ fin(k))
             tol[1][cols, kv] += sc * ((gerr + (e + (m + 4) * U) * G).T @ fin(q))
             tol[2][cols, kv] += (perr + (e + (m + 4) * U) * p).T @ fin(go)
             if which is not None:
@@ -449,6 +451,19 @@ def test_poisoned_queries_do_not_reach_hidden_keys(dtype):
         assert np.isnan(_np(grads[i])[:38]).all()
         _within(_np(grads[i])[38:], g[i][38:], t[i][38:], f"gradient {i}")
     _within(_np(grads[0])[rest], g[0][rest], t[0][rest], "g_q")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [40, 128])
+def test_keys_with_a_common_part(dtype, D):
+    """It cancels in the gradient of q, whose score gradients sum to zero; their
+    rounding, times the common part, would be many times the result's."""
+    _say(f"attention, keys with a common part, D {D} {dtype}")
+
+    def shift(c):
+        c.k = _round(c.k + 24.0, c.dtype)
+
+    _check(Case([70, 150], 4, 2, D, dtype, True, poison=shift))
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
