@@ -247,14 +247,6 @@ __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !FEW ? 3 : 2) void k
       const int first = wave_min(me.valid ? limit : end);     // keys that all rows see
       const int last = wave_max_int(me.valid ? limit : from);  // and that any does
 
-      const auto feed = [&](int key, int buf) {
-        const uint32_t at = lds_place(lds) + buf * 2 * F::TILE_BYTES;
-        sk.issue(kb + key * kt, end - key, g.D, at);
-        sv.issue(vb + key * vt, end - key, g.D, at + F::TILE_BYTES);
-      };
-      __syncthreads();  // the previous tile's reads are done
-      if (F::BUFS == 2 && from < end) feed(from, 0);
-
       Frag<DT> qf[DC];
       {
         const char* p = row_at<DT>(a.q, q0 + (me.valid ? me.token : 0), me.head);
@@ -388,6 +380,13 @@ __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !FEW ? 3 : 2) void k
         }
       };
 
+      const auto feed = [&](int key, int buf) {
+        const uint32_t at = lds_place(lds) + buf * 2 * F::TILE_BYTES;
+        sk.issue(kb + key * kt, end - key, g.D, at);
+        sv.issue(vb + key * vt, end - key, g.D, at + F::TILE_BYTES);
+      };
+      __syncthreads();  // the previous tile's reads are done
+      if (F::BUFS == 2 && from < end) feed(from, 0);
       int buf = 0;
       for (int key = from; key < end; key += F::KEYS, buf ^= F::BUFS - 1) {
         if (F::BUFS == 1) {
