@@ -11,6 +11,15 @@
 // of q, its 32 keys in the gradients of k and v.  Then P and dS leave the matrix
 // unit in the registers in which the next product takes them in, row statistics
 // are one value a lane, and nothing but the other operand's tiles goes through LDS.
+//
+// Measured, bf16, at the 1138 TFLOP/s of a large product and the 4.84 TB/s of a large
+// copy on the same card:
+//  - forward, 8192 tokens, 32 heads of 128 on 8: 1128 us (975 TFLOP/s), causal 586 (940);
+//    a quarter of the steps still wait for LDS or for a tile;
+//  - forward, ViT-B (64 x 197 tokens, 12 heads of 64): 28 us for 78 MB (2.8 TB/s): two
+//    rounds of workgroups that each wait for their rows and first tile;
+//  - backward, 8192 ragged tokens, 32 heads of 128 on 8: 333 + 523 us, the matrix units
+//    busy 50% and 34% of it; ViT-B 44 + 58 with g_q's second product 4 more.
 #include <utility>
 
 #include "hlq_attn.h"

@@ -160,10 +160,17 @@ struct FwdPlan {
 };
 
 // Tiles of 128 rows (or keys) that leave compute units without work are cut into
-// four, the waves of a workgroup sharing the other side.
+// four, the waves of a workgroup sharing the other side: 2048 causal tokens, 8 heads
+// of 64 take 23 us and backward 53, with tiles of 128 39 and 104; ViT-B's 1536 tiles
+// 28 and 101 as they are, cut 86 and 200.  With a causal mask the longest tile decides
+// up to twice as many (4096 such tokens 72 -> 51 and 195 -> 131 us, 6000 103 -> 91 and
+// 286 -> 224), but not where a cut tile fills the LDS (heads of 128, 256 tiles: 32 -> 43
+// and 101 -> 133).
 constexpr int64_t kUnits = 256;
-bool few_tiles(int64_t rows, int64_t units) {
-  return rows <= hlq::ATTN_FEW || (rows + hlq::ATTN_ROWS - 1) / hlq::ATTN_ROWS * units < kUnits;
+bool few_tiles(const hlq_attention* a, int64_t rows, int64_t units) {
+  const bool small = a->head_dim * esize(a->dtype) <= 128;
+  return rows <= hlq::ATTN_FEW || (rows + hlq::ATTN_ROWS - 1) / hlq::ATTN_ROWS * units <
+                                      (a->causal && small ? 2 * kUnits : kUnits);
 }
 int64_t tiles_of(int64_t rows, bool few) {
   const int per = few ? hlq::ATTN_FEW : hlq::ATTN_ROWS;
@@ -173,18 +180,24 @@ int64_t tiles_of(int64_t rows, bool few) {
 // If that is too few still, the keys are shared out: in shares of equal length, of
 // which all sequences together have about two a CU, 256 keys each at least.  As many
 // as the longest sequence is expected to need (at most 64); a longer one's are longer.
+// (8 tokens against 32700 keys 51 us, with eight shares a sequence whatever its length
+// 59; shares of 128 keys, or more than two a CU: up to 20% slower.)  The shares' sums
+// cost what they are long: tiles full of rows are left whole where they occupy half of
+// the CUs (512 causal tokens 11 us, shared out 14; 1024 tokens, 32 heads of 128 on 8, 32
+// and 61), single tokens only where every CU has one (48 of 700 keys 32, whole 34; 32 of
+// 1024, 256 items, 42 and 35).
 FwdPlan plan_forward(const hlq_attention* a) {
   const int shared = a->bias ? 1 : a->heads / a->kv_heads;
   const int64_t rows = expected(a, a->queries) * shared;
   FwdPlan p;
   p.units = a->sequences * (a->heads / shared);
-  p.few = few_tiles(rows, p.units);
+  p.few = few_tiles(a, rows, p.units);
   p.tiles = tiles_of(rows, p.few);
   p.splits = 1;
   p.share = 0;
   const int64_t slots = 2 * kUnits, groups = p.tiles * p.units;
   const int64_t mean = a->keys / a->sequences, longest = std::min(a->keys, 2 * mean);
-  if (groups >= slots || mean < 512) return p;
+  if (groups >= (rows <= hlq::ATTN_FEW ? kUnits : kUnits / 2) || mean < 512) return p;
   // groups < slots, so that the product of a 40-bit number is in range
   const int64_t share = std::max<int64_t>(256, (mean * groups + slots - 1) / slots);
   p.splits = std::min<int64_t>(64, (longest + share - 1) / share);
@@ -205,7 +218,7 @@ AttnShape backward_q_shape(const hlq_attention* a, bool* few) {
   const int64_t rows = expected(a, a->queries) * shared;
   const int64_t units = a->sequences * (a->heads / shared);
   // the sums of a bias's gradient leave no room for 128 rows of 512 bytes
-  *few = few_tiles(rows, units) && !(a->bias && a->dtype == HLQ_F32 && a->head_dim > 64);
+  *few = few_tiles(a, rows, units) && !(a->bias && a->dtype == HLQ_F32 && a->head_dim > 64);
   number(g, tiles_of(rows, *few), units, 1);
   return g;
 }
@@ -351,7 +364,7 @@ hlq_status hlq_attention_backward(const hlq_attention* a, const hlq_tokens* g_o,
     if ((shared & (shared - 1)) || shared > hlq::ATTN_PACK || far >= (int64_t(1) << 30)) b.g.pack = 1;
     b.g.groups = shared / b.g.pack;
     const int64_t keys = expected(a, a->keys, true), units = a->sequences * a->kv_heads;
-    few = few_tiles(keys, units);
+    few = few_tiles(a, keys, units);
     number(b.g, tiles_of(keys, few), units, 1);
     HLQ_TRY(HLQ_BY_SIZE(a->head_dim, launch_attention_backward_kv, b, a->dtype, few, s));
   }
