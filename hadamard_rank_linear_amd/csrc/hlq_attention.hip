@@ -159,9 +159,9 @@ __device__ __forceinline__ constexpr int beside(int i, int n, int all) {
 
 // ------------------------------------------------------------ forward
 
-// A work item is a tile of query rows of one sequence and head group, and a
-// share of its keys.  FEW: the tile has 32 rows and each wave a quarter of the
-// keys, joined through LDS at the end; else 32 rows a wave and every key.
+// A work item is a tile of query rows of one sequence and head group: 32 rows a wave
+// and every key, or, FEW, 32 rows in all and a share of the keys, of which each wave
+// takes a quarter, joined through LDS at the end.
 template <int DT, int DP, bool FEW>
 struct FwdShape {
   typedef Tile<DT, DP> T;
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !FEW ? 3 : 2) void k
     const int64_t from = bound(g.start_q, 0, g.Tq), to = bound(g.start_q, g.S, g.Tq);
     for (int part = 0; part < 2; ++part) {
       const int64_t x = part ? max(from, to) : 0, y = part ? g.Tq : from;
-      if (a.po) {
+      if (FEW && a.po) {
         for (int64_t i = id; i < (y - x) * g.heads * g.splits; i += step) {
           const int64_t p = i / ((y - x) * g.heads), r = i % ((y - x) * g.heads);
           float* ml = a.ml + ((p * g.Tq + x) * g.heads + r) * 2;
@@ -214,8 +214,8 @@ __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !FEW ? 3 : 2) void k
   for (unsigned item = blockIdx.x; item < g.items; item += g.launched) {
     unsigned u, t;
     if (!item_of(g, item, u, t)) continue;
-    const int split = (int)(t % g.splits);
-    const unsigned tile0 = g.tiles - 1 - t / g.splits;  // the longest first
+    const int split = FEW ? (int)(t % g.splits) : 0;
+    const unsigned tile0 = g.tiles - 1 - (FEW ? t / g.splits : t);  // the longest first
     const unsigned per = g.kv_heads * g.groups;
     const int64_t seq = u / per;
     const int unit = (int)(u % per), head0 = unit * g.pack, kvh = unit / g.groups;
@@ -245,8 +245,11 @@ __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !FEW ? 3 : 2) void k
         const int r = min(rows, (int)(tile + 1) * F::ROWS) - 1;
         end = max(0, min(nk, (int)((unsigned)r / (unsigned)g.pack) + off + 1));
       }
+      // where it is known to be zero the compiler runs out of scalar registers (ViT-B 28.0
+      // -> 29.3 us)
       int from = 0;
-      if (g.splits > 1) {
+      if (!FEW) asm volatile("" : "+s"(from));
+      if (FEW && g.splits > 1) {
         const int share =
             max(g.share, (int)(((end + F::KEYS - 1) / F::KEYS + g.splits - 1) / g.splits) * F::KEYS);
         from = (int)min((int64_t)end, (int64_t)split * share);
@@ -415,22 +418,6 @@ __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !FEW ? 3 : 2) void k
       if constexpr (!FEW) {
         if (!me.valid) continue;
         const int64_t token = (int64_t)q0 + me.token;
-        if (z.po) {
-          const int64_t at = ((int64_t)split * z.g.Tq + token) * z.g.heads + me.head;
-          if (half == 0) {
-            z.ml[2 * at] = m;
-            z.ml[2 * at + 1] = l;
-          }
-          float* p = z.po + at * z.g.D;
-#pragma unroll
-          for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const int e = 32 * d + acc_row(r) + 4 * half;
-              if (e < z.g.D) p[e] = o[d][r];
-            }
-          continue;
-        }
         if (half == 0)
           z.lse[me.head * z.g.Tq + token] =
               l == 0.f ? -kInf : (m + __builtin_amdgcn_logf(l)) * kLn2;

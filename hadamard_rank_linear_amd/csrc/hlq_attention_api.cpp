@@ -197,8 +197,7 @@ FwdPlan plan_forward(const hlq_attention* a) {
   p.share = 0;
   const int64_t slots = 2 * kUnits, groups = p.tiles * p.units;
   const int64_t mean = a->keys / a->sequences, longest = std::min(a->keys, 2 * mean);
-  if (groups >= (rows <= hlq::ATTN_FEW ? kUnits : kUnits / 2) || mean < 512) return p;
-  // groups < slots, so that the product of a 40-bit number is in range
+  if (!p.few || groups >= (rows <= hlq::ATTN_FEW ? kUnits : kUnits / 2) || mean < 512) return p;
   const int64_t share = std::max<int64_t>(256, (mean * groups + slots - 1) / slots);
   p.splits = std::min<int64_t>(64, (longest + share - 1) / share);
   p.share = ((longest + p.splits - 1) / p.splits + 127) / 128 * 128;

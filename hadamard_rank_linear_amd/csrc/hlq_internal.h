@@ -313,7 +313,7 @@ struct AttnFwd {
   AttnShape g;
   AttnRows q, k, v, o;
   float* lse;      // [heads][Tq]
-  float *po, *ml;  // splits > 1: [splits][Tq][heads][D] and [splits][Tq][heads][2]
+  float *po, *ml;  // splits > 1 (small tiles): [splits][Tq][heads][D] and [splits][Tq][heads][2]
 };
 struct AttnBwd {
   AttnShape g;
