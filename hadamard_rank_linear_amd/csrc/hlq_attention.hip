@@ -12,14 +12,15 @@
 // unit in the registers in which the next product takes them in, row statistics
 // are one value a lane, and nothing but the other operand's tiles goes through LDS.
 //
-// Measured, bf16, at the 1138 TFLOP/s of a large product and the 4.84 TB/s of a large
-// copy on the same card:
-//  - forward, 8192 tokens, 32 heads of 128 on 8: 1128 us (975 TFLOP/s), causal 586 (940);
-//    a quarter of the steps still wait for LDS or for a tile;
-//  - forward, ViT-B (64 x 197 tokens, 12 heads of 64): 28 us for 78 MB (2.8 TB/s): two
-//    rounds of workgroups that each wait for their rows and first tile;
-//  - backward, 8192 ragged tokens, 32 heads of 128 on 8: 333 + 523 us, the matrix units
-//    busy 50% and 34% of it; ViT-B 44 + 58 with g_q's second product 4 more.
+// Bound by the matrix unit for long sequences, by memory and the waits of a workgroup's
+// start for short ones.  Measured in bf16, where a large product reaches 1138 TFLOP/s
+// and a large copy 4.84 TB/s:
+//  - forward, 8192 tokens, 32 heads of 128 on 8: 1128 us (975 TFLOP/s), causal 595 (924);
+//    ViT-B (64 x 197 tokens, 12 heads of 64) 28 us for 78 MB; 8 tokens against 32700 keys
+//    46 us with the join (2.9 TB/s);
+//  - backward, 8192 ragged causal tokens, 32 heads of 128 on 8: 335 us for q (matrix units
+//    busy 50% of the time), 525 for k and v (34%: one wave a SIMD, of whose cycles a
+//    quarter go into its turns of the tiles' loads); ViT-B 48 + 59.
 #include <utility>
 
 #include "hlq_attn.h"
@@ -123,8 +124,8 @@ typedef std::false_type No;
 // A chain of matrix products whose fragments come from LDS, in steps whose order the
 // compiler keeps: fragment i + AHEAD is read, product i starts, and what the matrix
 // unit does not need runs beside it.  Left alone the compiler reads a fragment, waits
-// and multiplies: with one or two waves a SIMD the backward pass of 8192 tokens then
-// has the matrix units idle for three quarters of the time.
+// and multiplies: with one or two waves a SIMD the backward pass of 8192 ragged tokens
+// took 1203 us, in this order 814.  Reading 8 or 12 products ahead gains nothing.
 // read and use get the step's number as a constant.
 constexpr int AHEAD = 4;
 template <int I>
@@ -171,12 +172,15 @@ struct FwdShape {
   static constexpr int TILE_BYTES = KEYS * T::ROW_BYTES;
   static constexpr int JOIN_BYTES = FEW ? 4 * DP * 33 * 4 + 4 * 32 * 8 : 0;
   // buffers of a tile of keys and of values: one where two leave no room for a second
-  // workgroup (or do not fit the LDS)
+  // workgroup, which then loads while this one computes (1 token against 65536 keys, with
+  // equal shares, 96 -> 67 us)
   static constexpr int BUFS = TILE_BYTES > 16384 ? 1 : 2;
   static constexpr int LDS =
       2 * BUFS * TILE_BYTES > JOIN_BYTES ? 2 * BUFS * TILE_BYTES : JOIN_BYTES;
 };
 
+// Workgroups a CU: three of heads up to 64 (ViT-B 36 -> 31 us; a fourth costs spills),
+// one in fp32, whose fragments are twice as large.
 template <int DT, int DP, bool BIAS, bool FEW, bool VEC>
 __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !FEW ? 3 : 2) void k_attention_forward(AttnFwd a) {
   typedef FwdShape<DT, DP, FEW> F;
@@ -531,7 +535,8 @@ __device__ __forceinline__ void join_waves(char* lds, const f32x16 (&mine)[DP / 
 // Waves as in the forward pass.  Writes delta for the gradients of k and v, and
 // with a bias the sums of dS by bucket over the item: each wave adds its blocks'
 // diagonals to a line of distances of its own in LDS, blocks beyond reach in
-// registers.
+// registers (8190 ragged tokens, 12 heads of 64: 100 us).  Three workgroups a CU of
+// heads up to 64 as above (ViT-B 48 -> 44 us), two where the line takes registers too.
 template <int DT, int DP, bool BIAS, bool FEW, bool VEC>
 __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !BIAS && !FEW ? 3 : 2) void k_attention_backward_q(AttnBwd a) {
   typedef BwdShape<DT, DP, FEW, BIAS> F;
@@ -777,8 +782,12 @@ __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !BIAS && !FEW ? 3 : 
 
 // ------------------------------------------------------------ gradients of k and v
 
-// A work item is 128 keys of one sequence and key head, 32 a wave; it goes
-// through the query rows of the heads that share them.
+// A work item is 128 keys of one sequence and key head, 32 a wave (FEW: 32 keys, a
+// quarter of the rows a wave); it goes through the query rows of the heads that share
+// them.  Both gradients of 32 keys, keys and values stay in registers: 64 keys a wave
+// spill (ViT-B 59 -> 90 us), and heads of 128 leave room for one wave a SIMD.  The
+// probabilities are computed once more than in one kernel for all three gradients,
+// which would have to add up g_q over workgroups: with atomics, in any order.
 template <int DT, int DP, bool BIAS, bool FEW, bool VEC>
 __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_backward_kv(
     AttnBwd a) {

@@ -144,7 +144,9 @@ int64_t expected(const hlq_attention* a, int64_t total, bool keys = false) {
 // Numbers a launch's work items.  Tiles beyond 2^30 items are looped over.  A unit's
 // items (which read the same keys and values, or rows) go to one XCD, where they meet
 // in its L2, if that leaves the eight equally busy.  With a causal mask long tiles come
-// first, of all units, so that the last to end are short.
+// first, of all units, so that the last to end are short (8192 causal tokens 823 us in
+// plain order, 602 so); without one a unit's tiles stay together (8190 ragged tokens
+// with a bias, backward, 215 us tile by tile, 168 so).
 void number(AttnShape& g, int64_t tiles, int64_t units, int64_t splits) {
   g.splits = (unsigned)splits;
   g.units = (unsigned)units;

