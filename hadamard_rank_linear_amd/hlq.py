@@ -104,6 +104,10 @@ def _load():
         raise ImportError(
             f"{LIB_PATH} is missing: build it with "
             "`python -m hadamard_rank_linear_amd.build` (hipcc, gfx950)")
+    try:
+        import torch  # noqa: F401  its HIP runtime first: the library then binds to it too
+    except ImportError:
+        pass
     lib = ctypes.CDLL(LIB_PATH)
     P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
     lib.hlq_compress_act.argtypes = [P, I32, I64, I64, P, P, P]

@@ -1,6 +1,9 @@
 """Host-side checks of the attention block's operators (no GPU, nothing is
 launched): refusals of the C ABI and of the binding, workspace sizes, buckets."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -178,3 +181,14 @@ def test_dropout_binding_refuses(kw, error):
     a.update(kw)
     with pytest.raises(error):
         h.hlq_dropout_forward(_cpu(5), **a)
+
+
+def test_one_hip_runtime_whatever_is_imported_first():
+    """torch brings a HIP runtime of its own; the library loaded before it would bind
+    another one, and no call would work in either."""
+    code = ("import hadamard_rank_linear_amd as h; h.lib_handle(); import torch\n"
+            "print(len({l.split()[-1] for l in open('/proc/self/maps') if 'libamdhip64' in l}))")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert out.returncode == 0 and out.stdout.strip() == "1", out
