@@ -131,10 +131,11 @@ AttnShape shape_of(const hlq_attention* a) {
   return g;
 }
 
-// How long the sequences are taken to be, where the launch needs a number: the
-// caller's longest one (of queries, and of keys with the same bounds), or twice the
-// mean.  Longer ones are looped over.
+// How long the sequences are taken to be, where the launch needs a number: one without
+// bounds has all tokens; else the caller's longest one (of queries, and of keys with the
+// same bounds), or twice the mean.  Longer ones are looped over.
 int64_t expected(const hlq_attention* a, int64_t total, bool keys = false) {
+  if (!a->start_q) return std::max<int64_t>(1, total);
   const int64_t mean = (total + a->sequences - 1) / a->sequences;
   const int64_t guess = std::min(total, 2 * mean);
   return std::max<int64_t>(
@@ -188,6 +189,11 @@ int64_t tiles_of(int64_t rows, bool few) {
 // the CUs (512 causal tokens 11 us, shared out 14; 1024 tokens, 32 heads of 128 on 8, 32
 // and 61), single tokens only where every CU has one (48 of 700 keys 32, whole 34; 32 of
 // 1024, 256 items, 42 and 35).
+// Every query has room in the workspace for every share.  A true hint has up to 32 x 256
+// rows of queries and heads here, and 40960 with their shares: there are more where tokens
+// belong to no sequence, or where the hint is wrong, and then fewer shares (one sequence
+// of 65536 tokens, 32 heads of 128, said to be single tokens: 70 GB without that limit).
+constexpr int64_t kShareRows = int64_t(1) << 18;
 FwdPlan plan_forward(const hlq_attention* a) {
   const int shared = a->bias ? 1 : a->heads / a->kv_heads;
   const int64_t rows = expected(a, a->queries) * shared;
@@ -201,7 +207,8 @@ FwdPlan plan_forward(const hlq_attention* a) {
   const int64_t mean = a->keys / a->sequences, longest = std::min(a->keys, 2 * mean);
   if (!p.few || groups >= (rows <= hlq::ATTN_FEW ? kUnits : kUnits / 2) || mean < 512) return p;
   const int64_t share = std::max<int64_t>(256, (mean * groups + slots - 1) / slots);
-  p.splits = std::min<int64_t>(64, (longest + share - 1) / share);
+  const int64_t room = kShareRows / std::max<int64_t>(1, a->queries * a->heads);
+  p.splits = std::max<int64_t>(1, std::min({int64_t(64), room, (longest + share - 1) / share}));
   p.share = ((longest + p.splits - 1) / p.splits + 127) / 128 * 128;
   return p;
 }

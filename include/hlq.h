@@ -628,7 +628,7 @@ typedef struct hlq_tokens {
  * i + Lk - Lq of its sequence's Lk keys, so that new tokens follow those of a
  * cache.  Lengths may be zero.
  *   max_len   the longest sequence's queries, for the launch alone (0: unknown);
- *             longer ones are dealt with all the same.
+ *             longer ones are dealt with all the same.  Not looked at without bounds.
  *   heads     query heads; head h reads key head h / (heads / kv_heads).
  *   head_dim  1 to 128.
  *   causal    a query sees the keys up to its own position.
