@@ -175,9 +175,16 @@ bool few_tiles(const hlq_attention* a, int64_t rows, int64_t units) {
   return rows <= hlq::ATTN_FEW || (rows + hlq::ATTN_ROWS - 1) / hlq::ATTN_ROWS * units <
                                       (a->causal && small ? 2 * kUnits : kUnits);
 }
-int64_t tiles_of(int64_t rows, bool few) {
+// A launch has a sequence's tiles for each of them, and a bias's gradient a line of
+// buckets for each tile, so a sequence that is far longer than the rest pays for them all:
+// at most kSkew times the tiles that `all` rows can have, a longer one loops over its own
+// (131072 causal tokens in 1024 sequences, the longest 32768, 16 heads of 64: forward 6.8
+// ms, backward with a bias 25.6; 7.6 and 31.1 with four times as many, 9.4 and 38.9 and 540
+// MB of lines without a limit, 15.1 and 38.5 with a quarter).
+constexpr int64_t kSkew = 16;
+int64_t tiles_of(const hlq_attention* a, int64_t rows, int64_t all, bool few) {
   const int per = few ? hlq::ATTN_FEW : hlq::ATTN_ROWS;
-  return (rows + per - 1) / per;
+  return std::min((rows + per - 1) / per, kSkew * (all / per + a->sequences) / a->sequences);
 }
 
 // If that is too few still, the keys are shared out: in shares of equal length, of
@@ -200,7 +207,7 @@ FwdPlan plan_forward(const hlq_attention* a) {
   FwdPlan p;
   p.units = a->sequences * (a->heads / shared);
   p.few = few_tiles(a, rows, p.units);
-  p.tiles = tiles_of(rows, p.few);
+  p.tiles = tiles_of(a, rows, a->queries * shared, p.few);
   p.splits = 1;
   p.share = 0;
   const int64_t slots = 2 * kUnits, groups = p.tiles * p.units;
@@ -227,7 +234,7 @@ AttnShape backward_q_shape(const hlq_attention* a, bool* few) {
   const int64_t units = a->sequences * (a->heads / shared);
   // the sums of a bias's gradient leave no room for 128 rows of 512 bytes
   *few = few_tiles(a, rows, units) && !(a->bias && a->dtype == HLQ_F32 && a->head_dim > 64);
-  number(g, tiles_of(rows, *few), units, 1);
+  number(g, tiles_of(a, rows, a->queries * shared, *few), units, 1);
   return g;
 }
 
@@ -373,7 +380,7 @@ hlq_status hlq_attention_backward(const hlq_attention* a, const hlq_tokens* g_o,
     b.g.groups = shared / b.g.pack;
     const int64_t keys = expected(a, a->keys, true), units = a->sequences * a->kv_heads;
     few = few_tiles(a, keys, units);
-    number(b.g, tiles_of(keys, few), units, 1);
+    number(b.g, tiles_of(a, keys, a->keys, few), units, 1);
     HLQ_TRY(HLQ_BY_SIZE(a->head_dim, launch_attention_backward_kv, b, a->dtype, few, s));
   }
   return HLQ_OK;

@@ -629,6 +629,9 @@ typedef struct hlq_tokens {
  * cache.  Lengths may be zero.
  *   max_len   the longest sequence's queries, for the launch alone (0: unknown);
  *             longer ones are dealt with all the same.  Not looked at without bounds.
+ *             A launch has that many queries' tiles in every sequence, up to 16 times
+ *             what the tokens can need, and a bias's gradient [buckets] f32 of workspace
+ *             for each tile and head.
  *   heads     query heads; head h reads key head h / (heads / kv_heads).
  *   head_dim  1 to 128.
  *   causal    a query sees the keys up to its own position.

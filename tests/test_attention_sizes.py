@@ -50,3 +50,28 @@ def test_a_hint_that_is_too_short_asks_for_little():
     (8, 32700, 8, 32, 8, 16), (1, 65536, 1, 32, 8, 64), (4, 65536, 4, 8, 1, 64), (2, 8192, 2, 4, 2, 32)])
 def test_a_true_hint_keeps_its_shares(queries, keys, S, heads, kv, shares):
     assert _sizes(queries, keys, S, heads, kv, 128, 1)[0] == shares * queries * heads * 130 * 4
+
+
+def test_a_hint_for_one_of_many_sequences():
+    """With a bias a line of buckets for each tile and head: at most 16 times as many as
+    tiles of 32 there can be."""
+    rng = np.random.default_rng(2)
+    for _ in range(2000):
+        S, heads = int(2 ** rng.uniform(0, 16)), int(rng.integers(1, 17))
+        queries = S * int(2 ** rng.uniform(0, 8))
+        if queries * heads >= 1 << 30:
+            continue
+        hint = int(2 ** rng.uniform(0, 41))
+        _, size = _sizes(queries, queries, S, heads, heads, 64, hint, buckets=32)
+        lines = (size - (queries * heads * 4 + 15) // 16 * 16) / (32 * 4)
+        assert lines <= 16 * (queries / 32 + S) * heads
+    # 2^20 tokens in 2^16 sequences, one of them long: 137 GB
+    assert _sizes(1 << 20, 1 << 20, 1 << 16, 16, 16, 64, 1 << 20, buckets=32)[1] < 3e9
+
+
+@pytest.mark.parametrize("queries,S,heads,hint,tiles", [
+    (12608, 64, 12, 197, 2), (8192, 16, 12, 512, 4), (8190, 16, 12, 0, 8), (65536, 8, 16, 30000, 235),
+    (65536, 1, 16, 0, 512)])
+def test_a_true_hint_keeps_its_tiles(queries, S, heads, hint, tiles):
+    _, size = _sizes(queries, queries, S, heads, heads, 64, hint, buckets=32, causal=0)
+    assert size == queries * heads * 4 + tiles * S * heads * 32 * 4

@@ -4,6 +4,7 @@ import pytest
 
 from test_attention_sizes import _sizes
 from test_gpu_attention import Case, _check, _h, _say, _torch
+from test_gpu_attention_tiles import _tiles
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +32,13 @@ def test_one_sequence_without_bounds(dtype):
         again = h.hlq_attention_backward(want, *d.values(), want, lse, **kw, max_len=max_len)
         assert torch.equal(got[0], want) and torch.equal(got[1], lse)
         assert all(torch.equal(a, b) for a, b in zip(again[:3], grads[:3]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bias", [False, True])
+def test_one_long_sequence_among_many(dtype, bias):
+    """Its 18 tiles are more than the launch has: one workgroup takes two."""
+    _say(f"attention, one long sequence of 200, {dtype} bias {bias}")
+    lens = [2300] + [0, 1] * 3 + [0] * 193
+    assert _tiles(sum(lens), len(lens), 3, 2300, dtype, 8, not bias) == 17
+    _check(Case(lens, 3, 3, 8, dtype, not bias, buckets=16 if bias else 0), max_len=2300)
