@@ -21,6 +21,7 @@
 //  - backward, 8192 ragged causal tokens, 32 heads of 128 on 8: 335 us for q (matrix units
 //    busy 50% of the time), 525 for k and v (34%: one wave a SIMD, of whose cycles a
 //    quarter go into its turns of the tiles' loads); ViT-B 48 + 59.
+#include <algorithm>
 #include <utility>
 
 #include "hlq_attn.h"
@@ -47,16 +48,19 @@ __device__ __forceinline__ char* row_at(const R& t, int64_t token, int64_t head)
   return static_cast<char*>(t.data) + (token * t.token + head * t.head) * (DT == 0 ? 4 : 2);
 }
 
-// Outputs of tokens that belong to no sequence: zeros.
+// Outputs of tokens that belong to no sequence: zeros.  A thread of `groups` workgroups
+// has a 16-byte piece of every so many rows.
 template <int DT>
-__device__ void clear_tokens(const AttnRows& t, int64_t from, int64_t to, int heads, int D,
-                             int64_t id, int64_t step) {
-  typedef typename Piece<DT>::Elem E;
-  const int64_t n = (to - from) * heads * D;
-  for (int64_t i = id; i < n; i += step) {
-    const int64_t r = i / D;
-    reinterpret_cast<E*>(row_at<DT>(t, from + r / heads, r % heads))[i % D] = 0;
-  }
+__device__ void clear_tokens(const AttnRows& t, int64_t from, int64_t to, unsigned heads, int D,
+                             unsigned group, unsigned groups) {
+  constexpr int N = Piece<DT>::N;
+  const unsigned pieces = (unsigned)(D + N - 1) / N, per = 256 / pieces;
+  const unsigned piece = threadIdx.x % pieces, mine = threadIdx.x / pieces;
+  if (mine >= per) return;
+  const unsigned rows = (unsigned)(to - from) * heads;  // fewer than 2^30
+  for (unsigned r = group * per + mine; r < rows; r += groups * per)
+    store_piece<DT>(row_at<DT>(t, from + r / heads, r % heads), piece * N, D - (int)piece * N,
+                    (u32x4){0u, 0u, 0u, 0u});
 }
 __device__ __forceinline__ int64_t bound(const int64_t* start, int64_t s, int64_t T) {
   const int64_t a = start[s];
@@ -194,23 +198,23 @@ __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !FEW ? 3 : 2) void k
   const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
 
   if (blockIdx.x >= g.launched) {  // tokens of no sequence
-    const int64_t id = (int64_t)(blockIdx.x - g.launched) * 256 + threadIdx.x;
-    const int64_t step = (int64_t)(gridDim.x - g.launched) * 256;
+    const unsigned group = blockIdx.x - g.launched, groups = gridDim.x - g.launched;
     const int64_t from = bound(g.start_q, 0, g.Tq), to = bound(g.start_q, g.S, g.Tq);
     for (int part = 0; part < 2; ++part) {
       const int64_t x = part ? max(from, to) : 0, y = part ? g.Tq : from;
+      const unsigned tokens = (unsigned)(y - x), rows = tokens * g.heads;
       if (FEW && a.po) {
-        for (int64_t i = id; i < (y - x) * g.heads * g.splits; i += step) {
-          const int64_t p = i / ((y - x) * g.heads), r = i % ((y - x) * g.heads);
-          float* ml = a.ml + ((p * g.Tq + x) * g.heads + r) * 2;
-          ml[0] = -kInf;
-          ml[1] = 0.f;
-        }
+        for (unsigned p = 0; p < g.splits; ++p)
+          for (unsigned i = group * 256 + threadIdx.x; i < rows; i += groups * 256) {
+            float* ml = a.ml + ((p * g.Tq + x) * g.heads + i) * 2;
+            ml[0] = -kInf;
+            ml[1] = 0.f;
+          }
         continue;
       }
-      clear_tokens<DT>(a.o, x, y, g.heads, g.D, id, step);
-      for (int64_t i = id; i < (y - x) * g.heads; i += step)
-        a.lse[(i % g.heads) * g.Tq + x + i / g.heads] = -kInf;
+      clear_tokens<DT>(a.o, x, y, g.heads, g.D, group, groups);
+      for (unsigned i = group * 256 + threadIdx.x; i < rows; i += groups * 256)
+        a.lse[(int64_t)(i / tokens) * g.Tq + x + i % tokens] = -kInf;
     }
     return;
   }
@@ -554,11 +558,10 @@ __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !BIAS && !FEW ? 3 : 
   const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
 
   if (blockIdx.x >= g.launched) {
-    const int64_t id = (int64_t)(blockIdx.x - g.launched) * 256 + threadIdx.x;
-    const int64_t step = (int64_t)(gridDim.x - g.launched) * 256;
+    const unsigned group = blockIdx.x - g.launched, groups = gridDim.x - g.launched;
     const int64_t from = bound(g.start_q, 0, g.Tq), to = bound(g.start_q, g.S, g.Tq);
-    clear_tokens<DT>(a.g_q, 0, from, g.heads, g.D, id, step);
-    clear_tokens<DT>(a.g_q, max(from, to), g.Tq, g.heads, g.D, id, step);
+    clear_tokens<DT>(a.g_q, 0, from, g.heads, g.D, group, groups);
+    clear_tokens<DT>(a.g_q, max(from, to), g.Tq, g.heads, g.D, group, groups);
     return;
   }
 
@@ -803,13 +806,12 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
   const int lane = threadIdx.x & 63, half = lane >> 5, wave = threadIdx.x >> 6;
 
   if (blockIdx.x >= g.launched) {
-    const int64_t id = (int64_t)(blockIdx.x - g.launched) * 256 + threadIdx.x;
-    const int64_t step = (int64_t)(gridDim.x - g.launched) * 256;
+    const unsigned group = blockIdx.x - g.launched, groups = gridDim.x - g.launched;
     const int64_t from = bound(g.start_k, 0, g.Tk), to = bound(g.start_k, g.S, g.Tk);
     for (int part = 0; part < 2; ++part) {
       const int64_t x = part ? max(from, to) : 0, y = part ? g.Tk : from;
-      clear_tokens<DT>(a.g_k, x, y, g.kv_heads, g.D, id, step);
-      clear_tokens<DT>(a.g_v, x, y, g.kv_heads, g.D, id, step);
+      clear_tokens<DT>(a.g_k, x, y, g.kv_heads, g.D, group, groups);
+      clear_tokens<DT>(a.g_v, x, y, g.kv_heads, g.D, group, groups);
     }
     return;
   }
@@ -1034,14 +1036,22 @@ __global__ __launch_bounds__(256, DT == 1 && DP <= 64 ? 2 : 1) void k_attention_
 
 // ------------------------------------------------------------ launches
 
-constexpr unsigned GAP_GROUPS = 8;  // workgroups for the tokens of no sequence
+// Workgroups for the tokens of no sequence, of which only the device knows how many
+// there are: one for each 64 KB that all tokens would take, at most 256 (8192 tokens of 32
+// heads of 128 with as many behind them 586 us, with 64 workgroups 595, without the padding
+// 655; 64 x 197 tokens of 12 heads of 64 and 8192 behind them 29, with 64 workgroups 31).
+constexpr int64_t GAP_GROUPS = 256;
+unsigned gap_groups(const int64_t* start, int64_t rows, int D, int dtype) {
+  const int64_t bytes = rows * D * (dtype == 0 ? 4 : 2);
+  return start ? (unsigned)std::max<int64_t>(1, std::min(GAP_GROUPS, bytes >> 16)) : 0;
+}
 
 // Workgroups for the items: at most 2^20 (a launch holds fewer than 2^32
 // threads; the rest go by the loop), a multiple of 8 so that the loop keeps to an XCD.
 unsigned groups_for(unsigned items) { return items < (1u << 20) ? items : 1u << 20; }
 
 template <typename A>
-hipError_t launch_items(void (*kernel)(A), A a, int bytes, bool gaps, hipStream_t s) {
+hipError_t launch_items(void (*kernel)(A), A a, int bytes, unsigned gaps, hipStream_t s) {
   a.g.launched = groups_for(a.g.items);
   if (bytes > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
@@ -1053,7 +1063,7 @@ hipError_t launch_items(void (*kernel)(A), A a, int bytes, bool gaps, hipStream_
   }
   void* at[] = {&a};
   const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel),
-                                       dim3(a.g.launched + (gaps ? GAP_GROUPS : 0)), dim3(256), at,
+                                       dim3(a.g.launched + gaps), dim3(256), at,
                                        bytes, s);
   if (e != hipSuccess) (void)hipGetLastError();
   return e;
@@ -1084,7 +1094,7 @@ hipError_t choose(int dtype, bool bias, bool vec, F f) {
 template <>
 hipError_t launch_attention_forward<HLQ_ATTN_D>(const AttnFwd& a, int dtype, bool few,
                                                 hipStream_t s) {
-  const bool gaps = a.g.start_q != nullptr;
+  const unsigned gaps = gap_groups(a.g.start_q, a.g.Tq * a.g.heads, a.g.D, dtype);
   return choose(dtype, a.g.bias.table, a.q.vec && a.k.vec && a.v.vec, [&](auto t, auto b, auto v) {
     constexpr int DT = decltype(t)::value, DP = HLQ_ATTN_D;
     constexpr bool BIAS = decltype(b)::value, VEC = decltype(v)::value;
@@ -1104,7 +1114,7 @@ hipError_t launch_attention_backward_q<HLQ_ATTN_D>(const AttnBwd& a, int dtype, 
   return choose(dtype, a.g.bias.table, vec, [&](auto t, auto b, auto v) {
     constexpr int DT = decltype(t)::value, DP = HLQ_ATTN_D;
     constexpr bool BIAS = decltype(b)::value, VEC = decltype(v)::value;
-    const bool gaps = a.g.start_q != nullptr;
+    const unsigned gaps = gap_groups(a.g.start_q, a.g.Tq * a.g.heads, a.g.D, DT);
     if (few)
       return launch_items(k_attention_backward_q<DT, DP, BIAS, true, VEC>, a,
                           BwdShape<DT, DP, true, BIAS>::LDS + extra, gaps, s);
@@ -1120,7 +1130,7 @@ hipError_t launch_attention_backward_kv<HLQ_ATTN_D>(const AttnBwd& a, int dtype,
   return choose(dtype, a.g.bias.table, vec, [&](auto t, auto b, auto v) {
     constexpr int DT = decltype(t)::value, DP = HLQ_ATTN_D;
     constexpr bool BIAS = decltype(b)::value, VEC = decltype(v)::value;
-    const bool gaps = a.g.start_k != nullptr;
+    const unsigned gaps = gap_groups(a.g.start_k, a.g.Tk * a.g.kv_heads, a.g.D, DT);
     const int extra = bias_bytes(a.g, 1);
     if (few)
       return launch_items(
