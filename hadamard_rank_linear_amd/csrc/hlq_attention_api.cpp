@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
+#include <initializer_list>
 #include <stdint.h>
 
 #include "../../include/hlq.h"
@@ -89,6 +90,17 @@ hlq_status check_rows(const hlq_attention* a, const hlq_tokens* t, int64_t token
     if (tokens == 1 && heads > 1 && hs < D) return HLQ_ERR_SHAPE;
   }
   return HLQ_OK;
+}
+
+// Whether an output starts where another operand does.
+struct Operand {
+  const hlq_tokens* t;
+  int64_t tokens;
+};
+bool meets(const Operand& out, std::initializer_list<Operand> others) {
+  for (const Operand& x : others)
+    if (out.tokens && x.tokens && out.t->data == x.t->data) return true;
+  return false;
 }
 
 // The kernels' form of them: the stride of a single token, or head, is not looked at.
@@ -300,6 +312,8 @@ hlq_status hlq_attention_forward(const hlq_attention* a, const hlq_tokens* q, co
   const size_t need = forward_bytes(a, p);
   if (need && (!workspace || workspace_bytes < need)) return HLQ_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return HLQ_ERR_ALIGN;
+  // other workgroups still read keys and values when one writes its rows
+  if (meets({o, a->queries}, {{k, a->keys}, {v, a->keys}})) return HLQ_ERR_VALUE;
   if (a->queries == 0) return HLQ_OK;
   AttnFwd f = {};
   f.g = shape_of(a);
@@ -348,6 +362,11 @@ hlq_status hlq_attention_backward(const hlq_attention* a, const hlq_tokens* g_o,
   const size_t need = hlq_attention_backward_workspace_size(a);
   if (need && (!workspace || workspace_bytes < need)) return HLQ_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return HLQ_ERR_ALIGN;
+  // the gradients of k and v come from q and g_o after that of q is written
+  const Operand Q = {q, a->queries}, G = {g_o, a->queries}, GQ = {g_q, a->queries};
+  const Operand GK = {g_k, a->keys}, GV = {g_v, a->keys};
+  if (meets(GQ, {Q, G, {k, a->keys}, {v, a->keys}, GK, GV}) || meets(GK, {Q, G, GV}) || meets(GV, {Q, G}))
+    return HLQ_ERR_VALUE;
   AttnBwd b = {};
   b.g = shape_of(a);
   b.q = rows_of(a, q, a->queries, a->heads);

@@ -612,7 +612,9 @@ hlq_status hlq_clip_grad_norm(const void* const* grads, void* const* outs, const
    elements and not negative: a slice of what the qkv layer wrote, or of the
    gradient it will read.  Tokens are less than 2^22 elements apart, heads less than
    2^40 (a single token's or head's stride may be anything).  An input's strides may
-   be 0; outputs must not overlap themselves. */
+   be 0; outputs must not overlap themselves, each other or what the call reads (slices
+   that lie between each other are fine).  One that starts where another operand does, in
+   whose place it would give wrong results, is refused (HLQ_ERR_VALUE). */
 typedef struct hlq_tokens {
   void* data;
   int64_t token_stride, head_stride;
@@ -673,7 +675,7 @@ int hlq_relative_bucket(int distance, int buckets, int max_distance, int bidirec
  * it).  Scores, sums and statistics are fp32; for bf16 the
  * probabilities are rounded to bf16 in the product with v.
  * One launch, two with a workspace.  Errors: HLQ_ERR_NULL, HLQ_ERR_DTYPE,
- * HLQ_ERR_SHAPE, HLQ_ERR_VALUE (scale, buckets), HLQ_ERR_ALIGN,
+ * HLQ_ERR_SHAPE, HLQ_ERR_VALUE (scale, buckets, places), HLQ_ERR_ALIGN,
  * HLQ_ERR_WORKSPACE.
  */
 size_t hlq_attention_forward_workspace_size(const hlq_attention* a);
