@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import inspect
+import operator
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -786,7 +787,9 @@ def hlq_relative_bucket(distance, buckets, max_distance=128, bidirectional=True)
     near distances by themselves, farther ones by their logarithm up to
     ``max_distance``; ``bidirectional`` gives keys behind the query the table's
     second half, else they share bucket 0."""
-    b = int(_lib.hlq_relative_bucket(distance, buckets, max_distance, bool(bidirectional)))
+    low, high = -2 ** 31, 2 ** 31 - 1  # of the C int, in which ctypes would drop the bits above
+    sizes = [min(max(operator.index(n), low), high) for n in (distance, buckets, max_distance)]
+    b = int(_lib.hlq_relative_bucket(*sizes, bool(bidirectional)))
     if b < 0:
         raise ValueError(f"{buckets} buckets up to a distance of {max_distance}: out of range")
     return b

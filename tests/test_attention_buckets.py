@@ -19,3 +19,19 @@ def test_borders(side, reach, distance):
         if side <= 64:
             for s in (-d, d):
                 assert h.hlq_relative_bucket(s, 2 * side, reach, True) == o.bucket(s, 2 * side, reach, True)
+
+
+def test_numbers_beyond_32_bits():
+    """A distance is as far as the farthest; a size is out of range."""
+    far = h.hlq_relative_bucket(10 ** 6, 32), h.hlq_relative_bucket(-10 ** 6, 32)
+    for n in (2 ** 31, 2 ** 32, 2 ** 32 + 3, 2 ** 40 - 1, 2 ** 64 + 1):
+        assert (h.hlq_relative_bucket(n, 32), h.hlq_relative_bucket(-n, 32)) == far
+        for args in ((2 ** 32 + 32, 128), (32, 2 ** 32 + 128), (-2 ** 32 + 32, 128)):
+            with pytest.raises(ValueError):
+                h.hlq_relative_bucket(n, *args)
+
+
+@pytest.mark.parametrize("args", [(1.0,), (1, 32.0), (1, 32, 128.0), ("1",), (None,)])
+def test_no_integers(args):
+    with pytest.raises(TypeError):
+        h.hlq_relative_bucket(*args, *(32,)[:2 - len(args)])
