@@ -1115,9 +1115,10 @@ hipError_t launch_attention_backward_q<HLQ_ATTN_D>(const AttnBwd& a, int dtype, 
     constexpr int DT = decltype(t)::value, DP = HLQ_ATTN_D;
     constexpr bool BIAS = decltype(b)::value, VEC = decltype(v)::value;
     const unsigned gaps = gap_groups(a.g.start_q, a.g.Tq * a.g.heads, a.g.D, DT);
-    if (few)
-      return launch_items(k_attention_backward_q<DT, DP, BIAS, true, VEC>, a,
-                          BwdShape<DT, DP, true, BIAS>::LDS + extra, gaps, s);
+    if constexpr (attn_few_q(BIAS, DT, DP))
+      if (few)
+        return launch_items(k_attention_backward_q<DT, DP, BIAS, true, VEC>, a,
+                            BwdShape<DT, DP, true, BIAS>::LDS + extra, gaps, s);
     return launch_items(k_attention_backward_q<DT, DP, BIAS, false, VEC>, a,
                         BwdShape<DT, DP, false, BIAS>::LDS + extra, gaps, s);
   });

@@ -246,8 +246,7 @@ AttnShape backward_q_shape(const hlq_attention* a, bool* few) {
   g.causal = a->causal != 0;
   const int64_t rows = expected(a, a->queries) * shared;
   const int64_t units = a->sequences * (a->heads / shared);
-  // the sums of a bias's gradient leave no room for 128 rows of 512 bytes
-  *few = few_tiles(a, rows, units) && !(a->bias && a->dtype == HLQ_F32 && a->head_dim > 64);
+  *few = few_tiles(a, rows, units) && hlq::attn_few_q(a->bias != nullptr, a->dtype, a->head_dim);
   number(g, tiles_of(a, rows, a->queries * shared, *few), units, 1);
   return g;
 }

@@ -324,6 +324,9 @@ struct AttnBwd {
 };
 constexpr int ATTN_ROWS = 128;  // query rows, or keys, of a workgroup
 constexpr int ATTN_FEW = 32;    // rows of a workgroup whose waves share the keys
+// Whether the gradient of q has them: the sums of a bias's gradient leave no room in LDS
+// for a tile of 128 rows of 512 bytes.
+constexpr bool attn_few_q(bool bias, int dtype, int D) { return !(bias && dtype == 0 && D > 64); }
 constexpr int ATTN_PACK = 8;    // heads packed into the rows that go through LDS (a power of two)
 template <int DP>
 hipError_t launch_attention_forward(const AttnFwd& a, int dtype, bool few, hipStream_t s);
