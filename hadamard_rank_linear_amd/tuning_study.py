@@ -27,7 +27,7 @@ from .autograd import (HLQDropout, HLQLayerNorm, HLQLinear, HLQSelfAttention, hl
 class TokenModel(torch.nn.Module):
     """Logits [T, vocab] of the next token for tokens [T] (T a multiple of 16).
     With ``heads``, packed sequences of the bounds ``start``; ``seed`` moves on by
-    one step after each training step."""
+    one step after each batch."""
 
     def __init__(self, vocab=512, width=256, inner=512, device="cuda", dtype=torch.bfloat16,
                  heads=0, dropout=0.1):
@@ -83,9 +83,13 @@ def _update(model, lr, max_norm):
             if p.grad is not None:
                 p.add_(p.grad, alpha=-lr)
                 p.grad = None
-        if model.attention is not None:
-            model.seed[1] += 1
     return norm
+
+
+def _next_masks(model):
+    """Once per batch, whose updates are compared with its rollout under one mask."""
+    if model.attention is not None:
+        model.seed[1] += 1
 
 
 def tune_preferences(steps=20, pairs=16, length=32, vocab=512, lr=0.2, beta=0.1, seed=0, log=None,
@@ -104,6 +108,7 @@ def tune_preferences(steps=20, pairs=16, length=32, vocab=512, lr=0.2, beta=0.1,
                                            weight=(targets >= 0).float())
         loss.backward()
         norm = _update(model, lr, max_norm=1.0)
+        _next_masks(model)
         margins.append(margin.mean())
         if log:
             log(f"preference step {step:3d} loss {loss.item():.4f} margin "
@@ -135,6 +140,7 @@ def tune_policy(steps=20, tokens=1024, vocab=512, lr=0.5, updates=2, seed=0, log
                                                       kl_coef=0.01)
             logits.backward(g_x)
             norm = _update(model, lr, max_norm=1.0)
+        _next_masks(model)
         rewards.append(reward.mean())
         if log:
             log(f"policy step {step:3d} loss {sums[0].item():+.4f} KL {sums[1].item():.5f} clipped "
