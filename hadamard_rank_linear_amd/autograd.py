@@ -225,7 +225,7 @@ def hlq_clip_grad_norm_(parameters, max_norm, norm_kind=hlq.HLQ_NORM_L2):
 
 
 def _rows_dense(t):
-    return t if t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
+    return t if t.dim() == 0 or t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
 
 
 class HLQAttentionFunction(torch.autograd.Function):
@@ -264,8 +264,8 @@ class HLQPackedAttentionFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, qkv, heads, start, bias, causal, scale, max_distance, bidirectional, max_len):
-        kv = (qkv.shape[1] - heads) // 2
-        if qkv.dim() != 3 or kv < 1 or qkv.shape[1] != heads + 2 * kv:
+        kv = (qkv.shape[1] - heads) // 2 if qkv.dim() == 3 else 0
+        if heads < 1 or kv < 1 or qkv.shape[1] != heads + 2 * kv:
             raise ValueError("qkv must be [tokens, heads + 2 kv_heads, D]")
         qkv = _rows_dense(qkv)
         bias = None if bias is None else bias.contiguous()
