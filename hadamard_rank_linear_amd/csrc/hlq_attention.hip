@@ -15,12 +15,12 @@
 // Bound by the matrix unit for long sequences, by memory and the waits of a workgroup's
 // start for short ones.  Measured in bf16, where a large product reaches 1138 TFLOP/s
 // and a large copy 4.84 TB/s:
-//  - forward, 8192 tokens, 32 heads of 128 on 8: 1128 us (975 TFLOP/s), causal 595 (924);
-//    ViT-B (64 x 197 tokens, 12 heads of 64) 28 us for 78 MB; 8 tokens against 32700 keys
-//    46 us with the join (2.9 TB/s);
-//  - backward, 8192 ragged causal tokens, 32 heads of 128 on 8: 335 us for q (matrix units
-//    busy 50% of the time), 525 for k and v (34%: one wave a SIMD, of whose cycles a
-//    quarter go into its turns of the tiles' loads); ViT-B 48 + 59.
+//  - forward, 8192 tokens, 32 heads of 128 on 8: 1180 us (930 TFLOP/s), causal 577 to 667
+//    (952 to 824, with the inputs and the card's state); ViT-B (64 x 197 tokens, 12 heads of
+//    64) 29 us for 78 MB; 8 tokens against 32700 keys 51 us with the join (2.6 TB/s);
+//  - backward, 8192 ragged causal tokens, 32 heads of 128 on 8: 343 us for q (matrix units
+//    busy 50% of the time), 552 for k and v (34%: one wave a SIMD, of whose cycles a
+//    quarter go into its turns of the tiles' loads), under the profiler; ViT-B 48 + 59.
 #include <algorithm>
 #include <utility>
 
@@ -540,7 +540,8 @@ __device__ __forceinline__ void join_waves(char* lds, const f32x16 (&mine)[DP / 
 // with a bias the sums of dS by bucket over the item: each wave adds its blocks'
 // diagonals to a line of distances of its own in LDS, blocks beyond reach in
 // registers (8190 ragged tokens, 12 heads of 64: 100 us).  Three workgroups a CU of
-// heads up to 64 as above (ViT-B 48 -> 44 us), two where the line takes registers too.
+// heads up to 64 as above (ViT-B 48 -> 44 us, at 44 bytes of scratch a lane), two where the
+// line takes registers too.
 template <int DT, int DP, bool BIAS, bool FEW, bool VEC>
 __global__ __launch_bounds__(256, DT == 0 ? 1 : DP <= 64 && !BIAS && !FEW ? 3 : 2) void k_attention_backward_q(AttnBwd a) {
   typedef BwdShape<DT, DP, FEW, BIAS> F;

@@ -182,7 +182,11 @@ struct FwdPlan {
 // 28 and 101 as they are, cut 86 and 200.  With a causal mask the longest tile decides
 // up to twice as many (4096 such tokens 72 -> 51 and 195 -> 131 us, 6000 103 -> 91 and
 // 286 -> 224), but not where a cut tile fills the LDS (heads of 128, 256 tiles: 32 -> 43
-// and 101 -> 133).
+// and 101 -> 133).  All of this is bf16.  The rule takes fp32 along, where small tiles gain
+// up to here too (1024 causal tokens, 16 heads of 64: 40 and 111, whole 85 and 261) and
+// would beyond, in the forward pass and under a causal mask (4096 causal tokens, 8 heads of
+// 64: 323 and 980 as they are, cut 187 and 602; ViT-B 227 and 845, cut 204 and 720; 2048
+// tokens, 16 heads, no mask 170 and 505, cut 162 and 590).
 constexpr int64_t kUnits = 256;
 bool few_tiles(const hlq_attention* a, int64_t rows, int64_t units) {
   const bool small = a->head_dim * esize(a->dtype) <= 128;

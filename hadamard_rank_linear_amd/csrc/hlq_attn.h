@@ -78,11 +78,13 @@ __device__ __forceinline__ Frag<DT> acc_frag(const f32x16& s, int c) {
 }
 
 // What acc_frag(s, c) = f has rounded off, as a fragment of its own: the product with
-// it makes up for the rounding.  A row's score gradients sum to zero, so that the part
-// that keys have in common cancels in the gradient of q, but not in their rounding
-// errors: without this they are twice the gradient's own rounding where 0.7 of the keys'
-// size is common (ViT-B 0.0034 of g_q in all, with it 0.0017), and grow with that share.
-// It costs 2 of 46 us there, 62 of 297 on 8192 ragged tokens with heads of 128.
+// it makes up for the rounding.  With D_i from the o that is not rounded a row's score
+// gradients sum to zero, and what keys have in common cancels in the gradient of q, but not
+// in their rounding errors.  For the formula, which takes o as it is stored, this product
+// halves the error of g_q (ViT-B 0.0034 in all, with it 0.0017, that of rounding g_q).  For
+// the gradient itself it does little in bf16: there the rounding of o moves D_i, the sums
+// are not zero, and g_q is 0.0061 off (0.0068 without; keys of 24 in common 0.05).  It costs
+// 3 of 48 us there, 58 of 343 on 8192 ragged tokens with heads of 128.
 __device__ __forceinline__ bf16x8 acc_rest(const f32x16& s, int c, const bf16x8& f) {
   u32x4 w;
   __builtin_memcpy(&w, &f, 16);

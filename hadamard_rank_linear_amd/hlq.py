@@ -811,7 +811,8 @@ def hlq_attention_forward(q, k, v, start=None, start_k=None, causal=False, scale
     ``bias`` [buckets, heads] is added to the scores by
     :func:`hlq_relative_bucket` of ``max_distance`` and ``bidirectional`` (None:
     not causal).  ``max_len``: the longest sequence's queries, if known, makes the
-    launch fit; the result does not depend on it beyond rounding.  A query that
+    launch fit (without ``start`` it is not looked at); the result does not depend
+    on it beyond rounding.  Outputs share no memory with inputs.  A query that
     sees no key, and tokens outside every sequence, get o = 0 and lse = -inf.
     """
     return _native.attention_forward(q, k, v, start, start_k, causal, scale, bias, max_distance,

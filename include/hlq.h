@@ -693,8 +693,9 @@ hlq_status hlq_attention_forward(const hlq_attention* a, const hlq_tokens* q, co
  *   g_q, g_k, g_v  out, dtype;  g_bias [buckets][heads] out, bias_dtype, NULL
  *            exactly when there is no bias.
  * For bf16 P and G are rounded to bf16 in the products for g_k and g_v; that for g_q
- * takes G as two bf16 numbers (the sum of a row's G is zero, so that a part that all
- * keys share must cancel), and g_bias sums G unrounded.
+ * takes G as two bf16 numbers, and g_bias sums G unrounded.  D_i differs from that of
+ * the o before its rounding by up to 2^-8 sum_d |g_o o|, and then the sum of a row's G is
+ * not zero: a part c that all keys share leaves up to scale |c| times that in g_q.
  * Infinities and NaN reach the gradients of what they meet in a pair that is seen,
  * in elements that are not specified, and no others.
  * Two launches, three with a bias.  No atomics: a call repeats bit for bit.
