@@ -640,6 +640,8 @@ typedef struct hlq_tokens {
  *   scale     2^-64 to 2^64.
  *   bias      [buckets][heads] of bias_dtype or NULL: added to scale * q k, by the
  *             bucket of d = key position - query position (hlq_relative_bucket).
+ *             Entries below -2^127 * 1.4 (the types' lowest values among them) hide
+ *             their bucket as -inf does.
  * Fewer than 2^30 queries times heads and keys times heads, 2^16 heads.
  */
 typedef struct hlq_attention {
